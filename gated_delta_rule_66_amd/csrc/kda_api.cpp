@@ -1164,6 +1164,10 @@ int kda_profile_stop(const char** names, float* ms, int cap) {
 
 namespace kda {
 
+hipError_t profiled_launch(const char* name, hipStream_t st, hipError_t (*fn)(void*), void* arg) {
+    return launch_timed(name, st, [&] { return fn(arg); });
+}
+
 // kda_chunk_fwd_planned with the workspace bounded to ws_cap bytes (see
 // kda_internal.h).  launch false: checks and plan choice only.
 kda_status chunk_fwd_bounded(int B, int T, int H, int K, int V, kda_dtype dt, const void* q, const void* k,

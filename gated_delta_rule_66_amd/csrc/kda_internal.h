@@ -298,4 +298,11 @@ kda_status chunk_fwd_bounded(int B, int T, int H, int K, int V, kda_dtype dt, co
                              void* o, float* final_state, const kda_plan* plan, void* ws, size_t ws_cap,
                              bool launch, hipStream_t stream);
 
+// Per-launch timing (kda_profile_start) for launches outside the KDA calls:
+// runs fn(arg), bracketed by events while timing is on.
+hipError_t profiled_launch(const char* name, hipStream_t st, hipError_t (*fn)(void*), void* arg);
+template <class F> hipError_t profiled(const char* name, hipStream_t st, F&& f) {
+    return profiled_launch(name, st, [](void* a) { return (*static_cast<F*>(a))(); }, &f);
+}
+
 }  // namespace kda

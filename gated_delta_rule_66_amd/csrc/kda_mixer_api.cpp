@@ -1,0 +1,497 @@
+// C ABI of the mixer operators: argument validation, launch plans, launches.
+// The declarations and their contracts are in include/kda.h.
+#include "kda.h"
+#include "kda_internal.h"
+#include "kda_mixer.h"
+
+#include <stdint.h>
+
+#include <initializer_list>
+
+using namespace kda;
+
+namespace {
+
+size_t esize(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
+bool dtype_ok(kda_dtype dt) { return dt == KDA_F32 || dt == KDA_BF16; }
+bool act_ok(kda_activation a) { return a == KDA_ACT_NONE || a == KDA_ACT_SILU || a == KDA_ACT_SIGMOID; }
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// byte ranges [a, a + na) and [b, b + nb) share a byte
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    if (!a || !b || !na || !nb) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y ? y - x < na : x - y < nb;
+}
+// bytes from the first to the last element of `rows` rows of `width` elements
+size_t extent(long long rows, long long stride, long long width, size_t es) {
+    return rows > 0 ? (size_t)((rows - 1) * stride + width) * es : 0;
+}
+// tokens of a call; row indices are int in the kernels
+bool token_count(const int* cu, int N, int T, long long* M) {
+    *M = cu ? (long long)T : (long long)N * T;
+    return *M <= 2147483647LL - 4096;
+}
+bool vec_ok(kda_dtype dt, long long width, long long stride, const void* p) {
+    return width % (long long)(16 / esize(dt)) == 0 && stride % (long long)(16 / esize(dt)) == 0 && aligned(p, 16);
+}
+
+#define KDA_LAUNCH(name, call)                                                          \
+    do {                                                                                \
+        if (profiled(name, stream, [&] { return call; }) != hipSuccess) return KDA_ERR_HIP; \
+    } while (0)
+
+// ---- short convolution ---------------------------------------------------------------
+
+kda_status conv_sizes(int N, int T, int D, int W, kda_dtype dt, kda_activation act, const int* cu, long long* M) {
+    if (N < 0 || T < 0 || D < 0 || !dtype_ok(dt) || !act_ok(act)) return KDA_ERR_INVALID_ARG;
+    if (W < 2 || W > 4) return KDA_ERR_UNSUPPORTED;
+    if (!token_count(cu, N, T, M) || (long long)N * (W - 1) > 2147483647LL || D > (1 << 22)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// threads of a block along the channels: as many as the channels fill, at most `most`
+int cx_log2_for(int D, int V, int most_log2) {
+    int l = 0;
+    while (l < most_log2 && (V << l) < D) ++l;
+    return l;
+}
+
+// Tiles of a call.  A tile shorter than 16 tokens re-reads more halo rows (3 of
+// 8); a long one leaves a short call with few threads.
+void conv_tiles(ConvParams& p, long long M, int tile) {
+    p.tile_tokens = tile;
+    if (p.sv.cu) {
+        p.tiles_per_seq = 0;
+        p.tiles = (int)((M + tile - 1) / tile);
+    } else {
+        p.tiles_per_seq = (p.sv.T + tile - 1) / tile;
+        p.tiles = p.sv.N * p.tiles_per_seq;
+    }
+}
+
+// Blocks of the backward along the tiles: enough threads to cover the card,
+// each block leaving one partial row of parameter sums.
+struct ConvBwdPlan {
+    int cx_log2, tile, blocks;
+};
+ConvBwdPlan conv_bwd_plan(bool packed, int N, int T, int D, int V) {
+    ConvBwdPlan b;
+    b.cx_log2 = cx_log2_for(D, V, 5);
+    const long long tys = 256 >> b.cx_log2, cb = (D + (V << b.cx_log2) - 1) / (V << b.cx_log2);
+    b.tile = 32;
+    const long long M = packed ? (long long)T : (long long)N * T;
+    const long long tiles = packed ? (M + b.tile - 1) / b.tile : (long long)N * ((T + b.tile - 1) / b.tile);
+    long long want = (tiles + tys - 1) / tys, most = cb > 0 ? 2048 / cb : 1;
+    if (most < 64) most = 64;
+    if (want > most) want = most;
+    b.blocks = (int)(want > 0 ? want : 1);
+    return b;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_short_conv_fwd(int N, const int* cu_seqlens, int T, int D, int W, kda_dtype dt, kda_activation act,
+                              const void* x, long long x_stride, const float* weight, const float* bias,
+                              const void* initial_state, void* y, void* final_state, hipStream_t stream) {
+    long long M;
+    kda_status s = conv_sizes(N, T, D, W, dt, act, cu_seqlens, &M);
+    if (s != KDA_OK) return s;
+    if (N == 0 || D == 0) return KDA_OK;
+    const size_t es = esize(dt);
+    if (!weight || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
+    if (M > 0 && (!x || !y || x_stride < D)) return KDA_ERR_INVALID_ARG;
+    for (const void* t : {x, initial_state, (const void*)y, (const void*)final_state})
+        if (!aligned(t, es)) return KDA_ERR_INVALID_ARG;
+    const size_t state = (size_t)N * (W - 1) * D * es, xb = extent(M, x_stride, D, es), yb = (size_t)M * D * es;
+    if (overlap(x, xb, y, yb) || overlap(initial_state, state, final_state, state) || overlap(x, xb, final_state, state) ||
+        overlap(initial_state, state, y, yb))
+        return KDA_ERR_INVALID_ARG;
+    if (M == 0 && !final_state) return KDA_OK;
+    ConvParams p{};
+    p.sv = SeqView{cu_seqlens, N, T};
+    p.D = D; p.W = W; p.act = (int)act;
+    p.x = x; p.x_stride = (size_t)x_stride;
+    p.weight = weight; p.bias = bias; p.s0 = initial_state;
+    p.y = y; p.sT = final_state;
+    const bool vec = vec_ok(dt, D, M > 1 ? x_stride : D, x) && aligned(y, 16) && aligned(initial_state, 16) &&
+                     aligned(final_state, 16);
+    const int V = vec ? (int)(16 / es) : 1;
+    p.cx_log2 = cx_log2_for(D, V, 8);
+    conv_tiles(p, M, M * (D / V) >= (1LL << 21) ? 16 : 8);
+    const int tys = 256 >> p.cx_log2;
+    // one more row of blocks passes on the states of sequences without tokens
+    const int blocks = (p.tiles + tys - 1) / tys + (final_state && (cu_seqlens || T == 0) ? 1 : 0);
+    if (blocks == 0) return KDA_OK;
+    if ((long long)blocks * 256 >= 1LL << 32) return KDA_ERR_UNSUPPORTED;
+    KDA_LAUNCH("short_conv", launch_conv_fwd((int)dt, vec, p, blocks, stream));
+    return KDA_OK;
+}
+
+size_t kda_short_conv_bwd_workspace_size(int N, int packed, int T, int D, int W, kda_dtype dt) {
+    long long M;
+    const int some = 0;
+    if (conv_sizes(N, T, D, W, dt, KDA_ACT_NONE, packed ? &some : nullptr, &M) != KDA_OK) return (size_t)-1;
+    if (N == 0 || D == 0) return 0;
+    // either access width: the narrow one has the fewer channels a block
+    const ConvBwdPlan a = conv_bwd_plan(packed != 0, N, T, D, 1), b = conv_bwd_plan(packed != 0, N, T, D, (int)(16 / esize(dt)));
+    return (size_t)(a.blocks > b.blocks ? a.blocks : b.blocks) * (W + 1) * D * sizeof(float);
+}
+
+kda_status kda_short_conv_bwd(int N, const int* cu_seqlens, int T, int D, int W, kda_dtype dt, kda_activation act,
+                              const void* x, long long x_stride, const float* weight, const float* bias,
+                              const void* initial_state, const void* d_y, const void* d_final_state, void* dx,
+                              float* dweight, float* dbias, void* d_initial_state, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+    long long M;
+    kda_status s = conv_sizes(N, T, D, W, dt, act, cu_seqlens, &M);
+    if (s != KDA_OK) return s;
+    if (D == 0) return KDA_OK;
+    const size_t es = esize(dt);
+    if (!weight || !dweight) return KDA_ERR_INVALID_ARG;
+    for (const void* t : {(const void*)weight, (const void*)bias, (const void*)cu_seqlens, (const void*)dweight,
+                          (const void*)dbias})
+        if (!aligned(t, 4)) return KDA_ERR_INVALID_ARG;
+    if (M > 0 && N > 0 && (!x || !d_y || !dx || x_stride < D)) return KDA_ERR_INVALID_ARG;
+    for (const void* t : {x, initial_state, d_y, d_final_state, (const void*)dx, (const void*)d_initial_state})
+        if (!aligned(t, es)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return KDA_ERR_INVALID_ARG;
+    const size_t state = (size_t)N * (W - 1) * D * es, xb = extent(M, x_stride, D, es), yb = (size_t)M * D * es;
+    if (overlap(x, xb, dx, yb) || overlap(d_y, yb, dx, yb) || overlap(d_final_state, state, d_initial_state, state) ||
+        overlap(initial_state, state, d_initial_state, state) || overlap(initial_state, state, dx, yb) ||
+        overlap(d_final_state, state, dx, yb))
+        return KDA_ERR_INVALID_ARG;
+    if (N == 0) {
+        KDA_LAUNCH("short_conv_bwd_sums", launch_sum_rows(nullptr, 0, W + 1, D, dweight, W, dbias, stream));
+        return KDA_OK;
+    }
+    if (!workspace || workspace_bytes < kda_short_conv_bwd_workspace_size(N, cu_seqlens != nullptr, T, D, W, dt))
+        return KDA_ERR_WORKSPACE;
+    ConvParams p{};
+    p.sv = SeqView{cu_seqlens, N, T};
+    p.D = D; p.W = W; p.act = (int)act;
+    p.x = x; p.x_stride = (size_t)x_stride;
+    p.weight = weight; p.bias = bias; p.s0 = initial_state;
+    p.d_y = d_y; p.d_sT = d_final_state; p.dx = dx; p.d_s0 = d_initial_state;
+    p.part = reinterpret_cast<float*>(workspace);
+    bool vec = vec_ok(dt, D, M > 1 ? x_stride : D, x);
+    for (const void* t : {initial_state, d_y, d_final_state, (const void*)dx, (const void*)d_initial_state})
+        vec = vec && aligned(t, 16);
+    const ConvBwdPlan b = conv_bwd_plan(cu_seqlens != nullptr, N, T, D, vec ? (int)(16 / es) : 1);
+    p.cx_log2 = b.cx_log2;
+    conv_tiles(p, M, b.tile);
+    KDA_LAUNCH("short_conv_bwd", launch_conv_bwd((int)dt, vec, p, b.blocks, stream));
+    KDA_LAUNCH("short_conv_bwd_sums", launch_sum_rows(p.part, b.blocks, W + 1, D, dweight, W, dbias, stream));
+    return KDA_OK;
+}
+
+kda_status kda_short_conv_step(int N, int D, int W, kda_dtype dt, kda_activation act, const void* x,
+                               long long x_stride, const float* weight, const float* bias, void* state, void* y,
+                               hipStream_t stream) {
+    long long M;
+    kda_status s = conv_sizes(N, 1, D, W, dt, act, nullptr, &M);
+    if (s != KDA_OK) return s;
+    if (N == 0 || D == 0) return KDA_OK;
+    const size_t es = esize(dt);
+    if (!x || !weight || !state || !y || x_stride < D || !aligned(weight, 4) || !aligned(bias, 4)) return KDA_ERR_INVALID_ARG;
+    for (const void* t : {x, (const void*)state, (const void*)y})
+        if (!aligned(t, es)) return KDA_ERR_INVALID_ARG;
+    const size_t sb = (size_t)N * (W - 1) * D * es, xb = extent(N, x_stride, D, es), yb = (size_t)N * D * es;
+    if (overlap(x, xb, state, sb) || overlap(x, xb, y, yb) || overlap(state, sb, y, yb)) return KDA_ERR_INVALID_ARG;
+    const bool vec = vec_ok(dt, D, N > 1 ? x_stride : D, x) && aligned(state, 16) && aligned(y, 16);
+    if ((long long)N * D / (vec ? (long long)(16 / es) : 1) >= (1LL << 32) - 256) return KDA_ERR_UNSUPPORTED;
+    KDA_LAUNCH("short_conv_step", launch_conv_step((int)dt, vec, N, D, W, (int)act, x, (size_t)x_stride, weight, bias,
+                                                   state, y, stream));
+    return KDA_OK;
+}
+
+// ---- group norm ------------------------------------------------------------------------
+
+static kda_status norm_check(int rows, int C, int groups, kda_dtype dt, kda_activation act, const void* x,
+                             long long x_stride, const float* weight, const float* bias, const void* gate,
+                             long long gate_stride) {
+    if (rows < 0 || C <= 0 || groups <= 0 || C % groups || !dtype_ok(dt) || !act_ok(act)) return KDA_ERR_INVALID_ARG;
+    int R, team, block;
+    if (!norm_variant((int)dt, false, C / groups, &R, &team, &block) &&
+        !(norm_variant((int)dt, true, C / groups, &R, &team, &block) && (C / groups) % (16 / esize(dt)) == 0))
+        return KDA_ERR_UNSUPPORTED;
+    if ((long long)rows * groups > 2147483647LL) return KDA_ERR_UNSUPPORTED;
+    if (!aligned(weight, 4) || !aligned(bias, 4) || !aligned(x, esize(dt)) || !aligned(gate, esize(dt)))
+        return KDA_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || x_stride < C || (gate && gate_stride < C))) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+// fills the parameters and the kernel variant
+static kda_status norm_setup(int rows, int C, int groups, kda_dtype dt, kda_activation act, int center,
+                             int gate_first, float eps, const void* x, long long x_stride, const float* weight,
+                             const float* bias, const void* gate, long long gate_stride, bool vec, NormParams* p,
+                             int* R, int* block) {
+    *p = NormParams{};
+    p->rows = rows; p->C = C; p->G = groups; p->Cg = C / groups;
+    p->act = (int)act; p->center = center != 0; p->gate_first = gate_first != 0; p->eps = eps;
+    p->x = x; p->x_stride = (size_t)x_stride;
+    p->z = gate; p->z_stride = (size_t)gate_stride;
+    p->weight = weight; p->bias = bias;
+    if (!norm_variant((int)dt, vec, p->Cg, R, &p->team, block)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+kda_status kda_group_norm_fwd(int rows, int C, int groups, kda_dtype dt, kda_activation act, int center,
+                              int gate_first, float eps, const void* x, long long x_stride, const float* weight,
+                              const float* bias, const void* gate, long long gate_stride, void* y,
+                              hipStream_t stream) {
+    kda_status s = norm_check(rows, C, groups, dt, act, x, x_stride, weight, bias, gate, gate_stride);
+    if (s != KDA_OK) return s;
+    if (rows == 0) return KDA_OK;
+    const size_t es = esize(dt);
+    if (!y || !aligned(y, es)) return KDA_ERR_INVALID_ARG;
+    // a value is read before it is written only by its own team: y may be x or
+    // the gate exactly, not partly
+    const size_t yb = (size_t)rows * C * es, xb = extent(rows, x_stride, C, es);
+    if ((overlap(x, xb, y, yb) && !(x == y && (rows == 1 || x_stride == C))) ||
+        (gate && overlap(gate, extent(rows, gate_stride, C, es), y, yb) && !(gate == y && (rows == 1 || gate_stride == C))))
+        return KDA_ERR_INVALID_ARG;
+    bool vec = vec_ok(dt, C / groups, rows > 1 ? x_stride : C, x) && aligned(y, 16);
+    if (gate) vec = vec && vec_ok(dt, C / groups, rows > 1 ? gate_stride : C, gate);
+    NormParams p;
+    int R, block;
+    s = norm_setup(rows, C, groups, dt, act, center, gate_first, eps, x, x_stride, weight, bias, gate, gate_stride, vec,
+                   &p, &R, &block);
+    if (s != KDA_OK) return s;
+    p.y = y;
+    const long long per = p.team <= 64 ? 256 / p.team : 1;
+    if (((long long)rows * groups / per + 1) * block >= 1LL << 32) return KDA_ERR_UNSUPPORTED;
+    KDA_LAUNCH("group_norm", launch_norm_fwd((int)dt, vec, R, block, p, stream));
+    return KDA_OK;
+}
+
+// Row blocks of the backward: about eight blocks a CU over all groups, each
+// leaving one partial row of parameter sums.
+static int norm_row_blocks(int rows, int groups, int team) {
+    const long long teams = team <= 64 ? 256 / team : 1;
+    long long want = (rows + teams - 1) / teams, most = 2048 / groups;
+    if (most < 16) most = 16;
+    return (int)(want < most ? (want > 0 ? want : 1) : most);
+}
+
+size_t kda_group_norm_bwd_workspace_size(int rows, int C, int groups, kda_dtype dt) {
+    if (norm_check(0, C, groups, dt, KDA_ACT_NONE, nullptr, C, nullptr, nullptr, nullptr, C) != KDA_OK || rows < 0)
+        return (size_t)-1;
+    int R, team, block, most = 1;
+    for (int vec = 0; vec < 2; ++vec)
+        if (norm_variant((int)dt, vec != 0, C / groups, &R, &team, &block)) {
+            const int b = norm_row_blocks(rows, groups, team);
+            most = b > most ? b : most;
+        }
+    return (size_t)most * 2 * C * sizeof(float);
+}
+
+kda_status kda_group_norm_bwd(int rows, int C, int groups, kda_dtype dt, kda_activation act, int center,
+                              int gate_first, float eps, const void* x, long long x_stride, const float* weight,
+                              const float* bias, const void* gate, long long gate_stride, const void* d_y, void* dx,
+                              float* dweight, float* dbias, void* d_gate, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+    kda_status s = norm_check(rows, C, groups, dt, act, x, x_stride, weight, bias, gate, gate_stride);
+    if (s != KDA_OK) return s;
+    const size_t es = esize(dt);
+    for (const void* t : {d_y, (const void*)dx, (const void*)d_gate})
+        if (!aligned(t, es)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(dweight, 4) || !aligned(dbias, 4) || !aligned(workspace, 16)) return KDA_ERR_INVALID_ARG;
+    if (rows > 0 && (!d_y || !dx || (gate != nullptr) != (d_gate != nullptr))) return KDA_ERR_INVALID_ARG;
+    const size_t yb = (size_t)rows * C * es, xb = extent(rows, x_stride, C, es),
+                 zb = gate ? extent(rows, gate_stride, C, es) : 0;
+    // the outputs are written while other rows are still to be read
+    for (const void* o : {(const void*)dx, (const void*)d_gate})
+        if (overlap(o, o ? yb : 0, x, xb) || overlap(o, o ? yb : 0, gate, zb) || overlap(o, o ? yb : 0, d_y, yb))
+            return KDA_ERR_INVALID_ARG;
+    if (overlap(dx, yb, d_gate, d_gate ? yb : 0)) return KDA_ERR_INVALID_ARG;
+    const bool sums = dweight || dbias;
+    if (sums && rows > 0 &&
+        (!workspace || workspace_bytes < kda_group_norm_bwd_workspace_size(rows, C, groups, dt)))
+        return KDA_ERR_WORKSPACE;
+    int blocks = 0;
+    NormParams p;
+    if (rows > 0) {
+        bool vec = vec_ok(dt, C / groups, rows > 1 ? x_stride : C, x) && aligned(d_y, 16) && aligned(dx, 16) &&
+                   aligned(d_gate, 16);
+        if (gate) vec = vec && vec_ok(dt, C / groups, rows > 1 ? gate_stride : C, gate);
+        int R, block;
+        s = norm_setup(rows, C, groups, dt, act, center, gate_first, eps, x, x_stride, weight, bias, gate, gate_stride,
+                       vec, &p, &R, &block);
+        if (s != KDA_OK) return s;
+        p.d_y = d_y; p.dx = dx; p.dz = d_gate;
+        p.part = sums ? reinterpret_cast<float*>(workspace) : nullptr;
+        blocks = norm_row_blocks(rows, groups, p.team);
+        KDA_LAUNCH("group_norm_bwd", launch_norm_bwd((int)dt, vec, R, block, p, blocks, stream));
+    }
+    if (sums)
+        KDA_LAUNCH("group_norm_bwd_sums", launch_sum_rows(reinterpret_cast<const float*>(workspace), blocks, 2, C,
+                                                          dweight, 1, dbias, stream));
+    return KDA_OK;
+}
+
+// ---- selective scan ----------------------------------------------------------------------
+
+static kda_status ssm_sizes(int N, const int* cu, int T, int H, int G, int K, int P, kda_dtype dt, long long* M) {
+    if (N < 0 || T < 0 || H < 0 || G <= 0 || K <= 0 || P <= 0 || !dtype_ok(dt)) return KDA_ERR_INVALID_ARG;
+    if (H % G) return KDA_ERR_INVALID_ARG;
+    if (!(K == 64 || K == 128) || !(P == 64 || P == 128)) return KDA_ERR_UNSUPPORTED;
+    if (!token_count(cu, N, T, M)) return KDA_ERR_UNSUPPORTED;
+    // chunk and workgroup counts stay within int
+    if (*M / 64 + N > 1 << 26 || (long long)H * K * P > 1LL << 30 || (long long)N * H * (P / 64) >= 1 << 24) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// column tiles a wave: 128 columns a workgroup (one head of 128, or two heads
+// of 64 of one group, which share B, C and the scores) where the heads pair up
+static int ssm_nt(int H, int G, int P) { return P == 128 || (H / G) % 2 == 0 ? 2 : 1; }
+
+struct SsmPlan {
+    int nt, chunks, chunks_per_seq, n_seg, cps;
+};
+static SsmPlan ssm_plan(bool packed, int N, long long M, int T, int H, int G, int P) {
+    SsmPlan pl;
+    pl.nt = ssm_nt(H, G, P);
+    pl.chunks_per_seq = T > 0 ? (T + 63) / 64 : 1;
+    pl.chunks = packed ? (int)(M / 64 + N) : N * pl.chunks_per_seq;
+    const long long units = H / (64 * pl.nt / P);
+    // segments until two workgroups a CU run, each keeping at least four chunks
+    long long want = (512 + units - 1) / units, cap = pl.chunks / 4;
+    if (want > cap) want = cap;
+    if (want < 1 || units >= 256) want = 1;
+    pl.cps = (int)((pl.chunks + want - 1) / want);
+    if (pl.cps < 1) pl.cps = 1;
+    pl.n_seg = (pl.chunks + pl.cps - 1) / pl.cps;
+    return pl;
+}
+
+struct SsmLayout {
+    size_t off, seg, dec, s0, total;
+};
+static SsmLayout ssm_layout(bool packed, int N, int H, int K, int P, const SsmPlan& pl) {
+    SsmLayout L;
+    size_t o = 0;
+    const size_t kp = (size_t)K * P * sizeof(float);
+    L.off = o; o += packed ? align256((size_t)(N + 1) * sizeof(int)) : 0;
+    L.seg = o; o += pl.n_seg > 1 ? align256((size_t)pl.n_seg * H * kp) : 0;
+    L.dec = o; o += pl.n_seg > 1 ? align256((size_t)pl.n_seg * H * sizeof(float)) : 0;
+    // a copy of the initial states where the final states overwrite them
+    L.s0 = o; o += pl.n_seg > 1 ? align256((size_t)N * H * kp) : 0;
+    L.total = o;
+    return L;
+}
+
+size_t kda_selective_scan_fwd_workspace_size(int N, int packed, int T, int H, int G, int K, int P, kda_dtype dt) {
+    long long M;
+    const int some = 0;
+    if (ssm_sizes(N, packed ? &some : nullptr, T, H, G, K, P, dt, &M) != KDA_OK) return (size_t)-1;
+    if (N == 0 || H == 0) return 0;
+    return ssm_layout(packed != 0, N, H, K, P, ssm_plan(packed != 0, N, M, T, H, G, P)).total;
+}
+
+// pointer checks shared by the scan's calls
+static kda_status ssm_pointers(long long M, int H, int G, int K, int P, kda_dtype dt, const void* x, long long xs,
+                               const void* dtp, long long ds, const float* A, const void* B, long long bs, const void* Cm,
+                               long long cs, const float* D, const float* dt_bias, const float* s0) {
+    const size_t es = esize(dt);
+    if (!A || !aligned(A, 4) || !aligned(D, 4) || !aligned(dt_bias, 4) || !aligned(s0, 16)) return KDA_ERR_INVALID_ARG;
+    if (M == 0) return KDA_OK;
+    if (!x || !dtp || !B || !Cm || !aligned(dtp, es)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(B, 16) || !aligned(Cm, 16)) return KDA_ERR_INVALID_ARG;
+    const long long e = 16 / (long long)es;
+    if (ds < H || xs < (long long)H * P || bs < (long long)G * K || cs < (long long)G * K || xs % e || bs % e || cs % e)
+        return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, int G, int K, int P, kda_dtype dt,
+                                  int dt_softplus, const void* x, long long x_stride, const void* delta,
+                                  long long delta_stride, const float* A, const void* B, long long b_stride, const void* C,
+                                  long long c_stride, const float* D, const float* dt_bias,
+                                  const float* initial_state, void* y, float* final_state, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream) {
+    long long M;
+    kda_status s = ssm_sizes(N, cu_seqlens, T, H, G, K, P, dt, &M);
+    if (s != KDA_OK) return s;
+    if (N == 0 || H == 0) return KDA_OK;
+    s = ssm_pointers(M, H, G, K, P, dt, x, x_stride, delta, delta_stride, A, B, b_stride, C, c_stride, D, dt_bias, initial_state);
+    if (s != KDA_OK) return s;
+    if (!aligned(cu_seqlens, 4) || !aligned(workspace, 16) || !aligned(final_state, 16) || !aligned(y, 16))
+        return KDA_ERR_INVALID_ARG;
+    if (M > 0 && !y) return KDA_ERR_INVALID_ARG;
+    const size_t es = esize(dt), state = (size_t)N * H * K * P * sizeof(float), yb = (size_t)M * H * P * es;
+    const size_t xb = extent(M, x_stride, (long long)H * P, es), bb = extent(M, b_stride, (long long)G * K, es),
+                 cb = extent(M, c_stride, (long long)G * K, es);
+    if (overlap(y, yb, x, xb) || overlap(y, yb, B, bb) || overlap(y, yb, C, cb) ||
+        overlap(y, yb, delta, extent(M, delta_stride, H, es)) || overlap(y, yb, initial_state, state))
+        return KDA_ERR_INVALID_ARG;
+    if (initial_state != final_state && overlap(initial_state, state, final_state, state)) return KDA_ERR_INVALID_ARG;
+    const bool packed = cu_seqlens != nullptr;
+    const SsmPlan pl = ssm_plan(packed, N, M, T, H, G, P);
+    const SsmLayout L = ssm_layout(packed, N, H, K, P, pl);
+    if (L.total > 0 && (!workspace || workspace_bytes < L.total)) return KDA_ERR_WORKSPACE;
+    unsigned char* ws = reinterpret_cast<unsigned char*>(workspace);
+    SsmParams p{};
+    p.sv = SeqView{cu_seqlens, N, T};
+    p.H = H; p.G = G; p.K = K; p.P = P; p.softplus = dt_softplus != 0;
+    p.x = x; p.x_stride = (size_t)x_stride;
+    p.dt = delta; p.dt_stride = (size_t)delta_stride; p.A = A; p.dt_bias = dt_bias; p.Dskip = D;
+    p.B = B; p.b_stride = (size_t)b_stride;
+    p.C = C; p.c_stride = (size_t)c_stride;
+    p.s0 = initial_state;
+    p.chunks = pl.chunks; p.chunks_per_seq = pl.chunks_per_seq;
+    p.n_seg = pl.n_seg; p.cps = pl.cps;
+    if (packed) {
+        int* off = reinterpret_cast<int*>(ws + L.off);
+        KDA_LAUNCH("scan_prep", launch_ssm_prep(p.sv, off, pl.chunks, stream));
+        p.chunk_off = off;
+    }
+    if (pl.n_seg > 1) {
+        if (initial_state && initial_state == final_state) {
+            // segments read initial states while others write final ones
+            float* copy = reinterpret_cast<float*>(ws + L.s0);
+            KDA_LAUNCH("copy_state", launch_copy_state(initial_state, copy, (size_t)N * H * K * P, stream));
+            p.s0 = copy;
+        }
+        p.seg_state = reinterpret_cast<float*>(ws + L.seg);
+        p.seg_decay = reinterpret_cast<float*>(ws + L.dec);
+        KDA_LAUNCH("scan_summary", launch_ssm_chunks((int)dt, false, pl.nt, p, pl.n_seg - 1, stream));
+        KDA_LAUNCH("scan_combine", launch_ssm_combine(p, stream));
+    }
+    p.y = y;
+    p.sT = final_state;
+    KDA_LAUNCH("scan_output", launch_ssm_chunks((int)dt, true, pl.nt, p, pl.n_seg, stream));
+    return KDA_OK;
+}
+
+kda_status kda_selective_scan_step(int N, int H, int G, int K, int P, kda_dtype dt, int dt_softplus, const void* x,
+                                   long long x_stride, const void* delta, long long delta_stride, const float* A,
+                                   const void* B,
+                                   long long b_stride, const void* C, long long c_stride, const float* D,
+                                   const float* dt_bias, float* state, void* y, hipStream_t stream) {
+    long long M;
+    kda_status s = ssm_sizes(N, nullptr, 1, H, G, K, P, dt, &M);
+    if (s != KDA_OK) return s;
+    if (N == 0 || H == 0) return KDA_OK;
+    s = ssm_pointers(M, H, G, K, P, dt, x, x_stride, delta, delta_stride, A, B, b_stride, C, c_stride, D, dt_bias, state);
+    if (s != KDA_OK) return s;
+    if (!state || !y || !aligned(y, 16)) return KDA_ERR_INVALID_ARG;
+    const size_t es = esize(dt), sb = (size_t)N * H * K * P * sizeof(float), yb = (size_t)N * H * P * es;
+    const size_t xb = extent(N, x_stride, (long long)H * P, es), bb = extent(N, b_stride, (long long)G * K, es),
+                 cb = extent(N, c_stride, (long long)G * K, es), db = extent(N, delta_stride, H, es);
+    for (const void* o : {(const void*)y, (const void*)state}) {
+        const size_t n = o == y ? yb : sb;
+        if (overlap(o, n, x, xb) || overlap(o, n, B, bb) || overlap(o, n, C, cb) || overlap(o, n, delta, db))
+            return KDA_ERR_INVALID_ARG;
+    }
+    if (overlap(y, yb, state, sb)) return KDA_ERR_INVALID_ARG;
+    KDA_LAUNCH("scan_step", launch_ssm_step((int)dt, N, H, G, K, P, dt_softplus != 0, x, (size_t)x_stride, delta, (size_t)delta_stride, A, B,
+                                            (size_t)b_stride, C, (size_t)c_stride, D, dt_bias, state, y, stream));
+    return KDA_OK;
+}
+
+}  // extern "C"

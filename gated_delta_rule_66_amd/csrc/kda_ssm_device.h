@@ -1,0 +1,178 @@
+// Device helpers of the selective scan, forward and backward.
+#pragma once
+
+#include "kda_mixer.h"
+#include "kda_mixer_device.h"
+
+namespace kda {
+
+// delta = softplus(raw) = log1p(exp(raw)), kept from overflowing; its
+// derivative is sigmoid(raw)
+__device__ __forceinline__ float softplus_of(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+
+// 2^e for an fp64 exponent as fp32: the fraction on the transcendental unit,
+// the integer part exactly.  An fp32 e of magnitude 100 would be off by
+// 100 * 2^-24 already; here only the fraction is rounded.
+__device__ __forceinline__ float exp2_of(double e) {
+    const double r = rint(e);
+    const float f = fast_exp2((float)(e - r));
+    return ldexpf(f, (int)fmin(fmax(r, -1000.0), 1000.0));
+}
+
+// Position in the call's chunks.
+struct ChunkWalk {
+    SeqView sv;
+    const int* off;
+    int per_seq;
+    int seq, k, nk;     // sequence, chunk in it, its chunks
+    int s0, len_seq;
+
+    __device__ __forceinline__ void enter(int s) {
+        seq = s;
+        if (sv.cu) {
+            nk = off[s + 1] - off[s];
+            s0 = min(max(sv.cu[s], 0), sv.T);
+            len_seq = max(min(sv.cu[s + 1], sv.T) - s0, 0);
+        } else {
+            nk = per_seq;
+            s0 = s * sv.T;
+            len_seq = sv.T;
+        }
+    }
+    __device__ __forceinline__ void init(const SsmParams& p, int c) {
+        sv = p.sv;
+        off = p.chunk_off;
+        per_seq = p.chunks_per_seq;
+        if (sv.cu) {
+            int lo = 0, hi = sv.N;      // off[lo] <= c < off[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (off[mid] <= c)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            enter(lo);
+            k = c - off[lo];
+        } else {
+            const int s = c / per_seq;
+            enter(s);
+            k = c - s * per_seq;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        if (++k == nk && seq + 1 < sv.N) {
+            enter(seq + 1);
+            k = 0;
+        }
+    }
+    __device__ __forceinline__ void prev() {
+        if (--k < 0 && seq > 0) {
+            enter(seq - 1);
+            k = nk - 1;
+        }
+    }
+    __device__ __forceinline__ bool first() const { return k == 0; }
+    __device__ __forceinline__ bool last() const { return k == nk - 1; }
+    __device__ __forceinline__ int t0() const { return s0 + k * kSsmChunk; }
+    __device__ __forceinline__ int len() const { return min(kSsmChunk, max(len_seq - k * kSsmChunk, 0)); }
+};
+
+__device__ __forceinline__ int total_chunks(const SsmParams& p) {
+    return p.sv.cu ? min(p.chunk_off[p.sv.N], p.chunks) : p.chunks;
+}
+
+// Workgroups go to the 8 XCDs in turn.  The work index of a block such that
+// each XCD takes a contiguous range: the heads of a segment, which read the
+// same B and C rows, then meet in one XCD's L2.
+__device__ __forceinline__ int xcd_swizzle(int id, int total) {
+    const int q = total >> 3, r = total & 7, x = id & 7;
+    return x * q + min(x, r) + (id >> 3);
+}
+
+// ---- fragments whose slots run over the tokens (rows) of an LDS tile ----------------
+// lane l: column n0 + l % 16, slots (g, i) -> token tok0 + 16 (i / 4) + 4 g + i % 4
+// (the permuted slots of ld_frag_perm).
+// bf16: ds_read_b64_tr_b16 transposes 16 tokens x 16 columns across 16 lanes:
+// lane r of a group reads four columns of token r / 4, and gets four tokens of
+// column r.
+__device__ __forceinline__ bf16x4 ld_tr4(const bf16* p) {
+    typedef __attribute__((address_space(3))) bf16x4 lds_x4;
+    return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_x4*)p);
+}
+__device__ __forceinline__ bf16x8 ld_frag_tokens(const bf16* tile, int ld, int tok0, int n0, int lane) {
+    const int g = lane >> 4, r = lane & 15;
+    const bf16* p = tile + (tok0 + 4 * g + (r >> 2)) * ld + n0 + 4 * (r & 3);
+    const bf16x4 a = ld_tr4(p), b = ld_tr4(p + 16 * ld);
+    bf16x8 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { f[i] = a[i]; f[4 + i] = b[i]; }
+    return f;
+}
+__device__ __forceinline__ f32x8 ld_frag_tokens(const float* tile, int ld, int tok0, int n0, int lane) {
+    const int g = lane >> 4, r = lane & 15;
+    const float* p = tile + (tok0 + 4 * g) * ld + n0 + r;
+    f32x8 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { f[i] = p[i * ld]; f[4 + i] = p[(16 + i) * ld]; }
+    return f;
+}
+
+// ---- fp32 operands of bf16 products ---------------------------------------------------
+// v = hi + mid + lo with eight significant bits each, by truncation: exact for
+// fp32, so that three bf16 products keep an fp32 state at fp32 accuracy.
+struct Split3 {
+    bf16x8 hi, mid, lo;
+};
+__device__ __forceinline__ unsigned hi16_pair(float a, float b) {
+    // the upper halves of a (low lane) and b (high lane)
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float trunc_bf16(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
+__device__ __forceinline__ Split3 split3(const float* v) {
+    unsigned h[4], m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = v[2 * i], b = v[2 * i + 1];
+        h[i] = hi16_pair(a, b);
+        const float a1 = a - trunc_bf16(a), b1 = b - trunc_bf16(b);
+        m[i] = hi16_pair(a1, b1);
+        l[i] = hi16_pair(a1 - trunc_bf16(a1), b1 - trunc_bf16(b1));
+    }
+    Split3 s;
+    s.hi = *reinterpret_cast<bf16x8*>(h);
+    s.mid = *reinterpret_cast<bf16x8*>(m);
+    s.lo = *reinterpret_cast<bf16x8*>(l);
+    return s;
+}
+// acc += a * v over one slab, v fp32 (a exact in T)
+__device__ __forceinline__ f32x4 mma_exact(f32x4 acc, bf16x8 a, const Split3& v) {
+    acc = mma(acc, a, v.lo);
+    acc = mma(acc, a, v.mid);
+    return mma(acc, a, v.hi);
+}
+__device__ __forceinline__ f32x4 mma_exact(f32x4 acc, f32x8 a, const f32x8& v) { return mma(acc, a, v); }
+template <typename T> struct Exact;
+template <> struct Exact<bf16> {
+    typedef Split3 type;
+    static __device__ __forceinline__ Split3 of(const float* v) { return split3(v); }
+};
+template <> struct Exact<float> {
+    typedef f32x8 type;
+    static __device__ __forceinline__ f32x8 of(const float* v) { return frag_from<float>(v); }
+};
+
+// one token's delta for one head
+__device__ __forceinline__ float delta_of(float raw, int softplus) { return softplus ? softplus_of(raw) : raw; }
+
+// inclusive sum over the 64 lanes of a wave, fp64
+__device__ __forceinline__ double wave_prefix(double v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+}  // namespace kda

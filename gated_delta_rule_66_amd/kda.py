@@ -40,6 +40,16 @@ EXPORTED_SYMBOLS = (
     "kda_chunk_bwd",
     "kda_status_string",
     "kda_version",
+    "kda_short_conv_fwd",
+    "kda_short_conv_bwd_workspace_size",
+    "kda_short_conv_bwd",
+    "kda_short_conv_step",
+    "kda_selective_scan_fwd_workspace_size",
+    "kda_selective_scan_fwd",
+    "kda_selective_scan_step",
+    "kda_group_norm_fwd",
+    "kda_group_norm_bwd_workspace_size",
+    "kda_group_norm_bwd",
     "kda_profile_start",
     "kda_profile_stop",
 )
@@ -99,6 +109,20 @@ def load_library(path: str = LIB_PATH):
     lib.kda_chunk_bwd_workspace_size.restype = sz
     lib.kda_chunk_bwd.argtypes = [i, i, i, i, i, i] + [p] * 14 + [p, sz, p]
     lib.kda_chunk_bwd.restype = i
+    ll, f = ctypes.c_longlong, ctypes.c_float
+    lib.kda_short_conv_fwd.argtypes = [i, p, i, i, i, i, i, p, ll] + [p] * 5 + [p]
+    lib.kda_short_conv_bwd_workspace_size.argtypes = [i] * 6
+    lib.kda_short_conv_bwd.argtypes = [i, p, i, i, i, i, i, p, ll] + [p] * 9 + [p, sz, p]
+    lib.kda_short_conv_step.argtypes = [i, i, i, i, i, p, ll] + [p] * 4 + [p]
+    lib.kda_selective_scan_fwd_workspace_size.argtypes = [i] * 8
+    lib.kda_selective_scan_fwd.argtypes = [i, p] + [i] * 7 + [p, ll, p, ll, p, p, ll, p, ll] + [p] * 5 + [p, sz, p]
+    lib.kda_selective_scan_step.argtypes = [i] * 7 + [p, ll, p, ll, p, p, ll, p, ll] + [p] * 4 + [p]
+    lib.kda_group_norm_fwd.argtypes = [i] * 7 + [f, p, ll, p, p, p, ll, p, p]
+    lib.kda_group_norm_bwd_workspace_size.argtypes = [i] * 4
+    lib.kda_group_norm_bwd.argtypes = [i] * 7 + [f, p, ll, p, p, p, ll] + [p] * 5 + [p, sz, p]
+    for name in EXPORTED_SYMBOLS:
+        if name.startswith(("kda_short_conv", "kda_selective_scan", "kda_group_norm")):
+            getattr(lib, name).restype = sz if name.endswith("_workspace_size") else i
     lib.kda_status_string.argtypes = [i]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_version.argtypes = []

@@ -389,6 +389,161 @@ kda_status kda_chunk_bwd(int B, int T, int H, int K, int V, kda_dtype dt,
                          void* dq, void* dk, void* dv, void* dg, void* dbeta, float* d_initial_state,
                          void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---- mixer operators ----------------------------------------------------------
+ *
+ * What stands around the recurrence in a layer, and its sibling with a scalar
+ * decay a head: the short causal convolution on its inputs, the selective scan,
+ * and the group norm with its gate on its output.
+ *
+ * Conventions, beyond those at the top of this file:
+ *   - Token tensors share the dtype `dt`; parameters (weights, biases, A, D,
+ *     dt_bias) and their gradients are fp32; convolution states are `dt` (they
+ *     hold inputs), scan states fp32.
+ *   - Sequences: with cu_seqlens NULL a call has N sequences of T tokens each,
+ *     in order; else cu_seqlens is a DEVICE int32 [N + 1] array as in
+ *     kda_chunk_fwd_varlen, T is the number of token rows, and rows at or
+ *     behind cu_seqlens[N] are neither read nor written (they pad a batch).
+ *     Offsets outside the contract are clamped: every access stays in bounds.
+ *   - x_stride, delta_stride, b_stride, c_stride, gate_stride: elements between consecutive
+ *     token rows of an input (at least the row's width), so that a slice of a
+ *     wider projection is passed as it is.  Outputs are contiguous unless they
+ *     have a stride of their own.
+ *   - Outputs must not overlap inputs or each other unless a call says so; a
+ *     call that would is KDA_ERR_INVALID_ARG.
+ *   - All work goes to `stream`; a call may be captured into a graph.  Calls
+ *     that run at the same time need workspaces of their own.
+ *   - Results are deterministic: parameter gradients are summed in a fixed
+ *     order.
+ */
+typedef enum kda_activation {
+    KDA_ACT_NONE = 0,
+    KDA_ACT_SILU = 1,               /* v sigmoid(v) */
+    KDA_ACT_SIGMOID = 2,
+    KDA_ACT_RANGE_MIN_ = -2147483647 - 1,   /* never valid, as in kda_dtype */
+    KDA_ACT_RANGE_MAX_ = 2147483647
+} kda_activation;
+
+/*
+ * Short causal depthwise convolution over the tokens of each sequence:
+ *
+ *   y_t[d] = act( bias[d] + sum_{w < W} weight[d, w] x_{t - (W-1) + w}[d] )
+ *
+ *   W in {2, 3, 4}; D any.  Sums in fp32, rounded once.
+ *   x      : [tokens, D] dt, row stride x_stride
+ *   weight : [D, W] fp32;  bias : [D] fp32 or NULL
+ *   initial_state : [N, W-1, D] dt, the W - 1 rows before each sequence, or
+ *                   NULL (zeros)
+ *   y      : [tokens, D] dt
+ *   final_state   : [N, W-1, D] dt, the last W - 1 rows of (initial_state, x),
+ *                   or NULL.  It must not overlap initial_state.
+ * Pointers aligned to their element size; with every pointer 16-byte aligned
+ * and D and x_stride multiples of 16 bytes, accesses are 16 bytes wide.
+ */
+kda_status kda_short_conv_fwd(int N, const int* cu_seqlens, int T, int D, int W, kda_dtype dt, kda_activation act,
+                              const void* x, long long x_stride, const float* weight, const float* bias,
+                              const void* initial_state, void* y, void* final_state, hipStream_t stream);
+
+/*
+ * Its gradients, from dL/dy (d_y, [tokens, D]) and dL/dfinal_state
+ * (d_final_state or NULL):
+ *   dx : [tokens, D] dt;  dweight : [D, W] fp32;  dbias : [D] fp32 or NULL
+ *   d_initial_state : [N, W-1, D] dt or NULL
+ *   workspace : kda_short_conv_bwd_workspace_size(...) bytes (packed: 1 for a
+ *               call with cu_seqlens)
+ * The convolution is recomputed from x.  No tokens: dweight and dbias are
+ * zero, and dL/dfinal_state passes to d_initial_state.
+ */
+size_t kda_short_conv_bwd_workspace_size(int N, int packed, int T, int D, int W, kda_dtype dt);
+kda_status kda_short_conv_bwd(int N, const int* cu_seqlens, int T, int D, int W, kda_dtype dt, kda_activation act,
+                              const void* x, long long x_stride, const float* weight, const float* bias,
+                              const void* initial_state, const void* d_y, const void* d_final_state, void* dx,
+                              float* dweight, float* dbias, void* d_initial_state, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of N sequences: y [N, D] from x [N, D] (row stride x_stride) and
+ * state [N, W-1, D], whose rows move up IN PLACE.
+ */
+kda_status kda_short_conv_step(int N, int D, int W, kda_dtype dt, kda_activation act, const void* x,
+                               long long x_stride, const float* weight, const float* bias, void* state, void* y,
+                               hipStream_t stream);
+
+/*
+ * Selective scan: a state space recurrence with a scalar decay a head and
+ * input-dependent step size and projections.  Per sequence and head h, with
+ * delta_t = softplus(dt_t + dt_bias) (dt_softplus != 0) or dt_t + dt_bias:
+ *
+ *   S_t = exp(delta_t A) S_{t-1} + delta_t B_t x_t^T       (K x P, fp32)
+ *   y_t = S_t^T C_t + D x_t
+ *
+ *   x     : [tokens, H, P] dt, row stride x_stride;  P in {64, 128}
+ *   delta : [tokens, H] dt (row stride delta_stride), the step sizes dt_t before bias and softplus
+ *   A     : [H] fp32;  D, dt_bias : [H] fp32 or NULL (none)
+ *   B, C  : [tokens, G, K] dt, row strides b_stride, c_stride; K in {64, 128};
+ *           G divides H, and heads h G / H .. share a group
+ *   initial_state : [N, H, K, P] fp32 or NULL (zeros)
+ *   y     : [tokens, H, P] dt
+ *   final_state   : [N, H, K, P] fp32 or NULL; it may be initial_state exactly
+ *   workspace : kda_selective_scan_fwd_workspace_size(...) bytes
+ * x, B, C, y, states and workspace 16-byte aligned, strides multiples of 16
+ * bytes.  Meant for A delta <= 0 (decay); a growing state is computed as far
+ * as e^{sum A delta} over 64 tokens stays finite.  Non-finite inputs propagate
+ * to their sequence from the start of their 64-token chunk on, never to
+ * another sequence.  A sequence without tokens passes its state on.
+ */
+size_t kda_selective_scan_fwd_workspace_size(int N, int packed, int T, int H, int G, int K, int P, kda_dtype dt);
+kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, int G, int K, int P, kda_dtype dt,
+                                  int dt_softplus, const void* x, long long x_stride, const void* delta,
+                                  long long delta_stride, const float* A, const void* B, long long b_stride, const void* C,
+                                  long long c_stride, const float* D, const float* dt_bias,
+                                  const float* initial_state, void* y, float* final_state, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of N sequences: state [N, H, K, P] is updated IN PLACE and read
+ * and written once.  x [N, H, P], delta [N, H], B, C [N, G, K], y [N, H, P].
+ */
+kda_status kda_selective_scan_step(int N, int H, int G, int K, int P, kda_dtype dt, int dt_softplus, const void* x,
+                                   long long x_stride, const void* delta, long long delta_stride, const float* A,
+                                   const void* B,
+                                   long long b_stride, const void* C, long long c_stride, const float* D,
+                                   const float* dt_bias, float* state, void* y, hipStream_t stream);
+
+/*
+ * Group norm of token rows (channels last), with an activation or a gate.
+ * Each row's C channels form `groups` groups, normalised each by itself
+ * (statistics a token: over tokens they would look ahead):
+ *
+ *   u = x, or x act(gate) with gate_first
+ *   n = (u - m) / sqrt(mean((u - m)^2) + eps) weight + bias,
+ *       m = mean(u) with center, else 0 (root mean square)
+ *   y = act(n) without a gate; n act(gate); n with gate_first
+ *
+ *   x, gate : [rows, C] dt, row strides x_stride, gate_stride; gate or NULL
+ *   weight, bias : [C] fp32 or NULL (1, 0);  y : [rows, C] dt
+ * fp32 inside, rounded once.  y may be x or the gate exactly.  C / groups at
+ * most 4096 channels, or 16384 where rows and pointers allow 16-byte accesses
+ * (C / groups and strides multiples of 16 bytes); wider groups are
+ * KDA_ERR_UNSUPPORTED.
+ */
+kda_status kda_group_norm_fwd(int rows, int C, int groups, kda_dtype dt, kda_activation act, int center,
+                              int gate_first, float eps, const void* x, long long x_stride, const float* weight,
+                              const float* bias, const void* gate, long long gate_stride, void* y,
+                              hipStream_t stream);
+
+/*
+ * Its gradients from dL/dy (d_y, [rows, C]): dx [rows, C], dweight and dbias
+ * [C] fp32 (each or NULL), d_gate [rows, C] (exactly where there is a gate).
+ * workspace : kda_group_norm_bwd_workspace_size(...) bytes, needed where
+ * dweight or dbias is asked for.
+ */
+size_t kda_group_norm_bwd_workspace_size(int rows, int C, int groups, kda_dtype dt);
+kda_status kda_group_norm_bwd(int rows, int C, int groups, kda_dtype dt, kda_activation act, int center,
+                              int gate_first, float eps, const void* x, long long x_stride, const float* weight,
+                              const float* bias, const void* gate, long long gate_stride, const void* d_y, void* dx,
+                              float* dweight, float* dbias, void* d_gate, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
 /*
  * Optional per-launch timing, for benchmarks and tracing.  After
  * kda_profile_start(max_launches), each kernel launched by the library
@@ -400,7 +555,10 @@ kda_status kda_chunk_bwd(int B, int T, int H, int K, int V, kda_dtype dt,
  * "varlen_prep", "decode_step", "decode_steps", "backward"; the chunk-form
  * backward's "bwd_intra_chunk", "bwd_state_summary", "bwd_segment_scan",
  * "bwd_states", "bwd_reverse_summary", "bwd_reverse_scan", "bwd_state_reverse",
- * "bwd_value_side", "bwd_solve", "bwd_gated") and durations in milliseconds, releases the
+ * "bwd_value_side", "bwd_solve", "bwd_gated"; the mixer operators'
+ * "short_conv", "short_conv_bwd", "short_conv_bwd_sums", "short_conv_step",
+ * "scan_prep", "scan_summary", "scan_combine", "scan_output", "scan_step",
+ * "group_norm", "group_norm_bwd", "group_norm_bwd_sums") and durations in milliseconds, releases the
  * events, and returns the number of timed launches (-1: profiling was not
  * started or a HIP event query failed).  The record is process-wide (the one
  * piece of state the library keeps, opt-in): launches from several threads

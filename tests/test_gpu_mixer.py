@@ -1,0 +1,401 @@
+"""The mixer operators on the GPU against 64-bit references.
+
+Bounds.  An output rounded once to its dtype is off by half a step (2^-8
+relative for bf16, 2^-24 for fp32).  fp32 arithmetic inside is held to
+2^-20 .. 2^-18 of the sum of absolute values of the terms it adds (a chain of n
+fp32 operations is off by at most n 2^-24 of that sum; the hardware exp2 and
+reciprocal by 1 ulp).  The chunked bf16 scan rounds each score (decay and step
+size included) and the chunk's start state once to bf16 before its products:
+2^-8 more of the sum of absolute values.  States are carried in fp32 through
+exact three-way splits.
+"""
+import pytest
+import torch
+
+import gated_delta_rule_66_amd as kda
+import mixer_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DTYPES = [torch.bfloat16, torch.float32]
+
+
+def rnd(gen, *shape, dtype=torch.float32, std=1.0):
+    return (torch.randn(shape, generator=gen) * std).to(dtype)
+
+
+def up(t):
+    """float64 on the CPU"""
+    return None if t is None else t.detach().cpu().double()
+
+
+def dev(t):
+    return None if t is None else t.to(DEV)
+
+
+def packed(lens):
+    return torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+
+
+# ---- short convolution ------------------------------------------------------------------
+CONV = [
+    # (n, t, lens, d, w, bias, state, act)
+    (1, 1, None, 1, 2, True, True, "silu"),
+    (2, 2, None, 8, 4, False, True, "silu"),
+    (3, 17, None, 7, 3, True, False, None),
+    (2, 130, None, 72, 4, True, True, "silu"),
+    (1, 300, None, 2304, 4, False, False, "silu"),
+    (0, 0, [5, 0, 1, 2, 40, 0, 33, 3], 40, 4, True, True, "silu"),
+    (0, 0, [1, 1, 1, 200], 33, 3, False, True, "sigmoid"),
+    (0, 0, [0, 0], 16, 4, True, True, "silu"),
+    (0, 0, [97], 264, 2, True, False, "silu"),
+]
+
+
+def conv_case(case, dtype, seed=0):
+    n, t, lens, d, w, bias, state, act = case
+    gen = torch.Generator().manual_seed(seed)
+    cu = packed(lens) if lens is not None else None
+    n = len(lens) if lens is not None else n
+    m = sum(lens) if lens is not None else n * t
+    shape = (m, d) if lens is not None else (n, t, d)
+    c = {"x": rnd(gen, *shape, dtype=dtype), "w": rnd(gen, d, w), "b": rnd(gen, d) if bias else None,
+         "s": rnd(gen, n, w - 1, d, dtype=dtype) if state else None, "cu": cu, "act": act,
+         "dy": rnd(gen, *shape, dtype=dtype), "ds": rnd(gen, n, w - 1, d, dtype=dtype), "n": n,
+         "ranges": R.seqs(n, t, cu), "shape": shape}
+    return c
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", CONV, ids=[str(i) for i in range(len(CONV))])
+def test_short_conv_forward(case, dtype):
+    c = conv_case(case, dtype)
+    y, fin = kda.short_conv_fwd(dev(c["x"]), dev(c["w"]), dev(c["b"]), dev(c["s"]), activation=c["act"],
+                                cu_seqlens=dev(c["cu"]))
+    D = c["x"].shape[-1]
+    x = up(c["x"]).reshape(-1, D)
+    want, wfin = R.conv(x, up(c["w"]), up(c["b"]), up(c["s"]), c["ranges"], c["act"])
+    size, _ = R.conv(x.abs(), up(c["w"]).abs(), None if c["b"] is None else up(c["b"]).abs(),
+                     None if c["s"] is None else up(c["s"]).abs(), c["ranges"], None)
+    R.close(y.reshape(-1, D), want, R.HALF[dtype] * want.abs() + 2.0 ** -20 * (size + want.abs()), "y")
+    assert torch.equal(up(fin), wfin)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", CONV, ids=[str(i) for i in range(len(CONV))])
+def test_short_conv_backward(case, dtype):
+    c = conv_case(case, dtype, 1)
+    dx, dw, db, ds = kda.short_conv_bwd(dev(c["x"]), dev(c["w"]), dev(c["b"]), dev(c["dy"]), dev(c["s"]), dev(c["ds"]),
+                                        activation=c["act"], cu_seqlens=dev(c["cu"]), want_d_initial_state=True)
+    D = c["x"].shape[-1]
+    zero = torch.zeros(c["n"], c["w"].shape[1] - 1, D, dtype=torch.float64)
+
+    def grads(x, w, b, s, gy, gs, act):
+        leaves = [v.requires_grad_() for v in (x, w, b, s)]
+        y, fin = R.conv(x, w, b, s, c["ranges"], act)
+        loss = (y * gy).sum() + (fin * gs).sum()
+        return torch.autograd.grad(loss, leaves, allow_unused=True, materialize_grads=True)
+
+    x, w = up(c["x"]).reshape(-1, D), up(c["w"])
+    b = up(c["b"]) if c["b"] is not None else torch.zeros(D, dtype=torch.float64)
+    s = up(c["s"]) if c["s"] is not None else zero
+    dy, dsT = up(c["dy"]).reshape(-1, D), up(c["ds"])
+    want = grads(x.clone(), w.clone(), b.clone(), s.clone(), dy, dsT, c["act"])
+    # |act'| <= 1.1 and |act''| <= 0.5: the terms' sizes, with the error of the
+    # recomputed convolution in act'
+    size, _ = R.conv(x.abs(), w.abs(), b.abs(), s.abs(), c["ranges"], None)
+    q = dy.abs() * (1.1 + size)
+    sizes = grads(x.abs(), w.abs(), b.abs(), s.abs(), q, dsT.abs(), None)
+    m = x.shape[0]
+    R.close(dx.reshape(-1, D), want[0], R.HALF[dtype] * want[0].abs() + 2.0 ** -19 * sizes[0], "dx")
+    R.close(dw, want[1], (2.0 ** -19 + m * 2.0 ** -24) * sizes[1], "dweight")
+    if c["b"] is None:
+        assert db is None
+    else:
+        R.close(db, want[2], (2.0 ** -19 + m * 2.0 ** -24) * sizes[2], "dbias")
+    R.close(ds, want[3], R.HALF[dtype] * want[3].abs() + 2.0 ** -19 * sizes[3], "d_initial_state")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d,w", [(1, 2), (40, 3), (2304, 4), (33, 4)])
+def test_short_conv_step_is_the_forward_token_by_token(dtype, d, w):
+    gen = torch.Generator().manual_seed(2)
+    n, t = 5, 6
+    x, weight, bias = rnd(gen, n, t, d, dtype=dtype), rnd(gen, d, w), rnd(gen, d)
+    s = rnd(gen, n, w - 1, d, dtype=dtype)
+    y, fin = kda.short_conv_fwd(dev(x), dev(weight), dev(bias), dev(s))
+    state = dev(s).clone()
+    wide = torch.zeros(n, t, d + 8, dtype=dtype, device=DEV)
+    wide[..., :d] = dev(x)
+    size, _ = R.conv(up(x).reshape(-1, d).abs(), up(weight).abs(), up(bias).abs(), up(s).abs(), R.seqs(n, t, None), None)
+    size = size.reshape(n, t, d)
+    for i in range(t):
+        # a row of a wider projection
+        yi = kda.short_conv_step(wide[:, i, :d], dev(weight), dev(bias), state)
+        # the same sum in another order, each rounded once
+        R.close(yi, up(y[:, i]), 2 * R.HALF[dtype] * up(y[:, i]).abs() + 2.0 ** -19 * (size[:, i] + 1e-3), "step")
+    assert torch.equal(state, fin)
+
+
+def test_short_conv_leaves_padding_and_reads_strided_rows():
+    gen = torch.Generator().manual_seed(3)
+    lens, d = [9, 0, 20], 64
+    cu = packed(lens)
+    wide = rnd(gen, 50, 3 * d, dtype=torch.bfloat16).to(DEV)
+    wide[29:] = float("nan")                       # rows behind the last sequence
+    w, b = dev(rnd(gen, d, 4)), dev(rnd(gen, d))
+    x = wide[:, d:2 * d]
+    out = torch.full((50, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    y, fin = kda.short_conv_fwd(x, w, b, cu_seqlens=dev(cu), out=out)
+    y2, fin2 = kda.short_conv_fwd(x[:29].contiguous(), w, b, cu_seqlens=dev(cu))
+    assert torch.equal(y[:29], y2) and torch.equal(fin, fin2)
+    assert (y[29:] == 7.0).all()
+    dy = torch.full((50, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    dy[:29] = rnd(gen, 29, d, dtype=torch.bfloat16)
+    dx = torch.full((50, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    got = kda.short_conv_bwd(x, w, b, dy, cu_seqlens=dev(cu), dx=dx)
+    ref = kda.short_conv_bwd(x[:29].contiguous(), w, b, dy[:29].contiguous(), cu_seqlens=dev(cu))
+    assert torch.equal(got[0][:29], ref[0]) and (got[0][29:] == 7.0).all()
+    # the tiles of the longer axis are summed in another grouping
+    assert torch.allclose(got[1], ref[1], rtol=1e-4, atol=1e-4) and torch.allclose(got[2], ref[2], rtol=1e-4, atol=1e-4)
+
+
+# ---- group norm -------------------------------------------------------------------------
+NORM = [
+    # (rows, C, groups, act, gate, gate_first, center, affine)
+    (1, 1, 1, None, False, False, False, True),
+    (5, 7, 7, "silu", False, False, True, True),
+    (3, 64, 1, "silu", True, False, False, True),
+    (33, 4096, 32, "sigmoid", True, False, False, True),
+    (17, 2048, 1, "silu", True, True, False, True),
+    (9, 8192, 1, "silu", True, True, True, False),
+    (4, 16384, 1, None, False, False, True, True),
+    (6, 4095, 1, "silu", True, False, True, True),
+    (130, 120, 5, "silu", False, False, False, False),
+    (300, 264, 3, "sigmoid", True, True, True, True),
+    (7, 350, 2, "silu", True, False, False, True),
+    (0, 64, 2, "silu", True, False, False, True),
+]
+
+
+def norm_case(case, dtype, seed=0):
+    rows, C, groups, act, gate, first, center, affine = case
+    gen = torch.Generator().manual_seed(seed)
+    return {"x": rnd(gen, rows, C, dtype=dtype, std=2.0) + 0.5, "z": rnd(gen, rows, C, dtype=dtype) if gate else None,
+            "w": rnd(gen, C) if affine else None, "b": rnd(gen, C) if affine else None,
+            "dy": rnd(gen, rows, C, dtype=dtype), "groups": groups,
+            "how": dict(activation=act, gate_first=first, center=center, eps=1e-5)}
+
+
+def norm_sizes(c):
+    """hat's size: |u| and the mean it may lose, over the deviation; and the pieces."""
+    x, z, g, how = up(c["x"]), up(c["z"]), c["groups"], c["how"]
+    az = R.act(z, how["activation"]) if z is not None else None
+    u = x * az if z is not None and how["gate_first"] else x
+    ug = u.reshape(u.shape[0], g, u.shape[1] // g)
+    mid = ug - ug.mean(-1, keepdim=True) if how["center"] else ug
+    rstd = 1 / torch.sqrt(mid.square().mean(-1, keepdim=True) + how["eps"])
+    hat = ((ug.abs() + ug.abs().mean(-1, keepdim=True)) * rstd).reshape(x.shape)
+    return hat, rstd.expand(ug.shape).reshape(x.shape), az
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", NORM, ids=[str(i) for i in range(len(NORM))])
+def test_group_norm_forward(case, dtype):
+    c = norm_case(case, dtype)
+    y = kda.group_norm_fwd(dev(c["x"]), c["groups"], dev(c["w"]), dev(c["b"]), dev(c["z"]), **c["how"])
+    want = R.norm(up(c["x"]), c["groups"], up(c["w"]), up(c["b"]), up(c["z"]), **c["how"])
+    hat, _, az = norm_sizes(c)
+    size = hat * (up(c["w"]).abs() if c["w"] is not None else 1) + (up(c["b"]).abs() if c["b"] is not None else 0)
+    if az is not None and not c["how"]["gate_first"]:
+        size = size * az.abs()
+    R.close(y, want, R.HALF[dtype] * want.abs() + 2.0 ** -18 * (size + want.abs()), "y")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", NORM, ids=[str(i) for i in range(len(NORM))])
+def test_group_norm_backward(case, dtype):
+    c = norm_case(case, dtype, 1)
+    dx, dw, db, dz = kda.group_norm_bwd(dev(c["x"]), c["groups"], dev(c["w"]), dev(c["b"]), dev(c["z"]), dev(c["dy"]),
+                                        **c["how"])
+    leaves = [None if c[k] is None else up(c[k]).requires_grad_() for k in ("x", "w", "b", "z")]
+    y = R.norm(leaves[0], c["groups"], leaves[1], leaves[2], leaves[3], **c["how"])
+    used = [v for v in leaves if v is not None]
+    got = iter(torch.autograd.grad((y * up(c["dy"])).sum(), used, allow_unused=True, materialize_grads=True))
+    want = [None if v is None else next(got) for v in leaves]
+    hat, rstd, az = norm_sizes(c)
+    how, act = c["how"], c["how"]["activation"]
+    w = up(c["w"]).abs() if c["w"] is not None else torch.ones(c["x"].shape[-1], dtype=torch.float64)
+    b = up(c["b"]).abs() if c["b"] is not None else torch.zeros_like(w)
+    dn = up(c["dy"]).abs()
+    if az is None:
+        # the activation's derivative sees the error of n: |act''| <= 0.5
+        dn = dn * ((1.1 + hat * w + b) if act else 1.0)
+    elif not how["gate_first"]:
+        dn = dn * az.abs()
+    g = (dn * w).reshape(dn.shape[0], c["groups"], dn.shape[1] // c["groups"])
+    hg = hat.reshape(g.shape)
+    du = (g + hg * (g * hg).mean(-1, keepdim=True) + g.mean(-1, keepdim=True)).reshape(dn.shape) * rstd
+    half, rows = R.HALF[dtype], dn.shape[0]
+    if az is not None and how["gate_first"]:
+        R.close(dx, want[0], half * want[0].abs() + 2.0 ** -17 * du * az.abs(), "dx")
+        R.close(dz, want[3], half * want[3].abs() + 2.0 ** -17 * du * up(c["x"]).abs() * 1.1, "dz")
+    else:
+        R.close(dx, want[0], half * want[0].abs() + 2.0 ** -17 * du, "dx")
+        if az is not None:
+            R.close(dz, want[3], half * want[3].abs() + 2.0 ** -17 * up(c["dy"]).abs() * (hat * w + b) * 1.1, "dz")
+        else:
+            assert dz is None
+    if c["w"] is None:
+        assert dw is None and db is None
+    else:
+        R.close(dw, want[1], (2.0 ** -17 + rows * 2.0 ** -24) * (dn * hat).sum(0), "dweight")
+        R.close(db, want[2], (2.0 ** -17 + rows * 2.0 ** -24) * dn.sum(0), "dbias")
+
+
+def test_group_norm_in_place_and_strided():
+    gen = torch.Generator().manual_seed(5)
+    wide = rnd(gen, 6, 5, 512, dtype=torch.bfloat16).to(DEV)
+    x, z = wide[..., :256], wide[..., 256:]
+    w = dev(rnd(gen, 256))
+    want = kda.group_norm_fwd(x.contiguous(), 4, w, None, z.contiguous())
+    assert torch.equal(kda.group_norm_fwd(x, 4, w, None, z), want)
+    xc = x.contiguous()
+    assert torch.equal(kda.group_norm_fwd(xc, 4, w, None, z, out=xc), want)
+    with pytest.raises(kda.KDAError):
+        kda.group_norm_bwd(x, 3, w, None, z, want)
+
+
+# ---- selective scan ---------------------------------------------------------------------
+SCAN = [
+    # (n, t, lens, h, g, k, p, state, softplus, skip)
+    (1, 1, None, 1, 1, 64, 64, True, True, True),
+    (2, 5, None, 2, 1, 128, 64, False, True, True),
+    (1, 64, None, 3, 1, 64, 128, True, False, False),
+    (2, 65, None, 4, 2, 128, 128, True, True, True),
+    (1, 200, None, 3, 3, 128, 64, True, True, False),
+    (1, 700, None, 2, 1, 64, 64, False, False, True),
+    (0, 0, [3, 0, 64, 1, 130, 0, 63], 4, 2, 64, 64, True, True, True),
+    (0, 0, [1, 1, 2, 300], 2, 2, 128, 64, False, True, True),
+    (0, 0, [0, 0, 0], 2, 1, 64, 128, True, True, True),
+    (3, 0, None, 2, 1, 64, 64, True, True, True),
+]
+SCAN_IDS = [str(i) for i in range(len(SCAN))]
+
+
+def scan_case(case, dtype, seed=0, decay=16.0):
+    n, t, lens, h, g, k, p, state, softplus, skip = case
+    gen = torch.Generator().manual_seed(seed)
+    cu = packed(lens) if lens is not None else None
+    n = len(lens) if lens is not None else n
+    lead = (sum(lens),) if lens is not None else (n, t)
+    c = {"x": rnd(gen, *lead, h, p, dtype=dtype), "B": rnd(gen, *lead, g, k, dtype=dtype),
+         "C": rnd(gen, *lead, g, k, dtype=dtype), "A": -torch.rand(h, generator=gen) * decay - 0.5,
+         "D": rnd(gen, h) if skip else None, "s": rnd(gen, n, h, k, p) if state else None,
+         "dy": rnd(gen, *lead, h, p, dtype=dtype), "ds": rnd(gen, n, h, k, p),
+         "cu": cu, "n": n, "softplus": softplus, "ranges": R.seqs(n, t, cu), "lead": lead}
+    if softplus:
+        c["dt"], c["bias"] = rnd(gen, *lead, h, dtype=dtype), rnd(gen, h) - 3.0
+    else:
+        c["dt"], c["bias"] = (torch.rand(*lead, h, generator=gen) * 0.1).to(dtype), None
+    return c
+
+
+def scan_args(c):
+    return [dev(c[k]) for k in ("x", "dt", "A", "B", "C", "D", "bias")]
+
+
+def flat(c, name):
+    t = up(c[name])
+    return t.reshape(-1, *t.shape[len(c["lead"]):])
+
+
+def scan_ref(c, size=False):
+    f = (lambda v: None if v is None else v.abs()) if size else (lambda v: v)
+    return R.scan(f(flat(c, "x")), flat(c, "dt"), up(c["A"]), f(flat(c, "B")), f(flat(c, "C")), f(up(c["D"])),
+                  up(c["bias"]), f(up(c["s"])), c["ranges"], c["softplus"])
+
+
+def check_scan(c, dtype, y, fin):
+    (want, wfin), (size, sfin) = scan_ref(c), scan_ref(c, True)
+    steps = max([b - a for a, b in c["ranges"]] + [0]) + 64
+    chain = 2.0 ** -20 + steps * 2.0 ** -23
+    scores = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    R.close(y.reshape(want.shape), want, R.HALF[dtype] * want.abs() + (scores + chain) * size, "y")
+    R.close(fin, wfin, chain * sfin, "final_state")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", SCAN, ids=SCAN_IDS)
+def test_selective_scan_forward(case, dtype):
+    c = scan_case(case, dtype)
+    y, fin = kda.selective_scan_fwd(*scan_args(c), dev(c["s"]), dt_softplus=c["softplus"], cu_seqlens=dev(c["cu"]))
+    check_scan(c, dtype, y, fin)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", [SCAN[3], SCAN[6]], ids=["regular", "packed"])
+def test_selective_scan_strong_decay(case, dtype):
+    # exponents far below the smallest float: nothing overflows, old tokens vanish
+    c = scan_case(case, dtype, 4, decay=4000.0)
+    y, fin = kda.selective_scan_fwd(*scan_args(c), dev(c["s"]), dt_softplus=c["softplus"], cu_seqlens=dev(c["cu"]))
+    check_scan(c, dtype, y, fin)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_selective_scan_final_state_in_place(dtype):
+    for case in (SCAN[3], (9, 300, None, 2, 1, 64, 64, True, True, True), SCAN[6]):
+        c = scan_case(case, dtype, 5)
+        want = kda.selective_scan_fwd(*scan_args(c), dev(c["s"]), dt_softplus=True, cu_seqlens=dev(c["cu"]))
+        s = dev(c["s"]).clone()
+        y, fin = kda.selective_scan_fwd(*scan_args(c), s, dt_softplus=True, cu_seqlens=dev(c["cu"]), final_state=s)
+        assert fin is s and torch.equal(y, want[0]) and torch.equal(s, want[1])
+
+
+def test_selective_scan_slices_padding_and_neighbours():
+    # x, B, C and dt as slices of one projection; rows behind the last sequence
+    # and a poisoned neighbour change nothing
+    gen = torch.Generator().manual_seed(6)
+    h, g, k, p, lens = 4, 2, 64, 64, [70, 3, 90]
+    rows, width = 200, h * p + 2 * g * k + 8
+    wide = rnd(gen, rows, width, dtype=torch.bfloat16).to(DEV)
+    wide[163:] = float("nan")
+    cu = dev(packed(lens))
+    A, bias = dev(-torch.rand(h, generator=gen) - 0.1), dev(rnd(gen, h) - 3)
+
+    def parts(t):
+        x = t[:, :h * p].view(-1, h, p)
+        B = t[:, h * p:h * p + g * k].view(-1, g, k)
+        C = t[:, h * p + g * k:h * p + 2 * g * k].view(-1, g, k)
+        return x, t[:, width - 8:width - 8 + h], A, B, C, None, bias
+
+    out = torch.full((rows, h, p), 7.0, dtype=torch.bfloat16, device=DEV)
+    y, fin = kda.selective_scan_fwd(*parts(wide), dt_softplus=True, cu_seqlens=cu, out=out)
+    alone = [v.contiguous() if v is not None else None for v in parts(wide[:163])]
+    y2, fin2 = kda.selective_scan_fwd(*alone, dt_softplus=True, cu_seqlens=cu)
+    # the longer axis may be cut into other segments: states meet in another order
+    assert torch.allclose(y[:163].float(), y2.float(), rtol=2 ** -7, atol=2e-2)
+    assert torch.allclose(fin, fin2, rtol=1e-4, atol=1e-4)
+    assert (y[163:] == 7.0).all()
+    wide[71, :] = float("inf")                     # inside the second sequence
+    y3, fin3 = kda.selective_scan_fwd(*parts(wide), dt_softplus=True, cu_seqlens=cu)
+    assert torch.equal(y3[:70], y[:70]) and torch.equal(y3[73:163], y[73:163])
+    assert torch.equal(fin3[0], fin[0]) and torch.equal(fin3[2], fin[2])
+    assert not torch.isfinite(fin3[1]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,h,g,k,p", [(1, 1, 1, 64, 64), (3, 4, 2, 128, 64), (2, 6, 1, 64, 128), (70, 8, 8, 128, 128)])
+def test_selective_scan_step(dtype, n, h, g, k, p):
+    t = 3
+    c = scan_case((n, t, None, h, g, k, p, True, True, True), dtype, 7)
+    state = dev(c["s"]).clone()
+    ys = []
+    x, dt, A, B, C, D, bias = scan_args(c)
+    for i in range(t):
+        ys.append(kda.selective_scan_step(x[:, i], dt[:, i], A, B[:, i], C[:, i], D, bias, state, dt_softplus=True))
+    (want, wfin), (size, sfin) = scan_ref(c), scan_ref(c, True)
+    chain = 2.0 ** -20 + (k + t) * 2.0 ** -24
+    y = torch.stack(ys, 1).reshape(want.shape)
+    R.close(y, want, R.HALF[dtype] * want.abs() + chain * size, "y")
+    R.close(state, wfin, chain * sfin, "state")
