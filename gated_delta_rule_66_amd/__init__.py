@@ -29,6 +29,7 @@ from .kda import (  # noqa: F401
 from .mixer import (  # noqa: F401
     group_norm_bwd,
     group_norm_fwd,
+    selective_scan_bwd,
     selective_scan_fwd,
     selective_scan_step,
     short_conv_bwd,
@@ -38,5 +39,6 @@ from .mixer import (  # noqa: F401
 from .build import LIB_PATH, build_library  # noqa: F401
 
 __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "chunk_bwd", "chunk_bwd_workspace_size", "chunk_fwd_varlen", "chunk_fwd_varlen_workspace_size", "snapshot_count", "recurrent_step", "recurrent_steps", "chunk_plan", "chunk_workspace_size", "profile_start", "profile_stop",
-           "short_conv_fwd", "short_conv_bwd", "short_conv_step", "selective_scan_fwd", "selective_scan_step",
+           "short_conv_fwd", "short_conv_bwd", "short_conv_step", "selective_scan_fwd", "selective_scan_bwd",
+           "selective_scan_step",
            "group_norm_fwd", "group_norm_bwd", "load_library", "build_library", "version", "status_string", "KDAError", "Plan"]

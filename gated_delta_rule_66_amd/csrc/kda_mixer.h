@@ -109,7 +109,33 @@ constexpr int kSsmChunk = 64;
 hipError_t launch_ssm_prep(const SeqView& sv, int* chunk_off, int max_chunks, hipStream_t st);
 // out: the output pass; else states only (segment summaries or states per chunk)
 hipError_t launch_ssm_chunks(int dtype, bool out, int nt, const SsmParams& p, int segs, hipStream_t st);
-hipError_t launch_ssm_combine(const SsmParams& p, hipStream_t st);
+// d_s0 (reverse with one chunk a segment only; else null): the adjoint before
+// each sequence's first chunk
+hipError_t launch_ssm_combine(const SsmParams& p, float* d_s0, hipStream_t st);
+
+// Gradients of the scan from the state before each chunk and the adjoint
+// behind it.  A workgroup takes one chunk and heads_per of the heads of a group.
+struct SsmBwdParams {
+    SsmParams f;                // the forward's inputs (y, sT, segments unused)
+    const void* d_y;            // [tokens][H][P]
+    const float* start;         // [chunks][H][K][P]
+    const float* dend;          // [chunks][H][K][P]
+    void* dx;
+    size_t dx_stride;
+    void* ddt;                  // [tokens][H]
+    void* dB;                   // one part: [tokens][G][K] with its stride
+    size_t db_stride;
+    void* dC;
+    size_t dc_stride;
+    float* dB_part;             // [parts][tokens][G][K] (more than one part)
+    float* dC_part;
+    float* sums;                // [chunks][3][H]: dA, ddt_bias, dD of each chunk
+    int parts, heads_per;
+};
+hipError_t launch_ssm_bwd(int dtype, const SsmBwdParams& p, hipStream_t st);
+// dB, dC: the parts summed, rounded to dt
+hipError_t launch_ssm_bwd_join(int dtype, const SsmBwdParams& p, long long tokens, hipStream_t st);
+hipError_t launch_ssm_bwd_sums(const float* sums, int rows, int H, float* dA, float* dbias, float* dD, hipStream_t st);
 hipError_t launch_ssm_step(int dtype, int N, int H, int G, int K, int P, int softplus, const void* x, size_t x_stride,
                            const void* dt, size_t dt_stride, const float* A, const void* B, size_t b_stride, const void* C,
                            size_t c_stride, const float* Dskip, const float* dt_bias, float* state, void* y,

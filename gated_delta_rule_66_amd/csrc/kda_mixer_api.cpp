@@ -28,6 +28,27 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 size_t extent(long long rows, long long stride, long long width, size_t es) {
     return rows > 0 ? (size_t)((rows - 1) * stride + width) * es : 0;
 }
+// The bytes a tensor's token rows take: `rows` rows of `width` bytes, `stride`
+// bytes apart.
+struct Span {
+    const void* p;
+    long long rows, stride, width;
+};
+// Two tensors share a byte.  Rows of one spacing that keep to columns of their
+// own (views of one wider buffer) do not.
+bool overlap(const Span& a, const Span& b) {
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const long long na = (a.rows - 1) * a.stride + a.width, nb = (b.rows - 1) * b.stride + b.width;
+    if (!overlap(a.p, (size_t)na, b.p, (size_t)nb)) return false;
+    if (a.rows > 1 && b.rows > 1 && a.stride == b.stride) {
+        const long long s = a.stride;
+        const long long d = (long long)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+        const long long m = ((d % s) + s) % s;      // where b's row starts in a's
+        return m < a.width || m + b.width > s;
+    }
+    return true;
+}
+Span flat_span(const void* p, size_t bytes) { return Span{p, 1, (long long)bytes, (long long)bytes}; }
 // tokens of a call; row indices are int in the kernels
 bool token_count(const int* cu, int N, int T, long long* M) {
     *M = cu ? (long long)T : (long long)N * T;
@@ -460,11 +481,156 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
         p.seg_state = reinterpret_cast<float*>(ws + L.seg);
         p.seg_decay = reinterpret_cast<float*>(ws + L.dec);
         KDA_LAUNCH("scan_summary", launch_ssm_chunks((int)dt, false, pl.nt, p, pl.n_seg - 1, stream));
-        KDA_LAUNCH("scan_combine", launch_ssm_combine(p, stream));
+        KDA_LAUNCH("scan_combine", launch_ssm_combine(p, nullptr, stream));
     }
     p.y = y;
     p.sT = final_state;
     KDA_LAUNCH("scan_output", launch_ssm_chunks((int)dt, true, pl.nt, p, pl.n_seg, stream));
+    return KDA_OK;
+}
+
+// Workgroups of the gradient kernel: one a (chunk, group, part of the group's
+// heads); parts until two workgroups a CU run, since each part beyond the first
+// adds fp32 copies of dB and dC.
+struct SsmBwdLayout {
+    size_t off, start, dend, dec, sums, part_b, part_c, total;
+    int parts, heads_per;
+};
+static SsmBwdLayout ssm_bwd_layout(bool packed, int N, long long M, int H, int G, int K, int P, const SsmPlan& pl) {
+    SsmBwdLayout L;
+    const int hpg = H / G;
+    const long long base = (long long)pl.chunks * G;
+    long long parts = base > 0 ? (512 + base - 1) / base : 1;
+    if (parts > hpg) parts = hpg;
+    L.heads_per = (int)((hpg + parts - 1) / parts);
+    L.parts = (hpg + L.heads_per - 1) / L.heads_per;
+    const size_t states = (size_t)pl.chunks * H * K * P * sizeof(float);
+    const size_t part = L.parts > 1 ? (size_t)L.parts * M * G * K * sizeof(float) : 0;
+    size_t o = 0;
+    L.off = o; o += packed ? align256((size_t)(N + 1) * sizeof(int)) : 0;
+    L.start = o; o += align256(states);
+    L.dend = o; o += align256(states);
+    L.dec = o; o += align256((size_t)pl.chunks * H * sizeof(float));
+    L.sums = o; o += align256((size_t)pl.chunks * 3 * H * sizeof(float));
+    L.part_b = o; o += align256(part);
+    L.part_c = o; o += align256(part);
+    L.total = o;
+    return L;
+}
+
+size_t kda_selective_scan_bwd_workspace_size(int N, int packed, int T, int H, int G, int K, int P, kda_dtype dt) {
+    long long M;
+    const int some = 0;
+    if (ssm_sizes(N, packed ? &some : nullptr, T, H, G, K, P, dt, &M) != KDA_OK) return (size_t)-1;
+    if (N == 0 || H == 0) return 0;
+    return ssm_bwd_layout(packed != 0, N, M, H, G, K, P, ssm_plan(packed != 0, N, M, T, H, G, P)).total;
+}
+
+kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, int G, int K, int P, kda_dtype dt,
+                                  int dt_softplus, const void* x, long long x_stride, const void* delta,
+                                  long long delta_stride, const float* A, const void* B, long long b_stride,
+                                  const void* C, long long c_stride, const float* D, const float* dt_bias,
+                                  const float* initial_state, const void* d_y, const float* d_final_state, void* dx,
+                                  long long dx_stride, void* d_delta, float* dA, void* dB, long long db_stride,
+                                  void* dC, long long dc_stride, float* dD, float* d_dt_bias,
+                                  float* d_initial_state, void* workspace, size_t workspace_bytes,
+                                  hipStream_t stream) {
+    long long M;
+    kda_status s = ssm_sizes(N, cu_seqlens, T, H, G, K, P, dt, &M);
+    if (s != KDA_OK) return s;
+    if (H == 0) return KDA_OK;
+    s = ssm_pointers(M, H, G, K, P, dt, x, x_stride, delta, delta_stride, A, B, b_stride, C, c_stride, D, dt_bias,
+                     initial_state);
+    if (s != KDA_OK) return s;
+    const size_t es = esize(dt), state = (size_t)N * H * K * P * sizeof(float);
+    const long long e = 16 / (long long)es;
+    for (const void* t : {(const void*)cu_seqlens, (const void*)dA, (const void*)dD, (const void*)d_dt_bias})
+        if (!aligned(t, 4)) return KDA_ERR_INVALID_ARG;
+    for (const void* t : {d_y, (const void*)d_final_state, (const void*)dx, (const void*)dB, (const void*)dC,
+                          (const void*)d_initial_state, (const void*)workspace})
+        if (!aligned(t, 16)) return KDA_ERR_INVALID_ARG;
+    if (!dA || !aligned(d_delta, es)) return KDA_ERR_INVALID_ARG;
+    if (M > 0 && N > 0) {
+        if (!d_y || !dx || !d_delta || !dB || !dC) return KDA_ERR_INVALID_ARG;
+        if (dx_stride < (long long)H * P || db_stride < (long long)G * K || dc_stride < (long long)G * K ||
+            dx_stride % e || db_stride % e || dc_stride % e)
+            return KDA_ERR_INVALID_ARG;
+    }
+    const long long le = (long long)es;
+    const Span outs[] = {{dx, M, dx_stride * le, (long long)H * P * le},
+                         {dB, M, db_stride * le, (long long)G * K * le},
+                         {dC, M, dc_stride * le, (long long)G * K * le},
+                         flat_span(d_delta, (size_t)M * H * es),
+                         flat_span(d_initial_state, state)};
+    const Span ins[] = {{x, M, x_stride * le, (long long)H * P * le},
+                        {B, M, b_stride * le, (long long)G * K * le},
+                        {C, M, c_stride * le, (long long)G * K * le},
+                        {delta, M, delta_stride * le, H * le},
+                        flat_span(d_y, (size_t)M * H * P * es),
+                        flat_span(initial_state, state),
+                        flat_span(d_final_state, state)};
+    for (int i = 0; i < 5; ++i) {
+        for (const Span& in : ins)
+            if (overlap(outs[i], in)) return KDA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return KDA_ERR_INVALID_ARG;
+    }
+    if (N == 0) {
+        KDA_LAUNCH("scan_bwd_sums", launch_ssm_bwd_sums(nullptr, 0, H, dA, d_dt_bias, dD, stream));
+        return KDA_OK;
+    }
+    const bool packed = cu_seqlens != nullptr;
+    SsmPlan pl = ssm_plan(packed, N, M, T, H, G, P);
+    const SsmBwdLayout L = ssm_bwd_layout(packed, N, M, H, G, K, P, pl);
+    if (!workspace || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
+    unsigned char* ws = reinterpret_cast<unsigned char*>(workspace);
+    SsmParams p{};
+    p.sv = SeqView{cu_seqlens, N, T};
+    p.H = H; p.G = G; p.K = K; p.P = P; p.softplus = dt_softplus != 0;
+    p.x = x; p.x_stride = (size_t)x_stride;
+    p.dt = delta; p.dt_stride = (size_t)delta_stride; p.A = A; p.dt_bias = dt_bias; p.Dskip = D;
+    p.B = B; p.b_stride = (size_t)b_stride;
+    p.C = C; p.c_stride = (size_t)c_stride;
+    p.s0 = initial_state;
+    p.chunks = pl.chunks; p.chunks_per_seq = pl.chunks_per_seq;
+    p.n_seg = pl.chunks; p.cps = 1;
+    if (packed) {
+        int* off = reinterpret_cast<int*>(ws + L.off);
+        KDA_LAUNCH("scan_prep", launch_ssm_prep(p.sv, off, pl.chunks, stream));
+        p.chunk_off = off;
+    }
+    // the state before each chunk: every chunk's own share, then the passing on
+    p.seg_state = reinterpret_cast<float*>(ws + L.start);
+    p.seg_decay = reinterpret_cast<float*>(ws + L.dec);
+    KDA_LAUNCH("scan_bwd_states", launch_ssm_chunks((int)dt, false, pl.nt, p, pl.chunks, stream));
+    KDA_LAUNCH("scan_bwd_combine", launch_ssm_combine(p, nullptr, stream));
+    // the adjoint behind each chunk: the same recurrence backwards, with C for
+    // B and dy for x
+    SsmParams q = p;
+    q.reverse = 1;
+    q.x = d_y; q.x_stride = (size_t)H * P;
+    q.B = C; q.b_stride = (size_t)c_stride;
+    q.s0 = d_final_state;
+    q.seg_state = reinterpret_cast<float*>(ws + L.dend);
+    KDA_LAUNCH("scan_bwd_adjoints", launch_ssm_chunks((int)dt, false, pl.nt, q, pl.chunks, stream));
+    KDA_LAUNCH("scan_bwd_combine", launch_ssm_combine(q, d_initial_state, stream));
+    SsmBwdParams b{};
+    b.f = p;
+    b.f.sT = const_cast<float*>(d_final_state);
+    b.d_y = d_y;
+    b.start = p.seg_state;
+    b.dend = q.seg_state;
+    b.dx = dx; b.dx_stride = (size_t)dx_stride;
+    b.ddt = d_delta;
+    b.dB = dB; b.db_stride = (size_t)db_stride;
+    b.dC = dC; b.dc_stride = (size_t)dc_stride;
+    b.dB_part = reinterpret_cast<float*>(ws + L.part_b);
+    b.dC_part = reinterpret_cast<float*>(ws + L.part_c);
+    b.sums = reinterpret_cast<float*>(ws + L.sums);
+    b.parts = L.parts; b.heads_per = L.heads_per;
+    KDA_LAUNCH("scan_bwd_grads", launch_ssm_bwd((int)dt, b, stream));
+    if (L.parts > 1) KDA_LAUNCH("scan_bwd_join", launch_ssm_bwd_join((int)dt, b, M, stream));
+    KDA_LAUNCH("scan_bwd_sums", launch_ssm_bwd_sums(b.sums, pl.chunks, H, dA, d_dt_bias, dD, stream));
     return KDA_OK;
 }
 

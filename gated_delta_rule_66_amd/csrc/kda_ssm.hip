@@ -288,36 +288,48 @@ __global__ __launch_bounds__(256) void kda_ssm_chunk_kernel(SsmParams p) {
 // over the local states: start_{j+1} = decay_j start_j + local_j (local_j
 // alone where a sequence starts in segment j).  A thread owns four state
 // values of a head and keeps eight segments' loads in flight.
-__global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmParams p) {
+__global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmParams p, float* d_s0) {
     const size_t kp4 = (size_t)p.K * p.P / 4;
     const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
     if (at >= (size_t)p.H * kp4) return;
     const int h = (int)(at / kp4);
     float4* L = reinterpret_cast<float4*>(p.seg_state) + at;
     const size_t step = (size_t)p.H * kp4;
+    // segments that hold chunks (a packed call may have fewer than its bound)
+    const int all = total_chunks(p), n_seg = min(p.n_seg, (all + p.cps - 1) / p.cps);
+    // the last segment's local state is of use only to d_s0
+    const int used = d_s0 ? n_seg : n_seg - 1;
+    ChunkWalk walk;
+    if (d_s0 && n_seg > 0) walk.init(p, n_seg - 1);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 8;
-    for (int j = 0; j < p.n_seg; j += U) {
+    for (int j = 0; j < n_seg; j += U) {
         float4 l[U];
         float d[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (j + u < p.n_seg - 1) {
-                const int k = p.reverse ? p.n_seg - 1 - (j + u) : j + u;
+            if (j + u < used) {
+                const int k = p.reverse ? n_seg - 1 - (j + u) : j + u;
                 l[u] = L[(size_t)k * step];
                 d[u] = p.seg_decay[(size_t)k * p.H + h];
             }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (j + u < p.n_seg) {
-                const int k = p.reverse ? p.n_seg - 1 - (j + u) : j + u;
+            if (j + u < n_seg) {
+                const int k = p.reverse ? n_seg - 1 - (j + u) : j + u;
+                // a sequence that starts (in reverse: ends) in this segment
+                // takes its own start state, which an empty one passes on
                 L[(size_t)k * step] = s;
-                if (j + u < p.n_seg - 1) {
+                if (j + u < used) {
                     if (d[u] < 0.f)
                         s = l[u];
                     else
                         s = make_float4(fmaf(d[u], s.x, l[u].x), fmaf(d[u], s.y, l[u].y), fmaf(d[u], s.z, l[u].z),
                                         fmaf(d[u], s.w, l[u].w));
+                }
+                if (d_s0) {
+                    if (walk.first()) reinterpret_cast<float4*>(d_s0)[(size_t)walk.seq * step + at] = s;
+                    walk.prev();
                 }
             }
         }
@@ -468,9 +480,9 @@ hipError_t launch_ssm_chunks(int dtype, bool out, int nt, const SsmParams& p, in
     return p.K == 128 ? chunks_launch<float, 128>(out, nt, p, segs, st) : chunks_launch<float, 64>(out, nt, p, segs, st);
 }
 
-hipError_t launch_ssm_combine(const SsmParams& p, hipStream_t st) {
+hipError_t launch_ssm_combine(const SsmParams& p, float* d_s0, hipStream_t st) {
     const size_t n = (size_t)p.H * p.K * p.P / 4;
-    hipLaunchKernelGGL(kda_ssm_combine_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, p);
+    hipLaunchKernelGGL(kda_ssm_combine_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, p, d_s0);
     return hipGetLastError();
 }
 

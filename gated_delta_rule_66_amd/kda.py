@@ -46,6 +46,8 @@ EXPORTED_SYMBOLS = (
     "kda_short_conv_step",
     "kda_selective_scan_fwd_workspace_size",
     "kda_selective_scan_fwd",
+    "kda_selective_scan_bwd_workspace_size",
+    "kda_selective_scan_bwd",
     "kda_selective_scan_step",
     "kda_group_norm_fwd",
     "kda_group_norm_bwd_workspace_size",
@@ -116,6 +118,9 @@ def load_library(path: str = LIB_PATH):
     lib.kda_short_conv_step.argtypes = [i, i, i, i, i, p, ll] + [p] * 4 + [p]
     lib.kda_selective_scan_fwd_workspace_size.argtypes = [i] * 8
     lib.kda_selective_scan_fwd.argtypes = [i, p] + [i] * 7 + [p, ll, p, ll, p, p, ll, p, ll] + [p] * 5 + [p, sz, p]
+    lib.kda_selective_scan_bwd_workspace_size.argtypes = [i] * 8
+    lib.kda_selective_scan_bwd.argtypes = [i, p] + [i] * 7 + [p, ll, p, ll, p, p, ll, p, ll] + [p] * 6 + \
+        [ll, p, p, p, ll, p, ll, p, p, p, p, sz, p]
     lib.kda_selective_scan_step.argtypes = [i] * 7 + [p, ll, p, ll, p, p, ll, p, ll] + [p] * 4 + [p]
     lib.kda_group_norm_fwd.argtypes = [i] * 7 + [f, p, ll, p, p, p, ll, p, p]
     lib.kda_group_norm_bwd_workspace_size.argtypes = [i] * 4

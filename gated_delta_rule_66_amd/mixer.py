@@ -291,6 +291,55 @@ def selective_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     return out, final_state
 
 
+def _out_rows(t, name, shape, lead, dtype, dev):
+    """An output that may be a view of a wider buffer, or a new tensor; and its row stride."""
+    if t is None:
+        width = 1
+        for n in shape[lead:]:
+            width *= n
+        return torch.empty(shape, dtype=dtype, device=dev), width
+    return t, _rows(t, name, shape, lead, dtype, dev)
+
+
+def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                       D: Optional[torch.Tensor], dt_bias: Optional[torch.Tensor], d_y: torch.Tensor,
+                       initial_state: Optional[torch.Tensor] = None, d_final_state: Optional[torch.Tensor] = None, *,
+                       dt_softplus: bool = False, cu_seqlens: Optional[torch.Tensor] = None,
+                       want_d_initial_state: Optional[bool] = None, dx: Optional[torch.Tensor] = None,
+                       dB: Optional[torch.Tensor] = None, dC: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``selective_scan_fwd`` through ``kda_selective_scan_bwd``:
+    (dx, ddt, dA, dB, dC, dD, ddt_bias, d_initial_state), None where the
+    forward has no such input (d_initial_state: unless
+    ``want_d_initial_state`` says otherwise).  ``dx``, ``dB`` and ``dC`` may be
+    passed as views of one wider buffer."""
+    lead = 2 if cu_seqlens is None else 1
+    dev, H, G, K, P, code, xs, ds, bs, cs = _scan_args(x, dt, A, B, C, D, dt_bias, lead)
+    N, T = _seqs(x, cu_seqlens, lead)
+    ty = x.dtype
+    _check(d_y, "d_y", x.shape, ty, dev)
+    for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
+        if t is not None:
+            _check(t, name, (N, H, K, P), torch.float32, dev)
+    dx, dxs = _out_rows(dx, "dx", x.shape, lead, ty, dev)
+    dB, dbs = _out_rows(dB, "dB", B.shape, lead, ty, dev)
+    dC, dcs = _out_rows(dC, "dC", B.shape, lead, ty, dev)
+    ddt = torch.empty(x.shape[:-1], dtype=ty, device=dev)
+    dA = torch.empty((H,), dtype=torch.float32, device=dev)
+    dD = torch.empty((H,), dtype=torch.float32, device=dev) if D is not None else None
+    dbias = torch.empty((H,), dtype=torch.float32, device=dev) if dt_bias is not None else None
+    if want_d_initial_state is None:
+        want_d_initial_state = initial_state is not None
+    ds0 = torch.empty((N, H, K, P), dtype=torch.float32, device=dev) if want_d_initial_state else None
+    need = _size("kda_selective_scan_bwd_workspace_size", N, int(cu_seqlens is not None), T, H, G, K, P, code)
+    workspace, have = _workspace(workspace, need, dev)
+    _call("kda_selective_scan_bwd", dev, N, _p(cu_seqlens), T, H, G, K, P, code, int(bool(dt_softplus)), _p(x), xs,
+          _p(dt), ds, _p(A), _p(B), bs, _p(C), cs, _p(D), _p(dt_bias), _p(initial_state), _p(d_y),
+          _p(d_final_state), _p(dx), dxs, _p(ddt), _p(dA), _p(dB), dbs, _p(dC), dcs, _p(dD), _p(dbias), _p(ds0),
+          _p(workspace), have)
+    return dx, ddt, dA, dB, dC, dD, dbias, ds0
+
+
 def selective_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
                         D: Optional[torch.Tensor], dt_bias: Optional[torch.Tensor], state: torch.Tensor, *,
                         dt_softplus: bool = False, out: Optional[torch.Tensor] = None):

@@ -500,6 +500,32 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
                                   size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Its gradients, from dL/dy (d_y, [tokens, H, P] dt) and dL/dfinal_state
+ * (d_final_state fp32 or NULL):
+ *   dx : [tokens, H, P];  d_delta : [tokens, H] (of dt_t, before bias and
+ *        softplus);  dB, dC : [tokens, G, K], summed over the group's heads;
+ *        all dt, row strides dx_stride, db_stride, dc_stride (multiples of 16
+ *        bytes; columns of one wider buffer are fine)
+ *   dA : [H] fp32;  dD, d_dt_bias : [H] fp32 or NULL
+ *   d_initial_state : [N, H, K, P] fp32 or NULL
+ *   workspace : kda_selective_scan_bwd_workspace_size(...) bytes: the state
+ *        before and the adjoint behind every chunk of 64 tokens (fp32), and
+ *        fp32 parts of dB and dC
+ * The states are recomputed from the inputs.  No tokens: dA, dD and d_dt_bias
+ * are zero, and dL/dfinal_state passes to d_initial_state.
+ */
+size_t kda_selective_scan_bwd_workspace_size(int N, int packed, int T, int H, int G, int K, int P, kda_dtype dt);
+kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, int G, int K, int P, kda_dtype dt,
+                                  int dt_softplus, const void* x, long long x_stride, const void* delta,
+                                  long long delta_stride, const float* A, const void* B, long long b_stride,
+                                  const void* C, long long c_stride, const float* D, const float* dt_bias,
+                                  const float* initial_state, const void* d_y, const float* d_final_state, void* dx,
+                                  long long dx_stride, void* d_delta, float* dA, void* dB, long long db_stride,
+                                  void* dC, long long dc_stride, float* dD, float* d_dt_bias,
+                                  float* d_initial_state, void* workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+
+/*
  * One token of N sequences: state [N, H, K, P] is updated IN PLACE and read
  * and written once.  x [N, H, P], delta [N, H], B, C [N, G, K], y [N, H, P].
  */
@@ -558,6 +584,8 @@ kda_status kda_group_norm_bwd(int rows, int C, int groups, kda_dtype dt, kda_act
  * "bwd_value_side", "bwd_solve", "bwd_gated"; the mixer operators'
  * "short_conv", "short_conv_bwd", "short_conv_bwd_sums", "short_conv_step",
  * "scan_prep", "scan_summary", "scan_combine", "scan_output", "scan_step",
+ * "scan_bwd_states", "scan_bwd_combine", "scan_bwd_adjoints", "scan_bwd_grads",
+ * "scan_bwd_join", "scan_bwd_sums",
  * "group_norm", "group_norm_bwd", "group_norm_bwd_sums") and durations in milliseconds, releases the
  * events, and returns the number of timed launches (-1: profiling was not
  * started or a HIP event query failed).  The record is process-wide (the one

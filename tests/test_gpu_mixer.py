@@ -399,3 +399,127 @@ def test_selective_scan_step(dtype, n, h, g, k, p):
     y = torch.stack(ys, 1).reshape(want.shape)
     R.close(y, want, R.HALF[dtype] * want.abs() + chain * size, "y")
     R.close(state, wfin, chain * sfin, "state")
+
+
+def scan_grads(c, dy, ds, size=False):
+    """Gradients in 64 bits, or (size) the sums of absolute values behind them."""
+    f = (lambda v: None if v is None else v.abs()) if size else (lambda v: v)
+    x, B, C, D, s = (f(flat(c, "x")), f(flat(c, "B")), f(flat(c, "C")), f(up(c["D"])), f(up(c["s"])))
+    if s is None:
+        s = torch.zeros(c["n"], *c["ds"].shape[1:], dtype=torch.float64)
+    raw = flat(c, "dt") + (up(c["bias"]) if c["bias"] is not None else 0.0)
+    delta = torch.nn.functional.softplus(raw) if c["softplus"] else raw
+    slope = torch.sigmoid(raw) if c["softplus"] else torch.ones_like(raw)
+    la = delta * up(c["A"])                       # log decays: a leaf of their own
+    leaves = [v.clone().requires_grad_() for v in (x, B, C, s, delta, la)]
+    lx, lB, lC, ls, ldelta, lla = leaves
+    if D is not None:
+        D = D.clone().requires_grad_()
+    # the recurrence with the two uses of delta apart: exp(la) and delta B x^T
+    ys, fin = [], []
+    H, G = x.shape[1], B.shape[1]
+    Bh, Ch = (v.repeat_interleave(H // G, 1) for v in (lB, lC))
+    for i, (a, b) in enumerate(c["ranges"]):
+        S = ls[i]
+        for t in range(a, b):
+            S = torch.exp(lla[t])[:, None, None] * S + (ldelta[t][:, None] * Bh[t])[:, :, None] * lx[t][:, None, :]
+            y = torch.einsum("hk,hkp->hp", Ch[t], S)
+            ys.append(y + D[:, None] * lx[t] if D is not None else y)
+        fin.append(S)
+    loss = (torch.stack(fin) * ds).sum()
+    if ys:
+        loss = loss + (torch.stack(ys) * dy).sum()
+    got = torch.autograd.grad(loss, leaves + ([D] if D is not None else []), allow_unused=True, materialize_grads=True)
+    gx, gB, gC, gs, gdelta, gla = got[:6]
+    A = up(c["A"]).abs() if size else up(c["A"])
+    gd = (gdelta + A * gla) * slope
+    return {"dx": gx, "ddt": gd, "dA": (gla * delta).sum(0), "dB": gB, "dC": gC,
+            "dD": got[6] if D is not None else None, "ddt_bias": gd.sum(0) if c["bias"] is not None else None,
+            "dstate": gs}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", SCAN, ids=SCAN_IDS)
+def test_selective_scan_backward(case, dtype):
+    """bf16 outputs: each term goes through at most two roundings to bf16
+    (score or its gradient; state), 2 2^-8 of the sum of absolute values.  fp32
+    outputs: the chunk's values are fp32 throughout; a sum over m tokens in
+    fp64 adds nothing, chains over a sequence 2^-23 a step."""
+    c = scan_case(case, dtype, 8)
+    got = dict(zip(("dx", "ddt", "dA", "dB", "dC", "dD", "ddt_bias", "dstate"),
+                   kda.selective_scan_bwd(*scan_args(c), dev(c["dy"]), dev(c["s"]), dev(c["ds"]),
+                                          dt_softplus=c["softplus"], cu_seqlens=dev(c["cu"]),
+                                          want_d_initial_state=True)))
+    dy, ds = flat(c, "dy"), up(c["ds"])
+    want, size = scan_grads(c, dy, ds), scan_grads(c, dy.abs(), ds.abs(), True)
+    steps = max([b - a for a, b in c["ranges"]] + [0]) + 64
+    chain = 2.0 ** -19 + steps * 2.0 ** -23
+    inner = 2 * 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    for name in ("dx", "dB", "dC"):
+        R.close(got[name].reshape(want[name].shape), want[name],
+                R.HALF[dtype] * want[name].abs() + (inner + chain) * size[name], name)
+    R.close(got["ddt"].reshape(want["ddt"].shape), want["ddt"],
+            R.HALF[dtype] * want["ddt"].abs() + chain * size["ddt"], "ddt")
+    for name in ("dA", "dD", "ddt_bias", "dstate"):
+        if want[name] is None:
+            assert got[name] is None
+        else:
+            R.close(got[name], want[name], chain * size[name], name)
+
+
+def test_selective_scan_backward_against_differences():
+    # a directional difference of the library's own fp32 forward
+    c = scan_case((2, 90, None, 4, 2, 64, 64, True, True, True), torch.float32, 9)
+    args, s, dy, ds = scan_args(c), dev(c["s"]), dev(c["dy"]), dev(c["ds"])
+    grads = kda.selective_scan_bwd(*args, dy, s, ds, dt_softplus=True)
+    gen = torch.Generator().manual_seed(10)
+    eps = 1e-2
+
+    def loss(*v):
+        y, fin = kda.selective_scan_fwd(*v[:7], v[7], dt_softplus=True)
+        return float((y.double() * dy.double()).sum() + (fin.double() * ds.double()).sum())
+
+    order = args[:7] + [s]
+    for k, (v, g) in enumerate(zip(order, (grads[0], grads[1], grads[2], grads[3], grads[4], grads[5], grads[6], grads[7]))):
+        d = torch.randn(v.shape, generator=gen).to(DEV)
+        d = d / d.norm() * (0.1 * v.norm())
+        hi, lo = list(order), list(order)
+        hi[k], lo[k] = v + eps * d, v - eps * d
+        diff = (loss(*hi) - loss(*lo)) / (2 * eps)
+        along = float((g.double() * d.double()).sum())
+        # third-order term eps^2 / 6 of the direction, and fp32 cancellation in the loss
+        scale = float((g.double() * d.double()).abs().sum()) + 1e-3 * abs(loss(*order))
+        assert abs(diff - along) < 2e-3 * scale, (k, diff, along)
+
+
+def test_selective_scan_backward_into_one_buffer_and_padding():
+    gen = torch.Generator().manual_seed(11)
+    h, g, k, p, lens = 4, 2, 64, 64, [70, 3, 90]
+    rows, width = 200, h * p + 2 * g * k
+    cu = dev(packed(lens))
+
+    def data(n):
+        torch.manual_seed(0)
+        return [torch.randn(200, *s, device=DEV).to(torch.bfloat16)[:n].contiguous()
+                for s in ((h, p), (h,), (g, k), (g, k), (h, p))]
+    A, bias = dev(-torch.rand(h, generator=gen) - 0.1), dev(rnd(gen, h) - 3)
+    x, dt, B, C, dy = data(rows)
+    for v in (x, dt, B, C, dy):
+        v[163:] = float("nan")
+    buf = torch.full((rows, width), 7.0, dtype=torch.bfloat16, device=DEV)
+    views = [buf[:, :h * p].view(rows, h, p), buf[:, h * p:h * p + g * k].view(rows, g, k),
+             buf[:, h * p + g * k:].view(rows, g, k)]
+    got = kda.selective_scan_bwd(x, dt, A, B, C, None, bias, dy, dt_softplus=True, cu_seqlens=cu, dx=views[0],
+                                 dB=views[1], dC=views[2])
+    x, dt, B, C, dy = data(163)
+    want = kda.selective_scan_bwd(x, dt, A, B, C, None, bias, dy, dt_softplus=True, cu_seqlens=cu)
+    for i in (0, 1, 3, 4):
+        a, b = got[i][:163].float(), want[i].float()
+        # heads may be summed in other parts: one bf16 step
+        assert torch.allclose(a, b, rtol=2 ** -7, atol=2 ** -7 * float(b.abs().max()))
+    for i in (2, 6):
+        assert torch.allclose(got[i], want[i], rtol=1e-4, atol=1e-4 * float(want[i].abs().max()))
+    assert (buf[163:] == 7.0).all()
+    with pytest.raises(kda.KDAError):
+        kda.selective_scan_bwd(x, dt, A, B, C, None, bias, dy, dt_softplus=True, cu_seqlens=cu,
+                               dx=buf[:163, :h * p].view(163, h, p), dB=buf[:163, 64:64 + g * k].view(163, g, k))
