@@ -233,7 +233,8 @@ kda_status kda_short_conv_step(int N, int D, int W, kda_dtype dt, kda_activation
 
 static kda_status norm_check(int rows, int C, int groups, kda_dtype dt, kda_activation act, const void* x,
                              long long x_stride, const float* weight, const float* bias, const void* gate,
-                             long long gate_stride) {
+                             long long gate_stride, float eps) {
+    if (!(eps >= 0.f)) return KDA_ERR_INVALID_ARG;
     if (rows < 0 || C <= 0 || groups <= 0 || C % groups || !dtype_ok(dt) || !act_ok(act)) return KDA_ERR_INVALID_ARG;
     int R, team, block;
     if (!norm_variant((int)dt, false, C / groups, &R, &team, &block) &&
@@ -265,7 +266,7 @@ kda_status kda_group_norm_fwd(int rows, int C, int groups, kda_dtype dt, kda_act
                               int gate_first, float eps, const void* x, long long x_stride, const float* weight,
                               const float* bias, const void* gate, long long gate_stride, void* y,
                               hipStream_t stream) {
-    kda_status s = norm_check(rows, C, groups, dt, act, x, x_stride, weight, bias, gate, gate_stride);
+    kda_status s = norm_check(rows, C, groups, dt, act, x, x_stride, weight, bias, gate, gate_stride, eps);
     if (s != KDA_OK) return s;
     if (rows == 0) return KDA_OK;
     const size_t es = esize(dt);
@@ -300,7 +301,7 @@ static int norm_row_blocks(int rows, int groups, int team) {
 }
 
 size_t kda_group_norm_bwd_workspace_size(int rows, int C, int groups, kda_dtype dt) {
-    if (norm_check(0, C, groups, dt, KDA_ACT_NONE, nullptr, C, nullptr, nullptr, nullptr, C) != KDA_OK || rows < 0)
+    if (norm_check(0, C, groups, dt, KDA_ACT_NONE, nullptr, C, nullptr, nullptr, nullptr, C, 0.f) != KDA_OK || rows < 0)
         return (size_t)-1;
     int R, team, block, most = 1;
     for (int vec = 0; vec < 2; ++vec)
@@ -316,7 +317,7 @@ kda_status kda_group_norm_bwd(int rows, int C, int groups, kda_dtype dt, kda_act
                               const float* bias, const void* gate, long long gate_stride, const void* d_y, void* dx,
                               float* dweight, float* dbias, void* d_gate, void* workspace, size_t workspace_bytes,
                               hipStream_t stream) {
-    kda_status s = norm_check(rows, C, groups, dt, act, x, x_stride, weight, bias, gate, gate_stride);
+    kda_status s = norm_check(rows, C, groups, dt, act, x, x_stride, weight, bias, gate, gate_stride, eps);
     if (s != KDA_OK) return s;
     const size_t es = esize(dt);
     for (const void* t : {d_y, (const void*)dx, (const void*)d_gate})

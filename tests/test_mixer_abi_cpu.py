@@ -1,0 +1,197 @@
+"""Argument checks of the mixer operators' C ABI and binding (no GPU: nothing
+here is launched, addresses are never dereferenced)."""
+import ctypes
+
+import pytest
+import torch
+
+import gated_delta_rule_66_amd as kda
+from gated_delta_rule_66_amd import kda as K_
+from gated_delta_rule_66_amd import mixer
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+F32, BF16 = 0, 1
+M = 1 << 30             # distance between the made-up buffers
+BIG = ctypes.c_size_t(-1).value
+
+
+def lib():
+    import os
+    if not os.path.exists(kda.LIB_PATH):
+        kda.build_library()
+    return K_.load_library()
+
+
+def buffers(*names):
+    return {n: (i + 1) * M for i, n in enumerate(names)}
+
+
+def conv(call="fwd", n=2, cu=None, t=10, d=64, w=4, dt=BF16, act=1, xs=None, ws_bytes=1 << 40, **kw):
+    b = buffers("x", "weight", "bias", "s0", "y", "sT", "dy", "dsT", "dx", "dw", "db", "ds0", "ws")
+    b.update(kw)
+    xs = d if xs is None else xs
+    if call == "fwd":
+        return lib().kda_short_conv_fwd(n, cu, t, d, w, dt, act, b["x"], xs, b["weight"], b["bias"], b["s0"], b["y"],
+                                        b["sT"], None)
+    if call == "step":
+        return lib().kda_short_conv_step(n, d, w, dt, act, b["x"], xs, b["weight"], b["bias"], b["s0"], b["y"], None)
+    return lib().kda_short_conv_bwd(n, cu, t, d, w, dt, act, b["x"], xs, b["weight"], b["bias"], b["s0"], b["dy"],
+                                    b["dsT"], b["dx"], b["dw"], b["db"], b["ds0"], b["ws"], ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", ["fwd", "bwd", "step"])
+def test_short_conv_refusals(call):
+    assert conv(call, n=-1) == INVALID
+    assert conv(call, d=-1) == INVALID
+    assert conv(call, dt=5) == INVALID
+    assert conv(call, act=9) == INVALID
+    assert conv(call, w=1) == UNSUPPORTED
+    assert conv(call, w=5) == UNSUPPORTED
+    assert conv(call, x=None) == INVALID
+    assert conv(call, weight=None) == INVALID
+    assert conv(call, weight=M + 2) == INVALID
+    assert conv(call, x=M + 1) == INVALID
+    assert conv(call, xs=63) == INVALID
+    assert conv(call, d=0, x=None) == OK
+    if call != "step":
+        assert conv(call, t=-1) == INVALID
+        assert conv(call, n=1 << 20, t=1 << 20) == UNSUPPORTED
+
+
+def test_short_conv_overlaps():
+    assert conv(y=M) == INVALID                             # y is x
+    assert conv(y=M + 64) == INVALID
+    assert conv(sT=4 * M) == INVALID                        # final over initial state
+    assert conv("step", y=4 * M) == INVALID                 # y over the state
+    assert conv("bwd", dx=M) == INVALID
+    assert conv("bwd", dx=7 * M) == INVALID                 # over d_y
+    assert conv("bwd", ds0=8 * M) == INVALID                # over d_final_state
+    need = lib().kda_short_conv_bwd_workspace_size(2, 0, 10, 64, 4, BF16)
+    assert 0 < need < BIG
+    assert conv("bwd", ws_bytes=need - 1) == WORKSPACE
+    assert conv("bwd", ws=None) == WORKSPACE
+    assert lib().kda_short_conv_bwd_workspace_size(2, 0, 10, 64, 7, BF16) == BIG
+    assert conv(n=0, x=None, y=None) == OK
+
+
+def scan(call="fwd", n=2, cu=None, t=10, h=4, g=2, k=64, p=64, dt=BF16, xs=None, ds=None, bs=None, cs=None, dxs=None,
+         dbs=None, dcs=None, ws_bytes=1 << 40, **kw):
+    b = buffers("x", "delta", "A", "B", "C", "D", "bias", "s0", "y", "sT", "dy", "dsT", "dx", "ddt", "dA", "dB", "dC",
+                "dD", "dbias", "ds0", "ws")
+    b.update(kw)
+    pick = lambda v, width: width if v is None else v
+    xs, ds, bs, cs = pick(xs, h * p), pick(ds, h), pick(bs, g * k), pick(cs, g * k)
+    head = [b["x"], xs, b["delta"], ds, b["A"], b["B"], bs, b["C"], cs, b["D"], b["bias"]]
+    if call == "fwd":
+        return lib().kda_selective_scan_fwd(n, cu, t, h, g, k, p, dt, 1, *head, b["s0"], b["y"], b["sT"], b["ws"],
+                                            ws_bytes, None)
+    if call == "step":
+        return lib().kda_selective_scan_step(n, h, g, k, p, dt, 1, *head, b["s0"], b["y"], None)
+    return lib().kda_selective_scan_bwd(n, cu, t, h, g, k, p, dt, 1, *head, b["s0"], b["dy"], b["dsT"], b["dx"],
+                                        pick(dxs, h * p), b["ddt"], b["dA"], b["dB"], pick(dbs, g * k), b["dC"],
+                                        pick(dcs, g * k), b["dD"], b["dbias"], b["ds0"], b["ws"], ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", ["fwd", "bwd", "step"])
+def test_selective_scan_refusals(call):
+    assert scan(call, n=-1) == INVALID
+    assert scan(call, g=0) == INVALID
+    assert scan(call, h=3) == INVALID                       # groups divide heads
+    assert scan(call, k=96) == UNSUPPORTED
+    assert scan(call, p=32) == UNSUPPORTED
+    assert scan(call, dt=7) == INVALID
+    for name in ("x", "delta", "A", "B", "C"):
+        assert scan(call, **{name: None}) == INVALID, name
+    for name, at in (("x", M), ("B", 4 * M), ("C", 5 * M), ("s0", 8 * M)):
+        assert scan(call, **{name: at + 8}) == INVALID, name
+    assert scan(call, xs=4 * 64 - 8) == INVALID
+    assert scan(call, xs=4 * 64 + 4) == INVALID             # not a multiple of 16 bytes
+    assert scan(call, bs=2 * 64 + 1) == INVALID
+    assert scan(call, ds=3) == INVALID
+    assert scan(call, h=0) == OK
+    if call != "step":
+        assert scan(call, t=-1) == INVALID
+        assert scan(call, n=1 << 16, t=1 << 16) == UNSUPPORTED
+
+
+def test_selective_scan_overlaps_and_workspace():
+    assert scan(y=M) == INVALID                             # y over x
+    assert scan(sT=8 * M + 16) == INVALID                   # partly over the initial state
+    assert scan("step", y=8 * M) == INVALID
+    assert scan("bwd", dx=M) == INVALID
+    assert scan("bwd", ds0=12 * M) == INVALID               # over d_final_state
+    # dx, dB and dC as columns of one buffer: apart, or not
+    width = 4 * 64 + 2 * 2 * 64
+    views = dict(dx=13 * M, dB=13 * M + 2 * 256, dC=13 * M + 2 * 384, dxs=width, dbs=width, dcs=width)
+    assert scan("bwd", ws=None, **views) == WORKSPACE       # every check before the workspace passed
+    assert scan("bwd", ws=None, **dict(views, dB=13 * M + 2 * 248)) == INVALID
+    assert scan("bwd", ws=None, **dict(views, dC=13 * M + 2 * 392)) == INVALID     # into the next row
+    need = lib().kda_selective_scan_bwd_workspace_size(2, 0, 10, 4, 2, 64, 64, BF16)
+    assert 0 < need < BIG
+    assert scan("bwd", ws_bytes=need - 1) == WORKSPACE
+    need = lib().kda_selective_scan_fwd_workspace_size(1, 1, 100000, 4, 2, 64, 64, BF16)
+    assert scan(n=1, cu=9 << 40, t=100000, ws_bytes=need - 1) == WORKSPACE
+    assert lib().kda_selective_scan_fwd_workspace_size(1, 0, 100, 4, 3, 64, 64, BF16) == BIG
+
+
+def norm(call="fwd", rows=6, C=128, groups=2, dt=BF16, act=1, xs=None, zs=None, eps=1e-5, ws_bytes=1 << 40, **kw):
+    b = buffers("x", "w", "b", "z", "y", "dy", "dx", "dw", "db", "dz", "ws")
+    b.update(kw)
+    xs, zs = C if xs is None else xs, C if zs is None else zs
+    head = [rows, C, groups, dt, act, 0, 0, eps, b["x"], xs, b["w"], b["b"], b["z"], zs]
+    if call == "fwd":
+        return lib().kda_group_norm_fwd(*head, b["y"], None)
+    return lib().kda_group_norm_bwd(*head, b["dy"], b["dx"], b["dw"], b["db"], b["dz"], b["ws"], ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", ["fwd", "bwd"])
+def test_group_norm_refusals(call):
+    assert norm(call, rows=-1) == INVALID
+    assert norm(call, groups=3) == INVALID
+    assert norm(call, groups=0) == INVALID
+    assert norm(call, act=4) == INVALID
+    assert norm(call, dt=2) == INVALID
+    assert norm(call, x=None) == INVALID
+    assert norm(call, x=M + 1) == INVALID
+    assert norm(call, xs=127) == INVALID
+    assert norm(call, zs=127) == INVALID
+    assert norm(call, C=1 << 17, groups=1) == UNSUPPORTED
+    # a width that only 16-byte accesses hold, with rows that do not allow them
+    assert norm(call, C=16384, groups=1, xs=16385) == UNSUPPORTED
+    assert norm(call, eps=-1.0) == INVALID
+    assert norm(call, eps=float("nan")) == INVALID
+
+
+def test_group_norm_overlaps_and_workspace():
+    assert norm(y=M + 256) == INVALID                       # partly over x
+    assert norm(y=4 * M, zs=256) == INVALID                 # over a gate with other rows
+    assert norm("bwd", dx=M) == INVALID
+    assert norm("bwd", dz=6 * M) == INVALID
+    assert norm("bwd", dz=7 * M) == INVALID                 # over dx
+    assert norm("bwd", dz=None) == INVALID                  # a gate without its gradient
+    need = lib().kda_group_norm_bwd_workspace_size(6, 128, 2, BF16)
+    assert 0 < need < BIG
+    assert norm("bwd", ws_bytes=need - 1) == WORKSPACE
+    assert norm(rows=0, x=None, y=None) == OK
+
+
+def test_binding_refuses_before_the_call():
+    x = torch.zeros(2, 4, 64)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.short_conv_fwd(x, torch.zeros(64, 4))
+    with pytest.raises(ValueError, match="GPU"):
+        kda.group_norm_fwd(x, 1)
+    with pytest.raises(ValueError, match="activation"):
+        mixer._act("relu")
+    rows = lambda t, lead: mixer._rows(t, "x", t.shape, lead, t.dtype, t.device)
+    t = torch.zeros(3, 5, 4, 8)
+    assert rows(t, 2) == 32
+    assert rows(t[:, :, :2], 2) == 32                       # a slice of each token's row
+    assert rows(t[:, :1], 2) == 160                         # one token a sequence
+    assert rows(t[:1, :3], 2) == 32
+    with pytest.raises(ValueError, match="evenly"):
+        rows(t[:, :3], 2)
+    with pytest.raises(ValueError, match="contiguous"):
+        rows(t[..., :4], 2)
+    with pytest.raises(ValueError, match="contiguous"):
+        rows(t.transpose(2, 3), 2)
