@@ -63,9 +63,9 @@ struct NormParams {
     float* part;            // [row blocks][2][C] or null
     int team;               // lanes that share one group of one row
 };
-// variant (vec, R, block): see launch code; false if the group is too wide
+// lanes (team), accesses a lane (R) and block of a group; false: too wide
 bool norm_variant(int dtype, bool vec, int Cg, int* R, int* team, int* block);
-hipError_t launch_norm_fwd(int dtype, bool vec, int R, int block, const NormParams& p, hipStream_t st);
+hipError_t launch_norm_fwd(int dtype, bool vec, int R, int block, const NormParams& p, int blocks, hipStream_t st);
 hipError_t launch_norm_bwd(int dtype, bool vec, int R, int block, const NormParams& p, int row_blocks,
                            hipStream_t st);
 

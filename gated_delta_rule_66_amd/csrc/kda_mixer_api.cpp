@@ -99,7 +99,7 @@ struct ConvBwdPlan {
 };
 ConvBwdPlan conv_bwd_plan(bool packed, int N, int T, int D, int V) {
     ConvBwdPlan b;
-    b.cx_log2 = cx_log2_for(D, V, 5);
+    b.cx_log2 = cx_log2_for(D, V, 6);
     const long long tys = 256 >> b.cx_log2, cb = (D + (V << b.cx_log2) - 1) / (V << b.cx_log2);
     b.tile = 32;
     const long long M = packed ? (long long)T : (long long)N * T;
@@ -140,7 +140,7 @@ kda_status kda_short_conv_fwd(int N, const int* cu_seqlens, int T, int D, int W,
     p.y = y; p.sT = final_state;
     const bool vec = vec_ok(dt, D, M > 1 ? x_stride : D, x) && aligned(y, 16) && aligned(initial_state, 16) &&
                      aligned(final_state, 16);
-    const int V = vec ? (int)(16 / es) : 1;
+    const int V = vec ? 4 : 1;
     p.cx_log2 = cx_log2_for(D, V, 8);
     conv_tiles(p, M, M * (D / V) >= (1LL << 21) ? 16 : 8);
     const int tys = 256 >> p.cx_log2;
@@ -158,7 +158,7 @@ size_t kda_short_conv_bwd_workspace_size(int N, int packed, int T, int D, int W,
     if (conv_sizes(N, T, D, W, dt, KDA_ACT_NONE, packed ? &some : nullptr, &M) != KDA_OK) return (size_t)-1;
     if (N == 0 || D == 0) return 0;
     // either access width: the narrow one has the fewer channels a block
-    const ConvBwdPlan a = conv_bwd_plan(packed != 0, N, T, D, 1), b = conv_bwd_plan(packed != 0, N, T, D, (int)(16 / esize(dt)));
+    const ConvBwdPlan a = conv_bwd_plan(packed != 0, N, T, D, 1), b = conv_bwd_plan(packed != 0, N, T, D, (int)(8 / esize(dt)));
     return (size_t)(a.blocks > b.blocks ? a.blocks : b.blocks) * (W + 1) * D * sizeof(float);
 }
 
@@ -201,7 +201,7 @@ kda_status kda_short_conv_bwd(int N, const int* cu_seqlens, int T, int D, int W,
     bool vec = vec_ok(dt, D, M > 1 ? x_stride : D, x);
     for (const void* t : {initial_state, d_y, d_final_state, (const void*)dx, (const void*)d_initial_state})
         vec = vec && aligned(t, 16);
-    const ConvBwdPlan b = conv_bwd_plan(cu_seqlens != nullptr, N, T, D, vec ? (int)(16 / es) : 1);
+    const ConvBwdPlan b = conv_bwd_plan(cu_seqlens != nullptr, N, T, D, vec ? (int)(8 / es) : 1);
     p.cx_log2 = b.cx_log2;
     conv_tiles(p, M, b.tile);
     KDA_LAUNCH("short_conv_bwd", launch_conv_bwd((int)dt, vec, p, b.blocks, stream));
@@ -279,23 +279,28 @@ kda_status kda_group_norm_fwd(int rows, int C, int groups, kda_dtype dt, kda_act
         return KDA_ERR_INVALID_ARG;
     bool vec = vec_ok(dt, C / groups, rows > 1 ? x_stride : C, x) && aligned(y, 16);
     if (gate) vec = vec && vec_ok(dt, C / groups, rows > 1 ? gate_stride : C, gate);
+    vec = vec && aligned(weight, 16) && aligned(bias, 16);
     NormParams p;
     int R, block;
     s = norm_setup(rows, C, groups, dt, act, center, gate_first, eps, x, x_stride, weight, bias, gate, gate_stride, vec,
                    &p, &R, &block);
     if (s != KDA_OK) return s;
     p.y = y;
-    const long long per = p.team <= 64 ? 256 / p.team : 1;
-    if (((long long)rows * groups / per + 1) * block >= 1LL << 32) return KDA_ERR_UNSUPPORTED;
-    KDA_LAUNCH("group_norm", launch_norm_fwd((int)dt, vec, R, block, p, stream));
+    // teams keep to one group each: sixteen waves a CU, or all there is to do
+    const long long per = p.team <= 64 ? 256 / p.team : 1, units = (long long)rows * groups;
+    long long blocks = (units + per - 1) / per, most = 256LL * 16 * 64 / block;
+    const long long least = (groups + per - 1) / per;       // a row slot at least
+    if (blocks > most) blocks = most > least ? most : least;
+    KDA_LAUNCH("group_norm", launch_norm_fwd((int)dt, vec, R, block, p, (int)blocks, stream));
     return KDA_OK;
 }
 
-// Row blocks of the backward: about eight blocks a CU over all groups, each
-// leaving one partial row of parameter sums.
-static int norm_row_blocks(int rows, int groups, int team) {
+// Row blocks of the backward: about twelve waves a CU over all groups, each
+// block leaving one partial row of parameter sums (8 C bytes, against at least
+// 6 C bytes a row of bf16).
+static int norm_row_blocks(int rows, int groups, int team, int block) {
     const long long teams = team <= 64 ? 256 / team : 1;
-    long long want = (rows + teams - 1) / teams, most = 2048 / groups;
+    long long want = (rows + teams - 1) / teams, most = 256LL * 12 * 64 / block / groups;
     if (most < 16) most = 16;
     return (int)(want < most ? (want > 0 ? want : 1) : most);
 }
@@ -306,7 +311,7 @@ size_t kda_group_norm_bwd_workspace_size(int rows, int C, int groups, kda_dtype 
     int R, team, block, most = 1;
     for (int vec = 0; vec < 2; ++vec)
         if (norm_variant((int)dt, vec != 0, C / groups, &R, &team, &block)) {
-            const int b = norm_row_blocks(rows, groups, team);
+            const int b = norm_row_blocks(rows, groups, team, block);
             most = b > most ? b : most;
         }
     return (size_t)most * 2 * C * sizeof(float);
@@ -341,13 +346,14 @@ kda_status kda_group_norm_bwd(int rows, int C, int groups, kda_dtype dt, kda_act
         bool vec = vec_ok(dt, C / groups, rows > 1 ? x_stride : C, x) && aligned(d_y, 16) && aligned(dx, 16) &&
                    aligned(d_gate, 16);
         if (gate) vec = vec && vec_ok(dt, C / groups, rows > 1 ? gate_stride : C, gate);
+        vec = vec && aligned(weight, 16) && aligned(bias, 16);
         int R, block;
         s = norm_setup(rows, C, groups, dt, act, center, gate_first, eps, x, x_stride, weight, bias, gate, gate_stride,
                        vec, &p, &R, &block);
         if (s != KDA_OK) return s;
         p.d_y = d_y; p.dx = dx; p.dz = d_gate;
         p.part = sums ? reinterpret_cast<float*>(workspace) : nullptr;
-        blocks = norm_row_blocks(rows, groups, p.team);
+        blocks = norm_row_blocks(rows, groups, p.team, block);
         KDA_LAUNCH("group_norm_bwd", launch_norm_bwd((int)dt, vec, R, block, p, blocks, stream));
     }
     if (sums)

@@ -5,23 +5,25 @@
 
 namespace kda {
 
-// V consecutive elements of T kept raw; V = 16 / sizeof(T) (one 16-byte
-// access) or 1.
+// V consecutive elements of T kept raw: one access of 16 or 8 bytes, or V = 1.
 template <typename T, int V> struct Vec {
+    static_assert(V == 1 || V * sizeof(T) == 16 || V * sizeof(T) == 8, "one access");
     T v[V];
     __device__ __forceinline__ void load(const T* p) {
-        if constexpr (V == 1) {
-            v[0] = *p;
-        } else {
-            static_assert(V * sizeof(T) == 16, "one 16-byte access");
+        if constexpr (V * sizeof(T) == 16)
             *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
-        }
+        else if constexpr (V * sizeof(T) == 8)
+            *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
+        else
+            v[0] = *p;
     }
     __device__ __forceinline__ void store(T* p) const {
-        if constexpr (V == 1)
-            *p = v[0];
-        else
+        if constexpr (V * sizeof(T) == 16)
             *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+        else if constexpr (V * sizeof(T) == 8)
+            *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
+        else
+            *p = v[0];
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll

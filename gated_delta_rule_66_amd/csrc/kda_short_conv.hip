@@ -6,16 +6,18 @@
 // Memory bound: 2 W + 6 flops a value against 4 bytes moved (bf16).  A thread
 // owns 16 bytes of channels and a tile of consecutive tokens, the last W - 1
 // rows in registers, so every row is read once and W - 1 halo rows more per
-// tile; loads go out eight rows at a time.  No LDS: neighbouring tokens of a
+// tile; four rows are loaded while the four before them are worked on.  No LDS: neighbouring tokens of a
 // channel meet in one thread.
 #include "kda_mixer.h"
 #include "kda_mixer_device.h"
+
+#include <type_traits>
 
 namespace kda {
 
 namespace {
 
-constexpr int kRowsAhead = 8;    // token rows loaded together
+constexpr int kRowsAhead = 4;    // token rows loaded together, one group ahead
 
 // The runs of one sequence each that make up a tile [a, b) of token rows.
 // Offsets are clamped to [0, T], so that any cu keeps every access in bounds;
@@ -156,28 +158,39 @@ __global__ __launch_bounds__(256) void kda_conv_fwd_kernel(ConvParams p) {
         T* y = reinterpret_cast<T*>(p.y) + base * p.D;
         Vec<T, V> win[W - 1];
         load_halo<T, V, W>(p, x, run.seq, run.s0, run.a, c, win);
-        for (int t = run.a; t < run.end; t += kRowsAhead) {
-            Vec<T, V> row[kRowsAhead];
+        auto row_out = [&](int at, const Vec<T, V>& row) {
+            Vec<T, V> o;
 #pragma unroll
-            for (int u = 0; u < kRowsAhead; ++u)
-                if (t + u < run.end) row[u].load(x + (size_t)(t + u) * p.x_stride + c);
+            for (int i = 0; i < V; ++i) {
+                float acc = fmaf(wt[W - 1][i], row.f(i), bs[i]);
 #pragma unroll
-            for (int u = 0; u < kRowsAhead; ++u) {
-                if (t + u < run.end) {
-                    Vec<T, V> o;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        float acc = fmaf(wt[W - 1][i], row[u].f(i), bs[i]);
-#pragma unroll
-                        for (int w = 0; w < W - 1; ++w) acc = fmaf(wt[w][i], win[w].f(i), acc);
-                        o.set(i, act_of<T>(acc, p.act));
-                    }
-                    o.store(y + (size_t)(t + u) * p.D + c);
-#pragma unroll
-                    for (int w = 0; w + 1 < W - 1; ++w) win[w] = win[w + 1];
-                    win[W - 2] = row[u];
-                }
+                for (int w = 0; w < W - 1; ++w) acc = fmaf(wt[w][i], win[w].f(i), acc);
+                o.set(i, act_of<T>(acc, p.act));
             }
+            o.store(y + (size_t)at * p.D + c);
+#pragma unroll
+            for (int w = 0; w + 1 < W - 1; ++w) win[w] = win[w + 1];
+            win[W - 2] = row;
+        };
+        auto fetch = [&](int at, Vec<T, V>(&rows)[kRowsAhead]) {
+#pragma unroll
+            for (int u = 0; u < kRowsAhead; ++u) rows[u].load(x + (size_t)(at + u) * p.x_stride + c);
+        };
+        int t = run.a;
+        Vec<T, V> now[kRowsAhead], next[kRowsAhead];
+        if (t + kRowsAhead <= run.end) fetch(t, next);
+        while (t + kRowsAhead <= run.end) {
+#pragma unroll
+            for (int u = 0; u < kRowsAhead; ++u) now[u] = next[u];
+            if (t + 2 * kRowsAhead <= run.end) fetch(t + kRowsAhead, next);
+#pragma unroll
+            for (int u = 0; u < kRowsAhead; ++u) row_out(t + u, now[u]);
+            t += kRowsAhead;
+        }
+        for (; t < run.end; ++t) {
+            Vec<T, V> row;
+            row.load(x + (size_t)t * p.x_stride + c);
+            row_out(t, row);
         }
         if (p.sT && run.end == run.s1) {
 #pragma unroll
@@ -198,7 +211,7 @@ __global__ __launch_bounds__(256) void kda_conv_fwd_kernel(ConvParams p) {
 // added across the block's tile rows in LDS (fixed order) and leave as one
 // partial row per block, summed by kda_sum_rows_kernel.
 template <typename T, int V, int W>
-__global__ __launch_bounds__(256) void kda_conv_bwd_kernel(ConvParams p) {
+__global__ __launch_bounds__(256, 3) void kda_conv_bwd_kernel(ConvParams p) {
     const int cx = 1 << p.cx_log2;
     const int lane_c = threadIdx.x & (cx - 1);
     const int c = (blockIdx.y * cx + lane_c) * V;
@@ -242,74 +255,93 @@ __global__ __launch_bounds__(256) void kda_conv_bwd_kernel(ConvParams p) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) q[j][i] = 0.f;
             const bool opens = run.a == run.s0;
-            const int stop = run.end + W - 1;       // rows whose q this run uses, and where dx lags
-            constexpr int kAhead = 4;
-            for (int s = run.a; s < stop; s += kAhead) {
-                Vec<T, V> xr[kAhead], gr[kAhead];
+            // One row: q of row s (0 behind the sequence), its share of the
+            // parameter sums if it is the run's, and the gradient of row
+            // s - W + 1.  MAIN: row s and that row are both the run's, and that
+            // row is no row of the final state (it is W - 1 before a row that
+            // exists), so nothing needs asking.
+            auto step = [&](auto main, int s, const Vec<T, V>& xr, const Vec<T, V>& gr) {
+                constexpr bool MAIN = decltype(main)::value;
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    if (s + u < stop && s + u < run.s1) {
-                        xr[u].load(x + (size_t)(s + u) * p.x_stride + c);
-                        gr[u].load(dy + (size_t)(s + u) * p.D + c);
-                    }
-                }
+                for (int j = 0; j + 1 < W; ++j)
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    if (s + u < stop) {
-                        const int sr = s + u;
+                    for (int i = 0; i < V; ++i) q[j][i] = q[j + 1][i];
+                if (MAIN || s < run.s1) {
 #pragma unroll
-                        for (int j = 0; j + 1 < W; ++j)
+                    for (int i = 0; i < V; ++i) {
+                        float acc = fmaf(wt[W - 1][i], xr.f(i), bs[i]);
 #pragma unroll
-                            for (int i = 0; i < V; ++i) q[j][i] = q[j + 1][i];
-                        if (sr < run.s1) {
+                        for (int w = 0; w < W - 1; ++w) acc = fmaf(wt[w][i], win[w].f(i), acc);
+                        const float g = gr.f(i) * dact_of<T>(acc, p.act);
+                        q[W - 1][i] = g;
+                        if (MAIN || s < run.end) {
+                            db[i] += g;
 #pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                float acc = fmaf(wt[W - 1][i], xr[u].f(i), bs[i]);
-#pragma unroll
-                                for (int w = 0; w < W - 1; ++w) acc = fmaf(wt[w][i], win[w].f(i), acc);
-                                const float g = gr[u].f(i) * dact_of<T>(acc, p.act);
-                                q[W - 1][i] = g;
-                                if (sr < run.end) {
-                                    db[i] += g;
-#pragma unroll
-                                    for (int w = 0; w < W - 1; ++w) dw[w][i] = fmaf(g, win[w].f(i), dw[w][i]);
-                                    dw[W - 1][i] = fmaf(g, xr[u].f(i), dw[W - 1][i]);
-                                }
-                            }
-#pragma unroll
-                            for (int w = 0; w + 1 < W - 1; ++w) win[w] = win[w + 1];
-                            win[W - 2] = xr[u];
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < V; ++i) q[W - 1][i] = 0.f;
-                        }
-                        // q[j] is now row sr - W + 1 + j: the gradient of row t = sr - W + 1
-                        const int t = sr - (W - 1);
-                        const bool in_run = t >= run.a && t < run.end;
-                        const bool in_state = t < run.s0 && opens && p.d_s0;
-                        if (in_run || in_state) {
-                            const int fin = t - (run.s1 - (W - 1));      // row of the final state
-                            Vec<T, V> f, o;
-                            if (dsT && fin >= 0)
-                                f.load(dsT + (size_t)fin * p.D + c);
-                            else
-                                f.zero();
-#pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                float g = f.f(i);
-#pragma unroll
-                                for (int j = 0; j < W; ++j) g = fmaf(wt[W - 1 - j][i], q[j][i], g);
-                                o.set(i, g);
-                            }
-                            if (in_run)
-                                o.store(dx + (size_t)t * p.D + c);
-                            else
-                                o.store(reinterpret_cast<T*>(p.d_s0) +
-                                        ((size_t)run.seq * (W - 1) + (t - run.s0 + W - 1)) * p.D + c);
+                            for (int w = 0; w < W - 1; ++w) dw[w][i] = fmaf(g, win[w].f(i), dw[w][i]);
+                            dw[W - 1][i] = fmaf(g, xr.f(i), dw[W - 1][i]);
                         }
                     }
+#pragma unroll
+                    for (int w = 0; w + 1 < W - 1; ++w) win[w] = win[w + 1];
+                    win[W - 2] = xr;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) q[W - 1][i] = 0.f;
                 }
+                const int t = s - (W - 1);
+                const bool in_run = MAIN || (t >= run.a && t < run.end);
+                if (!in_run && !(t < run.s0 && opens && p.d_s0)) return;
+                Vec<T, V> f, o;
+                if constexpr (!MAIN) {
+                    const int fin = t - (run.s1 - (W - 1));      // row of the final state
+                    if (dsT && fin >= 0)
+                        f.load(dsT + (size_t)fin * p.D + c);
+                    else
+                        f.zero();
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float g = MAIN ? 0.f : f.f(i);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) g = fmaf(wt[W - 1 - j][i], q[j][i], g);
+                    o.set(i, g);
+                }
+                if (in_run)
+                    o.store(dx + (size_t)t * p.D + c);
+                else
+                    o.store(reinterpret_cast<T*>(p.d_s0) + ((size_t)run.seq * (W - 1) + (t - run.s0 + W - 1)) * p.D + c);
+            };
+            auto edge = [&](int s) {
+                Vec<T, V> xr, gr;
+                if (s < run.s1) {
+                    xr.load(x + (size_t)s * p.x_stride + c);
+                    gr.load(dy + (size_t)s * p.D + c);
+                }
+                step(std::false_type{}, s, xr, gr);
+            };
+            auto fetch = [&](int at, Vec<T, V>(&xs)[kRowsAhead], Vec<T, V>(&gs)[kRowsAhead]) {
+#pragma unroll
+                for (int u = 0; u < kRowsAhead; ++u) {
+                    xs[u].load(x + (size_t)(at + u) * p.x_stride + c);
+                    gs[u].load(dy + (size_t)(at + u) * p.D + c);
+                }
+            };
+            int s = run.a;
+            for (; s < run.a + W - 1; ++s) edge(s);
+            Vec<T, V> xn[kRowsAhead], gn[kRowsAhead], xs[kRowsAhead], gs[kRowsAhead];
+            if (s + kRowsAhead <= run.end) fetch(s, xn, gn);
+            while (s + kRowsAhead <= run.end) {
+#pragma unroll
+                for (int u = 0; u < kRowsAhead; ++u) {
+                    xs[u] = xn[u];
+                    gs[u] = gn[u];
+                }
+                if (s + 2 * kRowsAhead <= run.end) fetch(s + kRowsAhead, xn, gn);
+#pragma unroll
+                for (int u = 0; u < kRowsAhead; ++u) step(std::true_type{}, s + u, xs[u], gs[u]);
+                s += kRowsAhead;
             }
+            for (; s < run.end + W - 1; ++s) edge(s);
             more = false;
             if (packed) {
                 ++run.seq;
@@ -426,17 +458,17 @@ unsigned channel_blocks(const ConvParams& p, int V) {
 }  // namespace
 
 hipError_t launch_conv_fwd(int dtype, bool vec, const ConvParams& p, int tile_blocks, hipStream_t st) {
-    const int V = vec ? (dtype == 1 ? 8 : 4) : 1;
+    const int V = vec ? (dtype == 1 ? 4 : 4) : 1;
     const dim3 grid((unsigned)tile_blocks, channel_blocks(p, V));
-    if (dtype == 1) return vec ? conv_fwd_v<bf16, 8>(p, grid, st) : conv_fwd_v<bf16, 1>(p, grid, st);
+    if (dtype == 1) return vec ? conv_fwd_v<bf16, 4>(p, grid, st) : conv_fwd_v<bf16, 1>(p, grid, st);
     return vec ? conv_fwd_v<float, 4>(p, grid, st) : conv_fwd_v<float, 1>(p, grid, st);
 }
 
 hipError_t launch_conv_bwd(int dtype, bool vec, const ConvParams& p, int tile_blocks, hipStream_t st) {
-    const int V = vec ? (dtype == 1 ? 8 : 4) : 1;
+    const int V = vec ? (dtype == 1 ? 4 : 2) : 1;
     const dim3 grid((unsigned)tile_blocks, channel_blocks(p, V));
-    if (dtype == 1) return vec ? conv_bwd_v<bf16, 8>(p, grid, st) : conv_bwd_v<bf16, 1>(p, grid, st);
-    return vec ? conv_bwd_v<float, 4>(p, grid, st) : conv_bwd_v<float, 1>(p, grid, st);
+    if (dtype == 1) return vec ? conv_bwd_v<bf16, 4>(p, grid, st) : conv_bwd_v<bf16, 1>(p, grid, st);
+    return vec ? conv_bwd_v<float, 2>(p, grid, st) : conv_bwd_v<float, 1>(p, grid, st);
 }
 
 hipError_t launch_conv_step(int dtype, bool vec, int N, int D, int W, int act, const void* x, size_t xs,

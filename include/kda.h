@@ -548,8 +548,8 @@ kda_status kda_selective_scan_step(int N, int H, int G, int K, int P, kda_dtype 
  *   x, gate : [rows, C] dt, row strides x_stride, gate_stride; gate or NULL
  *   weight, bias : [C] fp32 or NULL (1, 0);  y : [rows, C] dt
  * fp32 inside, rounded once.  y may be x or the gate exactly.  C / groups at
- * most 4096 channels, or 16384 where rows and pointers allow 16-byte accesses
- * (C / groups and strides multiples of 16 bytes); wider groups are
+ * most 4096 channels, or 16384 where 16-byte accesses work (C / groups and
+ * strides multiples of 16 bytes, pointers 16-byte aligned); wider groups are
  * KDA_ERR_UNSUPPORTED.
  */
 kda_status kda_group_norm_fwd(int rows, int C, int groups, kda_dtype dt, kda_activation act, int center,
