@@ -458,9 +458,9 @@ unsigned channel_blocks(const ConvParams& p, int V) {
 }  // namespace
 
 hipError_t launch_conv_fwd(int dtype, bool vec, const ConvParams& p, int tile_blocks, hipStream_t st) {
-    const int V = vec ? (dtype == 1 ? 4 : 4) : 1;
+    const int V = vec ? (dtype == 1 ? 8 : 4) : 1;
     const dim3 grid((unsigned)tile_blocks, channel_blocks(p, V));
-    if (dtype == 1) return vec ? conv_fwd_v<bf16, 4>(p, grid, st) : conv_fwd_v<bf16, 1>(p, grid, st);
+    if (dtype == 1) return vec ? conv_fwd_v<bf16, 8>(p, grid, st) : conv_fwd_v<bf16, 1>(p, grid, st);
     return vec ? conv_fwd_v<float, 4>(p, grid, st) : conv_fwd_v<float, 1>(p, grid, st);
 }
 

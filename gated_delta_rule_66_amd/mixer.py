@@ -42,10 +42,10 @@ def _act(name) -> int:
 
 def _call(name: str, dev: torch.device, *args):
     """The C call on dev and its current stream."""
-    lib = _k.load_library()
-    fn = getattr(lib, name)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index is not None and dev.index != torch.cuda.current_device():
+    fn = getattr(_k.load_library(), name)
+    # the raw handle: a Stream object would cost as much as a small launch
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             st = fn(*args, stream)
     else:
@@ -75,14 +75,15 @@ def _workspace(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
 
 
 def _check(t: torch.Tensor, name: str, shape, dtype, dev):
+    if t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous():
+        return
     if t.device != dev:
         raise ValueError("%s must be on %s" % (name, dev))
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype != dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _rows(t: torch.Tensor, name: str, shape, lead: int, dtype, dev) -> int:
