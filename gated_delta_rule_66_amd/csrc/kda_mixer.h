@@ -102,7 +102,7 @@ struct SsmParams {
     // sequence starts in the segment, nothing of the start state is left)
     float* seg_state;
     float* seg_decay;
-    float* states;              // [chunks][H][K][P]: the state before each chunk, or null
+
 };
 constexpr int kSsmChunk = 64;
 // chunk_off[i] = chunks of the sequences before i

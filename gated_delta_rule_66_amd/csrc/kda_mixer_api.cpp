@@ -427,7 +427,8 @@ size_t kda_selective_scan_fwd_workspace_size(int N, int packed, int T, int H, in
     return ssm_layout(packed != 0, N, H, K, P, ssm_plan(packed != 0, N, M, T, H, G, P)).total;
 }
 
-// pointer checks shared by the scan's calls
+// pointer checks shared by the scan's calls; offsets inside a chunk's 64 rows
+// are 32 bits in the kernels
 static kda_status ssm_pointers(long long M, int H, int G, int K, int P, kda_dtype dt, const void* x, long long xs,
                                const void* dtp, long long ds, const float* A, const void* B, long long bs, const void* Cm,
                                long long cs, const float* D, const float* dt_bias, const float* s0) {
@@ -439,6 +440,8 @@ static kda_status ssm_pointers(long long M, int H, int G, int K, int P, kda_dtyp
     const long long e = 16 / (long long)es;
     if (ds < H || xs < (long long)H * P || bs < (long long)G * K || cs < (long long)G * K || xs % e || bs % e || cs % e)
         return KDA_ERR_INVALID_ARG;
+    const long long most = 1LL << 23;
+    if (xs > most || bs > most || cs > most || (long long)H * P > most) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

@@ -26,53 +26,60 @@ constexpr int C = kSsmChunk;
 // chunk's loads in flight meanwhile); the scores C B^T are computed once for
 // the workgroup's heads, scaled and masked per head, and passed through LDS.
 //   OUT:  y, and the final state where a sequence ends
-//   else: states only: each segment's local state and decay (p.seg_state) or
-//         the state before each chunk (p.states)
-template <typename T, int K, int NT, bool OUT>
-__global__ __launch_bounds__(256) void kda_ssm_chunk_kernel(SsmParams p) {
+//   else: each segment's local state and decay
+template <typename T, int K, int P, int NT, bool OUT>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_kernel(SsmParams p) {
     constexpr int COLS = 64 * NT;
+    constexpr int NH = COLS / P;                // heads of the workgroup
     constexpr int PAD = 16 / sizeof(T);
     constexpr int LDK = K + PAD, LDX = COLS + PAD, LDG = C + PAD;
     constexpr int NTK = K / 16;                 // state row tiles
     constexpr int EPP = 16 / sizeof(T);         // elements of a 16-byte piece
     constexpr int PK = C * K / EPP / 256, PX = C * COLS / EPP / 256;
+    constexpr int KP = K * P;
     __shared__ T sB[C * LDK];
     __shared__ T sX[C * LDX];
     __shared__ T sC[OUT ? C * LDK : 1];
-    __shared__ T sG[OUT ? NT * C * LDG : 1];
-    // per head: c (as hi + lo), delta, e^{c}, the state's token weights
-    __shared__ __align__(16) float s_c[NT][C], s_cl[NT][C], s_delta[NT][C], s_ec[NT][C], s_w[NT][C];
-    __shared__ float s_decay[NT];
+    __shared__ T sG[OUT ? NH * C * LDG : 1];
+    // per head, for this chunk and the next: c (as hi + lo), delta, e^{c}, the
+    // state's token weights
+    __shared__ __align__(16) float s_c[2][NH][C], s_cl[2][NH][C], s_delta[2][NH][C], s_ec[2][NH][C], s_w[2][NH][C];
+    __shared__ float s_decay[2][NH];
     typedef typename FragOf<T>::type Frag;
 
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, r16 = lane & 15;
-    const int nh = COLS / p.P;                  // heads of the workgroup
-    const int units = p.H / nh;
+    const int units = p.H / NH;
     const int flat = xcd_swizzle(blockIdx.x, gridDim.x);
-    const int seg = p.seg0 + flat / units, h0 = (flat % units) * nh;
+    const int seg = p.seg0 + flat / units, h0 = (flat % units) * NH;
     const int col0 = w * 16 * NT;
-    const int hl = col0 / p.P, pc = col0 - hl * p.P, h = h0 + hl;
+    const int hl = col0 / P, pc = col0 % P, h = h0 + hl;
     const int grp = h0 / (p.H / p.G);
     const int all = total_chunks(p);
     const int begin = min(seg * p.cps, all), end = min(begin + p.cps, all);
     const bool rev = !OUT && p.reverse;
-    const bool summary = !OUT && p.seg_state && !p.states;
-    float* seg_slot = p.seg_state ? p.seg_state + ((size_t)seg * p.H + h) * K * p.P : nullptr;
+    const bool summary = !OUT;
+    const int own = (4 * g) * P + pc + r16;     // the lane's first state element
+    float* seg_slot = p.seg_state ? p.seg_state + ((size_t)seg * p.H + h) * KP : nullptr;
 
     f32x4 S[NTK][NT];
 #pragma unroll
     for (int m = 0; m < NTK; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) S[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const size_t kp = (size_t)K * p.P;
-    auto load_state = [&](const float* src) {   // src: [K][P] of head h
+    auto load_state = [&](const float* src) {   // src: [K][P] of head h, or null
+        if (src) {
 #pragma unroll
-        for (int m = 0; m < NTK; ++m)
+            for (int m = 0; m < NTK; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    S[m][n][e] = src ? src[(size_t)(16 * m + 4 * g + e) * p.P + pc + 16 * n + r16] : 0.f;
+                    for (int e = 0; e < 4; ++e) S[m][n][e] = src[own + (16 * m + e) * P + 16 * n];
+        } else {
+#pragma unroll
+            for (int m = 0; m < NTK; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) S[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
     };
     auto store_state = [&](float* dst) {
 #pragma unroll
@@ -80,56 +87,92 @@ __global__ __launch_bounds__(256) void kda_ssm_chunk_kernel(SsmParams p) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    dst[(size_t)(16 * m + 4 * g + e) * p.P + pc + 16 * n + r16] = S[m][n][e];
+                for (int e = 0; e < 4; ++e) dst[own + (16 * m + e) * P + 16 * n] = S[m][n][e];
     };
+    if (begin >= end) {
+        if (summary) store_state(seg_slot);
+        if (summary && pc == 0 && lane == 0) p.seg_decay[(size_t)seg * p.H + h] = 1.f;
+        return;
+    }
+    ChunkWalk walk;
+    if (summary && !p.reverse) {
+        // nobody reads this segment's end if the next one opens a sequence
+        walk.init(p, end - 1);
+        if (walk.last()) {
+            if (pc == 0 && lane == 0) p.seg_decay[(size_t)seg * p.H + h] = -1.f;
+            return;
+        }
+    }
     // the start state: none for a summary, else what the segments before left
-    if (!summary && seg_slot && begin < end) load_state(seg_slot);
+    if (!summary && seg_slot) load_state(seg_slot);
 
     if constexpr (OUT) {
         // the score tiles above the diagonal that products read with their
         // neighbours: zero once, never written again
-        for (int k = tid; k < NT * C * LDG; k += 256) sG[k] = (T)0.f;
+        for (int k = tid; k < NH * C * LDG; k += 256) sG[k] = (T)0.f;
     }
 
-    ChunkWalk walk;
-    if (begin < end) walk.init(p, rev ? end - 1 : begin);
+    walk.init(p, rev ? end - 1 : begin);
+    // pieces of a chunk: the thread's rows and columns never change, so each
+    // load is a chunk's resource and a fixed offset
+    unsigned ob[PK], oc[OUT ? PK : 1], ox[PX];
+#pragma unroll
+    for (int i = 0; i < PK; ++i) {
+        const int q = tid + 256 * i, row = q / (K / EPP), col = (q % (K / EPP)) * EPP;
+        ob[i] = (unsigned)((row * p.b_stride + col) * sizeof(T));
+        if constexpr (OUT) oc[i] = (unsigned)((row * p.c_stride + col) * sizeof(T));
+    }
+#pragma unroll
+    for (int i = 0; i < PX; ++i) {
+        const int q = tid + 256 * i, row = q / (COLS / EPP), col = (q % (COLS / EPP)) * EPP;
+        ox[i] = (unsigned)((row * p.x_stride + col) * sizeof(T));
+    }
+    const T* xbase = reinterpret_cast<const T*>(p.x) + h0 * P;
+    const T* bbase = reinterpret_cast<const T*>(p.B) + grp * K;
+    const T* cbase = reinterpret_cast<const T*>(p.C) + grp * K;
+    // the waves with fewer score tiles (3, then 2) prepare the heads' decays
+    const int ph = 3 - w;
+    const bool preps = ph < NH;
+    const int hp = h0 + (preps ? ph : 0);
+    const float bias = p.dt_bias ? p.dt_bias[hp] : 0.f;
+    const double rate = (double)p.A[hp] * 1.4426950408889634;
     uint4 rb[PK], rx[PX], rc[OUT ? PK : 1];
     float rdt = 0.f;
+    int rlen = 0;
     auto fetch = [&](const ChunkWalk& at) {
         const int t0 = at.t0(), len = at.len();
-        const T* xp = reinterpret_cast<const T*>(p.x) + (size_t)t0 * p.x_stride + h0 * p.P;
-        const T* bp = reinterpret_cast<const T*>(p.B) + (size_t)t0 * p.b_stride + grp * K;
-        const T* cp = OUT ? reinterpret_cast<const T*>(p.C) + (size_t)t0 * p.c_stride + grp * K : nullptr;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const auto xr = row_rsrc<T>(xbase, p.x_stride, t0, len, COLS);
+        const auto br = row_rsrc<T>(bbase, p.b_stride, t0, len, K);
 #pragma unroll
-        for (int i = 0; i < PK; ++i) {
-            const int q = tid + 256 * i, row = q / (K / EPP), col = (q % (K / EPP)) * EPP;
-            rb[i] = row < len ? *reinterpret_cast<const uint4*>(bp + (size_t)row * p.b_stride + col) : zero;
-            if constexpr (OUT)
-                rc[i] = row < len ? *reinterpret_cast<const uint4*>(cp + (size_t)row * p.c_stride + col) : zero;
+        for (int i = 0; i < PK; ++i) rb[i] = buf_load16(br, ob[i]);
+        if constexpr (OUT) {
+            const auto cr = row_rsrc<T>(cbase, p.c_stride, t0, len, K);
+#pragma unroll
+            for (int i = 0; i < PK; ++i) rc[i] = buf_load16(cr, oc[i]);
         }
 #pragma unroll
-        for (int i = 0; i < PX; ++i) {
-            const int q = tid + 256 * i, row = q / (COLS / EPP), col = (q % (COLS / EPP)) * EPP;
-            rx[i] = row < len ? *reinterpret_cast<const uint4*>(xp + (size_t)row * p.x_stride + col) : zero;
-        }
-        if (w < nh && lane < len)
-            rdt = to_f32(reinterpret_cast<const T*>(p.dt)[(size_t)(t0 + lane) * p.dt_stride + h0 + w]);
+        for (int i = 0; i < PX; ++i) rx[i] = buf_load16(xr, ox[i]);
+        rlen = len;
+        if (preps && lane < len)
+            rdt = to_f32(reinterpret_cast<const T*>(p.dt)[(size_t)(t0 + lane) * p.dt_stride + hp]);
     };
-    if (begin < end) fetch(walk);
-    float seg_dec = 1.f;
-
-    for (int it = begin; it < end; ++it) {
-        const ChunkWalk at = walk;
-        const int t0 = at.t0(), len = at.len();
-        const bool opens = rev ? at.last() : at.first();
-        const bool closes = rev ? at.first() : at.last();
-        if (opens) {
-            load_state(p.s0 ? p.s0 + ((size_t)at.seq * p.H + h) * kp : nullptr);
-            seg_dec = -1.f;
-        }
-        // ---- stage the chunk, and the per-token values of each head
+    // decays and step sizes of the chunk last fetched, into buffer b
+    auto prepare = [&](int b) {
+        if (!preps) return;
+        const float delta = lane < rlen ? delta_of(rdt + bias, p.softplus) : 0.f;
+        const double c = wave_prefix((double)delta * rate);
+        const double ct = last_lane(c);
+        const float ch = (float)c;
+        s_c[b][ph][lane] = ch;
+        s_cl[b][ph][lane] = (float)(c - (double)ch);
+        s_delta[b][ph][lane] = delta;
+        const float ec = exp2_of(c);
+        s_ec[b][ph][lane] = ec;
+        // the recurrence's token weights; the adjoint's are e^{c}
+        s_w[b][ph][lane] = rev ? (lane < rlen ? ec : 0.f) : exp2_of(ct - c) * delta;
+        if (lane == 63) s_decay[b][ph] = ec;
+    };
+    auto stage = [&]() {
 #pragma unroll
         for (int i = 0; i < PK; ++i) {
             const int q = tid + 256 * i, row = q / (K / EPP), col = (q % (K / EPP)) * EPP;
@@ -141,22 +184,21 @@ __global__ __launch_bounds__(256) void kda_ssm_chunk_kernel(SsmParams p) {
             const int q = tid + 256 * i, row = q / (COLS / EPP), col = (q % (COLS / EPP)) * EPP;
             *reinterpret_cast<uint4*>(sX + row * LDX + col) = rx[i];
         }
-        if (w < nh) {
-            const int hh = h0 + w;
-            float delta = 0.f;
-            if (lane < len) delta = delta_of(rdt + (p.dt_bias ? p.dt_bias[hh] : 0.f), p.softplus);
-            const double c = wave_prefix((double)delta * (double)p.A[hh] * 1.4426950408889634, lane);
-            const double ct = __shfl(c, 63);
-            const float ch = (float)c;
-            s_c[w][lane] = ch;
-            s_cl[w][lane] = (float)(c - (double)ch);
-            s_delta[w][lane] = delta;
-            const float ec = exp2_of(c);
-            s_ec[w][lane] = ec;
-            // the recurrence's token weights; the adjoint's are e^{c}
-            s_w[w][lane] = rev ? (lane < len ? ec : 0.f) : exp2_of(ct - c) * delta;
-            if (lane == 0) s_decay[w] = exp2_of(ct);
+    };
+    fetch(walk);
+    prepare(begin & 1);
+    float seg_dec = 1.f;
+
+    for (int it = begin; it < end; ++it) {
+        const int b = it & 1;
+        const int t0 = walk.t0(), len = walk.len(), seq = walk.seq;
+        const bool opens = rev ? walk.last() : walk.first();
+        const bool closes = rev ? walk.first() : walk.last();
+        if (opens) {
+            load_state(p.s0 ? p.s0 + ((size_t)seq * p.H + h) * KP : nullptr);
+            seg_dec = -1.f;
         }
+        stage();
         __syncthreads();
         // the next chunk's loads run behind this chunk's products
         if (it + 1 < end) {
@@ -178,15 +220,16 @@ __global__ __launch_bounds__(256) void kda_ssm_chunk_kernel(SsmParams p) {
                     acc = mma(acc, ld_frag<T>(sB + (16 * tj + r16) * LDK + 32 * m + 8 * g),
                               ld_frag<T>(sC + (16 * ti + r16) * LDK + 32 * m + 8 * g));
                 const int i = 16 * ti + r16, j0 = 16 * tj + 4 * g;
-                for (int k = 0; k < nh; ++k) {
-                    const f32x4 cj = *reinterpret_cast<const f32x4*>(&s_c[k][j0]);
-                    const f32x4 dj = *reinterpret_cast<const f32x4*>(&s_delta[k][j0]);
-                    const float ci = s_c[k][i];
+#pragma unroll
+                for (int k = 0; k < NH; ++k) {
+                    const f32x4 cj = *reinterpret_cast<const f32x4*>(&s_c[b][k][j0]);
+                    const f32x4 dj = *reinterpret_cast<const f32x4*>(&s_delta[b][k][j0]);
+                    const float ci = s_c[b][k][i];
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float d = ci - cj[e];
-                        if constexpr (sizeof(T) == 4) d += s_cl[k][i] - s_cl[k][j0 + e];
+                        if constexpr (sizeof(T) == 4) d += s_cl[b][k][i] - s_cl[b][k][j0 + e];
                         v[e] = j0 + e <= i ? acc[e] * fast_exp2(d) * dj[e] : 0.f;
                     }
                     st_run<4>(sG + (k * C + i) * LDG + j0, v);
@@ -212,15 +255,14 @@ __global__ __launch_bounds__(256) void kda_ssm_chunk_kernel(SsmParams p) {
             }
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) {
-                const float e = s_ec[hl][16 * ti + r16];
+                const float e = s_ec[b][hl][16 * ti + r16];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) Y[ti][n] *= e;
             }
             __syncthreads();
         }
-        if (!OUT && p.states) store_state(p.states + ((size_t)(rev ? begin + end - 1 - it : it) * p.H + h) * kp);
         // ---- the chunk's own tokens: outputs and the state update
-        const float decay = s_decay[hl];
+        const float decay = s_decay[b][hl];
         seg_dec = seg_dec < 0.f ? seg_dec : seg_dec * decay;
 #pragma unroll
         for (int m = 0; m < NTK; ++m)
@@ -230,8 +272,8 @@ __global__ __launch_bounds__(256) void kda_ssm_chunk_kernel(SsmParams p) {
         for (int s = 0; s < 2; ++s) {
             Frag xf[NT];
             typename Exact<T>::type xw[NT];
-            f32x4 wa = *reinterpret_cast<const f32x4*>(&s_w[hl][32 * s + 4 * g]);
-            f32x4 wb = *reinterpret_cast<const f32x4*>(&s_w[hl][32 * s + 16 + 4 * g]);
+            const f32x4 wa = *reinterpret_cast<const f32x4*>(&s_w[b][hl][32 * s + 4 * g]);
+            const f32x4 wb = *reinterpret_cast<const f32x4*>(&s_w[b][hl][32 * s + 16 + 4 * g]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 xf[n] = ld_frag_tokens(sX, LDX, 32 * s, col0 + 16 * n, lane);
@@ -259,23 +301,22 @@ __global__ __launch_bounds__(256) void kda_ssm_chunk_kernel(SsmParams p) {
             }
         }
         if constexpr (OUT) {
+            const auto yr = row_rsrc<T>(reinterpret_cast<const T*>(p.y) + h * P + pc, (size_t)p.H * P, t0, len, 16 * NT);
             const float dskip = p.Dskip ? p.Dskip[h] : 0.f;
-            T* yp = reinterpret_cast<T*>(p.y) + ((size_t)t0 * p.H + h) * p.P + pc + 4 * g;
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) {
                 const int i = 16 * ti + r16;
-                if (i < len) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        f32x4 v = Y[ti][n];
-                        if (p.Dskip) v += ld4_as_f32<T>(sX + i * LDX + col0 + 16 * n + 4 * g) * dskip;
-                        float o[4] = {v[0], v[1], v[2], v[3]};
-                        st_run<4>(yp + (size_t)i * p.H * p.P + 16 * n, o);
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    f32x4 v = Y[ti][n];
+                    if (p.Dskip) v += ld4_as_f32<T>(sX + i * LDX + col0 + 16 * n + 4 * g) * dskip;
+                    float o[4] = {v[0], v[1], v[2], v[3]};
+                    buf_store4(yr, (unsigned)((i * p.H * P + 4 * g) * sizeof(T)), 16 * n * sizeof(T), o, (const T*)nullptr);
                 }
             }
         }
-        if (closes && p.sT && !summary) store_state(p.sT + ((size_t)at.seq * p.H + h) * kp);
+        if (it + 1 < end) prepare(b ^ 1);
+        if (closes && p.sT && !summary) store_state(p.sT + ((size_t)seq * p.H + h) * KP);
         __syncthreads();
     }
     if (summary) {
@@ -453,18 +494,17 @@ hipError_t step_launch(int N, int H, int G, int P, int softplus, const void* x, 
     return hipGetLastError();
 }
 
-template <typename T, int K>
-hipError_t chunks_launch(bool out, int nt, const SsmParams& p, int segs, hipStream_t st) {
-    const int nh = 64 * nt / p.P;
-    const dim3 grid((unsigned)((long long)segs * (p.H / nh)));
-    if (out) {
-        if (nt == 1) hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, 1, true>), grid, dim3(256), 0, st, p);
-        else hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, 2, true>), grid, dim3(256), 0, st, p);
-    } else {
-        if (nt == 1) hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, 1, false>), grid, dim3(256), 0, st, p);
-        else hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, 2, false>), grid, dim3(256), 0, st, p);
-    }
+template <typename T, int K, int P, int NT>
+hipError_t chunks_launch(bool out, const SsmParams& p, int segs, hipStream_t st) {
+    const dim3 grid((unsigned)((long long)segs * (p.H / (64 * NT / P))));
+    if (out) hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, NT, true>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, NT, false>), grid, dim3(256), 0, st, p);
     return hipGetLastError();
+}
+template <typename T, int K>
+hipError_t chunks_pick(bool out, int nt, const SsmParams& p, int segs, hipStream_t st) {
+    if (p.P == 128) return chunks_launch<T, K, 128, 2>(out, p, segs, st);
+    return nt == 2 ? chunks_launch<T, K, 64, 2>(out, p, segs, st) : chunks_launch<T, K, 64, 1>(out, p, segs, st);
 }
 
 }  // namespace
@@ -476,8 +516,8 @@ hipError_t launch_ssm_prep(const SeqView& sv, int* chunk_off, int max_chunks, hi
 
 hipError_t launch_ssm_chunks(int dtype, bool out, int nt, const SsmParams& p, int segs, hipStream_t st) {
     if (segs <= 0) return hipSuccess;
-    if (dtype == 1) return p.K == 128 ? chunks_launch<bf16, 128>(out, nt, p, segs, st) : chunks_launch<bf16, 64>(out, nt, p, segs, st);
-    return p.K == 128 ? chunks_launch<float, 128>(out, nt, p, segs, st) : chunks_launch<float, 64>(out, nt, p, segs, st);
+    if (dtype == 1) return p.K == 128 ? chunks_pick<bf16, 128>(out, nt, p, segs, st) : chunks_pick<bf16, 64>(out, nt, p, segs, st);
+    return p.K == 128 ? chunks_pick<float, 128>(out, nt, p, segs, st) : chunks_pick<float, 64>(out, nt, p, segs, st);
 }
 
 hipError_t launch_ssm_combine(const SsmParams& p, float* d_s0, hipStream_t st) {

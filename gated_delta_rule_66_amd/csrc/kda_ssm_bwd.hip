@@ -135,8 +135,8 @@ __global__ __launch_bounds__(256) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 delta = delta_of(raw, f.softplus);
                 sig = f.softplus ? 1.f / (1.f + expf(-raw)) : 1.f;
             }
-            const double c = wave_prefix((double)delta * (double)f.A[h] * 1.4426950408889634, lane);
-            const double ct = __shfl(c, 63);
+            const double c = wave_prefix((double)delta * (double)f.A[h] * 1.4426950408889634);
+            const double ct = last_lane(c);
             const float ch = (float)c;
             s_c[lane] = ch;
             s_cl[lane] = (float)(c - (double)ch);
@@ -305,10 +305,10 @@ __global__ __launch_bounds__(256) void kda_ssm_bwd_kernel(SsmBwdParams p) {
             const float zz = s_z[0][lane] + s_z[1][lane] + s_z[2][lane] + s_z[3][lane];
             const float rr = (s_r[0][lane] + s_r[1][lane] + s_r[2][lane] + s_r[3][lane]) * s_ec[lane];
             const double after = (double)row - (double)cs + (double)rr;     // summed over i >= t
-            const double pre = wave_prefix(after, lane);
-            const double suffix = __shfl(pre, 63) - pre + after;
+            const double pre = wave_prefix(after);
+            const double suffix = last_lane(pre) - pre + after;
             const double wz = (double)s_w[lane] * (double)zz;
-            const double before = wave_prefix(wz, lane) - wz;               // summed over j < t
+            const double before = wave_prefix(wz) - wz;               // summed over j < t
             const double thru = (double)s_decay * ((double)s_se[0] + s_se[1] + s_se[2] + s_se[3]);
             const double dla = suffix + before + thru;
             const float dd_raw =

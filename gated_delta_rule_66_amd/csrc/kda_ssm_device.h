@@ -165,14 +165,50 @@ template <> struct Exact<float> {
 // one token's delta for one head
 __device__ __forceinline__ float delta_of(float raw, int softplus) { return softplus ? softplus_of(raw) : raw; }
 
-// inclusive sum over the 64 lanes of a wave, fp64
-__device__ __forceinline__ double wave_prefix(double v, int lane) {
+// inclusive sum over the 64 lanes of a wave, fp64: data-parallel moves within
+// rows of 16 lanes (row_shr), then the rows' last lanes broadcast on
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+    const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, ROWS, 0xf, true);
+    const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, ROWS, 0xf, true);
+    return v + __builtin_bit_cast(double, ((unsigned long long)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_prefix(double v) {
+    v = dpp_add<0x111, 0xf>(v);
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);     // row_bcast:15 into rows 1 and 3
+    return dpp_add<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+}
+// lane 63's value, as a scalar
+__device__ __forceinline__ double last_lane(double v) {
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)u, 63);
+    const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(u >> 32), 63);
+    return __builtin_bit_cast(double, ((unsigned long long)hi << 32) | lo);
+}
+
+// A resource over the rows t0 .. t0 + len - 1 of a token tensor (row stride in
+// elements): loads of rows behind them return zeros, stores there do nothing.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* base, size_t stride, int t0, int len, int width) {
+    const int t = __builtin_amdgcn_readfirstlane(t0), n = __builtin_amdgcn_readfirstlane(len);
+    const unsigned bytes = n > 0 ? (unsigned)(((size_t)(n - 1) * stride + width) * sizeof(T)) : 0u;
+    return make_rsrc_n(reinterpret_cast<const T*>(base) + (size_t)t * stride, bytes);
+}
+__device__ __forceinline__ void buf_store4(__amdgpu_buffer_rsrc_t r, unsigned voff, unsigned soff, const float* x, const bf16*) {
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    bf16x4 v;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
+    for (int i = 0; i < 4; ++i) v[i] = (bf16)x[i];
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), r, (int)voff, (int)soff, 0);
+}
+__device__ __forceinline__ void buf_store4(__amdgpu_buffer_rsrc_t r, unsigned voff, unsigned soff, const float* x, const float*) {
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    const f32x4 v = {x[0], x[1], x[2], x[3]};
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, (int)voff, (int)soff, 0);
 }
 
 }  // namespace kda
