@@ -97,6 +97,7 @@ struct SsmParams {
     int n_seg, cps;
     int seg0;                   // first segment of the launch
     int reverse;                // 1: the adjoint's recurrence, from the last chunk to the first
+    float* gates;               // [chunks][H][5][64] (kda_ssm_device.h)
     // what one segment does to its start state: local states [n_seg][H][K][P]
     // (after the combine: start states) and decays [n_seg][H] (negative: a
     // sequence starts in the segment, nothing of the start state is left)
@@ -107,8 +108,11 @@ struct SsmParams {
 constexpr int kSsmChunk = 64;
 // chunk_off[i] = chunks of the sequences before i
 hipError_t launch_ssm_prep(const SeqView& sv, int* chunk_off, int max_chunks, hipStream_t st);
+// step sizes and decays of every chunk and head
+size_t ssm_gate_bytes(int chunks, int H);
+hipError_t launch_ssm_gates(int dtype, const SsmParams& p, hipStream_t st);
 // out: the output pass; else states only (segment summaries or states per chunk)
-hipError_t launch_ssm_chunks(int dtype, bool out, int nt, const SsmParams& p, int segs, hipStream_t st);
+hipError_t launch_ssm_chunks(int dtype, bool out, int cols, const SsmParams& p, int segs, hipStream_t st);
 // d_s0 (reverse with one chunk a segment only; else null): the adjoint before
 // each sequence's first chunk
 hipError_t launch_ssm_combine(const SsmParams& p, float* d_s0, hipStream_t st);

@@ -380,19 +380,19 @@ static kda_status ssm_sizes(int N, const int* cu, int T, int H, int G, int K, in
     return KDA_OK;
 }
 
-// column tiles a wave: 128 columns a workgroup (one head of 128, or two heads
+// columns a workgroup: 128 (one head of 128, or two heads
 // of 64 of one group, which share B, C and the scores) where the heads pair up
-static int ssm_nt(int H, int G, int P) { return P == 128 || (H / G) % 2 == 0 ? 2 : 1; }
+static int ssm_cols(int H, int G, int P) { return P == 128 || (H / G) % 2 == 0 ? 128 : 64; }
 
 struct SsmPlan {
-    int nt, chunks, chunks_per_seq, n_seg, cps;
+    int cols, chunks, chunks_per_seq, n_seg, cps;
 };
 static SsmPlan ssm_plan(bool packed, int N, long long M, int T, int H, int G, int P) {
     SsmPlan pl;
-    pl.nt = ssm_nt(H, G, P);
+    pl.cols = ssm_cols(H, G, P);
     pl.chunks_per_seq = T > 0 ? (T + 63) / 64 : 1;
     pl.chunks = packed ? (int)(M / 64 + N) : N * pl.chunks_per_seq;
-    const long long units = H / (64 * pl.nt / P);
+    const long long units = H / (pl.cols / P);
     // segments until two workgroups a CU run, each keeping at least four chunks
     long long want = (512 + units - 1) / units, cap = pl.chunks / 4;
     if (want > cap) want = cap;
@@ -404,13 +404,14 @@ static SsmPlan ssm_plan(bool packed, int N, long long M, int T, int H, int G, in
 }
 
 struct SsmLayout {
-    size_t off, seg, dec, s0, total;
+    size_t off, gates, seg, dec, s0, total;
 };
 static SsmLayout ssm_layout(bool packed, int N, int H, int K, int P, const SsmPlan& pl) {
     SsmLayout L;
     size_t o = 0;
     const size_t kp = (size_t)K * P * sizeof(float);
     L.off = o; o += packed ? align256((size_t)(N + 1) * sizeof(int)) : 0;
+    L.gates = o; o += align256(ssm_gate_bytes(pl.chunks, H));
     L.seg = o; o += pl.n_seg > 1 ? align256((size_t)pl.n_seg * H * kp) : 0;
     L.dec = o; o += pl.n_seg > 1 ? align256((size_t)pl.n_seg * H * sizeof(float)) : 0;
     // a copy of the initial states where the final states overwrite them
@@ -438,7 +439,7 @@ static kda_status ssm_pointers(long long M, int H, int G, int K, int P, kda_dtyp
     if (!x || !dtp || !B || !Cm || !aligned(dtp, es)) return KDA_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(B, 16) || !aligned(Cm, 16)) return KDA_ERR_INVALID_ARG;
     const long long e = 16 / (long long)es;
-    if (ds < H || xs < (long long)H * P || bs < (long long)G * K || cs < (long long)G * K || xs % e || bs % e || cs % e)
+    if (ds < H || ds > (1LL << 23) || xs < (long long)H * P || bs < (long long)G * K || cs < (long long)G * K || xs % e || bs % e || cs % e)
         return KDA_ERR_INVALID_ARG;
     const long long most = 1LL << 23;
     if (xs > most || bs > most || cs > most || (long long)H * P > most) return KDA_ERR_UNSUPPORTED;
@@ -487,6 +488,8 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
         KDA_LAUNCH("scan_prep", launch_ssm_prep(p.sv, off, pl.chunks, stream));
         p.chunk_off = off;
     }
+    p.gates = reinterpret_cast<float*>(ws + L.gates);
+    KDA_LAUNCH("scan_gates", launch_ssm_gates((int)dt, p, stream));
     if (pl.n_seg > 1) {
         if (initial_state && initial_state == final_state) {
             // segments read initial states while others write final ones
@@ -496,12 +499,12 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
         }
         p.seg_state = reinterpret_cast<float*>(ws + L.seg);
         p.seg_decay = reinterpret_cast<float*>(ws + L.dec);
-        KDA_LAUNCH("scan_summary", launch_ssm_chunks((int)dt, false, pl.nt, p, pl.n_seg - 1, stream));
+        KDA_LAUNCH("scan_summary", launch_ssm_chunks((int)dt, false, pl.cols, p, pl.n_seg - 1, stream));
         KDA_LAUNCH("scan_combine", launch_ssm_combine(p, nullptr, stream));
     }
     p.y = y;
     p.sT = final_state;
-    KDA_LAUNCH("scan_output", launch_ssm_chunks((int)dt, true, pl.nt, p, pl.n_seg, stream));
+    KDA_LAUNCH("scan_output", launch_ssm_chunks((int)dt, true, pl.cols, p, pl.n_seg, stream));
     return KDA_OK;
 }
 
@@ -509,7 +512,7 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
 // heads); parts until two workgroups a CU run, since each part beyond the first
 // adds fp32 copies of dB and dC.
 struct SsmBwdLayout {
-    size_t off, start, dend, dec, sums, part_b, part_c, total;
+    size_t off, gates, start, dend, dec, sums, part_b, part_c, total;
     int parts, heads_per;
 };
 static SsmBwdLayout ssm_bwd_layout(bool packed, int N, long long M, int H, int G, int K, int P, const SsmPlan& pl) {
@@ -524,6 +527,7 @@ static SsmBwdLayout ssm_bwd_layout(bool packed, int N, long long M, int H, int G
     const size_t part = L.parts > 1 ? (size_t)L.parts * M * G * K * sizeof(float) : 0;
     size_t o = 0;
     L.off = o; o += packed ? align256((size_t)(N + 1) * sizeof(int)) : 0;
+    L.gates = o; o += align256(ssm_gate_bytes(pl.chunks, H));
     L.start = o; o += align256(states);
     L.dend = o; o += align256(states);
     L.dec = o; o += align256((size_t)pl.chunks * H * sizeof(float));
@@ -615,10 +619,12 @@ kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, in
         KDA_LAUNCH("scan_prep", launch_ssm_prep(p.sv, off, pl.chunks, stream));
         p.chunk_off = off;
     }
+    p.gates = reinterpret_cast<float*>(ws + L.gates);
+    KDA_LAUNCH("scan_gates", launch_ssm_gates((int)dt, p, stream));
     // the state before each chunk: every chunk's own share, then the passing on
     p.seg_state = reinterpret_cast<float*>(ws + L.start);
     p.seg_decay = reinterpret_cast<float*>(ws + L.dec);
-    KDA_LAUNCH("scan_bwd_states", launch_ssm_chunks((int)dt, false, pl.nt, p, pl.chunks, stream));
+    KDA_LAUNCH("scan_bwd_states", launch_ssm_chunks((int)dt, false, pl.cols, p, pl.chunks, stream));
     KDA_LAUNCH("scan_bwd_combine", launch_ssm_combine(p, nullptr, stream));
     // the adjoint behind each chunk: the same recurrence backwards, with C for
     // B and dy for x
@@ -628,7 +634,7 @@ kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, in
     q.B = C; q.b_stride = (size_t)c_stride;
     q.s0 = d_final_state;
     q.seg_state = reinterpret_cast<float*>(ws + L.dend);
-    KDA_LAUNCH("scan_bwd_adjoints", launch_ssm_chunks((int)dt, false, pl.nt, q, pl.chunks, stream));
+    KDA_LAUNCH("scan_bwd_adjoints", launch_ssm_chunks((int)dt, false, pl.cols, q, pl.chunks, stream));
     KDA_LAUNCH("scan_bwd_combine", launch_ssm_combine(q, d_initial_state, stream));
     SsmBwdParams b{};
     b.f = p;

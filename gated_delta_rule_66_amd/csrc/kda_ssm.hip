@@ -19,35 +19,63 @@ namespace {
 
 constexpr int C = kSsmChunk;
 
-// One workgroup (4 waves) per (segment, 64 NT columns of x: one or two heads)
-// walks the segment's chunks with the state in registers: wave w owns columns
+// One workgroup per (segment, COLS columns of x: one or two heads) walks the
+// segment's chunks with the state in registers: wave w owns columns
 // [16 NT w, 16 NT (w + 1)) of all K state rows, as accumulator tiles that serve
 // as operands as they are.  B, C and x of a chunk are staged in LDS (the next
 // chunk's loads in flight meanwhile); the scores C B^T are computed once for
 // the workgroup's heads, scaled and masked per head, and passed through LDS.
 //   OUT:  y, and the final state where a sequence ends
 //   else: each segment's local state and decay
-template <typename T, int K, int P, int NT, bool OUT>
+// The gates of every chunk and head (kda_ssm_device.h): a wave a head, a lane a
+// token, eight heads a block, whose step sizes share cache lines.
+template <typename T>
+__global__ __launch_bounds__(256) void kda_ssm_gates_kernel(SsmParams p) {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int hb = (p.H + 7) / 8;
+    const int chunk = blockIdx.x / hb, first = (blockIdx.x - chunk * hb) * 8;
+    if (chunk >= total_chunks(p)) return;
+    ChunkWalk at;
+    at.init(p, chunk);
+    const int t0 = at.t0(), len = at.len();
+    for (int h = first + w; h < min(first + 8, p.H); h += 4) {
+        float delta = 0.f;
+        if (lane < len)
+            delta = delta_of(to_f32(reinterpret_cast<const T*>(p.dt)[(size_t)(t0 + lane) * p.dt_stride + h]) +
+                                 (p.dt_bias ? p.dt_bias[h] : 0.f),
+                             p.softplus);
+        const double c = wave_prefix((double)delta * (double)p.A[h] * 1.4426950408889634);
+        const float ch = (float)c;
+        float* out = p.gates + ((size_t)chunk * p.H + h) * (kGates * C) + lane;
+        out[kGateC * C] = ch;
+        out[kGateDelta * C] = delta;
+        out[kGateNear * C] = exp2_of(row_last(c) - c) * delta;
+        out[kGateW * C] = exp2_of(last_lane(c) - c) * delta;
+        out[kGateRest * C] = (float)(c - (double)ch);
+    }
+}
+
+template <typename T, int K, int P, int COLS, bool OUT>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_kernel(SsmParams p) {
-    constexpr int COLS = 64 * NT;
+    constexpr int TH = 256, NW = TH / 64;
+    constexpr int NT = COLS / 16 / NW;          // column tiles a wave
     constexpr int NH = COLS / P;                // heads of the workgroup
     constexpr int PAD = 16 / sizeof(T);
-    constexpr int LDK = K + PAD, LDX = COLS + PAD, LDG = C + PAD;
+    constexpr int LDB = K + tr_pad<T>(K), LDX = COLS + tr_pad<T>(COLS), LDK = K + PAD, LDG = C + PAD;
     constexpr int NTK = K / 16;                 // state row tiles
     constexpr int EPP = 16 / sizeof(T);         // elements of a 16-byte piece
-    constexpr int PK = C * K / EPP / 256, PX = C * COLS / EPP / 256;
+    constexpr int PK = C * K / EPP / TH, PX = C * COLS / EPP / TH;
     constexpr int KP = K * P;
-    __shared__ T sB[C * LDK];
+    __shared__ T sB[C * LDB];
     __shared__ T sX[C * LDX];
     __shared__ T sC[OUT ? C * LDK : 1];
     __shared__ T sG[OUT ? NH * C * LDG : 1];
-    // per head, for this chunk and the next: c (as hi + lo), delta, e^{c}, the
-    // state's token weights
-    __shared__ __align__(16) float s_c[2][NH][C], s_cl[2][NH][C], s_delta[2][NH][C], s_ec[2][NH][C], s_w[2][NH][C];
-    __shared__ float s_decay[2][NH];
+    __shared__ __align__(16) float s_gate[NH][kGates][C];
     typedef typename FragOf<T>::type Frag;
 
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, r16 = lane & 15;
+    // the wave's index as a scalar: resources and addresses built on it stay scalar
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, r16 = lane & 15;
     const int units = p.H / NH;
     const int flat = xcd_swizzle(blockIdx.x, gridDim.x);
     const int seg = p.seg0 + flat / units, h0 = (flat % units) * NH;
@@ -57,7 +85,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
     const int all = total_chunks(p);
     const int begin = min(seg * p.cps, all), end = min(begin + p.cps, all);
     const bool rev = !OUT && p.reverse;
-    const bool summary = !OUT;
+    constexpr bool summary = !OUT;
     const int own = (4 * g) * P + pc + r16;     // the lane's first state element
     float* seg_slot = p.seg_state ? p.seg_state + ((size_t)seg * p.H + h) * KP : nullptr;
 
@@ -66,14 +94,25 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
     for (int m = 0; m < NTK; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) S[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // states go by one lane offset and scalar offsets: per-element addresses
+    // would be kept in registers across the chunk loop
     auto load_state = [&](const float* src) {   // src: [K][P] of head h, or null
         if (src) {
+            const auto r = make_rsrc_n(src, KP * sizeof(float));
 #pragma unroll
             for (int m = 0; m < NTK; ++m)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) S[m][n][e] = src[own + (16 * m + e) * P + 16 * n];
+                    for (int e = 0; e < 4; ++e)
+                        S[m][n][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                            r, own * 4, ((16 * m + e) * P + 16 * n) * 4, 0));
+            // waited for here: a wait where S is next used would also stand on
+            // the way without these loads, and hold up the chunk loads there
+#pragma unroll
+            for (int m = 0; m < NTK; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) asm volatile("" : "+v"(S[m][n]));
         } else {
 #pragma unroll
             for (int m = 0; m < NTK; ++m)
@@ -82,12 +121,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
         }
     };
     auto store_state = [&](float* dst) {
+        const auto r = make_rsrc_n(dst, KP * sizeof(float));
 #pragma unroll
         for (int m = 0; m < NTK; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dst[own + (16 * m + e) * P + 16 * n] = S[m][n][e];
+                for (int e = 0; e < 4; ++e)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[m][n][e]), r, own * 4,
+                                                          ((16 * m + e) * P + 16 * n) * 4, 0);
     };
     if (begin >= end) {
         if (summary) store_state(seg_slot);
@@ -109,88 +151,76 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
     if constexpr (OUT) {
         // the score tiles above the diagonal that products read with their
         // neighbours: zero once, never written again
-        for (int k = tid; k < NH * C * LDG; k += 256) sG[k] = (T)0.f;
+        for (int k = tid; k < NH * C * LDG; k += TH) sG[k] = (T)0.f;
     }
 
     walk.init(p, rev ? end - 1 : begin);
-    // pieces of a chunk: the thread's rows and columns never change, so each
-    // load is a chunk's resource and a fixed offset
-    unsigned ob[PK], oc[OUT ? PK : 1], ox[PX];
-#pragma unroll
-    for (int i = 0; i < PK; ++i) {
-        const int q = tid + 256 * i, row = q / (K / EPP), col = (q % (K / EPP)) * EPP;
-        ob[i] = (unsigned)((row * p.b_stride + col) * sizeof(T));
-        if constexpr (OUT) oc[i] = (unsigned)((row * p.c_stride + col) * sizeof(T));
-    }
-#pragma unroll
-    for (int i = 0; i < PX; ++i) {
-        const int q = tid + 256 * i, row = q / (COLS / EPP), col = (q % (COLS / EPP)) * EPP;
-        ox[i] = (unsigned)((row * p.x_stride + col) * sizeof(T));
-    }
     const T* xbase = reinterpret_cast<const T*>(p.x) + h0 * P;
     const T* bbase = reinterpret_cast<const T*>(p.B) + grp * K;
     const T* cbase = reinterpret_cast<const T*>(p.C) + grp * K;
-    // the waves with fewer score tiles (3, then 2) prepare the heads' decays
-    const int ph = 3 - w;
-    const bool preps = ph < NH;
-    const int hp = h0 + (preps ? ph : 0);
-    const float bias = p.dt_bias ? p.dt_bias[hp] : 0.f;
-    const double rate = (double)p.A[hp] * 1.4426950408889634;
+    float dskip[NH];
+#pragma unroll
+    for (int k = 0; k < NH; ++k) dskip[k] = OUT && p.Dskip ? p.Dskip[h0 + k] : 0.f;
     uint4 rb[PK], rx[PX], rc[OUT ? PK : 1];
-    float rdt = 0.f;
-    int rlen = 0;
-    auto fetch = [&](const ChunkWalk& at) {
+    uint4 rg;
+    constexpr int PG = NH * kGates * C / 4;     // 16-byte pieces of a chunk's gates
+    auto fetch = [&](const ChunkWalk& at, int chunk) {
         const int t0 = at.t0(), len = at.len();
         const auto xr = row_rsrc<T>(xbase, p.x_stride, t0, len, COLS);
         const auto br = row_rsrc<T>(bbase, p.b_stride, t0, len, K);
+        const int td = opaque(tid);
 #pragma unroll
-        for (int i = 0; i < PK; ++i) rb[i] = buf_load16(br, ob[i]);
+        for (int i = 0; i < PK; ++i) {
+            const int q = td + TH * i, row = q / (K / EPP), col = (q % (K / EPP)) * EPP;
+            rb[i] = buf_load16(br, (unsigned)(row * (int)p.b_stride + col) * sizeof(T));
+        }
         if constexpr (OUT) {
             const auto cr = row_rsrc<T>(cbase, p.c_stride, t0, len, K);
 #pragma unroll
-            for (int i = 0; i < PK; ++i) rc[i] = buf_load16(cr, oc[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < PX; ++i) rx[i] = buf_load16(xr, ox[i]);
-        rlen = len;
-        if (preps && lane < len)
-            rdt = to_f32(reinterpret_cast<const T*>(p.dt)[(size_t)(t0 + lane) * p.dt_stride + hp]);
-    };
-    // decays and step sizes of the chunk last fetched, into buffer b
-    auto prepare = [&](int b) {
-        if (!preps) return;
-        const float delta = lane < rlen ? delta_of(rdt + bias, p.softplus) : 0.f;
-        const double c = wave_prefix((double)delta * rate);
-        const double ct = last_lane(c);
-        const float ch = (float)c;
-        s_c[b][ph][lane] = ch;
-        s_cl[b][ph][lane] = (float)(c - (double)ch);
-        s_delta[b][ph][lane] = delta;
-        const float ec = exp2_of(c);
-        s_ec[b][ph][lane] = ec;
-        // the recurrence's token weights; the adjoint's are e^{c}
-        s_w[b][ph][lane] = rev ? (lane < rlen ? ec : 0.f) : exp2_of(ct - c) * delta;
-        if (lane == 63) s_decay[b][ph] = ec;
-    };
-    auto stage = [&]() {
-#pragma unroll
-        for (int i = 0; i < PK; ++i) {
-            const int q = tid + 256 * i, row = q / (K / EPP), col = (q % (K / EPP)) * EPP;
-            *reinterpret_cast<uint4*>(sB + row * LDK + col) = rb[i];
-            if constexpr (OUT) *reinterpret_cast<uint4*>(sC + row * LDK + col) = rc[i];
+            for (int i = 0; i < PK; ++i) {
+                const int q = td + TH * i, row = q / (K / EPP), col = (q % (K / EPP)) * EPP;
+                rc[i] = buf_load16(cr, (unsigned)(row * (int)p.c_stride + col) * sizeof(T));
+            }
         }
 #pragma unroll
         for (int i = 0; i < PX; ++i) {
-            const int q = tid + 256 * i, row = q / (COLS / EPP), col = (q % (COLS / EPP)) * EPP;
+            const int q = td + TH * i, row = q / (COLS / EPP), col = (q % (COLS / EPP)) * EPP;
+            rx[i] = buf_load16(xr, (unsigned)(row * (int)p.x_stride + col) * sizeof(T));
+        }
+        // the heads' gates lie together; threads behind them read zeros
+        const auto gr = make_rsrc_n(p.gates + ((size_t)chunk * p.H + h0) * (kGates * C), PG * 16);
+        rg = buf_load16(gr, 16u * (unsigned)td);
+    };
+    auto stage = [&]() {
+        const int td = opaque(tid);
+#pragma unroll
+        for (int i = 0; i < PK; ++i) {
+            const int q = td + TH * i, row = q / (K / EPP), col = (q % (K / EPP)) * EPP;
+            *reinterpret_cast<uint4*>(sB + row * LDB + col) = rb[i];
+            if constexpr (OUT) st_slots(sC + row * LDK, col, rc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            const int q = td + TH * i, row = q / (COLS / EPP), col = (q % (COLS / EPP)) * EPP;
             *reinterpret_cast<uint4*>(sX + row * LDX + col) = rx[i];
         }
+        if (td < PG) *reinterpret_cast<uint4*>(&s_gate[0][0][0] + 4 * td) = rg;
     };
-    fetch(walk);
-    prepare(begin & 1);
+    auto store_y = [&](int t0, int len) {
+        const int td = opaque(tid);
+        const auto yr = row_rsrc<T>(reinterpret_cast<const T*>(p.y) + h0 * P, (size_t)p.H * P, t0, len, COLS);
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            const int q = td + TH * i, row = q / (COLS / EPP), col = (q % (COLS / EPP)) * EPP;
+            buf_store16(yr, (unsigned)(row * p.H * P + col) * sizeof(T), 0,
+                        *reinterpret_cast<const uint4*>(sX + row * LDX + col));
+        }
+    };
+    fetch(walk, rev ? end - 1 : begin);
     float seg_dec = 1.f;
+    int y_t0 = 0, y_len = 0;
 
     for (int it = begin; it < end; ++it) {
-        const int b = it & 1;
         const int t0 = walk.t0(), len = walk.len(), seq = walk.seq;
         const bool opens = rev ? walk.last() : walk.first();
         const bool closes = rev ? walk.first() : walk.last();
@@ -198,6 +228,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
             load_state(p.s0 ? p.s0 + ((size_t)seq * p.H + h) * KP : nullptr);
             seg_dec = -1.f;
         }
+        // y of the chunk before leaves from the pieces that stage() writes next
+        if (OUT && it > begin) store_y(y_t0, y_len);
+        y_t0 = t0;
+        y_len = len;
         stage();
         __syncthreads();
         // the next chunk's loads run behind this chunk's products
@@ -206,41 +240,74 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
                 walk.prev();
             else
                 walk.next();
-            fetch(walk);
+            fetch(walk, rev ? begin + end - 2 - it : it + 1);
         }
         f32x4 Y[OUT ? 4 : 1][NT];
         if constexpr (OUT) {
-            // ---- scores, transposed: a lane gets four tokens j of one row i
-            for (int q = w; q < 10; q += 4) {
-                const int ti = q < 1 ? 0 : q < 3 ? 1 : q < 6 ? 2 : 3;
-                const int tj = q - ti * (ti + 1) / 2;
+            // LDS addresses are worked out again in each phase (opaque): kept in
+            // registers across the loop they spill
+            const int ln = opaque(lane), g = ln >> 4, r16 = ln & 15;
+            // ---- scores, transposed: a lane gets four tokens j of one row i.
+            // On the diagonal each pair takes its own decay (and i = j the skip
+            // weight D: it multiplies the same x_i); below it the decay is the
+            // product of j's to the end of its tile and i's from there on, both
+            // at most 1, so one exponential a lane does.
+            auto score = [&](int ti, int tj) {
                 f32x4 acc{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int m = 0; m < K / 32; ++m)
-                    acc = mma(acc, ld_frag<T>(sB + (16 * tj + r16) * LDK + 32 * m + 8 * g),
+                    acc = mma(acc, ld_frag_perm<T>(sB + (16 * tj + r16) * LDB + 32 * m + 4 * g),
                               ld_frag<T>(sC + (16 * ti + r16) * LDK + 32 * m + 8 * g));
-                const int i = 16 * ti + r16, j0 = 16 * tj + 4 * g;
+                return acc;
+            };
+            auto put = [&](int k, int ti, int tj, const float* v) {
+                st_run<4>(sG + (k * C + 16 * ti + r16) * LDG + slot_col(16 * tj + 4 * g), v);
+            };
+            auto below = [&](int ti, int tj, f32x4 acc) {
+                const int i = 16 * ti + r16, last = 16 * tj + 15;
 #pragma unroll
                 for (int k = 0; k < NH; ++k) {
-                    const f32x4 cj = *reinterpret_cast<const f32x4*>(&s_c[b][k][j0]);
-                    const f32x4 dj = *reinterpret_cast<const f32x4*>(&s_delta[b][k][j0]);
-                    const float ci = s_c[b][k][i];
+                    float d = s_gate[k][kGateC][i] - s_gate[k][kGateC][last];
+                    if constexpr (sizeof(T) == 4) d += s_gate[k][kGateRest][i] - s_gate[k][kGateRest][last];
+                    const float f = fast_exp2(d);
+                    const f32x4 dj = *reinterpret_cast<const f32x4*>(&s_gate[k][kGateNear][16 * tj + 4 * g]);
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = acc[e] * dj[e] * f;
+                    put(k, ti, tj, v);
+                }
+            };
+            auto diagonal = [&](int t, f32x4 acc) {
+                const int i = 16 * t + r16, j0 = 16 * t + 4 * g;
+#pragma unroll
+                for (int k = 0; k < NH; ++k) {
+                    const f32x4 cj = *reinterpret_cast<const f32x4*>(&s_gate[k][kGateC][j0]);
+                    const f32x4 dj = *reinterpret_cast<const f32x4*>(&s_gate[k][kGateDelta][j0]);
+                    const float ci = s_gate[k][kGateC][i];
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float d = ci - cj[e];
-                        if constexpr (sizeof(T) == 4) d += s_cl[b][k][i] - s_cl[b][k][j0 + e];
+                        if constexpr (sizeof(T) == 4) d += s_gate[k][kGateRest][i] - s_gate[k][kGateRest][j0 + e];
                         v[e] = j0 + e <= i ? acc[e] * fast_exp2(d) * dj[e] : 0.f;
+                        if (j0 + e == i) v[e] += dskip[k];
                     }
-                    st_run<4>(sG + (k * C + i) * LDG + j0, v);
+                    put(k, t, t, v);
                 }
-            }
+            };
+            // tile (w, w), one below it and, in two waves, another: the products
+            // of all first, so that they wait for each other's reads only once
+            const int ti1 = w == 0 ? 1 : w == 3 ? 3 : 2, tj1 = w == 2 ? 1 : 0;
+            const f32x4 a0 = score(w, w), a1 = score(ti1, tj1);
+            f32x4 a2{0.f, 0.f, 0.f, 0.f};
+            if (w < 2) a2 = score(3, 1 + w);
+            diagonal(w, a0);
+            below(ti1, tj1, a1);
+            if (w < 2) below(3, 1 + w, a2);
+            {
+            const int ln = opaque(lane), g = ln >> 4, r16 = ln & 15;
             // ---- what the start state gives, transposed: a lane holds four
             // columns of one token
-#pragma unroll
-            for (int ti = 0; ti < 4; ++ti)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) Y[ti][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int m = 0; m < K / 32; ++m) {
                 Frag sf[NT];
@@ -248,21 +315,24 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
                 for (int n = 0; n < NT; ++n) sf[n] = frag_from_tiles<T>(S[2 * m][n], S[2 * m + 1][n]);
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) {
-                    const Frag cf = ld_frag_perm<T>(sC + (16 * ti + r16) * LDK + 32 * m + 4 * g);
+                    const Frag cf = ld_frag<T>(sC + (16 * ti + r16) * LDK + 32 * m + 8 * g);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) Y[ti][n] = mma(Y[ti][n], sf[n], cf);
+                    for (int n = 0; n < NT; ++n)
+                        Y[ti][n] = mma(m == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : Y[ti][n], sf[n], cf);
                 }
             }
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) {
-                const float e = s_ec[b][hl][16 * ti + r16];
+                const float e = exp2_pair(s_gate[hl][kGateC][16 * ti + r16], s_gate[hl][kGateRest][16 * ti + r16]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) Y[ti][n] *= e;
+            }
             }
             __syncthreads();
         }
         // ---- the chunk's own tokens: outputs and the state update
-        const float decay = s_decay[b][hl];
+        const int ln = opaque(lane), g = ln >> 4, r16 = ln & 15;
+        const float decay = exp2_pair(s_gate[hl][kGateC][C - 1], s_gate[hl][kGateRest][C - 1]);
         seg_dec = seg_dec < 0.f ? seg_dec : seg_dec * decay;
 #pragma unroll
         for (int m = 0; m < NTK; ++m)
@@ -272,11 +342,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
         for (int s = 0; s < 2; ++s) {
             Frag xf[NT];
             typename Exact<T>::type xw[NT];
-            const f32x4 wa = *reinterpret_cast<const f32x4*>(&s_w[b][hl][32 * s + 4 * g]);
-            const f32x4 wb = *reinterpret_cast<const f32x4*>(&s_w[b][hl][32 * s + 16 + 4 * g]);
+            f32x4 wa = *reinterpret_cast<const f32x4*>(&s_gate[hl][kGateW][32 * s + 4 * g]);
+            f32x4 wb = *reinterpret_cast<const f32x4*>(&s_gate[hl][kGateW][32 * s + 16 + 4 * g]);
+            if (rev) {
+                // the adjoint's token weights: the decay from the chunk's start
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = 32 * s + 4 * g + e;
+                    wa[e] = exp2_pair(s_gate[hl][kGateC][j], s_gate[hl][kGateRest][j]);
+                    wb[e] = exp2_pair(s_gate[hl][kGateC][j + 16], s_gate[hl][kGateRest][j + 16]);
+                }
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                xf[n] = ld_frag_tokens(sX, LDX, 32 * s, col0 + 16 * n, lane);
+                xf[n] = ld_frag_tokens(sX, LDX, 32 * s, col0 + 16 * n, ln);
                 float v[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -288,37 +367,48 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
             if constexpr (OUT) {
 #pragma unroll
                 for (int ti = 2 * s; ti < 4; ++ti) {
-                    const Frag gf = ld_frag_perm<T>(sG + (hl * C + 16 * ti + r16) * LDG + 32 * s + 4 * g);
+                    const Frag gf = ld_frag<T>(sG + (hl * C + 16 * ti + r16) * LDG + 32 * s + 8 * g);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) Y[ti][n] = mma(Y[ti][n], xf[n], gf);
                 }
             }
 #pragma unroll
-            for (int m = 0; m < NTK; ++m) {
-                const Frag bf = ld_frag_tokens(sB, LDK, 32 * s, 16 * m, lane);
+            for (int m = 0; m < NTK; m += 2) {
+                // independent products between two of one tile
+                const Frag b0 = ld_frag_tokens(sB, LDB, 32 * s, 16 * m, ln);
+                const Frag b1 = ld_frag_tokens(sB, LDB, 32 * s, 16 * m + 16, ln);
+                if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) S[m][n] = mma_exact(S[m][n], bf, xw[n]);
-            }
-        }
-        if constexpr (OUT) {
-            const auto yr = row_rsrc<T>(reinterpret_cast<const T*>(p.y) + h * P + pc, (size_t)p.H * P, t0, len, 16 * NT);
-            const float dskip = p.Dskip ? p.Dskip[h] : 0.f;
+                    for (int part = 0; part < 3; ++part)
 #pragma unroll
-            for (int ti = 0; ti < 4; ++ti) {
-                const int i = 16 * ti + r16;
+                        for (int n = 0; n < NT; ++n) {
+                            const bf16x8 v = part == 0 ? xw[n].lo : part == 1 ? xw[n].mid : xw[n].hi;
+                            S[m][n] = mma(S[m][n], b0, v);
+                            S[m + 1][n] = mma(S[m + 1][n], b1, v);
+                        }
+                } else {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4 v = Y[ti][n];
-                    if (p.Dskip) v += ld4_as_f32<T>(sX + i * LDX + col0 + 16 * n + 4 * g) * dskip;
-                    float o[4] = {v[0], v[1], v[2], v[3]};
-                    buf_store4(yr, (unsigned)((i * p.H * P + 4 * g) * sizeof(T)), 16 * n * sizeof(T), o, (const T*)nullptr);
+                    for (int n = 0; n < NT; ++n) {
+                        S[m][n] = mma(S[m][n], b0, xw[n]);
+                        S[m + 1][n] = mma(S[m + 1][n], b1, xw[n]);
+                    }
                 }
             }
         }
-        if (it + 1 < end) prepare(b ^ 1);
+        if constexpr (OUT) {
+            // y takes the place of x, whose columns only this wave reads
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float o[4] = {Y[ti][n][0], Y[ti][n][1], Y[ti][n][2], Y[ti][n][3]};
+                    st_run<4>(sX + (16 * ti + r16) * LDX + col0 + 16 * n + 4 * g, o);
+                }
+        }
         if (closes && p.sT && !summary) store_state(p.sT + ((size_t)seq * p.H + h) * KP);
         __syncthreads();
     }
+    if constexpr (OUT) store_y(y_t0, y_len);
     if (summary) {
         store_state(seg_slot);
         if (pc == 0 && lane == 0) p.seg_decay[(size_t)seg * p.H + h] = seg_dec;
@@ -328,7 +418,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
 // Segment start states from the segments' local states and decays, written
 // over the local states: start_{j+1} = decay_j start_j + local_j (local_j
 // alone where a sequence starts in segment j).  A thread owns four state
-// values of a head and keeps eight segments' loads in flight.
+// values of a head and keeps sixteen segments' loads in flight.
 __global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmParams p, float* d_s0) {
     const size_t kp4 = (size_t)p.K * p.P / 4;
     const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
@@ -343,7 +433,7 @@ __global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmParams p, float
     ChunkWalk walk;
     if (d_s0 && n_seg > 0) walk.init(p, n_seg - 1);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int U = 8;
+    constexpr int U = 16;
     for (int j = 0; j < n_seg; j += U) {
         float4 l[U];
         float d[U];
@@ -494,17 +584,17 @@ hipError_t step_launch(int N, int H, int G, int P, int softplus, const void* x, 
     return hipGetLastError();
 }
 
-template <typename T, int K, int P, int NT>
+template <typename T, int K, int P, int COLS>
 hipError_t chunks_launch(bool out, const SsmParams& p, int segs, hipStream_t st) {
-    const dim3 grid((unsigned)((long long)segs * (p.H / (64 * NT / P))));
-    if (out) hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, NT, true>), grid, dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, NT, false>), grid, dim3(256), 0, st, p);
+    const dim3 grid((unsigned)((long long)segs * (p.H / (COLS / P)))), block(256);
+    if (out) hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, COLS, true>), grid, block, 0, st, p);
+    else hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, COLS, false>), grid, block, 0, st, p);
     return hipGetLastError();
 }
 template <typename T, int K>
-hipError_t chunks_pick(bool out, int nt, const SsmParams& p, int segs, hipStream_t st) {
-    if (p.P == 128) return chunks_launch<T, K, 128, 2>(out, p, segs, st);
-    return nt == 2 ? chunks_launch<T, K, 64, 2>(out, p, segs, st) : chunks_launch<T, K, 64, 1>(out, p, segs, st);
+hipError_t chunks_pick(bool out, int cols, const SsmParams& p, int segs, hipStream_t st) {
+    if (p.P == 128) return chunks_launch<T, K, 128, 128>(out, p, segs, st);
+    return cols == 128 ? chunks_launch<T, K, 64, 128>(out, p, segs, st) : chunks_launch<T, K, 64, 64>(out, p, segs, st);
 }
 
 }  // namespace
@@ -514,10 +604,19 @@ hipError_t launch_ssm_prep(const SeqView& sv, int* chunk_off, int max_chunks, hi
     return hipGetLastError();
 }
 
-hipError_t launch_ssm_chunks(int dtype, bool out, int nt, const SsmParams& p, int segs, hipStream_t st) {
+size_t ssm_gate_bytes(int chunks, int H) { return (size_t)chunks * H * kGates * C * sizeof(float); }
+
+hipError_t launch_ssm_gates(int dtype, const SsmParams& p, hipStream_t st) {
+    const dim3 grid((unsigned)((long long)p.chunks * ((p.H + 7) / 8)));
+    if (dtype == 1) hipLaunchKernelGGL(kda_ssm_gates_kernel<bf16>, grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL(kda_ssm_gates_kernel<float>, grid, dim3(256), 0, st, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_ssm_chunks(int dtype, bool out, int cols, const SsmParams& p, int segs, hipStream_t st) {
     if (segs <= 0) return hipSuccess;
-    if (dtype == 1) return p.K == 128 ? chunks_pick<bf16, 128>(out, nt, p, segs, st) : chunks_pick<bf16, 64>(out, nt, p, segs, st);
-    return p.K == 128 ? chunks_pick<float, 128>(out, nt, p, segs, st) : chunks_pick<float, 64>(out, nt, p, segs, st);
+    if (dtype == 1) return p.K == 128 ? chunks_pick<bf16, 128>(out, cols, p, segs, st) : chunks_pick<bf16, 64>(out, cols, p, segs, st);
+    return p.K == 128 ? chunks_pick<float, 128>(out, cols, p, segs, st) : chunks_pick<float, 64>(out, cols, p, segs, st);
 }
 
 hipError_t launch_ssm_combine(const SsmParams& p, float* d_s0, hipStream_t st) {

@@ -56,7 +56,8 @@ __global__ __launch_bounds__(256) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     __shared__ float s_decay;
 
     const SsmParams& f = p.f;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, r16 = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, r16 = lane & 15;
     const int flat = xcd_swizzle(blockIdx.x, gridDim.x);
     const int part = flat % p.parts, grp = (flat / p.parts) % f.G, ci = flat / (p.parts * f.G);
     const int hpg = f.H / f.G;

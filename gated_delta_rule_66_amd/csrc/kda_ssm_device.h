@@ -27,12 +27,14 @@ struct ChunkWalk {
     int seq, k, nk;     // sequence, chunk in it, its chunks
     int s0, len_seq;
 
+    // a wave's chunks are the wave's: what is read stays in scalar registers
+    static __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
     __device__ __forceinline__ void enter(int s) {
         seq = s;
         if (sv.cu) {
-            nk = off[s + 1] - off[s];
-            s0 = min(max(sv.cu[s], 0), sv.T);
-            len_seq = max(min(sv.cu[s + 1], sv.T) - s0, 0);
+            nk = scalar(off[s + 1] - off[s]);
+            s0 = scalar(min(max(sv.cu[s], 0), sv.T));
+            len_seq = scalar(max(min(sv.cu[s + 1], sv.T) - s0, 0));
         } else {
             nk = per_seq;
             s0 = s * sv.T;
@@ -47,13 +49,13 @@ struct ChunkWalk {
             int lo = 0, hi = sv.N;      // off[lo] <= c < off[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (off[mid] <= c)
+                if (scalar(off[mid]) <= c)
                     lo = mid;
                 else
                     hi = mid;
             }
             enter(lo);
-            k = c - off[lo];
+            k = c - scalar(off[lo]);
         } else {
             const int s = c / per_seq;
             enter(s);
@@ -79,7 +81,7 @@ struct ChunkWalk {
 };
 
 __device__ __forceinline__ int total_chunks(const SsmParams& p) {
-    return p.sv.cu ? min(p.chunk_off[p.sv.N], p.chunks) : p.chunks;
+    return p.sv.cu ? min(__builtin_amdgcn_readfirstlane(p.chunk_off[p.sv.N]), p.chunks) : p.chunks;
 }
 
 // Workgroups go to the 8 XCDs in turn.  The work index of a block such that
@@ -89,6 +91,11 @@ __device__ __forceinline__ int xcd_swizzle(int id, int total) {
     const int q = total >> 3, r = total & 7, x = id & 7;
     return x * q + min(x, r) + (id >> 3);
 }
+
+// Padding of an LDS tile's rows (elements of T) that transposing reads touch:
+// four rows of 32 bytes go out together, which rows of 256 bytes need 32 bytes
+// between them for; shorter and longer rows do with 16.
+template <typename T> constexpr int tr_pad(int width) { return width * (int)sizeof(T) == 256 ? 32 / (int)sizeof(T) : 16 / (int)sizeof(T); }
 
 // ---- fragments whose slots run over the tokens (rows) of an LDS tile ----------------
 // lane l: column n0 + l % 16, slots (g, i) -> token tok0 + 16 (i / 4) + 4 g + i % 4
@@ -116,6 +123,21 @@ __device__ __forceinline__ f32x8 ld_frag_tokens(const float* tile, int ld, int t
 #pragma unroll
     for (int i = 0; i < 4; ++i) { f[i] = p[i * ld]; f[4 + i] = p[(16 + i) * ld]; }
     return f;
+}
+
+// LDS tiles whose columns are a reduction axis, in slot order: in every 32
+// columns the groups of four go 0, 4, 1, 5, 2, 6, 3, 7, so that a lane's eight
+// permuted slots (4 g .. and 16 + 4 g ..) are one 16-byte read.
+__device__ __forceinline__ int slot_col(int col) {      // of a multiple of four
+    return (col & ~31) + ((col & 12) << 1) + ((col & 16) >> 2);
+}
+// a 16-byte piece of a row (columns col ..), stored in slot order
+__device__ __forceinline__ void st_slots(bf16* row, int col, uint4 v) {
+    *reinterpret_cast<uint2*>(row + slot_col(col)) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(row + slot_col(col + 4)) = make_uint2(v.z, v.w);
+}
+__device__ __forceinline__ void st_slots(float* row, int col, uint4 v) {
+    *reinterpret_cast<uint4*>(row + slot_col(col)) = v;
 }
 
 // ---- fp32 operands of bf16 products ---------------------------------------------------
@@ -162,6 +184,18 @@ template <> struct Exact<float> {
     static __device__ __forceinline__ f32x8 of(const float* v) { return frag_from<float>(v); }
 };
 
+// Step sizes and decays of one chunk and head, five arrays of 64 floats:
+//   c      log2 of the decay from the chunk's start to token j, rounded
+//   delta
+//   near   delta times the decay from j to the end of its 16 tokens
+//   w      delta times the decay from j to the chunk's end
+//   rest   c's rounding error
+enum Gate { kGateC = 0, kGateDelta = 1, kGateNear = 2, kGateW = 3, kGateRest = 4, kGates = 5 };
+// 2^{c + rest}
+__device__ __forceinline__ float exp2_pair(float c, float rest) {
+    return fast_exp2(c) * fmaf(rest, 0.6931471805599453f, 1.f);
+}
+
 // one token's delta for one head
 __device__ __forceinline__ float delta_of(float raw, int softplus) { return softplus ? softplus_of(raw) : raw; }
 
@@ -181,6 +215,13 @@ __device__ __forceinline__ double wave_prefix(double v) {
     v = dpp_add<0x118, 0xf>(v);
     v = dpp_add<0x142, 0xa>(v);     // row_bcast:15 into rows 1 and 3
     return dpp_add<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+}
+// the value of lane 15 of each row of 16 lanes
+__device__ __forceinline__ double row_last(double v) {
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+    const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)u, 0x15f, 0xf, 0xf, true);
+    const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), 0x15f, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, ((unsigned long long)hi << 32) | lo);
 }
 // lane 63's value, as a scalar
 __device__ __forceinline__ double last_lane(double v) {
