@@ -575,6 +575,7 @@ kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, in
         if (dx_stride < (long long)H * P || db_stride < (long long)G * K || dc_stride < (long long)G * K ||
             dx_stride % e || db_stride % e || dc_stride % e)
             return KDA_ERR_INVALID_ARG;
+        if (dx_stride > 1LL << 23) return KDA_ERR_UNSUPPORTED;
     }
     const long long le = (long long)es;
     const Span outs[] = {{dx, M, dx_stride * le, (long long)H * P * le},

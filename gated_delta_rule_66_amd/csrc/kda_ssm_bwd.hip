@@ -42,18 +42,30 @@ __device__ __forceinline__ float sum_groups(float v) {
     return v + __shfl_xor(v, 32);
 }
 
+// One workgroup (8 waves) per (chunk, group, part of the group's heads), head by
+// head.  The group's B, C and scores stay; a head's x, dy and states are loaded
+// into registers behind the head before and staged in LDS (states in fp32,
+// where they fit; else their fragments come from memory).  Work of the waves:
+//   pairs:   the ten lower 16 x 16 tiles, one or two a wave
+//   states:  E^T B and S^T C, a 16-column tile of one of them a wave (P = 64)
+//            or a tile of each (P = 128); products with exact state operands
+//   dB, dC:  16 state rows of both (K = 128) or of one of them (K = 64) a wave,
+//            summed over the heads in registers
 template <typename T, int K, int P>
-__global__ __launch_bounds__(256) void kda_ssm_bwd_kernel(SsmBwdParams p) {
-    constexpr int PAD = 16 / sizeof(T);
+__global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
+    constexpr int TH = 512;
     constexpr int EPP = 16 / sizeof(T);
-    constexpr int LDK = K + PAD, LDP = P + PAD, LDM = C + PAD;
-    constexpr int PT = P / 64;          // column tiles a wave
-    constexpr int NT = K / 64;          // state row tiles a wave
+    constexpr int LDK = K + tr_pad<T>(K), LDP = P + tr_pad<T>(P), LDM = C + 16 / sizeof(T);
+    constexpr bool STAGED = sizeof(T) == 2 && K * P <= 8192;
+    constexpr int LDS_ = P + 4;             // fp32 state rows
+    constexpr int TU = P / 64, TK = K / 64; // state and dB/dC tasks a wave
+    constexpr int PX = C * P / EPP / TH, PS = STAGED ? K * P / 4 / TH : 1;
+    static_assert(C * P / EPP % TH == 0 && (K * P / 4) % TH == 0, "whole pieces");
     typedef typename FragOf<T>::type Frag;
     __shared__ T sB[C * LDK], sC[C * LDK], sX[C * LDP], sDY[C * LDP], sM[C * LDM];
-    __shared__ __align__(16) float s_c[C], s_cl[C], s_delta[C], s_ec[C], s_w[C], s_out[C], s_sig[C];
-    __shared__ float s_row[10][16], s_colf[10][16], s_cols[10][16], s_z[4][C], s_r[4][C], s_se[4], s_dd[4];
-    __shared__ float s_decay;
+    __shared__ __align__(16) float sS[STAGED ? K * LDS_ : 1], sE[STAGED ? K * LDS_ : 1];
+    __shared__ __align__(16) float s_gate[kGates][C];
+    __shared__ float s_row[10][16], s_colf[10][16], s_cols[10][16], s_z[P / 16][C], s_r[P / 16][C], s_se[8], s_dd[8];
 
     const SsmParams& f = p.f;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -62,38 +74,90 @@ __global__ __launch_bounds__(256) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     const int part = flat % p.parts, grp = (flat / p.parts) % f.G, ci = flat / (p.parts * f.G);
     const int hpg = f.H / f.G;
     const int ha = grp * hpg + min(part * p.heads_per, hpg), hb = grp * hpg + min((part + 1) * p.heads_per, hpg);
-    const size_t kp = (size_t)K * P;
+    constexpr int KP = K * P;
     if (ci >= total_chunks(f)) {
         // chunks that a packed call's bound counts and its lengths do not have
-        for (int h = ha + tid; h < hb; h += 256)
+        for (int h = ha + tid; h < hb; h += TH)
             for (int m = 0; m < 3; ++m) p.sums[((size_t)ci * 3 + m) * f.H + h] = 0.f;
         return;
     }
     ChunkWalk at;
     at.init(f, ci);
     const int t0 = at.t0(), len = at.len();
+    const bool first = at.first(), last = at.last();
+    auto start_of = [&](int h) {
+        return first ? (f.s0 ? f.s0 + ((size_t)at.seq * f.H + h) * KP : nullptr) : p.start + ((size_t)ci * f.H + h) * KP;
+    };
+    auto dend_of = [&](int h) {
+        return last ? (f.sT ? f.sT + ((size_t)at.seq * f.H + h) * KP : nullptr) : p.dend + ((size_t)ci * f.H + h) * KP;
+    };
+
+    // ---- a head's rows, states and gates: loads, then LDS
+    uint4 rx[PX], rg[PX], rs[PS], re[PS], rgate;
+    T rdt = (T)0.f;
+    auto fetch = [&](int h) {
+        const int td = opaque(tid);
+        const auto xr = row_rsrc<T>(reinterpret_cast<const T*>(f.x) + h * P, f.x_stride, t0, len, P);
+        const auto gr = row_rsrc<T>(reinterpret_cast<const T*>(p.d_y) + h * P, (size_t)f.H * P, t0, len, P);
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            const int q = td + TH * i, row = q / (P / EPP), col = (q % (P / EPP)) * EPP;
+            rx[i] = buf_load16(xr, (unsigned)(row * (int)f.x_stride + col) * sizeof(T));
+            rg[i] = buf_load16(gr, (unsigned)(row * f.H * P + col) * sizeof(T));
+        }
+        if constexpr (STAGED) {
+            // a missing state is zeros: a resource of no bytes
+            const float *sp = start_of(h), *ep = dend_of(h);
+            const auto sr = make_rsrc_n(sp, sp ? KP * 4 : 0), er = make_rsrc_n(ep, ep ? KP * 4 : 0);
+#pragma unroll
+            for (int i = 0; i < PS; ++i) {
+                rs[i] = buf_load16(sr, 16u * (unsigned)(td + TH * i));
+                re[i] = buf_load16(er, 16u * (unsigned)(td + TH * i));
+            }
+        }
+        const auto ar = make_rsrc_n(f.gates + ((size_t)ci * f.H + h) * (kGates * C), kGates * C * 4);
+        rgate = buf_load16(ar, 16u * (unsigned)td);
+        const auto dr = row_rsrc<T>(reinterpret_cast<const T*>(f.dt) + h, f.dt_stride, t0, len, 1);
+        buf_load1(rdt, dr, (unsigned)(opaque(lane) * (int)f.dt_stride) * sizeof(T), 0);
+    };
+    auto stage = [&]() {
+        const int td = opaque(tid);
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            const int q = td + TH * i, row = q / (P / EPP), col = (q % (P / EPP)) * EPP;
+            *reinterpret_cast<uint4*>(sX + row * LDP + col) = rx[i];
+            *reinterpret_cast<uint4*>(sDY + row * LDP + col) = rg[i];
+        }
+        if constexpr (STAGED) {
+#pragma unroll
+            for (int i = 0; i < PS; ++i) {
+                const int q = td + TH * i, row = q / (P / 4), col = (q % (P / 4)) * 4;
+                *reinterpret_cast<uint4*>(sS + row * LDS_ + col) = rs[i];
+                *reinterpret_cast<uint4*>(sE + row * LDS_ + col) = re[i];
+            }
+        }
+        if (td < kGates * C / 4) *reinterpret_cast<uint4*>(&s_gate[0][0] + 4 * td) = rgate;
+    };
+    if (ha < hb) fetch(ha);
 
     // ---- B and C of the chunk, and the score tiles the wave keeps
     {
-        const T* bp = reinterpret_cast<const T*>(f.B) + (size_t)t0 * f.b_stride + grp * K;
-        const T* cp = reinterpret_cast<const T*>(f.C) + (size_t)t0 * f.c_stride + grp * K;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int q = tid; q < C * K / EPP; q += 256) {
+        const auto br = row_rsrc<T>(reinterpret_cast<const T*>(f.B) + grp * K, f.b_stride, t0, len, K);
+        const auto cr = row_rsrc<T>(reinterpret_cast<const T*>(f.C) + grp * K, f.c_stride, t0, len, K);
+        for (int q = tid; q < C * K / EPP; q += TH) {
             const int row = q / (K / EPP), col = (q % (K / EPP)) * EPP;
-            *reinterpret_cast<uint4*>(sB + row * LDK + col) =
-                row < len ? *reinterpret_cast<const uint4*>(bp + (size_t)row * f.b_stride + col) : zero;
-            *reinterpret_cast<uint4*>(sC + row * LDK + col) =
-                row < len ? *reinterpret_cast<const uint4*>(cp + (size_t)row * f.c_stride + col) : zero;
+            *reinterpret_cast<uint4*>(sB + row * LDK + col) = buf_load16(br, (unsigned)(row * (int)f.b_stride + col) * sizeof(T));
+            *reinterpret_cast<uint4*>(sC + row * LDK + col) = buf_load16(cr, (unsigned)(row * (int)f.c_stride + col) * sizeof(T));
         }
-        for (int q = tid; q < C * LDM; q += 256) sM[q] = (T)0.f;
+        for (int q = tid; q < C * LDM; q += TH) sM[q] = (T)0.f;
     }
     __syncthreads();
-    // tile k of wave w is lower tile q = w + 4 k: rows 16 ti + 4 g + e, column 16 tj + r16
-    f32x4 Gt[3], dG[3];
-    int ti[3], tj[3];
+    // tile k of wave w is lower tile q = w + 8 k: rows 16 ti + 4 g + e, column 16 tj + r16
+    f32x4 Gt[2], dG[2];
+    int ti[2], tj[2];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const int q = w + 4 * k;
+    for (int k = 0; k < 2; ++k) {
+        const int q = w + 8 * k;
         ti[k] = q < 1 ? 0 : q < 3 ? 1 : q < 6 ? 2 : 3;
         tj[k] = q - ti[k] * (ti[k] + 1) / 2;
         Gt[k] = dG[k] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -103,58 +167,26 @@ __global__ __launch_bounds__(256) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 Gt[k] = mma(Gt[k], ld_frag<T>(sC + (16 * ti[k] + r16) * LDK + 32 * m + 8 * g),
                             ld_frag<T>(sB + (16 * tj[k] + r16) * LDK + 32 * m + 8 * g));
     }
-    // gradients of B and C, transposed: state rows 16 (NT w + n) + 4 g + e, token 16 t + r16
-    f32x4 dBt[NT][4], dCt[NT][4];
+    // gradients of B and C, transposed: task k is state rows 16 nrow + 4 g + e
+    // of dC (K = 128: k = 0; K = 64: waves 0..3) or dB, tokens 16 t + r16
+    const int nrow = K == 128 ? w : (w & 3);
+    f32x4 acc[TK][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int k = 0; k < TK; ++k)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) dBt[n][t] = dCt[n][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 4; ++t) acc[k][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     for (int h = ha; h < hb; ++h) {
-        const float* start = at.first() ? (f.s0 ? f.s0 + ((size_t)at.seq * f.H + h) * kp : nullptr)
-                                        : p.start + ((size_t)ci * f.H + h) * kp;
-        const float* dend = at.last() ? (f.sT ? f.sT + ((size_t)at.seq * f.H + h) * kp : nullptr)
-                                      : p.dend + ((size_t)ci * f.H + h) * kp;
+        const float *start = start_of(h), *dend = dend_of(h);
+        const T my_dt = rdt;
+        stage();
         __syncthreads();
-        {
-            const T* xp = reinterpret_cast<const T*>(f.x) + (size_t)t0 * f.x_stride + h * P;
-            const T* gp = reinterpret_cast<const T*>(p.d_y) + ((size_t)t0 * f.H + h) * P;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            for (int q = tid; q < C * P / EPP; q += 256) {
-                const int row = q / (P / EPP), col = (q % (P / EPP)) * EPP;
-                *reinterpret_cast<uint4*>(sX + row * LDP + col) =
-                    row < len ? *reinterpret_cast<const uint4*>(xp + (size_t)row * f.x_stride + col) : zero;
-                *reinterpret_cast<uint4*>(sDY + row * LDP + col) =
-                    row < len ? *reinterpret_cast<const uint4*>(gp + (size_t)row * f.H * P + col) : zero;
-            }
-        }
-        if (w == 0) {
-            float delta = 0.f, sig = 0.f;
-            if (lane < len) {
-                const float raw = to_f32(reinterpret_cast<const T*>(f.dt)[(size_t)(t0 + lane) * f.dt_stride + h]) +
-                                  (f.dt_bias ? f.dt_bias[h] : 0.f);
-                delta = delta_of(raw, f.softplus);
-                sig = f.softplus ? 1.f / (1.f + expf(-raw)) : 1.f;
-            }
-            const double c = wave_prefix((double)delta * (double)f.A[h] * 1.4426950408889634);
-            const double ct = last_lane(c);
-            const float ch = (float)c;
-            s_c[lane] = ch;
-            s_cl[lane] = (float)(c - (double)ch);
-            s_delta[lane] = delta;
-            s_ec[lane] = exp2_of(c);
-            const float out = exp2_of(ct - c);
-            s_out[lane] = out;
-            s_w[lane] = out * delta;
-            s_sig[lane] = sig;
-            if (lane == 0) s_decay = exp2_of(ct);
-        }
-        __syncthreads();
+        if (h + 1 < hb) fetch(h + 1);
         // ---- pairs of tokens
         float dd = 0.f;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const int q = w + 4 * k;
+        for (int k = 0; k < 2; ++k) {
+            const int q = w + 8 * k;
             if (q >= 10) continue;
             f32x4 dm{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -162,13 +194,13 @@ __global__ __launch_bounds__(256) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 dm = mma(dm, ld_frag<T>(sDY + (16 * ti[k] + r16) * LDP + 32 * m + 8 * g),
                          ld_frag<T>(sX + (16 * tj[k] + r16) * LDP + 32 * m + 8 * g));
             const int j = 16 * tj[k] + r16, i0 = 16 * ti[k] + 4 * g;
-            const float cj = s_c[j], cjl = s_cl[j], dj = s_delta[j];
+            const float cj = s_gate[kGateC][j], cjl = s_gate[kGateRest][j], dj = s_gate[kGateDelta][j];
             float mv[4], colf = 0.f, cols = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = i0 + e;
                 const bool in = j <= i, below = j < i;
-                const float l = fast_exp2(in ? (s_c[i] - cj) + (s_cl[i] - cjl) : 0.f);
+                const float l = fast_exp2(in ? (s_gate[kGateC][i] - cj) + (s_gate[kGateRest][i] - cjl) : 0.f);
                 const float ql = in ? dm[e] * l : 0.f;
                 const float pr = in ? ql * Gt[k][e] : 0.f;
                 mv[e] = in ? Gt[k][e] * l * dj : 0.f;
@@ -191,55 +223,51 @@ __global__ __launch_bounds__(256) void kda_ssm_bwd_kernel(SsmBwdParams p) {
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) dd += __shfl_xor(dd, m);
         if (lane == 0) s_dd[w] = dd;
-        // ---- what passes through the states: U = E^T B and Y = S^T C, columns
-        // 16 (PT w + n) + 4 g + e of token 16 t + r16
-        f32x4 dx[PT][4];
+        // ---- what passes through the states: U = E^T B or Y = S^T C, columns
+        // col + 4 g + e of token 16 t + r16
+        f32x4 dx[4];
         float se = 0.f;
-        float z[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int n = 0; n < PT; ++n) {
-            const int col = 16 * (PT * w + n);
-            f32x4 U[4], Y[4];
+        for (int k = 0; k < TU; ++k) {
+            const bool is_y = P == 64 ? w >= 4 : k == 1;
+            const int ct = P == 64 ? (w & 3) : w, col = 16 * ct;
+            const T* rows = is_y ? sC : sB;
+            f32x4 U[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) U[t] = Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < 4; ++t) U[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int m = 0; m < K / 32; ++m) {
-                float ev[8], sv[8];
+                float v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const size_t o = (size_t)(32 * m + 16 * (i >> 2) + 4 * g + (i & 3)) * P + col + r16;
-                    ev[i] = dend ? dend[o] : 0.f;
-                    sv[i] = start ? start[o] : 0.f;
-                    se = fmaf(ev[i], sv[i], se);
+                    const int n = 32 * m + 16 * (i >> 2) + 4 * g + (i & 3);
+                    if constexpr (STAGED) {
+                        v[i] = (is_y ? sS : sE)[n * LDS_ + col + r16];
+                        if (!is_y) se = fmaf(v[i], sS[n * LDS_ + col + r16], se);
+                    } else {
+                        const float* st = is_y ? start : dend;
+                        v[i] = st ? st[(size_t)n * P + col + r16] : 0.f;
+                        if (!is_y && start) se = fmaf(v[i], start[(size_t)n * P + col + r16], se);
+                    }
                 }
-                const auto ef = Exact<T>::of(ev);
-                const auto sf = Exact<T>::of(sv);
+                const auto vf = Exact<T>::of(v);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    U[t] = mma_exact_a(U[t], ef, ld_frag_perm<T>(sB + (16 * t + r16) * LDK + 32 * m + 4 * g));
-                    Y[t] = mma_exact_a(Y[t], sf, ld_frag_perm<T>(sC + (16 * t + r16) * LDK + 32 * m + 4 * g));
-                }
+                for (int t = 0; t < 4; ++t)
+                    U[t] = mma_exact_a(U[t], vf, ld_frag_perm<T>(rows + (16 * t + r16) * LDK + 32 * m + 4 * g));
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const f32x4 xv = ld4_as_f32<T>(sX + (16 * t + r16) * LDP + col + 4 * g);
                 const f32x4 gv = ld4_as_f32<T>(sDY + (16 * t + r16) * LDP + col + 4 * g);
+                const f32x4 o = is_y ? gv : ld4_as_f32<T>(sX + (16 * t + r16) * LDP + col + 4 * g);
+                float z = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    z[t] = fmaf(U[t][e], xv[e], z[t]);
-                    r[t] = fmaf(Y[t][e], gv[e], r[t]);
+                for (int e = 0; e < 4; ++e) z = fmaf(U[t][e], o[e], z);
+                z = sum_groups(z);
+                if (g == 0) (is_y ? s_r : s_z)[ct][16 * t + r16] = z;
+                if (!is_y) {
+                    dx[t] = U[t] * s_gate[kGateW][16 * t + r16];
+                    if (f.Dskip) dx[t] += gv * f.Dskip[h];
                 }
-                dx[n][t] = U[t] * s_w[16 * t + r16];
-                if (f.Dskip) dx[n][t] += gv * f.Dskip[h];
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            z[t] = sum_groups(z[t]);
-            r[t] = sum_groups(r[t]);
-            if (g == 0) {
-                s_z[w][16 * t + r16] = z[t];
-                s_r[w][16 * t + r16] = r[t];
             }
         }
 #pragma unroll
@@ -247,55 +275,51 @@ __global__ __launch_bounds__(256) void kda_ssm_bwd_kernel(SsmBwdParams p) {
         if (lane == 0) s_se[w] = se;
         __syncthreads();
         // ---- dx: the chunk's own tokens
+        if (P == 128 || w < 4) {
+            const int col = 16 * w;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-            for (int n = 0; n < PT; ++n) {
-                const Frag gf = ld_frag_tokens(sDY, LDP, 32 * s, 16 * (PT * w + n), lane);
+            for (int s = 0; s < 2; ++s) {
+                const Frag gf = ld_frag_tokens(sDY, LDP, 32 * s, col, lane);
 #pragma unroll
                 for (int t = 0; t < 2 + 2 * s; ++t)
-                    dx[n][t] = mma(dx[n][t], gf, ld_frag_perm<T>(sM + (16 * t + r16) * LDM + 32 * s + 4 * g));
+                    dx[t] = mma(dx[t], gf, ld_frag_perm<T>(sM + (16 * t + r16) * LDM + 32 * s + 4 * g));
             }
-        }
-        {
-            T* xp = reinterpret_cast<T*>(p.dx) + (size_t)t0 * p.dx_stride + h * P;
+            const auto xr = row_rsrc<T>(reinterpret_cast<const T*>(p.dx) + h * P + col, p.dx_stride, t0, len, 16);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const int j = 16 * t + r16;
-                if (j < len)
-#pragma unroll
-                    for (int n = 0; n < PT; ++n) {
-                        float o[4] = {dx[n][t][0], dx[n][t][1], dx[n][t][2], dx[n][t][3]};
-                        st_run<4>(xp + (size_t)j * p.dx_stride + 16 * (PT * w + n) + 4 * g, o);
-                    }
+                float o[4] = {dx[t][0], dx[t][1], dx[t][2], dx[t][3]};
+                buf_store4(xr, (unsigned)((16 * t + r16) * (int)p.dx_stride + 4 * g) * sizeof(T), 0, o, (const T*)nullptr);
             }
         }
         // ---- dB and dC through the states
-        auto through = [&](const float* state, const T* tok, const float* scale, f32x4(&acc)[NT][4]) {
-            if (!state) return;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                Frag sf[P / 32];
+        for (int k = 0; k < TK; ++k) {
+            const bool is_c = K == 128 ? k == 0 : w < 4;
+            const float* st = is_c ? start : dend;
+            if (!st) continue;
+            const T* tok = is_c ? sDY : sX;
+            Frag sf[P / 32];
 #pragma unroll
-                for (int m = 0; m < P / 32; ++m) {
-                    float v[8];
-                    ld8f(state + (size_t)(16 * (NT * w + n) + r16) * P + 32 * m + 8 * g, v);
-                    sf[m] = frag_from<T>(v);
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    f32x4 v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int m = 0; m < P / 32; ++m)
-                        v = mma(v, sf[m], ld_frag<T>(tok + (16 * t + r16) * LDP + 32 * m + 8 * g));
-                    acc[n][t] += v * scale[16 * t + r16];
-                }
+            for (int m = 0; m < P / 32; ++m) {
+                float v[8];
+                if constexpr (STAGED)
+                    ld8f((is_c ? sS : sE) + (16 * nrow + r16) * LDS_ + 32 * m + 8 * g, v);
+                else
+                    ld8f(st + (size_t)(16 * nrow + r16) * P + 32 * m + 8 * g, v);
+                sf[m] = frag_from<T>(v);
             }
-        };
-        through(start, sDY, s_ec, dCt);
-        through(dend, sX, s_w, dBt);
-        // ---- step sizes and decays
-        if (w == 0) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f32x4 v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int m = 0; m < P / 32; ++m)
+                    v = mma(v, sf[m], ld_frag<T>(tok + (16 * t + r16) * LDP + 32 * m + 8 * g));
+                const int j = 16 * t + r16;
+                acc[k][t] += v * (is_c ? exp2_pair(s_gate[kGateC][j], s_gate[kGateRest][j]) : s_gate[kGateW][j]);
+            }
+        }
+        // ---- step sizes and decays, in the last wave
+        if (w == 7) {
             const int t = lane >> 4, q = lane & 15;
             float row = 0.f, cf = 0.f, cs = 0.f;
             for (int b = 0; b <= t; ++b) row += s_row[t * (t + 1) / 2 + b][q];
@@ -303,75 +327,82 @@ __global__ __launch_bounds__(256) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 cf += s_colf[a * (a + 1) / 2 + t][q];
                 cs += s_cols[a * (a + 1) / 2 + t][q];
             }
-            const float zz = s_z[0][lane] + s_z[1][lane] + s_z[2][lane] + s_z[3][lane];
-            const float rr = (s_r[0][lane] + s_r[1][lane] + s_r[2][lane] + s_r[3][lane]) * s_ec[lane];
+            float zz = 0.f, rr = 0.f, sev = 0.f, ddv = 0.f;
+#pragma unroll
+            for (int k = 0; k < P / 16; ++k) {
+                zz += s_z[k][lane];
+                rr += s_r[k][lane];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                sev += s_se[k];
+                ddv += s_dd[k];
+            }
+            const float c = s_gate[kGateC][lane], rest = s_gate[kGateRest][lane], delta = s_gate[kGateDelta][lane];
+            const float cT = s_gate[kGateC][C - 1], restT = s_gate[kGateRest][C - 1];
+            rr *= exp2_pair(c, rest);
             const double after = (double)row - (double)cs + (double)rr;     // summed over i >= t
             const double pre = wave_prefix(after);
             const double suffix = last_lane(pre) - pre + after;
-            const double wz = (double)s_w[lane] * (double)zz;
-            const double before = wave_prefix(wz) - wz;               // summed over j < t
-            const double thru = (double)s_decay * ((double)s_se[0] + s_se[1] + s_se[2] + s_se[3]);
-            const double dla = suffix + before + thru;
-            const float dd_raw =
-                (float)(((double)cf + (double)s_out[lane] * (double)zz + (double)f.A[h] * dla) * (double)s_sig[lane]);
+            const double wz = (double)s_gate[kGateW][lane] * (double)zz;
+            const double before = wave_prefix(wz) - wz;                     // summed over j < t
+            const double dla = suffix + before + (double)exp2_pair(cT, restT) * (double)sev;
             const bool in = lane < len;
+            const float raw = to_f32(my_dt) + (f.dt_bias ? f.dt_bias[h] : 0.f);
+            const float sig = f.softplus ? 1.f / (1.f + expf(-raw)) : 1.f;
+            const float out = fast_exp2((cT - c) + (restT - rest));
+            const float dd_raw = (float)(((double)cf + (double)out * (double)zz + (double)f.A[h] * dla) * (double)sig);
             if (in) reinterpret_cast<T*>(p.ddt)[(size_t)(t0 + lane) * f.H + h] = from_f32<T>(dd_raw);
-            double a = in ? dla * (double)s_delta[lane] : 0.0, b = in ? (double)dd_raw : 0.0;
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                a += __shfl_xor(a, m);
-                b += __shfl_xor(b, m);
-            }
+            const double sa = last_lane(wave_prefix(in ? dla * (double)delta : 0.0));
+            const double sb = last_lane(wave_prefix(in ? (double)dd_raw : 0.0));
             if (lane == 0) {
-                float* out = p.sums + (size_t)ci * 3 * f.H + h;
-                out[0] = (float)a;
-                out[f.H] = (float)b;
-                out[2 * f.H] = s_dd[0] + s_dd[1] + s_dd[2] + s_dd[3];
+                float* o = p.sums + (size_t)ci * 3 * f.H + h;
+                o[0] = (float)sa;
+                o[f.H] = (float)sb;
+                o[2 * f.H] = ddv;
             }
         }
+        __syncthreads();
     }
     // ---- the heads' summed score gradients, times C and B
-    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        if (w + 4 * k < 10) {
+    for (int k = 0; k < 2; ++k) {
+        if (w + 8 * k < 10) {
             float v[4] = {dG[k][0], dG[k][1], dG[k][2], dG[k][3]};
             st_run<4>(sM + (16 * tj[k] + r16) * LDM + 16 * ti[k] + 4 * g, v);
         }
     }
     __syncthreads();
+    const size_t tokens = f.sv.cu ? (size_t)f.sv.T : (size_t)f.sv.N * f.sv.T;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int k = 0; k < TK; ++k) {
+        const bool is_c = K == 128 ? k == 0 : w < 4;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const Frag cf = ld_frag_tokens(sC, LDK, 32 * s, 16 * (NT * w + n), lane);
-            const Frag bf = ld_frag_tokens(sB, LDK, 32 * s, 16 * (NT * w + n), lane);
+        for (int s = 0; s < 2; ++s) {
+            const Frag rf = ld_frag_tokens(is_c ? sB : sC, LDK, 32 * s, 16 * nrow, lane);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 // dB_j: rows i of the slab at or behind j's tile; dC_i: rows j up to i's tile
-                if (t < 2 + 2 * s)
-                    dBt[n][t] = mma(dBt[n][t], cf, ld_frag_perm<T>(sM + (16 * t + r16) * LDM + 32 * s + 4 * g));
-                if (t >= 2 * s) dCt[n][t] = mma(dCt[n][t], bf, ld_frag_tokens(sM, LDM, 32 * s, 16 * t, lane));
+                if (is_c) {
+                    if (t >= 2 * s) acc[k][t] = mma(acc[k][t], rf, ld_frag_tokens(sM, LDM, 32 * s, 16 * t, lane));
+                } else {
+                    if (t < 2 + 2 * s)
+                        acc[k][t] = mma(acc[k][t], rf, ld_frag_perm<T>(sM + (16 * t + r16) * LDM + 32 * s + 4 * g));
+                }
             }
         }
-    }
+        const int row = grp * K + 16 * nrow + 4 * g;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int j = 16 * t + r16;
-        if (j >= len) continue;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int row = grp * K + 16 * (NT * w + n) + 4 * g;
-            float vb[4] = {dBt[n][t][0], dBt[n][t][1], dBt[n][t][2], dBt[n][t][3]};
-            float vc[4] = {dCt[n][t][0], dCt[n][t][1], dCt[n][t][2], dCt[n][t][3]};
+        for (int t = 0; t < 4; ++t) {
+            const int j = 16 * t + r16;
+            if (j >= len) continue;
+            float v[4] = {acc[k][t][0], acc[k][t][1], acc[k][t][2], acc[k][t][3]};
             if (p.parts == 1) {
-                st_run<4>(reinterpret_cast<T*>(p.dB) + (size_t)(t0 + j) * p.db_stride + row, vb);
-                st_run<4>(reinterpret_cast<T*>(p.dC) + (size_t)(t0 + j) * p.dc_stride + row, vc);
+                T* o = is_c ? reinterpret_cast<T*>(p.dC) + (size_t)(t0 + j) * p.dc_stride
+                            : reinterpret_cast<T*>(p.dB) + (size_t)(t0 + j) * p.db_stride;
+                st_run<4>(o + row, v);
             } else {
-                const size_t tokens = f.sv.cu ? (size_t)f.sv.T : (size_t)f.sv.N * f.sv.T;
-                const size_t o = ((size_t)part * tokens + t0 + j) * f.G * K + row;
-                st_run<4>(p.dB_part + o, vb);
-                st_run<4>(p.dC_part + o, vc);
+                st_run<4>((is_c ? p.dC_part : p.dB_part) + ((size_t)part * tokens + t0 + j) * f.G * K + row, v);
             }
         }
     }
@@ -419,10 +450,10 @@ __global__ __launch_bounds__(256) void kda_ssm_bwd_sums_kernel(const float* sums
 template <typename T>
 hipError_t bwd_launch(const SsmBwdParams& p, hipStream_t st) {
     const dim3 grid((unsigned)((long long)p.f.chunks * p.f.G * p.parts));
-    if (p.f.K == 128 && p.f.P == 128) hipLaunchKernelGGL((kda_ssm_bwd_kernel<T, 128, 128>), grid, dim3(256), 0, st, p);
-    else if (p.f.K == 128) hipLaunchKernelGGL((kda_ssm_bwd_kernel<T, 128, 64>), grid, dim3(256), 0, st, p);
-    else if (p.f.P == 128) hipLaunchKernelGGL((kda_ssm_bwd_kernel<T, 64, 128>), grid, dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((kda_ssm_bwd_kernel<T, 64, 64>), grid, dim3(256), 0, st, p);
+    if (p.f.K == 128 && p.f.P == 128) hipLaunchKernelGGL((kda_ssm_bwd_kernel<T, 128, 128>), grid, dim3(512), 0, st, p);
+    else if (p.f.K == 128) hipLaunchKernelGGL((kda_ssm_bwd_kernel<T, 128, 64>), grid, dim3(512), 0, st, p);
+    else if (p.f.P == 128) hipLaunchKernelGGL((kda_ssm_bwd_kernel<T, 64, 128>), grid, dim3(512), 0, st, p);
+    else hipLaunchKernelGGL((kda_ssm_bwd_kernel<T, 64, 64>), grid, dim3(512), 0, st, p);
     return hipGetLastError();
 }
 
