@@ -30,17 +30,25 @@ __device__ __forceinline__ f32x4 mma_exact_a(f32x4 acc, const Split3& v, bf16x8 
 }
 __device__ __forceinline__ f32x4 mma_exact_a(f32x4 acc, const f32x8& v, f32x8 b) { return mma(acc, v, b); }
 
-// sum over the 16 lanes of a row group
+// Sums across lanes without LDS: rotations within rows of 16 lanes, and the
+// exchange of rows and halves between two registers (v' = a's rows 0, 2 next to
+// b's, v'' = rows 1, 3; with a = b = v, v' + v'' adds neighbouring rows).
+template <int ROT> __device__ __forceinline__ float row_rotate(float v) {
+    return __uint_as_float((unsigned)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x120 + ROT, 0xf, 0xf, true));
+}
 __device__ __forceinline__ float sum16(float v) {
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1) v += __shfl_xor(v, m);
-    return v;
+    v += row_rotate<8>(v);
+    v += row_rotate<4>(v);
+    v += row_rotate<2>(v);
+    return v + row_rotate<1>(v);
 }
-// sum over the four lane groups
 __device__ __forceinline__ float sum_groups(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
+__device__ __forceinline__ float sum64(float v) { return sum_groups(sum16(v)); }
 
 // One workgroup (8 waves) per (chunk, group, part of the group's heads), head by
 // head.  The group's B, C and scores stay; a head's x, dy and states are loaded
@@ -64,8 +72,13 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     typedef typename FragOf<T>::type Frag;
     __shared__ T sB[C * LDK], sC[C * LDK], sX[C * LDP], sDY[C * LDP], sM[C * LDM];
     __shared__ __align__(16) float sS[STAGED ? K * LDS_ : 1], sE[STAGED ? K * LDS_ : 1];
-    __shared__ __align__(16) float s_gate[kGates][C];
-    __shared__ float s_row[10][16], s_colf[10][16], s_cols[10][16], s_z[P / 16][C], s_r[P / 16][C], s_se[8], s_dd[8];
+    // what the step sizes' gradients need of a head, for two heads in turn: the
+    // last wave works on it beside the next head's pairs (fp32 at K = P = 128
+    // has no LDS for two, and does it at the head's end)
+    constexpr int NB = sizeof(T) == 4 && K * P > 8192 ? 1 : 2;
+    __shared__ __align__(16) float s_gate_[NB][kGates][C];
+    __shared__ float s_row_[NB][10][16], s_colf_[NB][10][16], s_cols_[NB][10][16], s_z_[NB][P / 16][C],
+        s_r_[NB][P / 16][C], s_se_[NB][8], s_dd_[NB][8];
 
     const SsmParams& f = p.f;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -120,8 +133,10 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
         const auto dr = row_rsrc<T>(reinterpret_cast<const T*>(f.dt) + h, f.dt_stride, t0, len, 1);
         buf_load1(rdt, dr, (unsigned)(opaque(lane) * (int)f.dt_stride) * sizeof(T), 0);
     };
-    auto stage = [&]() {
+    float se = 0.f;         // the thread's share of <S, E>
+    auto stage = [&](float* gate) {
         const int td = opaque(tid);
+        se = 0.f;
 #pragma unroll
         for (int i = 0; i < PX; ++i) {
             const int q = td + TH * i, row = q / (P / EPP), col = (q % (P / EPP)) * EPP;
@@ -134,9 +149,13 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 const int q = td + TH * i, row = q / (P / 4), col = (q % (P / 4)) * 4;
                 *reinterpret_cast<uint4*>(sS + row * LDS_ + col) = rs[i];
                 *reinterpret_cast<uint4*>(sE + row * LDS_ + col) = re[i];
+                se = fmaf(__uint_as_float(rs[i].x), __uint_as_float(re[i].x), se);
+                se = fmaf(__uint_as_float(rs[i].y), __uint_as_float(re[i].y), se);
+                se = fmaf(__uint_as_float(rs[i].z), __uint_as_float(re[i].z), se);
+                se = fmaf(__uint_as_float(rs[i].w), __uint_as_float(re[i].w), se);
             }
         }
-        if (td < kGates * C / 4) *reinterpret_cast<uint4*>(&s_gate[0][0] + 4 * td) = rgate;
+        if (td < kGates * C / 4) *reinterpret_cast<uint4*>(gate + 4 * td) = rgate;
     };
     if (ha < hb) fetch(ha);
 
@@ -152,12 +171,12 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
         for (int q = tid; q < C * LDM; q += TH) sM[q] = (T)0.f;
     }
     __syncthreads();
-    // tile k of wave w is lower tile q = w + 8 k: rows 16 ti + 4 g + e, column 16 tj + r16
+    // tile k of wave w is lower tile q = (w + 4) % 8 + 8 k: rows 16 ti + 4 g + e, column 16 tj + r16
     f32x4 Gt[2], dG[2];
     int ti[2], tj[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int q = w + 8 * k;
+        const int q = ((w + 4) & 7) + 8 * k;
         ti[k] = q < 1 ? 0 : q < 3 ? 1 : q < 6 ? 2 : 3;
         tj[k] = q - ti[k] * (ti[k] + 1) / 2;
         Gt[k] = dG[k] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -176,17 +195,82 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[k][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    // ---- step sizes and decays of head h, in one wave
+    auto step_sizes = [&](int h, int nb, T head_dt) {
+        auto& s_gate = s_gate_[nb];
+        auto& s_row = s_row_[nb];
+        auto& s_colf = s_colf_[nb];
+        auto& s_cols = s_cols_[nb];
+        auto& s_z = s_z_[nb];
+        auto& s_r = s_r_[nb];
+        auto& s_se = s_se_[nb];
+        auto& s_dd = s_dd_[nb];
+        const int t = lane >> 4, q = lane & 15;
+        float row = 0.f, cf = 0.f, cs = 0.f;
+        for (int b = 0; b <= t; ++b) row += s_row[t * (t + 1) / 2 + b][q];
+        for (int a = t; a < 4; ++a) {
+            cf += s_colf[a * (a + 1) / 2 + t][q];
+            cs += s_cols[a * (a + 1) / 2 + t][q];
+        }
+        float zz = 0.f, rr = 0.f, sev = 0.f, ddv = 0.f;
+#pragma unroll
+        for (int k = 0; k < P / 16; ++k) {
+            zz += s_z[k][lane];
+            rr += s_r[k][lane];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            sev += s_se[k];
+            ddv += s_dd[k];
+        }
+        const float c = s_gate[kGateC][lane], rest = s_gate[kGateRest][lane], delta = s_gate[kGateDelta][lane];
+        const float cT = s_gate[kGateC][C - 1], restT = s_gate[kGateRest][C - 1];
+        rr *= exp2_pair(c, rest);
+        const double after = (double)row - (double)cs + (double)rr;     // summed over i >= t
+        const double pre = wave_prefix(after);
+        const double suffix = last_lane(pre) - pre + after;
+        const double wz = (double)s_gate[kGateW][lane] * (double)zz;
+        const double before = wave_prefix(wz) - wz;                     // summed over j < t
+        const double dla = suffix + before + (double)exp2_pair(cT, restT) * (double)sev;
+        const bool in = lane < len;
+        const float raw = to_f32(head_dt) + (f.dt_bias ? f.dt_bias[h] : 0.f);
+        const float sig = f.softplus ? 1.f / (1.f + expf(-raw)) : 1.f;
+        const float out = fast_exp2((cT - c) + (restT - rest));
+        const float dd_raw = (float)(((double)cf + (double)out * (double)zz + (double)f.A[h] * dla) * (double)sig);
+        if (in) reinterpret_cast<T*>(p.ddt)[(size_t)(t0 + lane) * f.H + h] = from_f32<T>(dd_raw);
+        const double sa = last_lane(wave_prefix(in ? dla * (double)delta : 0.0));
+        const double sb = last_lane(wave_prefix(in ? (double)dd_raw : 0.0));
+        if (lane == 0) {
+            float* o = p.sums + (size_t)ci * 3 * f.H + h;
+            o[0] = (float)sa;
+            o[f.H] = (float)sb;
+            o[2 * f.H] = ddv;
+        }
+    };
+    T my_dt = (T)0.f;
+
     for (int h = ha; h < hb; ++h) {
         const float *start = start_of(h), *dend = dend_of(h);
-        const T my_dt = rdt;
-        stage();
+        const int nb = NB == 2 ? (h - ha) & 1 : 0;
+        auto& s_gate = s_gate_[nb];
+        auto& s_row = s_row_[nb];
+        auto& s_colf = s_colf_[nb];
+        auto& s_cols = s_cols_[nb];
+        auto& s_z = s_z_[nb];
+        auto& s_r = s_r_[nb];
+        auto& s_se = s_se_[nb];
+        auto& s_dd = s_dd_[nb];
+        const T last_dt = my_dt;
+        my_dt = rdt;
+        stage(&s_gate[0][0]);
         __syncthreads();
         if (h + 1 < hb) fetch(h + 1);
+        if (NB == 2 && w == 7 && h > ha) step_sizes(h - 1, nb ^ 1, last_dt);
         // ---- pairs of tokens
         float dd = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int q = w + 8 * k;
+            const int q = ((w + 4) & 7) + 8 * k;
             if (q >= 10) continue;
             f32x4 dm{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -220,13 +304,11 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 s_cols[q][r16] = cols;
             }
         }
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) dd += __shfl_xor(dd, m);
+        dd = sum64(dd);
         if (lane == 0) s_dd[w] = dd;
         // ---- what passes through the states: U = E^T B or Y = S^T C, columns
         // col + 4 g + e of token 16 t + r16
         f32x4 dx[4];
-        float se = 0.f;
 #pragma unroll
         for (int k = 0; k < TU; ++k) {
             const bool is_y = P == 64 ? w >= 4 : k == 1;
@@ -240,10 +322,9 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 float v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int n = 32 * m + 16 * (i >> 2) + 4 * g + (i & 3);
+                    const int n = 32 * m + 8 * g + i;
                     if constexpr (STAGED) {
                         v[i] = (is_y ? sS : sE)[n * LDS_ + col + r16];
-                        if (!is_y) se = fmaf(v[i], sS[n * LDS_ + col + r16], se);
                     } else {
                         const float* st = is_y ? start : dend;
                         v[i] = st ? st[(size_t)n * P + col + r16] : 0.f;
@@ -253,7 +334,7 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 const auto vf = Exact<T>::of(v);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    U[t] = mma_exact_a(U[t], vf, ld_frag_perm<T>(rows + (16 * t + r16) * LDK + 32 * m + 4 * g));
+                    U[t] = mma_exact_a(U[t], vf, ld_frag<T>(rows + (16 * t + r16) * LDK + 32 * m + 8 * g));
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -270,8 +351,7 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 }
             }
         }
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) se += __shfl_xor(se, m);
+        se = sum64(se);
         if (lane == 0) s_se[w] = se;
         __syncthreads();
         // ---- dx: the chunk's own tokens
@@ -318,56 +398,14 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 acc[k][t] += v * (is_c ? exp2_pair(s_gate[kGateC][j], s_gate[kGateRest][j]) : s_gate[kGateW][j]);
             }
         }
-        // ---- step sizes and decays, in the last wave
-        if (w == 7) {
-            const int t = lane >> 4, q = lane & 15;
-            float row = 0.f, cf = 0.f, cs = 0.f;
-            for (int b = 0; b <= t; ++b) row += s_row[t * (t + 1) / 2 + b][q];
-            for (int a = t; a < 4; ++a) {
-                cf += s_colf[a * (a + 1) / 2 + t][q];
-                cs += s_cols[a * (a + 1) / 2 + t][q];
-            }
-            float zz = 0.f, rr = 0.f, sev = 0.f, ddv = 0.f;
-#pragma unroll
-            for (int k = 0; k < P / 16; ++k) {
-                zz += s_z[k][lane];
-                rr += s_r[k][lane];
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                sev += s_se[k];
-                ddv += s_dd[k];
-            }
-            const float c = s_gate[kGateC][lane], rest = s_gate[kGateRest][lane], delta = s_gate[kGateDelta][lane];
-            const float cT = s_gate[kGateC][C - 1], restT = s_gate[kGateRest][C - 1];
-            rr *= exp2_pair(c, rest);
-            const double after = (double)row - (double)cs + (double)rr;     // summed over i >= t
-            const double pre = wave_prefix(after);
-            const double suffix = last_lane(pre) - pre + after;
-            const double wz = (double)s_gate[kGateW][lane] * (double)zz;
-            const double before = wave_prefix(wz) - wz;                     // summed over j < t
-            const double dla = suffix + before + (double)exp2_pair(cT, restT) * (double)sev;
-            const bool in = lane < len;
-            const float raw = to_f32(my_dt) + (f.dt_bias ? f.dt_bias[h] : 0.f);
-            const float sig = f.softplus ? 1.f / (1.f + expf(-raw)) : 1.f;
-            const float out = fast_exp2((cT - c) + (restT - rest));
-            const float dd_raw = (float)(((double)cf + (double)out * (double)zz + (double)f.A[h] * dla) * (double)sig);
-            if (in) reinterpret_cast<T*>(p.ddt)[(size_t)(t0 + lane) * f.H + h] = from_f32<T>(dd_raw);
-            const double sa = last_lane(wave_prefix(in ? dla * (double)delta : 0.0));
-            const double sb = last_lane(wave_prefix(in ? (double)dd_raw : 0.0));
-            if (lane == 0) {
-                float* o = p.sums + (size_t)ci * 3 * f.H + h;
-                o[0] = (float)sa;
-                o[f.H] = (float)sb;
-                o[2 * f.H] = ddv;
-            }
-        }
+        if (NB == 1 && w == 7) step_sizes(h, 0, my_dt);
         __syncthreads();
     }
+    if (NB == 2 && w == 7 && hb > ha) step_sizes(hb - 1, (hb - 1 - ha) & 1, my_dt);
     // ---- the heads' summed score gradients, times C and B
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        if (w + 8 * k < 10) {
+        if (((w + 4) & 7) + 8 * k < 10) {
             float v[4] = {dG[k][0], dG[k][1], dG[k][2], dG[k][3]};
             st_run<4>(sM + (16 * tj[k] + r16) * LDM + 16 * ti[k] + 4 * g, v);
         }
