@@ -103,6 +103,7 @@ struct SsmParams {
     // sequence starts in the segment, nothing of the start state is left)
     float* seg_state;
     float* seg_decay;
+    float* states;              // [chunks][H][K][P]: the state before each chunk (the states pass)
 
 };
 constexpr int kSsmChunk = 64;
@@ -111,16 +112,23 @@ hipError_t launch_ssm_prep(const SeqView& sv, int* chunk_off, int max_chunks, hi
 // step sizes and decays of every chunk and head
 size_t ssm_gate_bytes(int chunks, int H);
 hipError_t launch_ssm_gates(int dtype, const SsmParams& p, hipStream_t st);
-// out: the output pass; else states only (segment summaries or states per chunk)
-hipError_t launch_ssm_chunks(int dtype, bool out, int cols, const SsmParams& p, int segs, hipStream_t st);
-// d_s0 (reverse with one chunk a segment only; else null): the adjoint before
-// each sequence's first chunk
-hipError_t launch_ssm_combine(const SsmParams& p, float* d_s0, hipStream_t st);
+// One or two recurrences of the same sizes in one launch (the second: the
+// backward's adjoint)
+struct SsmPair {
+    SsmParams p[2];
+};
+enum SsmPass {
+    kSsmOutput,     // y and the final states
+    kSsmSummary,    // each segment's local state and decay
+    kSsmStates      // the state before each chunk, and the final states
+};
+hipError_t launch_ssm_chunks(int dtype, SsmPass pass, int cols, const SsmPair& a, int n, int segs, hipStream_t st);
+hipError_t launch_ssm_combine(const SsmPair& a, int n, hipStream_t st);
 
 // Gradients of the scan from the state before each chunk and the adjoint
 // behind it.  A workgroup takes one chunk and heads_per of the heads of a group.
 struct SsmBwdParams {
-    SsmParams f;                // the forward's inputs (y, sT, segments unused)
+    SsmParams f;                // the forward's inputs and gates
     const void* d_y;            // [tokens][H][P]
     const float* start;         // [chunks][H][K][P]
     const float* dend;          // [chunks][H][K][P]

@@ -384,19 +384,23 @@ static kda_status ssm_sizes(int N, const int* cu, int T, int H, int G, int K, in
 // of 64 of one group, which share B, C and the scores) where the heads pair up
 static int ssm_cols(int H, int G, int P) { return P == 128 || (H / G) % 2 == 0 ? 128 : 64; }
 
+// Workgroups of a pass: two a CU.  The backward's passes run two recurrences
+// in one launch, so each takes half, in longer segments.
+constexpr int kScanGroups = 512, kScanBwdGroups = 256;
+
 struct SsmPlan {
     int cols, chunks, chunks_per_seq, n_seg, cps;
 };
-static SsmPlan ssm_plan(bool packed, int N, long long M, int T, int H, int G, int P) {
+static SsmPlan ssm_plan(bool packed, int N, long long M, int T, int H, int G, int P, int workgroups) {
     SsmPlan pl;
     pl.cols = ssm_cols(H, G, P);
     pl.chunks_per_seq = T > 0 ? (T + 63) / 64 : 1;
     pl.chunks = packed ? (int)(M / 64 + N) : N * pl.chunks_per_seq;
     const long long units = H / (pl.cols / P);
-    // segments until two workgroups a CU run, each keeping at least four chunks
-    long long want = (512 + units - 1) / units, cap = pl.chunks / 4;
+    // segments until `workgroups` run, each keeping at least four chunks
+    long long want = (workgroups + units - 1) / units, cap = pl.chunks / 4;
     if (want > cap) want = cap;
-    if (want < 1 || units >= 256) want = 1;
+    if (want < 1 || units >= workgroups / 2) want = 1;
     pl.cps = (int)((pl.chunks + want - 1) / want);
     if (pl.cps < 1) pl.cps = 1;
     pl.n_seg = (pl.chunks + pl.cps - 1) / pl.cps;
@@ -425,7 +429,7 @@ size_t kda_selective_scan_fwd_workspace_size(int N, int packed, int T, int H, in
     const int some = 0;
     if (ssm_sizes(N, packed ? &some : nullptr, T, H, G, K, P, dt, &M) != KDA_OK) return (size_t)-1;
     if (N == 0 || H == 0) return 0;
-    return ssm_layout(packed != 0, N, H, K, P, ssm_plan(packed != 0, N, M, T, H, G, P)).total;
+    return ssm_layout(packed != 0, N, H, K, P, ssm_plan(packed != 0, N, M, T, H, G, P, kScanGroups)).total;
 }
 
 // pointer checks shared by the scan's calls; offsets inside a chunk's 64 rows
@@ -469,7 +473,7 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
         return KDA_ERR_INVALID_ARG;
     if (initial_state != final_state && overlap(initial_state, state, final_state, state)) return KDA_ERR_INVALID_ARG;
     const bool packed = cu_seqlens != nullptr;
-    const SsmPlan pl = ssm_plan(packed, N, M, T, H, G, P);
+    const SsmPlan pl = ssm_plan(packed, N, M, T, H, G, P, kScanGroups);
     const SsmLayout L = ssm_layout(packed, N, H, K, P, pl);
     if (L.total > 0 && (!workspace || workspace_bytes < L.total)) return KDA_ERR_WORKSPACE;
     unsigned char* ws = reinterpret_cast<unsigned char*>(workspace);
@@ -499,12 +503,14 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
         }
         p.seg_state = reinterpret_cast<float*>(ws + L.seg);
         p.seg_decay = reinterpret_cast<float*>(ws + L.dec);
-        KDA_LAUNCH("scan_summary", launch_ssm_chunks((int)dt, false, pl.cols, p, pl.n_seg - 1, stream));
-        KDA_LAUNCH("scan_combine", launch_ssm_combine(p, nullptr, stream));
+        const SsmPair a{{p, p}};
+        KDA_LAUNCH("scan_summary", launch_ssm_chunks((int)dt, kSsmSummary, pl.cols, a, 1, pl.n_seg - 1, stream));
+        KDA_LAUNCH("scan_combine", launch_ssm_combine(a, 1, stream));
     }
     p.y = y;
     p.sT = final_state;
-    KDA_LAUNCH("scan_output", launch_ssm_chunks((int)dt, true, pl.cols, p, pl.n_seg, stream));
+    const SsmPair a{{p, p}};
+    KDA_LAUNCH("scan_output", launch_ssm_chunks((int)dt, kSsmOutput, pl.cols, a, 1, pl.n_seg, stream));
     return KDA_OK;
 }
 
@@ -512,7 +518,7 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
 // heads); parts until two workgroups a CU run, since each part beyond the first
 // adds fp32 copies of dB and dC.
 struct SsmBwdLayout {
-    size_t off, gates, start, dend, dec, sums, part_b, part_c, total;
+    size_t off, gates, seg, dec, start, dend, sums, part_b, part_c, total;
     int parts, heads_per;
 };
 static SsmBwdLayout ssm_bwd_layout(bool packed, int N, long long M, int H, int G, int K, int P, const SsmPlan& pl) {
@@ -528,9 +534,11 @@ static SsmBwdLayout ssm_bwd_layout(bool packed, int N, long long M, int H, int G
     size_t o = 0;
     L.off = o; o += packed ? align256((size_t)(N + 1) * sizeof(int)) : 0;
     L.gates = o; o += align256(ssm_gate_bytes(pl.chunks, H));
+    // segments of both recurrences
+    L.seg = o; o += pl.n_seg > 1 ? 2 * align256((size_t)pl.n_seg * H * K * P * sizeof(float)) : 0;
+    L.dec = o; o += pl.n_seg > 1 ? 2 * align256((size_t)pl.n_seg * H * sizeof(float)) : 0;
     L.start = o; o += align256(states);
     L.dend = o; o += align256(states);
-    L.dec = o; o += align256((size_t)pl.chunks * H * sizeof(float));
     L.sums = o; o += align256((size_t)pl.chunks * 3 * H * sizeof(float));
     L.part_b = o; o += align256(part);
     L.part_c = o; o += align256(part);
@@ -543,7 +551,7 @@ size_t kda_selective_scan_bwd_workspace_size(int N, int packed, int T, int H, in
     const int some = 0;
     if (ssm_sizes(N, packed ? &some : nullptr, T, H, G, K, P, dt, &M) != KDA_OK) return (size_t)-1;
     if (N == 0 || H == 0) return 0;
-    return ssm_bwd_layout(packed != 0, N, M, H, G, K, P, ssm_plan(packed != 0, N, M, T, H, G, P)).total;
+    return ssm_bwd_layout(packed != 0, N, M, H, G, K, P, ssm_plan(packed != 0, N, M, T, H, G, P, kScanBwdGroups)).total;
 }
 
 kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, int G, int K, int P, kda_dtype dt,
@@ -601,7 +609,7 @@ kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, in
         return KDA_OK;
     }
     const bool packed = cu_seqlens != nullptr;
-    SsmPlan pl = ssm_plan(packed, N, M, T, H, G, P);
+    const SsmPlan pl = ssm_plan(packed, N, M, T, H, G, P, kScanBwdGroups);
     const SsmBwdLayout L = ssm_bwd_layout(packed, N, M, H, G, K, P, pl);
     if (!workspace || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
     unsigned char* ws = reinterpret_cast<unsigned char*>(workspace);
@@ -614,7 +622,7 @@ kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, in
     p.C = C; p.c_stride = (size_t)c_stride;
     p.s0 = initial_state;
     p.chunks = pl.chunks; p.chunks_per_seq = pl.chunks_per_seq;
-    p.n_seg = pl.chunks; p.cps = 1;
+    p.n_seg = pl.n_seg; p.cps = pl.cps;
     if (packed) {
         int* off = reinterpret_cast<int*>(ws + L.off);
         KDA_LAUNCH("scan_prep", launch_ssm_prep(p.sv, off, pl.chunks, stream));
@@ -622,27 +630,34 @@ kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, in
     }
     p.gates = reinterpret_cast<float*>(ws + L.gates);
     KDA_LAUNCH("scan_gates", launch_ssm_gates((int)dt, p, stream));
-    // the state before each chunk: every chunk's own share, then the passing on
-    p.seg_state = reinterpret_cast<float*>(ws + L.start);
-    p.seg_decay = reinterpret_cast<float*>(ws + L.dec);
-    KDA_LAUNCH("scan_bwd_states", launch_ssm_chunks((int)dt, false, pl.cols, p, pl.chunks, stream));
-    KDA_LAUNCH("scan_bwd_combine", launch_ssm_combine(p, nullptr, stream));
-    // the adjoint behind each chunk: the same recurrence backwards, with C for
-    // B and dy for x
+    // the state before each chunk, and the adjoint behind it: the same
+    // recurrence backwards, with C for B and dy for x
+    p.states = reinterpret_cast<float*>(ws + L.start);
     SsmParams q = p;
     q.reverse = 1;
     q.x = d_y; q.x_stride = (size_t)H * P;
     q.B = C; q.b_stride = (size_t)c_stride;
     q.s0 = d_final_state;
-    q.seg_state = reinterpret_cast<float*>(ws + L.dend);
-    KDA_LAUNCH("scan_bwd_adjoints", launch_ssm_chunks((int)dt, false, pl.cols, q, pl.chunks, stream));
-    KDA_LAUNCH("scan_bwd_combine", launch_ssm_combine(q, d_initial_state, stream));
+    q.sT = d_initial_state;
+    q.states = reinterpret_cast<float*>(ws + L.dend);
+    SsmPair a{{p, q}};
+    if (pl.n_seg > 1) {
+        for (int i = 0; i < 2; ++i) {
+            a.p[i].seg_state = reinterpret_cast<float*>(ws + L.seg + i * align256((size_t)pl.n_seg * H * K * P * sizeof(float)));
+            a.p[i].seg_decay = reinterpret_cast<float*>(ws + L.dec + i * align256((size_t)pl.n_seg * H * sizeof(float)));
+        }
+        // the last segment's end is read by nobody: the first's, backwards
+        a.p[1].seg0 = 1;
+        KDA_LAUNCH("scan_bwd_summary", launch_ssm_chunks((int)dt, kSsmSummary, pl.cols, a, 2, pl.n_seg - 1, stream));
+        KDA_LAUNCH("scan_bwd_combine", launch_ssm_combine(a, 2, stream));
+        a.p[1].seg0 = 0;
+    }
+    KDA_LAUNCH("scan_bwd_states", launch_ssm_chunks((int)dt, kSsmStates, pl.cols, a, 2, pl.n_seg, stream));
     SsmBwdParams b{};
     b.f = p;
-    b.f.sT = const_cast<float*>(d_final_state);
     b.d_y = d_y;
-    b.start = p.seg_state;
-    b.dend = q.seg_state;
+    b.start = p.states;
+    b.dend = q.states;
     b.dx = dx; b.dx_stride = (size_t)dx_stride;
     b.ddt = d_delta;
     b.dB = dB; b.db_stride = (size_t)db_stride;

@@ -25,8 +25,11 @@ constexpr int C = kSsmChunk;
 // as operands as they are.  B, C and x of a chunk are staged in LDS (the next
 // chunk's loads in flight meanwhile); the scores C B^T are computed once for
 // the workgroup's heads, scaled and masked per head, and passed through LDS.
-//   OUT:  y, and the final state where a sequence ends
-//   else: each segment's local state and decay
+//   output:  y, and the final state where a sequence ends
+//   summary: each segment's local state and decay
+//   states:  the state before each chunk, and the final state
+// blockIdx.y picks one of two recurrences (the backward runs the states and,
+// with C for B, dy for x and the chunks in reverse, their adjoints).
 // The gates of every chunk and head (kda_ssm_device.h): a wave a head, a lane a
 // token, eight heads a block, whose step sizes share cache lines.
 template <typename T>
@@ -55,8 +58,10 @@ __global__ __launch_bounds__(256) void kda_ssm_gates_kernel(SsmParams p) {
     }
 }
 
-template <typename T, int K, int P, int COLS, bool OUT>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_kernel(SsmParams p) {
+template <typename T, int K, int P, int COLS, SsmPass PASS>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_kernel(SsmPair a) {
+    constexpr bool OUT = PASS == kSsmOutput, summary = PASS == kSsmSummary;
+    const SsmParams& p = a.p[PASS == kSsmOutput ? 0 : blockIdx.y];
     constexpr int TH = 256, NW = TH / 64;
     constexpr int NT = COLS / 16 / NW;          // column tiles a wave
     constexpr int NH = COLS / P;                // heads of the workgroup
@@ -85,7 +90,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
     const int all = total_chunks(p);
     const int begin = min(seg * p.cps, all), end = min(begin + p.cps, all);
     const bool rev = !OUT && p.reverse;
-    constexpr bool summary = !OUT;
     const int own = (4 * g) * P + pc + r16;     // the lane's first state element
     float* seg_slot = p.seg_state ? p.seg_state + ((size_t)seg * p.H + h) * KP : nullptr;
 
@@ -233,6 +237,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
         y_t0 = t0;
         y_len = len;
         stage();
+        if (PASS == kSsmStates)
+            store_state(p.states + ((size_t)(rev ? begin + end - 1 - it : it) * p.H + h) * KP);
         __syncthreads();
         // the next chunk's loads run behind this chunk's products
         if (it + 1 < end) {
@@ -418,8 +424,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
 // Segment start states from the segments' local states and decays, written
 // over the local states: start_{j+1} = decay_j start_j + local_j (local_j
 // alone where a sequence starts in segment j).  A thread owns four state
-// values of a head and keeps sixteen segments' loads in flight.
-__global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmParams p, float* d_s0) {
+// values of a head and keeps sixteen segments' loads in flight.  Bound by
+// memory: 64 MiB in 14 us for 32 segments of 32 heads.
+__global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmPair a) {
+    const SsmParams& p = a.p[blockIdx.y];
     const size_t kp4 = (size_t)p.K * p.P / 4;
     const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
     if (at >= (size_t)p.H * kp4) return;
@@ -428,10 +436,6 @@ __global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmParams p, float
     const size_t step = (size_t)p.H * kp4;
     // segments that hold chunks (a packed call may have fewer than its bound)
     const int all = total_chunks(p), n_seg = min(p.n_seg, (all + p.cps - 1) / p.cps);
-    // the last segment's local state is of use only to d_s0
-    const int used = d_s0 ? n_seg : n_seg - 1;
-    ChunkWalk walk;
-    if (d_s0 && n_seg > 0) walk.init(p, n_seg - 1);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 16;
     for (int j = 0; j < n_seg; j += U) {
@@ -439,7 +443,7 @@ __global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmParams p, float
         float d[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (j + u < used) {
+            if (j + u < n_seg - 1) {
                 const int k = p.reverse ? n_seg - 1 - (j + u) : j + u;
                 l[u] = L[(size_t)k * step];
                 d[u] = p.seg_decay[(size_t)k * p.H + h];
@@ -448,19 +452,13 @@ __global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmParams p, float
         for (int u = 0; u < U; ++u) {
             if (j + u < n_seg) {
                 const int k = p.reverse ? n_seg - 1 - (j + u) : j + u;
-                // a sequence that starts (in reverse: ends) in this segment
-                // takes its own start state, which an empty one passes on
                 L[(size_t)k * step] = s;
-                if (j + u < used) {
+                if (j + u < n_seg - 1) {
                     if (d[u] < 0.f)
                         s = l[u];
                     else
                         s = make_float4(fmaf(d[u], s.x, l[u].x), fmaf(d[u], s.y, l[u].y), fmaf(d[u], s.z, l[u].z),
                                         fmaf(d[u], s.w, l[u].w));
-                }
-                if (d_s0) {
-                    if (walk.first()) reinterpret_cast<float4*>(d_s0)[(size_t)walk.seq * step + at] = s;
-                    walk.prev();
                 }
             }
         }
@@ -585,16 +583,17 @@ hipError_t step_launch(int N, int H, int G, int P, int softplus, const void* x, 
 }
 
 template <typename T, int K, int P, int COLS>
-hipError_t chunks_launch(bool out, const SsmParams& p, int segs, hipStream_t st) {
-    const dim3 grid((unsigned)((long long)segs * (p.H / (COLS / P)))), block(256);
-    if (out) hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, COLS, true>), grid, block, 0, st, p);
-    else hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, COLS, false>), grid, block, 0, st, p);
+hipError_t chunks_launch(SsmPass pass, const SsmPair& a, int n, int segs, hipStream_t st) {
+    const dim3 grid((unsigned)((long long)segs * (a.p[0].H / (COLS / P))), (unsigned)n), block(256);
+    if (pass == kSsmOutput) hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, COLS, kSsmOutput>), grid, block, 0, st, a);
+    else if (pass == kSsmSummary) hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, COLS, kSsmSummary>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((kda_ssm_chunk_kernel<T, K, P, COLS, kSsmStates>), grid, block, 0, st, a);
     return hipGetLastError();
 }
 template <typename T, int K>
-hipError_t chunks_pick(bool out, int cols, const SsmParams& p, int segs, hipStream_t st) {
-    if (p.P == 128) return chunks_launch<T, K, 128, 128>(out, p, segs, st);
-    return cols == 128 ? chunks_launch<T, K, 64, 128>(out, p, segs, st) : chunks_launch<T, K, 64, 64>(out, p, segs, st);
+hipError_t chunks_pick(SsmPass pass, int cols, const SsmPair& a, int n, int segs, hipStream_t st) {
+    if (a.p[0].P == 128) return chunks_launch<T, K, 128, 128>(pass, a, n, segs, st);
+    return cols == 128 ? chunks_launch<T, K, 64, 128>(pass, a, n, segs, st) : chunks_launch<T, K, 64, 64>(pass, a, n, segs, st);
 }
 
 }  // namespace
@@ -613,15 +612,16 @@ hipError_t launch_ssm_gates(int dtype, const SsmParams& p, hipStream_t st) {
     return hipGetLastError();
 }
 
-hipError_t launch_ssm_chunks(int dtype, bool out, int cols, const SsmParams& p, int segs, hipStream_t st) {
+hipError_t launch_ssm_chunks(int dtype, SsmPass pass, int cols, const SsmPair& a, int n, int segs, hipStream_t st) {
     if (segs <= 0) return hipSuccess;
-    if (dtype == 1) return p.K == 128 ? chunks_pick<bf16, 128>(out, cols, p, segs, st) : chunks_pick<bf16, 64>(out, cols, p, segs, st);
-    return p.K == 128 ? chunks_pick<float, 128>(out, cols, p, segs, st) : chunks_pick<float, 64>(out, cols, p, segs, st);
+    if (dtype == 1)
+        return a.p[0].K == 128 ? chunks_pick<bf16, 128>(pass, cols, a, n, segs, st) : chunks_pick<bf16, 64>(pass, cols, a, n, segs, st);
+    return a.p[0].K == 128 ? chunks_pick<float, 128>(pass, cols, a, n, segs, st) : chunks_pick<float, 64>(pass, cols, a, n, segs, st);
 }
 
-hipError_t launch_ssm_combine(const SsmParams& p, float* d_s0, hipStream_t st) {
-    const size_t n = (size_t)p.H * p.K * p.P / 4;
-    hipLaunchKernelGGL(kda_ssm_combine_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, p, d_s0);
+hipError_t launch_ssm_combine(const SsmPair& a, int n, hipStream_t st) {
+    const size_t values = (size_t)a.p[0].H * a.p[0].K * a.p[0].P / 4;
+    hipLaunchKernelGGL(kda_ssm_combine_kernel, dim3((unsigned)((values + 255) / 256), (unsigned)n), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 

@@ -97,13 +97,8 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     ChunkWalk at;
     at.init(f, ci);
     const int t0 = at.t0(), len = at.len();
-    const bool first = at.first(), last = at.last();
-    auto start_of = [&](int h) {
-        return first ? (f.s0 ? f.s0 + ((size_t)at.seq * f.H + h) * KP : nullptr) : p.start + ((size_t)ci * f.H + h) * KP;
-    };
-    auto dend_of = [&](int h) {
-        return last ? (f.sT ? f.sT + ((size_t)at.seq * f.H + h) * KP : nullptr) : p.dend + ((size_t)ci * f.H + h) * KP;
-    };
+    auto start_of = [&](int h) { return p.start + ((size_t)ci * f.H + h) * KP; };
+    auto dend_of = [&](int h) { return p.dend + ((size_t)ci * f.H + h) * KP; };
 
     // ---- a head's rows, states and gates: loads, then LDS
     uint4 rx[PX], rg[PX], rs[PS], re[PS], rgate;
@@ -119,9 +114,7 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
             rg[i] = buf_load16(gr, (unsigned)(row * f.H * P + col) * sizeof(T));
         }
         if constexpr (STAGED) {
-            // a missing state is zeros: a resource of no bytes
-            const float *sp = start_of(h), *ep = dend_of(h);
-            const auto sr = make_rsrc_n(sp, sp ? KP * 4 : 0), er = make_rsrc_n(ep, ep ? KP * 4 : 0);
+            const auto sr = make_rsrc_n(start_of(h), KP * 4), er = make_rsrc_n(dend_of(h), KP * 4);
 #pragma unroll
             for (int i = 0; i < PS; ++i) {
                 rs[i] = buf_load16(sr, 16u * (unsigned)(td + TH * i));
@@ -327,8 +320,8 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                         v[i] = (is_y ? sS : sE)[n * LDS_ + col + r16];
                     } else {
                         const float* st = is_y ? start : dend;
-                        v[i] = st ? st[(size_t)n * P + col + r16] : 0.f;
-                        if (!is_y && start) se = fmaf(v[i], start[(size_t)n * P + col + r16], se);
+                        v[i] = st[(size_t)n * P + col + r16];
+                        if (!is_y) se = fmaf(v[i], start[(size_t)n * P + col + r16], se);
                     }
                 }
                 const auto vf = Exact<T>::of(v);
@@ -376,7 +369,6 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
         for (int k = 0; k < TK; ++k) {
             const bool is_c = K == 128 ? k == 0 : w < 4;
             const float* st = is_c ? start : dend;
-            if (!st) continue;
             const T* tok = is_c ? sDY : sX;
             Frag sf[P / 32];
 #pragma unroll
