@@ -162,9 +162,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
     const T* xbase = reinterpret_cast<const T*>(p.x) + h0 * P;
     const T* bbase = reinterpret_cast<const T*>(p.B) + grp * K;
     const T* cbase = reinterpret_cast<const T*>(p.C) + grp * K;
-    float dskip[NH];
-#pragma unroll
-    for (int k = 0; k < NH; ++k) dskip[k] = OUT && p.Dskip ? p.Dskip[h0 + k] : 0.f;
+    const bool skips = OUT && p.Dskip;
+    const float dskip = skips ? p.Dskip[h] : 0.f;
     uint4 rb[PK], rx[PX], rc[OUT ? PK : 1];
     uint4 rg;
     constexpr int PG = NH * kGates * C / 4;     // 16-byte pieces of a chunk's gates
@@ -254,10 +253,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
             // registers across the loop they spill
             const int ln = opaque(lane), g = ln >> 4, r16 = ln & 15;
             // ---- scores, transposed: a lane gets four tokens j of one row i.
-            // On the diagonal each pair takes its own decay (and i = j the skip
-            // weight D: it multiplies the same x_i); below it the decay is the
-            // product of j's to the end of its tile and i's from there on, both
-            // at most 1, so one exponential a lane does.
+            // On the diagonal each pair takes its own decay; below it the decay is
+            // the product of j's to the end of its tile and i's from there on,
+            // both at most 1, so one exponential a lane does.
             auto score = [&](int ti, int tj) {
                 f32x4 acc{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -296,7 +294,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
                         float d = ci - cj[e];
                         if constexpr (sizeof(T) == 4) d += s_gate[k][kGateRest][i] - s_gate[k][kGateRest][j0 + e];
                         v[e] = j0 + e <= i ? acc[e] * fast_exp2(d) * dj[e] : 0.f;
-                        if (j0 + e == i) v[e] += dskip[k];
                     }
                     put(k, t, t, v);
                 }
@@ -402,13 +399,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
             }
         }
         if constexpr (OUT) {
-            // y takes the place of x, whose columns only this wave reads
+            // y, with D x in fp32 (of a short or fast decaying sequence the
+            // largest part), takes the place of x, whose columns only this wave
+            // reads
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float o[4] = {Y[ti][n][0], Y[ti][n][1], Y[ti][n][2], Y[ti][n][3]};
-                    st_run<4>(sX + (16 * ti + r16) * LDX + col0 + 16 * n + 4 * g, o);
+                    T* at = sX + (16 * ti + r16) * LDX + col0 + 16 * n + 4 * g;
+                    f32x4 v = Y[ti][n];
+                    if (skips) v += ld4_as_f32<T>(at) * dskip;
+                    float o[4] = {v[0], v[1], v[2], v[3]};
+                    st_run<4>(at, o);
                 }
         }
         if (closes && p.sT && !summary) store_state(p.sT + ((size_t)seq * p.H + h) * KP);
@@ -423,23 +425,25 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
 
 // Segment start states from the segments' local states and decays, written
 // over the local states: start_{j+1} = decay_j start_j + local_j (local_j
-// alone where a sequence starts in segment j).  A thread owns four state
-// values of a head and keeps sixteen segments' loads in flight.  Bound by
-// memory: 64 MiB in 14 us for 32 segments of 32 heads.
+// alone where a sequence starts in segment j).  A thread owns V state values of
+// a head and has 32 segments' loads in flight, so a call of up to 33 segments
+// waits for memory once.  V = 2 where that still fills the card (8K x 32
+// heads, both recurrences: 12 us against 17 us), else 1 (13K tokens x 5 heads
+// of 64 x 64: 9 us against 13 us).
+template <int V>
 __global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmPair a) {
+    typedef float vec __attribute__((ext_vector_type(V)));
     const SsmParams& p = a.p[blockIdx.y];
-    const size_t kp4 = (size_t)p.K * p.P / 4;
-    const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (at >= (size_t)p.H * kp4) return;
-    const int h = (int)(at / kp4);
-    float4* L = reinterpret_cast<float4*>(p.seg_state) + at;
-    const size_t step = (size_t)p.H * kp4;
+    const unsigned kp = (unsigned)(p.K * p.P);              // a multiple of a block's 256 V
+    const unsigned h = blockIdx.x / (kp / (256 * V));
+    vec* L = reinterpret_cast<vec*>(p.seg_state) + (size_t)blockIdx.x * 256 + threadIdx.x;
+    const size_t step = (size_t)p.H * kp / V;
     // segments that hold chunks (a packed call may have fewer than its bound)
     const int all = total_chunks(p), n_seg = min(p.n_seg, (all + p.cps - 1) / p.cps);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int U = 16;
+    vec s = (vec)(0.f);
+    constexpr int U = 32;
     for (int j = 0; j < n_seg; j += U) {
-        float4 l[U];
+        vec l[U];
         float d[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -453,13 +457,7 @@ __global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmPair a) {
             if (j + u < n_seg) {
                 const int k = p.reverse ? n_seg - 1 - (j + u) : j + u;
                 L[(size_t)k * step] = s;
-                if (j + u < n_seg - 1) {
-                    if (d[u] < 0.f)
-                        s = l[u];
-                    else
-                        s = make_float4(fmaf(d[u], s.x, l[u].x), fmaf(d[u], s.y, l[u].y), fmaf(d[u], s.z, l[u].z),
-                                        fmaf(d[u], s.w, l[u].w));
-                }
+                if (j + u < n_seg - 1) s = d[u] < 0.f ? l[u] : d[u] * s + l[u];
             }
         }
     }
@@ -620,8 +618,11 @@ hipError_t launch_ssm_chunks(int dtype, SsmPass pass, int cols, const SsmPair& a
 }
 
 hipError_t launch_ssm_combine(const SsmPair& a, int n, hipStream_t st) {
-    const size_t values = (size_t)a.p[0].H * a.p[0].K * a.p[0].P / 4;
-    hipLaunchKernelGGL(kda_ssm_combine_kernel, dim3((unsigned)((values + 255) / 256), (unsigned)n), dim3(256), 0, st, a);
+    const size_t values = (size_t)a.p[0].H * a.p[0].K * a.p[0].P;
+    if (values >= (1u << 16))
+        hipLaunchKernelGGL(kda_ssm_combine_kernel<2>, dim3((unsigned)(values / 512), (unsigned)n), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL(kda_ssm_combine_kernel<1>, dim3((unsigned)(values / 256), (unsigned)n), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 

@@ -27,10 +27,21 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _device(x: torch.Tensor) -> torch.device:
-    if x.device.type != "cuda":
+def _device(x: torch.Tensor) -> int:
+    """The GPU's index.  (The checks compare indices and let torch make outputs
+    like their inputs: on one-token calls the host's steps are what counts.)"""
+    if not x.is_cuda:
         raise ValueError("the mixer operators run on the GPU, got a tensor on %s" % x.device)
-    return x.device
+    return x.get_device()
+
+
+def _like(x: torch.Tensor) -> torch.Tensor:
+    """A new contiguous tensor of x's shape and dtype."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
+def _f32(dev: int, *shape) -> torch.Tensor:
+    return torch.empty(shape, dtype=torch.float32, device=dev)
 
 
 def _act(name) -> int:
@@ -40,12 +51,12 @@ def _act(name) -> int:
         raise ValueError("activation is None, 'silu' or 'sigmoid', got %r" % (name,)) from None
 
 
-def _call(name: str, dev: torch.device, *args):
-    """The C call on dev and its current stream."""
+def _call(name: str, dev: int, *args):
+    """The C call on GPU dev and its current stream."""
     fn = getattr(_k.load_library(), name)
     # the raw handle: a Stream object would cost as much as a small launch
-    stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    if dev.index != torch.cuda.current_device():
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             st = fn(*args, stream)
     else:
@@ -61,11 +72,11 @@ def _size(name: str, *args) -> int:
     return int(n)
 
 
-def _workspace(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
+def _workspace(workspace: Optional[torch.Tensor], need: int, dev: int):
     """The caller's workspace if it is large enough, else a new one; and its bytes."""
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous on %s" % dev)
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous on cuda:%d" % dev)
         have = workspace.numel() * workspace.element_size()
         if have >= need:
             return workspace, have
@@ -74,27 +85,28 @@ def _workspace(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
     return torch.empty(need, dtype=torch.uint8, device=dev), need
 
 
-def _check(t: torch.Tensor, name: str, shape, dtype, dev):
-    if t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous():
-        return
-    if t.device != dev:
-        raise ValueError("%s must be on %s" % (name, dev))
+def _refuse(t: torch.Tensor, name: str, shape, dtype, dev: int):
+    """What is wrong with a tensor, in the order the checks name it."""
+    if t.get_device() != dev:
+        raise ValueError("%s must be on cuda:%d" % (name, dev))
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype != dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+
+
+def _check(t: torch.Tensor, name: str, shape, dtype, dev: int):
+    if t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.get_device() == dev:
+        return
+    _refuse(t, name, shape, dtype, dev)
     raise ValueError("%s must be contiguous" % name)
 
 
-def _rows(t: torch.Tensor, name: str, shape, lead: int, dtype, dev) -> int:
+def _rows(t: torch.Tensor, name: str, shape, lead: int, dtype, dev: int) -> int:
     """Checks a token tensor whose first `lead` dimensions count tokens;
     returns the elements between its token rows."""
-    if t.device != dev:
-        raise ValueError("%s must be on %s" % (name, dev))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype != dtype:
-        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        _refuse(t, name, shape, dtype, dev)
     width = 1
     for n in shape[lead:]:
         width *= n
@@ -127,7 +139,7 @@ def _seqs(x: torch.Tensor, cu_seqlens: Optional[torch.Tensor], lead: int):
         return x.shape[0], x.shape[1]
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or cu_seqlens.dtype != torch.int32:
         raise ValueError("cu_seqlens must be int32 [N + 1]")
-    if cu_seqlens.device != x.device or not cu_seqlens.is_contiguous():
+    if cu_seqlens.get_device() != x.get_device() or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be contiguous on %s" % x.device)
     return cu_seqlens.numel() - 1, x.shape[0]
 
@@ -167,7 +179,7 @@ def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     dev, N, T, D, W, code, stride = _conv_args(x, weight, bias, initial_state, cu_seqlens)
     act = _act(activation)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = _like(x)
     else:
         _check(out, "out", x.shape, x.dtype, dev)
     if final_state is not None:
@@ -194,11 +206,11 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     if d_final_state is not None:
         _check(d_final_state, "d_final_state", (N, W - 1, D), x.dtype, dev)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = _like(x)
     else:
         _check(dx, "dx", x.shape, x.dtype, dev)
-    dw = torch.empty((D, W), dtype=torch.float32, device=dev)
-    db = torch.empty((D,), dtype=torch.float32, device=dev) if bias is not None else None
+    dw = _f32(dev, D, W)
+    db = _f32(dev, D) if bias is not None else None
     if want_d_initial_state is None:
         want_d_initial_state = initial_state is not None
     ds = torch.empty((N, W - 1, D), dtype=x.dtype, device=dev) if want_d_initial_state else None
@@ -225,7 +237,7 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.
         _check(bias, "bias", (D,), torch.float32, dev)
     _check(state, "state", (N, W - 1, D), x.dtype, dev)
     if out is None:
-        out = torch.empty((N, D), dtype=x.dtype, device=dev)
+        out = _like(x)
     else:
         _check(out, "out", (N, D), x.dtype, dev)
     _call("kda_short_conv_step", dev, N, D, W, _dtype_code(x.dtype), act, _p(x), stride, _p(weight), _p(bias),
@@ -277,13 +289,13 @@ def selective_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     if initial_state is not None:
         _check(initial_state, "initial_state", (N, H, K, P), torch.float32, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = _like(x)
     else:
         _check(out, "out", x.shape, x.dtype, dev)
     if final_state is not None:
         _check(final_state, "final_state", (N, H, K, P), torch.float32, dev)
     elif output_final_state:
-        final_state = torch.empty((N, H, K, P), dtype=torch.float32, device=dev)
+        final_state = _f32(dev, N, H, K, P)
     need = _size("kda_selective_scan_fwd_workspace_size", N, int(cu_seqlens is not None), T, H, G, K, P, code)
     workspace, have = _workspace(workspace, need, dev)
     _call("kda_selective_scan_fwd", dev, N, _p(cu_seqlens), T, H, G, K, P, code, int(bool(dt_softplus)), _p(x), xs,
@@ -326,12 +338,12 @@ def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     dB, dbs = _out_rows(dB, "dB", B.shape, lead, ty, dev)
     dC, dcs = _out_rows(dC, "dC", B.shape, lead, ty, dev)
     ddt = torch.empty(x.shape[:-1], dtype=ty, device=dev)
-    dA = torch.empty((H,), dtype=torch.float32, device=dev)
-    dD = torch.empty((H,), dtype=torch.float32, device=dev) if D is not None else None
-    dbias = torch.empty((H,), dtype=torch.float32, device=dev) if dt_bias is not None else None
+    dA = _f32(dev, H)
+    dD = _f32(dev, H) if D is not None else None
+    dbias = _f32(dev, H) if dt_bias is not None else None
     if want_d_initial_state is None:
         want_d_initial_state = initial_state is not None
-    ds0 = torch.empty((N, H, K, P), dtype=torch.float32, device=dev) if want_d_initial_state else None
+    ds0 = _f32(dev, N, H, K, P) if want_d_initial_state else None
     need = _size("kda_selective_scan_bwd_workspace_size", N, int(cu_seqlens is not None), T, H, G, K, P, code)
     workspace, have = _workspace(workspace, need, dev)
     _call("kda_selective_scan_bwd", dev, N, _p(cu_seqlens), T, H, G, K, P, code, int(bool(dt_softplus)), _p(x), xs,
@@ -351,7 +363,7 @@ def selective_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: t
     N = x.shape[0]
     _check(state, "state", (N, H, K, P), torch.float32, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = _like(x)
     else:
         _check(out, "out", x.shape, x.dtype, dev)
     _call("kda_selective_scan_step", dev, N, H, G, K, P, code, int(bool(dt_softplus)), _p(x), xs, _p(dt), ds, _p(A),
@@ -390,7 +402,7 @@ def group_norm_fwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
     dev, rows, C, code, xs, zs = _norm_args(x, groups, weight, bias, gate)
     act = _act(activation)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = _like(x)
     else:
         _check(out, "out", x.shape, x.dtype, dev)
     _call("kda_group_norm_fwd", dev, rows, C, int(groups), code, act, int(bool(center)), int(bool(gate_first)),
@@ -407,10 +419,10 @@ def group_norm_bwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor],
     dev, rows, C, code, xs, zs = _norm_args(x, groups, weight, bias, gate)
     act = _act(activation)
     _check(d_y, "d_y", x.shape, x.dtype, dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dz = torch.empty(x.shape, dtype=x.dtype, device=dev) if gate is not None else None
-    dw = torch.empty((C,), dtype=torch.float32, device=dev) if weight is not None else None
-    db = torch.empty((C,), dtype=torch.float32, device=dev) if bias is not None else None
+    dx = _like(x)
+    dz = _like(x) if gate is not None else None
+    dw = _f32(dev, C) if weight is not None else None
+    db = _f32(dev, C) if bias is not None else None
     need = 0
     if dw is not None or db is not None:
         need = _size("kda_group_norm_bwd_workspace_size", rows, C, int(groups), code)

@@ -183,7 +183,7 @@ def test_binding_refuses_before_the_call():
         kda.group_norm_fwd(x, 1)
     with pytest.raises(ValueError, match="activation"):
         mixer._act("relu")
-    rows = lambda t, lead: mixer._rows(t, "x", t.shape, lead, t.dtype, t.device)
+    rows = lambda t, lead: mixer._rows(t, "x", t.shape, lead, t.dtype, t.get_device())
     t = torch.zeros(3, 5, 4, 8)
     assert rows(t, 2) == 32
     assert rows(t[:, :, :2], 2) == 32                       # a slice of each token's row
