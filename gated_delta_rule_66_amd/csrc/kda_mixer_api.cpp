@@ -24,10 +24,6 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y ? y - x < na : x - y < nb;
 }
-// bytes from the first to the last element of `rows` rows of `width` elements
-size_t extent(long long rows, long long stride, long long width, size_t es) {
-    return rows > 0 ? (size_t)((rows - 1) * stride + width) * es : 0;
-}
 // The bytes a tensor's token rows take: `rows` rows of `width` bytes, `stride`
 // bytes apart.
 struct Span {
@@ -49,6 +45,16 @@ bool overlap(const Span& a, const Span& b) {
     return true;
 }
 Span flat_span(const void* p, size_t bytes) { return Span{p, 1, (long long)bytes, (long long)bytes}; }
+// an output shares a byte with an input or with another output
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span& in : ins)
+            if (overlap(*o, in)) return true;
+        for (const Span* other = outs.begin(); other != o; ++other)
+            if (overlap(*o, *other)) return true;
+    }
+    return false;
+}
 // tokens of a call; row indices are int in the kernels
 bool token_count(const int* cu, int N, int T, long long* M) {
     *M = cu ? (long long)T : (long long)N * T;
@@ -68,7 +74,7 @@ bool vec_ok(kda_dtype dt, long long width, long long stride, const void* p) {
 kda_status conv_sizes(int N, int T, int D, int W, kda_dtype dt, kda_activation act, const int* cu, long long* M) {
     if (N < 0 || T < 0 || D < 0 || !dtype_ok(dt) || !act_ok(act)) return KDA_ERR_INVALID_ARG;
     if (W < 2 || W > 4) return KDA_ERR_UNSUPPORTED;
-    if (!token_count(cu, N, T, M) || (long long)N * (W - 1) > 2147483647LL || D > (1 << 22)) return KDA_ERR_UNSUPPORTED;
+    if (!token_count(cu, N, T, M) || (long long)N * (W - 1) > 2147483647LL || D > (1 << 21)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -130,9 +136,10 @@ kda_status kda_short_conv_fwd(int N, const int* cu_seqlens, int T, int D, int W,
     if (M > 0 && (!x || !y || x_stride < D)) return KDA_ERR_INVALID_ARG;
     for (const void* t : {x, initial_state, (const void*)y, (const void*)final_state})
         if (!aligned(t, es)) return KDA_ERR_INVALID_ARG;
-    const size_t state = (size_t)N * (W - 1) * D * es, xb = extent(M, x_stride, D, es), yb = (size_t)M * D * es;
-    if (overlap(x, xb, y, yb) || overlap(initial_state, state, final_state, state) || overlap(x, xb, final_state, state) ||
-        overlap(initial_state, state, y, yb))
+    const long long le = (long long)es, row = D * le;
+    const size_t state = (size_t)N * (W - 1) * D * es, par = (size_t)D * sizeof(float);
+    if (clash({{y, M, row, row}, flat_span(final_state, state)},
+              {{x, M, x_stride * le, row}, flat_span(initial_state, state), flat_span(weight, W * par), flat_span(bias, par)}))
         return KDA_ERR_INVALID_ARG;
     if (M == 0 && !final_state) return KDA_OK;
     ConvParams p{};
@@ -150,8 +157,10 @@ kda_status kda_short_conv_fwd(int N, const int* cu_seqlens, int T, int D, int W,
     const long long work = M * (D / V);
     conv_tiles(p, M, work >= (1LL << 23) ? 32 : work >= (1LL << 21) ? 16 : 8);
     const int tys = 256 >> p.cx_log2;
-    // one more row of blocks passes on the states of sequences without tokens
-    const int blocks = (p.tiles + tys - 1) / tys + (final_state && (cu_seqlens || T == 0) ? 1 : 0);
+    // blocks of their own pass on the states of sequences without tokens, at
+    // most 64 sequences a thread
+    const int pass = final_state && (cu_seqlens || T == 0) ? (N + 64 * tys - 1) / (64 * tys) : 0;
+    const int blocks = (p.tiles + tys - 1) / tys + pass;
     if (blocks == 0) return KDA_OK;
     if ((long long)blocks * 256 >= 1LL << 32) return KDA_ERR_UNSUPPORTED;
     KDA_LAUNCH("short_conv", launch_conv_fwd((int)dt, vec, p, blocks, stream));
@@ -186,10 +195,11 @@ kda_status kda_short_conv_bwd(int N, const int* cu_seqlens, int T, int D, int W,
     for (const void* t : {x, initial_state, d_y, d_final_state, (const void*)dx, (const void*)d_initial_state})
         if (!aligned(t, es)) return KDA_ERR_INVALID_ARG;
     if (!aligned(workspace, 16)) return KDA_ERR_INVALID_ARG;
-    const size_t state = (size_t)N * (W - 1) * D * es, xb = extent(M, x_stride, D, es), yb = (size_t)M * D * es;
-    if (overlap(x, xb, dx, yb) || overlap(d_y, yb, dx, yb) || overlap(d_final_state, state, d_initial_state, state) ||
-        overlap(initial_state, state, d_initial_state, state) || overlap(initial_state, state, dx, yb) ||
-        overlap(d_final_state, state, dx, yb))
+    const long long le = (long long)es, row = D * le;
+    const size_t state = (size_t)N * (W - 1) * D * es, par = (size_t)D * sizeof(float);
+    if (clash({{dx, M, row, row}, flat_span(d_initial_state, state), flat_span(dweight, W * par), flat_span(dbias, par)},
+              {{x, M, x_stride * le, row}, {d_y, M, row, row}, flat_span(initial_state, state),
+               flat_span(d_final_state, state), flat_span(weight, W * par), flat_span(bias, par)}))
         return KDA_ERR_INVALID_ARG;
     if (N == 0) {
         KDA_LAUNCH("short_conv_bwd_sums", launch_sum_rows(nullptr, 0, W + 1, D, dweight, W, dbias, stream));
@@ -226,8 +236,11 @@ kda_status kda_short_conv_step(int N, int D, int W, kda_dtype dt, kda_activation
     if (!x || !weight || !state || !y || x_stride < D || !aligned(weight, 4) || !aligned(bias, 4)) return KDA_ERR_INVALID_ARG;
     for (const void* t : {x, (const void*)state, (const void*)y})
         if (!aligned(t, es)) return KDA_ERR_INVALID_ARG;
-    const size_t sb = (size_t)N * (W - 1) * D * es, xb = extent(N, x_stride, D, es), yb = (size_t)N * D * es;
-    if (overlap(x, xb, state, sb) || overlap(x, xb, y, yb) || overlap(state, sb, y, yb)) return KDA_ERR_INVALID_ARG;
+    const long long le = (long long)es, row = D * le;
+    const size_t par = (size_t)D * sizeof(float);
+    if (clash({{y, N, row, row}, flat_span(state, (size_t)N * (W - 1) * D * es)},
+              {{x, N, x_stride * le, row}, flat_span(weight, W * par), flat_span(bias, par)}))
+        return KDA_ERR_INVALID_ARG;
     const bool vec = vec_ok(dt, D, N > 1 ? x_stride : D, x) && aligned(state, 16) && aligned(y, 16);
     if ((long long)N * D / (vec ? (long long)(16 / es) : 1) >= (1LL << 32) - 256) return KDA_ERR_UNSUPPORTED;
     KDA_LAUNCH("short_conv_step", launch_conv_step((int)dt, vec, N, D, W, (int)act, x, (size_t)x_stride, weight, bias,
@@ -246,7 +259,7 @@ static kda_status norm_check(int rows, int C, int groups, kda_dtype dt, kda_acti
     if (!norm_variant((int)dt, false, C / groups, &R, &team, &block) &&
         !(norm_variant((int)dt, true, C / groups, &R, &team, &block) && (C / groups) % (16 / esize(dt)) == 0))
         return KDA_ERR_UNSUPPORTED;
-    if ((long long)rows * groups > 2147483647LL) return KDA_ERR_UNSUPPORTED;
+    if ((long long)rows * groups > 2147483647LL || groups > 65535) return KDA_ERR_UNSUPPORTED;
     if (!aligned(weight, 4) || !aligned(bias, 4) || !aligned(x, esize(dt)) || !aligned(gate, esize(dt)))
         return KDA_ERR_INVALID_ARG;
     if (rows > 0 && (!x || x_stride < C || (gate && gate_stride < C))) return KDA_ERR_INVALID_ARG;
@@ -277,11 +290,14 @@ kda_status kda_group_norm_fwd(int rows, int C, int groups, kda_dtype dt, kda_act
     if (rows == 0) return KDA_OK;
     const size_t es = esize(dt);
     if (!y || !aligned(y, es)) return KDA_ERR_INVALID_ARG;
-    // a value is read before it is written only by its own team: y may be x or
-    // the gate exactly, not partly
-    const size_t yb = (size_t)rows * C * es, xb = extent(rows, x_stride, C, es);
-    if ((overlap(x, xb, y, yb) && !(x == y && (rows == 1 || x_stride == C))) ||
-        (gate && overlap(gate, extent(rows, gate_stride, C, es), y, yb) && !(gate == y && (rows == 1 || gate_stride == C))))
+    // every value is read by the team that writes its place: y may be x or the
+    // gate exactly, not partly
+    const long long le = (long long)es, row = C * le;
+    const size_t par = (size_t)C * sizeof(float);
+    const bool as_x = x == y && (rows == 1 || x_stride == C), as_z = gate == y && (rows == 1 || gate_stride == C);
+    if (clash({{y, rows, row, row}}, {{as_x ? nullptr : x, rows, x_stride * le, row},
+                                      {as_z ? nullptr : gate, rows, gate_stride * le, row},
+                                      flat_span(weight, par), flat_span(bias, par)}))
         return KDA_ERR_INVALID_ARG;
     bool vec = vec_ok(dt, C / groups, rows > 1 ? x_stride : C, x) && aligned(y, 16);
     if (gate) vec = vec && vec_ok(dt, C / groups, rows > 1 ? gate_stride : C, gate);
@@ -335,13 +351,12 @@ kda_status kda_group_norm_bwd(int rows, int C, int groups, kda_dtype dt, kda_act
         if (!aligned(t, es)) return KDA_ERR_INVALID_ARG;
     if (!aligned(dweight, 4) || !aligned(dbias, 4) || !aligned(workspace, 16)) return KDA_ERR_INVALID_ARG;
     if (rows > 0 && (!d_y || !dx || (gate != nullptr) != (d_gate != nullptr))) return KDA_ERR_INVALID_ARG;
-    const size_t yb = (size_t)rows * C * es, xb = extent(rows, x_stride, C, es),
-                 zb = gate ? extent(rows, gate_stride, C, es) : 0;
-    // the outputs are written while other rows are still to be read
-    for (const void* o : {(const void*)dx, (const void*)d_gate})
-        if (overlap(o, o ? yb : 0, x, xb) || overlap(o, o ? yb : 0, gate, zb) || overlap(o, o ? yb : 0, d_y, yb))
-            return KDA_ERR_INVALID_ARG;
-    if (overlap(dx, yb, d_gate, d_gate ? yb : 0)) return KDA_ERR_INVALID_ARG;
+    const long long le = (long long)es, row = C * le;
+    const size_t par = (size_t)C * sizeof(float);
+    if (clash({{dx, rows, row, row}, {d_gate, rows, row, row}, flat_span(dweight, par), flat_span(dbias, par)},
+              {{x, rows, x_stride * le, row}, {gate, rows, gate_stride * le, row}, {d_y, rows, row, row},
+               flat_span(weight, par), flat_span(bias, par)}))
+        return KDA_ERR_INVALID_ARG;
     const bool sums = dweight || dbias;
     if (sums && rows > 0 &&
         (!workspace || workspace_bytes < kda_group_norm_bwd_workspace_size(rows, C, groups, dt)))
@@ -376,7 +391,7 @@ static kda_status ssm_sizes(int N, const int* cu, int T, int H, int G, int K, in
     if (!(K == 64 || K == 128) || !(P == 64 || P == 128)) return KDA_ERR_UNSUPPORTED;
     if (!token_count(cu, N, T, M)) return KDA_ERR_UNSUPPORTED;
     // chunk and workgroup counts stay within int
-    if (*M / 64 + N > 1 << 26 || (long long)H * K * P > 1LL << 30 || (long long)N * H * (P / 64) >= 1 << 24) return KDA_ERR_UNSUPPORTED;
+    if (*M / 64 + N > 1 << 26 || (long long)H * K * P > 1LL << 30 || (*M / 64 + N) * H >= 1LL << 27 || (long long)N * H * (P / 64) >= 1 << 24) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -465,13 +480,13 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
     if (!aligned(cu_seqlens, 4) || !aligned(workspace, 16) || !aligned(final_state, 16) || !aligned(y, 16))
         return KDA_ERR_INVALID_ARG;
     if (M > 0 && !y) return KDA_ERR_INVALID_ARG;
-    const size_t es = esize(dt), state = (size_t)N * H * K * P * sizeof(float), yb = (size_t)M * H * P * es;
-    const size_t xb = extent(M, x_stride, (long long)H * P, es), bb = extent(M, b_stride, (long long)G * K, es),
-                 cb = extent(M, c_stride, (long long)G * K, es);
-    if (overlap(y, yb, x, xb) || overlap(y, yb, B, bb) || overlap(y, yb, C, cb) ||
-        overlap(y, yb, delta, extent(M, delta_stride, H, es)) || overlap(y, yb, initial_state, state))
+    const size_t state = (size_t)N * H * K * P * sizeof(float), par = (size_t)H * sizeof(float);
+    const long long le = (long long)esize(dt), xw = (long long)H * P * le, bw = (long long)G * K * le, dw = H * le;
+    if (clash({{y, M, xw, xw}, flat_span(final_state, state)},
+              {{x, M, x_stride * le, xw}, {B, M, b_stride * le, bw}, {C, M, c_stride * le, bw}, {delta, M, delta_stride * le, dw},
+               flat_span(initial_state == final_state ? nullptr : initial_state, state), flat_span(A, par),
+               flat_span(D, par), flat_span(dt_bias, par)}))
         return KDA_ERR_INVALID_ARG;
-    if (initial_state != final_state && overlap(initial_state, state, final_state, state)) return KDA_ERR_INVALID_ARG;
     const bool packed = cu_seqlens != nullptr;
     const SsmPlan pl = ssm_plan(packed, N, M, T, H, G, P, kScanGroups);
     const SsmLayout L = ssm_layout(packed, N, H, K, P, pl);
@@ -586,24 +601,15 @@ kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, in
         if (dx_stride > 1LL << 23) return KDA_ERR_UNSUPPORTED;
     }
     const long long le = (long long)es;
-    const Span outs[] = {{dx, M, dx_stride * le, (long long)H * P * le},
-                         {dB, M, db_stride * le, (long long)G * K * le},
-                         {dC, M, dc_stride * le, (long long)G * K * le},
-                         flat_span(d_delta, (size_t)M * H * es),
-                         flat_span(d_initial_state, state)};
-    const Span ins[] = {{x, M, x_stride * le, (long long)H * P * le},
-                        {B, M, b_stride * le, (long long)G * K * le},
-                        {C, M, c_stride * le, (long long)G * K * le},
-                        {delta, M, delta_stride * le, H * le},
-                        flat_span(d_y, (size_t)M * H * P * es),
-                        flat_span(initial_state, state),
-                        flat_span(d_final_state, state)};
-    for (int i = 0; i < 5; ++i) {
-        for (const Span& in : ins)
-            if (overlap(outs[i], in)) return KDA_ERR_INVALID_ARG;
-        for (int j = 0; j < i; ++j)
-            if (overlap(outs[i], outs[j])) return KDA_ERR_INVALID_ARG;
-    }
+    const long long xw = (long long)H * P * le, bw = (long long)G * K * le, dw = H * le;
+    const size_t par = (size_t)H * sizeof(float);
+    if (clash({{dx, M, dx_stride * le, xw}, {dB, M, db_stride * le, bw}, {dC, M, dc_stride * le, bw}, {d_delta, M, dw, dw},
+               flat_span(d_initial_state, state), flat_span(dA, par), flat_span(dD, par), flat_span(d_dt_bias, par)},
+              {{x, M, x_stride * le, xw}, {B, M, b_stride * le, bw}, {C, M, c_stride * le, bw}, {delta, M, delta_stride * le, dw},
+               {d_y, M, xw, xw}, flat_span(initial_state, state), flat_span(d_final_state, state), flat_span(A, par),
+               flat_span(D, par), flat_span(dt_bias, par)}))
+        return KDA_ERR_INVALID_ARG;
+    if ((M / 64 + N) * G >= 1LL << 23) return KDA_ERR_UNSUPPORTED;
     if (N == 0) {
         KDA_LAUNCH("scan_bwd_sums", launch_ssm_bwd_sums(nullptr, 0, H, dA, d_dt_bias, dD, stream));
         return KDA_OK;
@@ -684,15 +690,12 @@ kda_status kda_selective_scan_step(int N, int H, int G, int K, int P, kda_dtype 
     s = ssm_pointers(M, H, G, K, P, dt, x, x_stride, delta, delta_stride, A, B, b_stride, C, c_stride, D, dt_bias, state);
     if (s != KDA_OK) return s;
     if (!state || !y || !aligned(y, 16)) return KDA_ERR_INVALID_ARG;
-    const size_t es = esize(dt), sb = (size_t)N * H * K * P * sizeof(float), yb = (size_t)N * H * P * es;
-    const size_t xb = extent(N, x_stride, (long long)H * P, es), bb = extent(N, b_stride, (long long)G * K, es),
-                 cb = extent(N, c_stride, (long long)G * K, es), db = extent(N, delta_stride, H, es);
-    for (const void* o : {(const void*)y, (const void*)state}) {
-        const size_t n = o == y ? yb : sb;
-        if (overlap(o, n, x, xb) || overlap(o, n, B, bb) || overlap(o, n, C, cb) || overlap(o, n, delta, db))
-            return KDA_ERR_INVALID_ARG;
-    }
-    if (overlap(y, yb, state, sb)) return KDA_ERR_INVALID_ARG;
+    const size_t par = (size_t)H * sizeof(float);
+    const long long le = (long long)esize(dt), xw = (long long)H * P * le, bw = (long long)G * K * le, dw = H * le;
+    if (clash({{y, N, xw, xw}, flat_span(state, (size_t)N * H * K * P * sizeof(float))},
+              {{x, N, x_stride * le, xw}, {B, N, b_stride * le, bw}, {C, N, c_stride * le, bw}, {delta, N, delta_stride * le, dw},
+               flat_span(A, par), flat_span(D, par), flat_span(dt_bias, par)}))
+        return KDA_ERR_INVALID_ARG;
     KDA_LAUNCH("scan_step", launch_ssm_step((int)dt, N, H, G, K, P, dt_softplus != 0, x, (size_t)x_stride, delta, (size_t)delta_stride, A, B,
                                             (size_t)b_stride, C, (size_t)c_stride, D, dt_bias, state, y, stream));
     return KDA_OK;

@@ -109,8 +109,8 @@ __device__ __forceinline__ void load_halo(const ConvParams& p, const T* x, int s
     }
 }
 
-// Sequences without tokens: their state passes through.  One block row of the
-// grid behind the tiles, threads over (sequence, channels).
+// Sequences without tokens: their state passes through.  Threads over
+// (sequence, channels), `step` sequences apart.
 template <typename T, int V>
 __device__ __forceinline__ void pass_empty(const SeqView& sv, int W, int D, const void* from, void* to, int first,
                                            int step, int c) {
@@ -136,8 +136,10 @@ __global__ __launch_bounds__(256) void kda_conv_fwd_kernel(ConvParams p) {
     const int c = (blockIdx.y * cx + (threadIdx.x & (cx - 1))) * V;
     const int ty = threadIdx.x >> p.cx_log2, tys = 256 >> p.cx_log2;
     if (c >= p.D) return;
-    if ((int)blockIdx.x >= (p.tiles + tys - 1) / tys) {
-        pass_empty<T, V>(p.sv, W, p.D, p.s0, p.sT, ty, tys, c);
+    const int tile_blocks = (p.tiles + tys - 1) / tys;
+    if ((int)blockIdx.x >= tile_blocks) {
+        pass_empty<T, V>(p.sv, W, p.D, p.s0, p.sT, ((int)blockIdx.x - tile_blocks) * tys + ty,
+                         ((int)gridDim.x - tile_blocks) * tys, c);
         return;
     }
     const int tile = blockIdx.x * tys + ty;
@@ -228,7 +230,7 @@ __global__ __launch_bounds__(256, 3) void kda_conv_bwd_kernel(ConvParams p) {
     const int slots = gridDim.x * tys;
     float wt[W][V], bs[V];
     if (live) load_params<T, V, W>(p, c, wt, bs);
-    if (live && p.d_s0 && blockIdx.x == 0) pass_empty<T, V>(p.sv, W, p.D, p.d_sT, p.d_s0, ty, tys, c);
+    if (live && p.d_s0) pass_empty<T, V>(p.sv, W, p.D, p.d_sT, p.d_s0, blockIdx.x * tys + ty, slots, c);
     for (int tile = blockIdx.x * tys + ty; live && tile < p.tiles; tile += slots) {
         Runs run;
         bool more = true;

@@ -408,8 +408,9 @@ kda_status kda_chunk_bwd(int B, int T, int H, int K, int V, kda_dtype dt,
  *     token rows of an input (at least the row's width), so that a slice of a
  *     wider projection is passed as it is.  Outputs are contiguous unless they
  *     have a stride of their own.
- *   - Outputs must not overlap inputs or each other unless a call says so; a
- *     call that would is KDA_ERR_INVALID_ARG.
+ *   - Outputs must not overlap inputs or each other unless a call says so: a
+ *     shared byte is KDA_ERR_INVALID_ARG (rows of one spacing that keep to
+ *     columns of their own share none).
  *   - All work goes to `stream`; a call may be captured into a graph.  Calls
  *     that run at the same time need workspaces of their own.
  *   - Results are deterministic: parameter gradients are summed in a fixed
@@ -428,7 +429,7 @@ typedef enum kda_activation {
  *
  *   y_t[d] = act( bias[d] + sum_{w < W} weight[d, w] x_{t - (W-1) + w}[d] )
  *
- *   W in {2, 3, 4}; D any.  Sums in fp32, rounded once.
+ *   W in {2, 3, 4}; D up to 2^21.  Sums in fp32, rounded once.
  *   x      : [tokens, D] dt, row stride x_stride
  *   weight : [D, W] fp32;  bias : [D] fp32 or NULL
  *   initial_state : [N, W-1, D] dt, the W - 1 rows before each sequence, or
@@ -547,6 +548,7 @@ kda_status kda_selective_scan_step(int N, int H, int G, int K, int P, kda_dtype 
  *
  *   x, gate : [rows, C] dt, row strides x_stride, gate_stride; gate or NULL
  *   weight, bias : [C] fp32 or NULL (1, 0);  y : [rows, C] dt
+ *   groups at most 65535
  * fp32 inside, rounded once.  y may be x or the gate exactly.  C / groups at
  * most 4096 channels, or 16384 where 16-byte accesses work (C / groups and
  * strides multiples of 16 bytes, pointers 16-byte aligned); wider groups are

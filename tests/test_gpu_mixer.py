@@ -49,6 +49,7 @@ CONV = [
     (0, 0, [1, 1, 1, 200], 33, 3, False, True, "sigmoid"),
     (0, 0, [0, 0], 16, 4, True, True, "silu"),
     (0, 0, [97], 264, 2, True, False, "silu"),
+    (0, 0, [0] * 150 + [3] + [0] * 100 + [1, 9] + [0] * 60, 24, 4, True, True, "silu"),
 ]
 
 
@@ -279,6 +280,7 @@ SCAN = [
     (0, 0, [1, 1, 2, 300], 2, 2, 128, 64, False, True, True),
     (0, 0, [0, 0, 0], 2, 1, 64, 128, True, True, True),
     (3, 0, None, 2, 1, 64, 64, True, True, True),
+    (0, 0, [1, 0, 2] * 110, 2, 1, 64, 64, True, True, True),
 ]
 SCAN_IDS = [str(i) for i in range(len(SCAN))]
 

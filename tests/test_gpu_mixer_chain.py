@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import gated_delta_rule_66_amd as kda
+import mixer_ref as R
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -41,6 +42,24 @@ def token(L, proj, conv_state, state):
     x, B, C = split(L, kda.short_conv_step(u, L["conv"], L["cbias"], conv_state))
     y = kda.selective_scan_step(x, dt, L["A"], B, C, L["D"], L["bias"], state, dt_softplus=True)
     return kda.group_norm_fwd(y.flatten(-2), L["g"], L["norm"], None, z, gate_first=True)
+
+
+def gradients(L, proj, d_out, conv_state, state, cu):
+    """The layer's backward: norm, scan (dx, dB and dC as columns of one
+    buffer), convolution.  Returns d_proj and the parameters' gradients."""
+    d, hp = L["d"], L["h"] * L["p"]
+    u, z, dt = proj[..., :d], proj[..., d:d + hp], proj[..., d + hp:]
+    c, _ = kda.short_conv_fwd(u, L["conv"], L["cbias"], conv_state, cu_seqlens=cu)
+    x, B, C = split(L, c)
+    y, _ = kda.selective_scan_fwd(x, dt, L["A"], B, C, L["D"], L["bias"], state, dt_softplus=True, cu_seqlens=cu)
+    dy, dnorm, _, dz = kda.group_norm_bwd(y.flatten(-2), L["g"], L["norm"], None, z, d_out, gate_first=True)
+    dc = torch.empty_like(c)
+    vx, vB, vC = split(L, dc)
+    _, ddt, dA, _, _, dD, dbias, dstate = kda.selective_scan_bwd(
+        x, dt, L["A"], B, C, L["D"], L["bias"], dy.view(y.shape), state, None, dt_softplus=True, cu_seqlens=cu, dx=vx,
+        dB=vB, dC=vC)
+    du, dw, dcb, dconv = kda.short_conv_bwd(u, L["conv"], L["cbias"], dc, conv_state, None, cu_seqlens=cu)
+    return (torch.cat([du, dz, ddt], -1), dw, dcb, dA, dD, dbias, dnorm, dconv, dstate)
 
 
 def inputs(L, *lead, dtype, seed=0):
@@ -84,6 +103,70 @@ def test_packed_prompts_equal_single_ones(dtype, tol):
         assert rel(y[at:at + m], y1[0]) < tol
         assert torch.equal(cs[i], cs1[0]) and rel(s[i], s1[0]) < 1e-5
         at += m
+
+
+def layer_reference(L, proj, conv_state, state, ranges):
+    d, hp, h, g, k, p = L["d"], L["h"] * L["p"], L["h"], L["g"], L["k"], L["p"]
+    u, z, dt = proj[:, :d], proj[:, d:d + hp], proj[:, d + hp:]
+    c, _ = R.conv(u, L["conv"], L["cbias"], conv_state, ranges, "silu")
+    x, B, C = c[:, :hp].reshape(-1, h, p), c[:, hp:hp + g * k].reshape(-1, g, k), c[:, hp + g * k:].reshape(-1, g, k)
+    y, _ = R.scan(x, dt, L["A"], B, C, L["D"], L["bias"], state, ranges, True)
+    return R.norm(y.reshape(-1, hp), g, L["norm"], None, z, "silu", True, False, 1e-5)
+
+
+def layer_leaves(L, proj, conv_state, state):
+    D = {n: (v.detach().cpu().double().requires_grad_() if isinstance(v, torch.Tensor) else v) for n, v in L.items()}
+    return D, [v.detach().cpu().double().requires_grad_() for v in (proj, conv_state, state)]
+
+
+@pytest.mark.parametrize("dtype,tol", [(torch.float32, 1e-4), (torch.bfloat16, 5e-2)])
+def test_layer_gradients_over_packed_prompts(dtype, tol):
+    # fp32: three operators, each within 2^-19 of its terms' absolute sums, which
+    # pass a gradient's norm by less than 50 here.  bf16: six roundings to half a
+    # step on the way back (c, y, dy, dc, d_proj and the scan's operands), 2^-8
+    # each in the worst case and at random about a fifth of their sum: 6 2^-8 = 2.3e-2,
+    # twice that where they meet the convolution's activation
+    L = layer(5)
+    lens = [65, 0, 3, 90]
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).to(DEV)
+    proj = inputs(L, sum(lens), dtype=dtype)
+    gen = torch.Generator().manual_seed(6)
+    cs = torch.randn(4, L["w"] - 1, L["d"], generator=gen).to(dtype).to(DEV)
+    s = torch.randn(4, L["h"], L["k"], L["p"], generator=gen).to(DEV)
+    d_out = torch.randn(sum(lens), L["h"] * L["p"], generator=gen).to(dtype).to(DEV)
+    got = gradients(L, proj, d_out, cs, s, cu)
+    D, (p64, c64, s64) = layer_leaves(L, proj, cs, s)
+    y = layer_reference(D, p64, c64, s64, R.seqs(4, 0, cu.tolist()))
+    leaves = [p64, D["conv"], D["cbias"], D["A"], D["D"], D["bias"], D["norm"], c64, s64]
+    want = torch.autograd.grad((y * d_out.cpu().double()).sum(), leaves)
+    for name, a, b in zip(("proj", "conv", "cbias", "A", "D", "bias", "norm", "conv_state", "state"), got, want):
+        assert rel(a.cpu(), b) < tol, (name, rel(a.cpu(), b))
+
+
+def test_backward_in_a_graph_replayed():
+    L = layer(7)
+    lens = [130, 70]
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).to(DEV)
+    m = sum(lens)
+    proj, d_out = inputs(L, m, dtype=torch.bfloat16), inputs(L, m, dtype=torch.bfloat16, seed=1)[:, :L["h"] * L["p"]].contiguous()
+    cs = torch.zeros(2, L["w"] - 1, L["d"], dtype=torch.bfloat16, device=DEV)
+    s = torch.zeros(2, L["h"], L["k"], L["p"], device=DEV)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        gradients(L, proj, d_out, cs, s, cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        got = gradients(L, proj, d_out, cs, s, cu)
+    for i in range(3):
+        proj.copy_(inputs(L, m, dtype=torch.bfloat16, seed=40 + i))
+        s.copy_(torch.randn(s.shape, device=DEV))
+        want = gradients(L, proj, d_out, cs, s, cu)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
 
 
 def test_kda_layer_with_convolution_and_gated_norm():
