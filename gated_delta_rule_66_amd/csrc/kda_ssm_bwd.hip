@@ -257,7 +257,9 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
         my_dt = rdt;
         stage(&s_gate[0][0]);
         __syncthreads();
-        if (h + 1 < hb) fetch(h + 1);
+        // the next head's loads: half the waves issue theirs before their pairs,
+        // half behind (all at once queue, and hold up the waves with two tiles)
+        if (h + 1 < hb && w < 4) fetch(h + 1);
         if (NB == 2 && w == 7 && h > ha) step_sizes(h - 1, nb ^ 1, last_dt);
         // ---- pairs of tokens
         float dd = 0.f;
@@ -299,6 +301,7 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
         }
         dd = sum64(dd);
         if (lane == 0) s_dd[w] = dd;
+        if (h + 1 < hb && w >= 4) fetch(h + 1);
         // ---- what passes through the states: U = E^T B or Y = S^T C, columns
         // col + 4 g + e of token 16 t + r16
         f32x4 dx[4];
