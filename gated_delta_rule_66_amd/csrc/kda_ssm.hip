@@ -425,25 +425,22 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
 
 // Segment start states from the segments' local states and decays, written
 // over the local states: start_{j+1} = decay_j start_j + local_j (local_j
-// alone where a sequence starts in segment j).  A thread owns V state values of
-// a head and has 32 segments' loads in flight, so a call of up to 33 segments
-// waits for memory once.  V = 2 where that still fills the card (8K x 32
-// heads, both recurrences: 12 us against 17 us), else 1 (13K tokens x 5 heads
-// of 64 x 64: 9 us against 13 us).
-template <int V>
+// alone where a sequence starts in segment j).  A thread owns four state values
+// of a head and has 32 segments' loads in flight, so a call of up to 33
+// segments waits for memory once (8K x 32 heads, 64 MiB: 12 us; two values a
+// thread 14 us, one 31 us).
 __global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmPair a) {
-    typedef float vec __attribute__((ext_vector_type(V)));
     const SsmParams& p = a.p[blockIdx.y];
-    const unsigned kp = (unsigned)(p.K * p.P);              // a multiple of a block's 256 V
-    const unsigned h = blockIdx.x / (kp / (256 * V));
-    vec* L = reinterpret_cast<vec*>(p.seg_state) + (size_t)blockIdx.x * 256 + threadIdx.x;
-    const size_t step = (size_t)p.H * kp / V;
+    const unsigned kp = (unsigned)(p.K * p.P);              // a multiple of a block's 1024
+    const unsigned h = blockIdx.x / (kp / 1024);
+    f32x4* L = reinterpret_cast<f32x4*>(p.seg_state) + (size_t)blockIdx.x * 256 + threadIdx.x;
+    const size_t step = (size_t)p.H * kp / 4;
     // segments that hold chunks (a packed call may have fewer than its bound)
     const int all = total_chunks(p), n_seg = min(p.n_seg, (all + p.cps - 1) / p.cps);
-    vec s = (vec)(0.f);
+    f32x4 s{0.f, 0.f, 0.f, 0.f};
     constexpr int U = 32;
     for (int j = 0; j < n_seg; j += U) {
-        vec l[U];
+        f32x4 l[U];
         float d[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -619,10 +616,7 @@ hipError_t launch_ssm_chunks(int dtype, SsmPass pass, int cols, const SsmPair& a
 
 hipError_t launch_ssm_combine(const SsmPair& a, int n, hipStream_t st) {
     const size_t values = (size_t)a.p[0].H * a.p[0].K * a.p[0].P;
-    if (values >= (1u << 16))
-        hipLaunchKernelGGL(kda_ssm_combine_kernel<2>, dim3((unsigned)(values / 512), (unsigned)n), dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL(kda_ssm_combine_kernel<1>, dim3((unsigned)(values / 256), (unsigned)n), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(kda_ssm_combine_kernel, dim3((unsigned)(values / 1024), (unsigned)n), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
