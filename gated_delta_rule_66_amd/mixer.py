@@ -20,6 +20,7 @@ import torch
 from . import kda as _k
 from .kda import KDA_OK, KDAError, _dtype_code
 
+_INT_MAX = 2 ** 31 - 1
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "sigmoid": 2}
 
 
@@ -102,11 +103,22 @@ def _check(t: torch.Tensor, name: str, shape, dtype, dev: int):
     raise ValueError("%s must be contiguous" % name)
 
 
+def _fits(shape, lead: int, name: str):
+    """Refuses sizes that the C calls' ints do not hold."""
+    tokens = 1
+    for n in shape[:lead]:
+        tokens *= n
+    if tokens > _INT_MAX or max(shape) > _INT_MAX:
+        raise KDAError(_k.KDA_ERR_UNSUPPORTED, "%s of %d rows" % (name, tokens))
+
+
 def _rows(t: torch.Tensor, name: str, shape, lead: int, dtype, dev: int) -> int:
     """Checks a token tensor whose first `lead` dimensions count tokens;
     returns the elements between its token rows."""
     if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
         _refuse(t, name, shape, dtype, dev)
+    if t.numel() > _INT_MAX:
+        _fits(shape, lead, name)
     width = 1
     for n in shape[lead:]:
         width *= n
@@ -118,21 +130,23 @@ def _rows(t: torch.Tensor, name: str, shape, lead: int, dtype, dev: int) -> int:
         if shape[d] != 1 and stride[d] != inner:
             raise ValueError("%s must be contiguous in its last %d dimensions" % (name, len(shape) - lead))
         inner *= shape[d]
-    row, span = 0, 0        # token stride, and the stride the next outer dimension must have
+    row, span = None, 0     # token stride, and the stride the next outer dimension must have
     for d in range(lead - 1, -1, -1):
         if shape[d] == 1:
             continue
-        if row == 0:
+        if row is None:
             row, span = stride[d], stride[d] * shape[d]
+            if row < width:     # one row for all tokens (an expanded tensor), or rows that overlap
+                raise ValueError("%s must have token rows of its own" % name)
         elif stride[d] != span:
             raise ValueError("%s must have evenly spaced token rows" % name)
         else:
             span *= shape[d]
-    return row or width
+    return width if row is None else row
 
 
 def _seqs(x: torch.Tensor, cu_seqlens: Optional[torch.Tensor], lead: int):
-    """(N, T, tokens) of a call: N sequences of T tokens, or a packed axis of T."""
+    """(N, T) of a call: N sequences of T tokens, or of a packed axis of T."""
     if cu_seqlens is None:
         if x.dim() < lead + 1:
             raise ValueError("x has too few dimensions")

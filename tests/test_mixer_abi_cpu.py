@@ -195,3 +195,18 @@ def test_binding_refuses_before_the_call():
         rows(t[..., :4], 2)
     with pytest.raises(ValueError, match="contiguous"):
         rows(t.transpose(2, 3), 2)
+
+
+def test_binding_refuses_expanded_rows_and_sizes_beyond_int():
+    rows = lambda t, lead: mixer._rows(t, "x", t.shape, lead, t.dtype, t.get_device())
+    one = torch.zeros(1, 8)
+    assert rows(one, 1) == 8
+    for t, lead in ((one.expand(5, 8), 1), (one.expand(1, 5, 8), 2), (one.expand(3, 5, 8), 2),
+                    (torch.zeros(3, 1, 8).expand(3, 5, 8), 2), (torch.zeros(64).as_strided((9, 8), (4, 1)), 1)):
+        with pytest.raises(ValueError, match="rows"):
+            rows(t, lead)
+    far = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device="meta")
+    assert rows(far(2 ** 31 - 1, 2), 1) == 2
+    for t, lead in ((far(2 ** 31, 1), 1), (far(2 ** 20, 2 ** 12, 1), 2), (far(1, 2 ** 32), 1)):
+        with pytest.raises(kda.KDAError):
+            rows(t, lead)
