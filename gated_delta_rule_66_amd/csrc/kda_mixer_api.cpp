@@ -390,8 +390,13 @@ static kda_status ssm_sizes(int N, const int* cu, int T, int H, int G, int K, in
     if (H % G) return KDA_ERR_INVALID_ARG;
     if (!(K == 64 || K == 128) || !(P == 64 || P == 128)) return KDA_ERR_UNSUPPORTED;
     if (!token_count(cu, N, T, M)) return KDA_ERR_UNSUPPORTED;
-    // chunk and workgroup counts stay within int
-    if (*M / 64 + N > 1 << 26 || (long long)H * K * P > 1LL << 30 || (*M / 64 + N) * H >= 1LL << 27 || (long long)N * H * (P / 64) >= 1 << 24) return KDA_ERR_UNSUPPORTED;
+    // chunks and workgroups stay within int, and every launch of 256 threads a
+    // workgroup (gates: eight heads of a chunk; step: 64 columns of a head)
+    // below 2^32 threads
+    const long long chunks = *M / 64 + N;
+    if (chunks >= 1LL << 24 || (long long)H * K * P > 1LL << 30 || chunks * ((H + 7) / 8) >= 1LL << 24 ||
+        (long long)N * H * (P / 64) >= 1LL << 24)
+        return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

@@ -210,3 +210,13 @@ def test_binding_refuses_expanded_rows_and_sizes_beyond_int():
     for t, lead in ((far(2 ** 31, 1), 1), (far(2 ** 20, 2 ** 12, 1), 2), (far(1, 2 ** 32), 1)):
         with pytest.raises(kda.KDAError):
             rows(t, lead)
+
+
+def test_selective_scan_refuses_more_workgroups_than_a_launch_holds():
+    # one-token sequences of one head: the gates' launch has a workgroup a chunk
+    # (without states: they would reach into the made-up buffers behind them)
+    few = dict(t=0, h=1, g=1, ws=None, s0=None, sT=None)
+    assert scan(n=(1 << 24) - 1, **few) == WORKSPACE
+    assert scan(n=1 << 24, **few) == UNSUPPORTED
+    # a long axis of many heads
+    assert scan(n=1, t=1 << 24, h=512, g=512, ws=None) == UNSUPPORTED
