@@ -256,14 +256,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
             // On the diagonal each pair takes its own decay; below it the decay is
             // the product of j's to the end of its tile and i's from there on,
             // both at most 1, so one exponential a lane does.
-            auto score = [&](int ti, int tj) {
-                f32x4 acc{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int m = 0; m < K / 32; ++m)
-                    acc = mma(acc, ld_frag_perm<T>(sB + (16 * tj + r16) * LDB + 32 * m + 4 * g),
-                              ld_frag<T>(sC + (16 * ti + r16) * LDK + 32 * m + 8 * g));
-                return acc;
-            };
+            auto b_frag = [&](int tj, int m) { return ld_frag_perm<T>(sB + (16 * tj + r16) * LDB + 32 * m + 4 * g); };
+            auto c_frag = [&](int ti, int m) { return ld_frag<T>(sC + (16 * ti + r16) * LDK + 32 * m + 8 * g); };
             auto put = [&](int k, int ti, int tj, const float* v) {
                 st_run<4>(sG + (k * C + 16 * ti + r16) * LDG + slot_col(16 * tj + 4 * g), v);
             };
@@ -298,15 +292,28 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
                     put(k, t, t, v);
                 }
             };
-            // tile (w, w), one below it and, in two waves, another: the products
-            // of all first, so that they wait for each other's reads only once
-            const int ti1 = w == 0 ? 1 : w == 3 ? 3 : 2, tj1 = w == 2 ? 1 : 0;
-            const f32x4 a0 = score(w, w), a1 = score(ti1, tj1);
-            f32x4 a2{0.f, 0.f, 0.f, 0.f};
-            if (w < 2) a2 = score(3, 1 + w);
+            // waves 0 to 2 take up to three tiles down from (w, w), which share
+            // B's rows; wave 3 takes (3, 3) and (3, 0), which share C's
+            f32x4 a0{0.f, 0.f, 0.f, 0.f}, a1 = a0, a2 = a0;
+            if (w < 3) {
+#pragma unroll
+                for (int m = 0; m < K / 32; ++m) {
+                    const Frag bf = b_frag(w, m);
+                    a0 = mma(a0, bf, c_frag(w, m));
+                    a1 = mma(a1, bf, c_frag(w + 1, m));
+                    if (w < 2) a2 = mma(a2, bf, c_frag(w + 2, m));
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < K / 32; ++m) {
+                    const Frag cf = c_frag(3, m);
+                    a0 = mma(a0, b_frag(3, m), cf);
+                    a1 = mma(a1, b_frag(0, m), cf);
+                }
+            }
             diagonal(w, a0);
-            below(ti1, tj1, a1);
-            if (w < 2) below(3, 1 + w, a2);
+            below(w < 3 ? w + 1 : 3, w < 3 ? w : 0, a1);
+            if (w < 2) below(w + 2, w, a2);
             {
             const int ln = opaque(lane), g = ln >> 4, r16 = ln & 15;
             // ---- what the start state gives, transposed: a lane holds four
