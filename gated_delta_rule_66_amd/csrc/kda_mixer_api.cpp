@@ -535,8 +535,11 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
 }
 
 // Workgroups of the gradient kernel: one a (chunk, group, part of the group's
-// heads); parts until two workgroups a CU run, since each part beyond the first
-// adds fp32 copies of dB and dC.
+// heads).  One fills a CU's LDS, so they run in rounds of 256; a workgroup costs
+// its heads and about one head more for its start (8K x 32 heads: 256
+// workgroups of 16 heads 145 us, 512 of eight 154 us, 1024 of four 178 us).
+// The parts with the fewest such steps; each beyond the first adds fp32 copies
+// of dB and dC, so no more than four rounds' worth of workgroups from parts.
 struct SsmBwdLayout {
     size_t off, gates, seg, dec, start, dend, sums, part_b, part_c, total;
     int parts, heads_per;
@@ -545,10 +548,19 @@ static SsmBwdLayout ssm_bwd_layout(bool packed, int N, long long M, int H, int G
     SsmBwdLayout L;
     const int hpg = H / G;
     const long long base = (long long)pl.chunks * G;
-    long long parts = base > 0 ? (512 + base - 1) / base : 1;
-    if (parts > hpg) parts = hpg;
-    L.heads_per = (int)((hpg + parts - 1) / parts);
-    L.parts = (hpg + L.heads_per - 1) / L.heads_per;
+    L.parts = 1;
+    L.heads_per = hpg;
+    long long best = -1;
+    for (int per = hpg; per > 0; --per) {
+        const int parts = (hpg + per - 1) / per;
+        if (parts > 1 && base * parts > 1024) break;
+        const long long steps = (base * parts + 255) / 256 * (per + 1);
+        if (best < 0 || steps < best) {
+            best = steps;
+            L.parts = parts;
+            L.heads_per = per;
+        }
+    }
     const size_t states = (size_t)pl.chunks * H * K * P * sizeof(float);
     const size_t part = L.parts > 1 ? (size_t)L.parts * M * G * K * sizeof(float) : 0;
     size_t o = 0;
