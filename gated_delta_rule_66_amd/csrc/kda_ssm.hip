@@ -19,19 +19,10 @@ namespace {
 
 constexpr int C = kSsmChunk;
 
-// One workgroup per (segment, COLS columns of x: one or two heads) walks the
-// segment's chunks with the state in registers: wave w owns columns
-// [16 NT w, 16 NT (w + 1)) of all K state rows, as accumulator tiles that serve
-// as operands as they are.  B, C and x of a chunk are staged in LDS (the next
-// chunk's loads in flight meanwhile); the scores C B^T are computed once for
-// the workgroup's heads, scaled and masked per head, and passed through LDS.
-//   output:  y, and the final state where a sequence ends
-//   summary: each segment's local state and decay
-//   states:  the state before each chunk, and the final state
-// blockIdx.y picks one of two recurrences (the backward runs the states and,
-// with C for B, dy for x and the chunks in reverse, their adjoints).
 // The gates of every chunk and head (kda_ssm_device.h): a wave a head, a lane a
-// token, eight heads a block, whose step sizes share cache lines.
+// token, eight heads a block, whose step sizes share cache lines.  Memory
+// bound: 20 bytes written a token and head (8K x 32 heads 6 us, 8 x 32K x 32
+// heads 57 us, 168 MB).
 template <typename T>
 __global__ __launch_bounds__(256) void kda_ssm_gates_kernel(SsmParams p) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -58,6 +49,36 @@ __global__ __launch_bounds__(256) void kda_ssm_gates_kernel(SsmParams p) {
     }
 }
 
+// One workgroup per (segment, COLS columns of x: one or two heads) walks the
+// segment's chunks with the state in registers: wave w owns columns
+// [16 NT w, 16 NT (w + 1)) of all K state rows, as accumulator tiles that serve
+// as operands as they are.  B, C and x of a chunk are staged in LDS (the next
+// chunk's loads in flight meanwhile); the scores C B^T are computed once for
+// the workgroup's heads, scaled and masked per head, and passed through LDS.
+//   output:  y, and the final state where a sequence ends
+//   summary: each segment's local state and decay
+//   states:  the state before each chunk, and the final state
+// blockIdx.y picks one of two recurrences (the backward runs the states and,
+// with C for B, dy for x and the chunks in reverse, their adjoints).
+//
+// The state is exact to fp32: delta x e^{..} is split into three bf16 for its
+// product with B, two thirds of the output pass's and all of the summary's
+// matrix work.  y, a bf16, takes the state and the scaled scores rounded once
+// (fp32 tensors: fp32 products throughout).
+// What bounds it: nothing alone.  By count, a chunk of two heads (K = 128,
+// P = 64) takes a CU 2400 cycles of matrix instructions in the output pass,
+// 2600 of LDS accesses and about 3000 of vector operations; it takes 9500 with
+// two workgroups a CU.  Left out one at a time, loads, stores, scores or update
+// products save 12 to 15 % each.  The summary: 1500 cycles of matrix
+// instructions and 1600 of vector operations out of 5400; without its loads
+// 424 us instead of 485.  Tried on 8 x 32K x 32 heads: one workgroup a CU
+// 1477 us instead of 1117, and more than two do not fit; eight waves of 16
+// columns as long as four of 32 in all passes (more operands read from LDS);
+// scores kept in registers by each wave 1357 us; y stored from registers, 32
+// bytes a token, 1093 instead of 1072.
+// Measured, K = 128, P = 64: output 8K x 32 heads 41 us, 8 x 32K x 32 heads
+// 1072 us (2.1 GB); summary 22 and 470 us; 2 x 8K x 16 heads of 128: output 69,
+// summary 35 us.
 template <typename T, int K, int P, int COLS, SsmPass PASS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_kernel(SsmPair a) {
     constexpr bool OUT = PASS == kSsmOutput, summary = PASS == kSsmSummary;
@@ -467,6 +488,8 @@ __global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmPair a) {
     }
 }
 
+// The chunk offsets of a packed call: a prefix sum over the sequences' chunks.
+// One block: 4 us, which the host cannot take over without the lengths.
 __global__ __launch_bounds__(256) void kda_ssm_prep_kernel(SeqView sv, int* chunk_off, int max_chunks) {
     __shared__ int buf[256];
     __shared__ int carry;
@@ -503,7 +526,9 @@ __global__ __launch_bounds__(256) void kda_ssm_prep_kernel(SeqView sv, int* chun
 
 // One token of N sequences.  A workgroup takes COLB columns of one (n, head):
 // its state slice is read, decayed, written and dotted with C in one pass
-// (memory bound: 8 bytes a state value).
+// (memory bound: 8 bytes a state value).  256 sequences x 32 heads, K = 128,
+// P = 64 (539 MB): 77 us, 7.0 TB/s, part of the state from the cache behind the
+// L2s; one sequence 3.9 us.
 template <typename T, int K, int COLB>
 __global__ __launch_bounds__(256) void kda_ssm_step_kernel(int H, int G, int P, int softplus, const T* x,
                                                            size_t x_stride, const T* dt, size_t dt_stride, const float* A, const T* B,

@@ -59,6 +59,11 @@ __device__ __forceinline__ float sum64(float v) { return sum_groups(sum16(v)); }
 //            or a tile of each (P = 128); products with exact state operands
 //   dB, dC:  16 state rows of both (K = 128) or of one of them (K = 64) a wave,
 //            summed over the heads in registers
+// A head's rows and states are 80 KB (K = 128, P = 64), which alone take 4 of
+// the 9 us a head, and the LDS holds one workgroup a CU; the rest is the three
+// phases' LDS reads (0.5 MB a head) between barriers.  8K x 32 heads: 145 us
+// (336 MB); four waves with states from memory 314 us, all waves loading the
+// next head at once 166 us.  K = 64, P = 128, 6 heads packed: 64 us.
 template <typename T, int K, int P>
 __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     constexpr int TH = 512;
