@@ -419,8 +419,16 @@ static SsmPlan ssm_plan(bool packed, int N, long long M, int T, int H, int G, in
     pl.chunks_per_seq = T > 0 ? (T + 63) / 64 : 1;
     pl.chunks = packed ? (int)(M / 64 + N) : N * pl.chunks_per_seq;
     const long long units = H / (pl.cols / P);
-    // segments until `workgroups` run, each keeping at least four chunks
+    // Segments until `workgroups` run, each keeping at least four chunks: the
+    // summaries and the combine cost as much as the walk they shorten.  In calls
+    // short enough for the combine to load at most 32 segments at once, two; one
+    // where even that leaves fewer than 128 workgroups.  bf16, K = 128, P = 64,
+    // segments of four, two, one chunks: 512 tokens x 8 heads 45, 31, 25 us;
+    // 1500 x 8 heads 46, 33, 30; 1024 x 32 heads 48, 40, 45; 256 x 32 heads in
+    // one segment 29, in four 26.
     long long want = (workgroups + units - 1) / units, cap = pl.chunks / 4;
+    const long long least = pl.chunks >= 4 && pl.chunks * units < 128 ? 1 : pl.chunks >= 8 ? 2 : 4;
+    if (cap < 32) cap = pl.chunks / least < 32 ? pl.chunks / least : 32;
     if (want > cap) want = cap;
     if (want < 1 || units >= workgroups / 2) want = 1;
     pl.cps = (int)((pl.chunks + want - 1) / want);
