@@ -525,3 +525,15 @@ def test_selective_scan_backward_into_one_buffer_and_padding():
     with pytest.raises(kda.KDAError):
         kda.selective_scan_bwd(x, dt, A, B, C, None, bias, dy, dt_softplus=True, cu_seqlens=cu,
                                dx=buf[:163, :h * p].view(163, h, p), dB=buf[:163, 64:64 + g * k].view(163, g, k))
+
+
+# calls of 16, 8 and 66 chunks: segments of one, two and three chunks
+SEGMENTS = [(1, 1000, None, 4, 1, 128, 64, True, True, True), (1, 500, None, 16, 2, 64, 128, False, True, True),
+            (1, 4200, None, 2, 1, 64, 64, True, True, False), (0, 0, [150, 0, 257, 64, 30], 4, 2, 64, 64, True, True, True)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", SEGMENTS, ids=["one", "two", "three", "packed"])
+def test_selective_scan_segments_of_short_calls(case, dtype):
+    test_selective_scan_forward(case, dtype)
+    test_selective_scan_backward(case, dtype)
