@@ -61,9 +61,9 @@ __device__ __forceinline__ float sum64(float v) { return sum_groups(sum16(v)); }
 //            summed over the heads in registers
 // A head's rows and states are 80 KB (K = 128, P = 64), which alone take 4 of
 // the 9 us a head, and the LDS holds one workgroup a CU; the rest is the three
-// phases' LDS reads (0.5 MB a head) between barriers.  8K x 32 heads: 145 us
+// phases' LDS reads (0.5 MB a head) between barriers.  8K x 32 heads: 148 us
 // (336 MB); four waves with states from memory 314 us, all waves loading the
-// next head at once 166 us.  K = 64, P = 128, 6 heads packed: 64 us.
+// next head at once 166 us.  K = 64, P = 128, 6 heads packed: 65 us.
 template <typename T, int K, int P>
 __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     constexpr int TH = 512;
@@ -204,12 +204,22 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
         auto& s_se = s_se_[nb];
         auto& s_dd = s_dd_[nb];
         const int t = lane >> 4, q = lane & 15;
-        float row = 0.f, cf = 0.f, cs = 0.f;
-        for (int b = 0; b <= t; ++b) row += s_row[t * (t + 1) / 2 + b][q];
-        for (int a = t; a < 4; ++a) {
+        // Pairs across token t (i >= t > j) without pairs that cancel, whose
+        // rounding would stay: of tiles in t's row of tiles the rows from t on,
+        // of those in its column of tiles the columns before t, all of the tiles
+        // behind and before it; only t's own tile takes rows less columns.
+        const int own = t * (t + 1) / 2 + t;
+        const double diag = (double)s_row[own][q] - (double)s_cols[own][q];
+        double left = 0.0, under = 0.0;
+        float cf = s_colf[own][q];
+        for (int b = 0; b < t; ++b) left += (double)s_row[t * (t + 1) / 2 + b][q];
+        for (int a = t + 1; a < 4; ++a) {
             cf += s_colf[a * (a + 1) / 2 + t][q];
-            cs += s_cols[a * (a + 1) / 2 + t][q];
+            under += (double)s_cols[a * (a + 1) / 2 + t][q];
         }
+        // tiles (2, 0), (3, 0) pass token tile 1; (3, 0), (3, 1) pass tile 2
+        const double past = t == 1 ? (double)s_row[3][q] + (double)s_row[6][q]
+                            : t == 2 ? (double)s_row[6][q] + (double)s_row[7][q] : 0.0;
         float zz = 0.f, rr = 0.f, sev = 0.f, ddv = 0.f;
 #pragma unroll
         for (int k = 0; k < P / 16; ++k) {
@@ -224,9 +234,10 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
         const float c = s_gate[kGateC][lane], rest = s_gate[kGateRest][lane], delta = s_gate[kGateDelta][lane];
         const float cT = s_gate[kGateC][C - 1], restT = s_gate[kGateRest][C - 1];
         rr *= exp2_pair(c, rest);
-        const double after = (double)row - (double)cs + (double)rr;     // summed over i >= t
-        const double pre = wave_prefix(after);
-        const double suffix = last_lane(pre) - pre + after;
+        const double rows = diag + left, pr = row_prefix(rows), pu = row_prefix(under);
+        const double pairs = row_last(pr) - pr + rows + pu - under + row_last(row_prefix(past));
+        const double through = (double)rr, pre = wave_prefix(through);  // summed over i >= t
+        const double suffix = pairs + last_lane(pre) - pre + through;
         const double wz = (double)s_gate[kGateW][lane] * (double)zz;
         const double before = wave_prefix(wz) - wz;                     // summed over j < t
         const double dla = suffix + before + (double)exp2_pair(cT, restT) * (double)sev;

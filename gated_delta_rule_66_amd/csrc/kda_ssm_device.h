@@ -199,8 +199,8 @@ __device__ __forceinline__ float exp2_pair(float c, float rest) {
 // one token's delta for one head
 __device__ __forceinline__ float delta_of(float raw, int softplus) { return softplus ? softplus_of(raw) : raw; }
 
-// inclusive sum over the 64 lanes of a wave, fp64: data-parallel moves within
-// rows of 16 lanes (row_shr), then the rows' last lanes broadcast on
+// inclusive sums over each row of 16 lanes (row_shr) and over the 64 lanes of a
+// wave (the rows' last lanes broadcast on), fp64
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double dpp_add(double v) {
     const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
@@ -208,11 +208,14 @@ __device__ __forceinline__ double dpp_add(double v) {
     const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, ROWS, 0xf, true);
     return v + __builtin_bit_cast(double, ((unsigned long long)hi << 32) | lo);
 }
-__device__ __forceinline__ double wave_prefix(double v) {
+__device__ __forceinline__ double row_prefix(double v) {
     v = dpp_add<0x111, 0xf>(v);
     v = dpp_add<0x112, 0xf>(v);
     v = dpp_add<0x114, 0xf>(v);
-    v = dpp_add<0x118, 0xf>(v);
+    return dpp_add<0x118, 0xf>(v);
+}
+__device__ __forceinline__ double wave_prefix(double v) {
+    v = row_prefix(v);
     v = dpp_add<0x142, 0xa>(v);     // row_bcast:15 into rows 1 and 3
     return dpp_add<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
 }
