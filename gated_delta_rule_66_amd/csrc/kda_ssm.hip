@@ -286,9 +286,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
                 const int i = 16 * ti + r16, last = 16 * tj + 15;
 #pragma unroll
                 for (int k = 0; k < NH; ++k) {
-                    float d = s_gate[k][kGateC][i] - s_gate[k][kGateC][last];
-                    if constexpr (sizeof(T) == 4) d += s_gate[k][kGateRest][i] - s_gate[k][kGateRest][last];
-                    const float f = fast_exp2(d);
+                    const float f = fast_exp2((s_gate[k][kGateC][i] - s_gate[k][kGateC][last]) +
+                                              (s_gate[k][kGateRest][i] - s_gate[k][kGateRest][last]));
                     const f32x4 dj = *reinterpret_cast<const f32x4*>(&s_gate[k][kGateNear][16 * tj + 4 * g]);
                     float v[4];
 #pragma unroll
@@ -301,15 +300,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
 #pragma unroll
                 for (int k = 0; k < NH; ++k) {
                     const f32x4 cj = *reinterpret_cast<const f32x4*>(&s_gate[k][kGateC][j0]);
+                    const f32x4 rj = *reinterpret_cast<const f32x4*>(&s_gate[k][kGateRest][j0]);
                     const f32x4 dj = *reinterpret_cast<const f32x4*>(&s_gate[k][kGateDelta][j0]);
-                    const float ci = s_gate[k][kGateC][i];
+                    const float ci = s_gate[k][kGateC][i], ri = s_gate[k][kGateRest][i];
                     float v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float d = ci - cj[e];
-                        if constexpr (sizeof(T) == 4) d += s_gate[k][kGateRest][i] - s_gate[k][kGateRest][j0 + e];
-                        v[e] = j0 + e <= i ? acc[e] * fast_exp2(d) * dj[e] : 0.f;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = j0 + e <= i ? acc[e] * fast_exp2((ci - cj[e]) + (ri - rj[e])) * dj[e] : 0.f;
                     put(k, t, t, v);
                 }
             };
