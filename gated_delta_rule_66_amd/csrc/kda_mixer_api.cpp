@@ -71,10 +71,17 @@ bool vec_ok(kda_dtype dt, long long width, long long stride, const void* p) {
 
 // ---- short convolution ---------------------------------------------------------------
 
+// Tiles (no more than tokens) and sequences are counted in ints that step past
+// their end: by the tile slots of the backward's grid (2^19 at most), and by the
+// threads that pass on empty sequences (a 64th of the sequences and 256).
+constexpr long long kConvCount = (1LL << 31) - (1LL << 26);
+
 kda_status conv_sizes(int N, int T, int D, int W, kda_dtype dt, kda_activation act, const int* cu, long long* M) {
     if (N < 0 || T < 0 || D < 0 || !dtype_ok(dt) || !act_ok(act)) return KDA_ERR_INVALID_ARG;
     if (W < 2 || W > 4) return KDA_ERR_UNSUPPORTED;
-    if (!token_count(cu, N, T, M) || (long long)N * (W - 1) > 2147483647LL || D > (1 << 21)) return KDA_ERR_UNSUPPORTED;
+    if (!token_count(cu, N, T, M) || *M > kConvCount || N > kConvCount || (long long)N * (W - 1) > 2147483647LL ||
+        D > (1 << 21))
+        return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

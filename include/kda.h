@@ -429,7 +429,8 @@ typedef enum kda_activation {
  *
  *   y_t[d] = act( bias[d] + sum_{w < W} weight[d, w] x_{t - (W-1) + w}[d] )
  *
- *   W in {2, 3, 4}; D up to 2^21.  Sums in fp32, rounded once.
+ *   W in {2, 3, 4}; D up to 2^21; tokens and sequences up to 2^31 - 2^26
+ *   (more are KDA_ERR_UNSUPPORTED).  Sums in fp32, rounded once.
  *   x      : [tokens, D] dt, row stride x_stride
  *   weight : [D, W] fp32;  bias : [D] fp32 or NULL
  *   initial_state : [N, W-1, D] dt, the W - 1 rows before each sequence, or

@@ -220,3 +220,24 @@ def test_selective_scan_refuses_more_workgroups_than_a_launch_holds():
     assert scan(n=1 << 24, **few) == UNSUPPORTED
     # a long axis of many heads
     assert scan(n=1, t=1 << 24, h=512, g=512, ws=None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("call", ["fwd", "bwd"])
+def test_short_conv_counts_that_would_wrap(call):
+    # the kernels' int counters step past the last tile or sequence; one channel,
+    # so that no other limit is met.  Sizes that fit end at a check behind the
+    # sizes': outputs over inputs, or no workspace.
+    most = 2 ** 31 - 2 ** 26
+    far = {n: i << 40 for i, n in enumerate(("x", "weight", "bias", "s0", "y", "sT", "dy", "dsT", "dx", "dw", "db",
+                                            "ds0"), 1)}
+    if call == "fwd":
+        last, end = dict(far, y=far["x"], sT=far["s0"]), INVALID
+    else:
+        last, end = dict(far, ws=None), WORKSPACE
+    for sizes in (dict(n=most, t=1), dict(n=most, t=0), dict(n=1, t=most)):
+        assert conv(call, d=1, w=2, **sizes, **last) == end, sizes
+    for sizes in (dict(n=most + 1, t=1), dict(n=most + 1, t=0), dict(n=1, t=most + 1), dict(n=2 ** 31 - 4097, t=1),
+                  dict(n=2 ** 31 - 1, t=0)):
+        assert conv(call, d=1, w=2, **sizes, **last) == UNSUPPORTED, sizes
+    if call == "bwd":
+        assert lib().kda_short_conv_bwd_workspace_size(2 ** 31 - 4097, 0, 1, 1, 2, BF16) == BIG
