@@ -4,6 +4,7 @@
 #include "kda_internal.h"
 #include "kda_mixer.h"
 
+#include <limits.h>
 #include <stdint.h>
 
 #include <initializer_list>
@@ -469,21 +470,25 @@ size_t kda_selective_scan_fwd_workspace_size(int N, int packed, int T, int H, in
     return ssm_layout(packed != 0, N, H, K, P, ssm_plan(packed != 0, N, M, T, H, G, P, kScanGroups)).total;
 }
 
-// pointer checks shared by the scan's calls; offsets inside a chunk's 64 rows
-// are 32 bits in the kernels
+// Elements between token rows in the chunk kernels, whose offsets inside a
+// chunk's 64 rows are 32 bits (64 x 2^23 fp32: 2^31 bytes).
+constexpr long long kScanStride = 1LL << 23;
+
+// pointer checks shared by the scan's calls; most: the longest row stride
 static kda_status ssm_pointers(long long M, int H, int G, int K, int P, kda_dtype dt, const void* x, long long xs,
                                const void* dtp, long long ds, const float* A, const void* B, long long bs, const void* Cm,
-                               long long cs, const float* D, const float* dt_bias, const float* s0) {
+                               long long cs, const float* D, const float* dt_bias, const float* s0,
+                               long long most = kScanStride) {
     const size_t es = esize(dt);
     if (!A || !aligned(A, 4) || !aligned(D, 4) || !aligned(dt_bias, 4) || !aligned(s0, 16)) return KDA_ERR_INVALID_ARG;
     if (M == 0) return KDA_OK;
     if (!x || !dtp || !B || !Cm || !aligned(dtp, es)) return KDA_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(B, 16) || !aligned(Cm, 16)) return KDA_ERR_INVALID_ARG;
     const long long e = 16 / (long long)es;
-    if (ds < H || ds > (1LL << 23) || xs < (long long)H * P || bs < (long long)G * K || cs < (long long)G * K || xs % e || bs % e || cs % e)
+    if (ds < H || xs < (long long)H * P || bs < (long long)G * K || cs < (long long)G * K || xs % e || bs % e || cs % e)
         return KDA_ERR_INVALID_ARG;
-    const long long most = 1LL << 23;
-    if (xs > most || bs > most || cs > most || (long long)H * P > most) return KDA_ERR_UNSUPPORTED;
+    for (const long long stride : {xs, ds, bs, cs, (long long)H * P})
+        if (stride > most) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -632,7 +637,7 @@ kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, in
         if (dx_stride < (long long)H * P || db_stride < (long long)G * K || dc_stride < (long long)G * K ||
             dx_stride % e || db_stride % e || dc_stride % e)
             return KDA_ERR_INVALID_ARG;
-        if (dx_stride > 1LL << 23) return KDA_ERR_UNSUPPORTED;
+        if (dx_stride > kScanStride) return KDA_ERR_UNSUPPORTED;
     }
     const long long le = (long long)es;
     const long long xw = (long long)H * P * le, bw = (long long)G * K * le, dw = H * le;
@@ -721,7 +726,9 @@ kda_status kda_selective_scan_step(int N, int H, int G, int K, int P, kda_dtype 
     kda_status s = ssm_sizes(N, nullptr, 1, H, G, K, P, dt, &M);
     if (s != KDA_OK) return s;
     if (N == 0 || H == 0) return KDA_OK;
-    s = ssm_pointers(M, H, G, K, P, dt, x, x_stride, delta, delta_stride, A, B, b_stride, C, c_stride, D, dt_bias, state);
+    // the step addresses its rows in 64 bits
+    s = ssm_pointers(M, H, G, K, P, dt, x, x_stride, delta, delta_stride, A, B, b_stride, C, c_stride, D, dt_bias, state,
+                     LLONG_MAX);
     if (s != KDA_OK) return s;
     if (!state || !y || !aligned(y, 16)) return KDA_ERR_INVALID_ARG;
     const size_t par = (size_t)H * sizeof(float);

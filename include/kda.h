@@ -487,11 +487,13 @@ kda_status kda_short_conv_step(int N, int D, int W, kda_dtype dt, kda_activation
  *   y     : [tokens, H, P] dt
  *   final_state   : [N, H, K, P] fp32 or NULL; it may be initial_state exactly
  *   workspace : kda_selective_scan_fwd_workspace_size(...) bytes
- * x, B, C, y, states and workspace 16-byte aligned, strides multiples of 16
- * bytes.  Meant for A delta <= 0 (decay); a growing state is computed as far
- * as e^{sum A delta} over 64 tokens stays finite.  Non-finite inputs propagate
- * to their sequence from the start of their 64-token chunk on, never to
- * another sequence.  A sequence without tokens passes its state on.
+ * x, B, C, y, states and workspace 16-byte aligned, strides of x, B and C
+ * multiples of 16 bytes; every row stride, and H P, at most 2^23 elements in the
+ * prompt and gradient calls (more are KDA_ERR_UNSUPPORTED).  Meant for
+ * A delta <= 0 (decay); a growing state is computed as far as e^{sum A delta}
+ * over 64 tokens stays finite.  Non-finite inputs propagate to their sequence
+ * from the start of their 64-token chunk on, never to another sequence.  A
+ * sequence without tokens passes its state on.
  */
 size_t kda_selective_scan_fwd_workspace_size(int N, int packed, int T, int H, int G, int K, int P, kda_dtype dt);
 kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, int G, int K, int P, kda_dtype dt,
@@ -507,7 +509,7 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
  *   dx : [tokens, H, P];  d_delta : [tokens, H] (of dt_t, before bias and
  *        softplus);  dB, dC : [tokens, G, K], summed over the group's heads;
  *        all dt, row strides dx_stride, db_stride, dc_stride (multiples of 16
- *        bytes; columns of one wider buffer are fine)
+ *        bytes, dx_stride at most 2^23 elements; columns of one wider buffer are fine)
  *   dA : [H] fp32;  dD, d_dt_bias : [H] fp32 or NULL
  *   d_initial_state : [N, H, K, P] fp32 or NULL
  *   workspace : kda_selective_scan_bwd_workspace_size(...) bytes: the state
@@ -529,7 +531,8 @@ kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, in
 
 /*
  * One token of N sequences: state [N, H, K, P] is updated IN PLACE and read
- * and written once.  x [N, H, P], delta [N, H], B, C [N, G, K], y [N, H, P].
+ * and written once.  x [N, H, P], delta [N, H], B, C [N, G, K], y [N, H, P],
+ * with row strides of any length.
  */
 kda_status kda_selective_scan_step(int N, int H, int G, int K, int P, kda_dtype dt, int dt_softplus, const void* x,
                                    long long x_stride, const void* delta, long long delta_stride, const float* A,

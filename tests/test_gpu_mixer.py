@@ -537,3 +537,18 @@ SEGMENTS = [(1, 1000, None, 4, 1, 128, 64, True, True, True), (1, 500, None, 16,
 def test_selective_scan_segments_of_short_calls(case, dtype):
     test_selective_scan_forward(case, dtype)
     test_selective_scan_backward(case, dtype)
+
+
+def test_selective_scan_step_of_a_long_batch():
+    # one token of long sequences: 16.8M elements between the rows of x
+    gen = torch.Generator().manual_seed(12)
+    n, t, h, g, k, p = 2, 65600, 4, 2, 64, 64
+    r = lambda *s: rnd(gen, *s, dtype=torch.bfloat16).to(DEV)
+    x = torch.zeros(n, t, h, p, dtype=torch.bfloat16, device=DEV)
+    x[:, 7], dt, B, C = r(n, h, p), r(n, h), r(n, g, k), r(n, g, k)
+    A, D, bias, s = dev(-torch.rand(h, generator=gen) - 0.1), dev(rnd(gen, h)), dev(rnd(gen, h)), dev(rnd(gen, n, h, k, p))
+    s2 = s.clone()
+    assert x[:, 7].stride(0) > 2 ** 23
+    y = kda.selective_scan_step(x[:, 7], dt, A, B, C, D, bias, s, dt_softplus=True)
+    y2 = kda.selective_scan_step(x[:, 7].contiguous(), dt, A, B, C, D, bias, s2, dt_softplus=True)
+    assert torch.equal(y, y2) and torch.equal(s, s2) and torch.isfinite(y).all()

@@ -241,3 +241,15 @@ def test_short_conv_counts_that_would_wrap(call):
         assert conv(call, d=1, w=2, **sizes, **last) == UNSUPPORTED, sizes
     if call == "bwd":
         assert lib().kda_short_conv_bwd_workspace_size(2 ** 31 - 4097, 0, 1, 1, 2, BF16) == BIG
+
+
+@pytest.mark.parametrize("name,at", [("xs", 4 * 64), ("ds", 4), ("bs", 2 * 64), ("cs", 2 * 64)])
+def test_selective_scan_row_strides(name, at):
+    # a chunk's offsets are 32 bits; the step's rows are addressed in 64 (its
+    # call here ends at the check behind the strides': y over the state)
+    most = 1 << 23
+    for call, over in (("fwd", dict(ws=None)), ("bwd", dict(ws=None))):
+        assert scan(call, n=1, **{name: most}, **over) == WORKSPACE
+        assert scan(call, n=1, **{name: most + 8}, **over) == UNSUPPORTED
+    assert scan("step", y=8 * M, **{name: most + 8}) == INVALID
+    assert scan("step", y=8 * M, **{name: at}) == INVALID
