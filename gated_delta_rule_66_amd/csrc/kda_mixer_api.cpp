@@ -61,8 +61,10 @@ bool token_count(const int* cu, int N, int T, long long* M) {
     *M = cu ? (long long)T : (long long)N * T;
     return *M <= 2147483647LL - 4096;
 }
-bool vec_ok(kda_dtype dt, long long width, long long stride, const void* p) {
-    return width % (long long)(16 / esize(dt)) == 0 && stride % (long long)(16 / esize(dt)) == 0 && aligned(p, 16);
+// rows of `width` elements, `stride` apart, start and end on whole accesses
+bool vec_ok(kda_dtype dt, long long width, long long stride, const void* p, size_t bytes = 16) {
+    const long long n = (long long)(bytes / esize(dt));
+    return width % n == 0 && stride % n == 0 && aligned(p, bytes);
 }
 
 #define KDA_LAUNCH(name, call)                                                          \
@@ -222,9 +224,10 @@ kda_status kda_short_conv_bwd(int N, const int* cu_seqlens, int T, int D, int W,
     p.weight = weight; p.bias = bias; p.s0 = initial_state;
     p.d_y = d_y; p.d_sT = d_final_state; p.dx = dx; p.d_s0 = d_initial_state;
     p.part = reinterpret_cast<float*>(workspace);
-    bool vec = vec_ok(dt, D, M > 1 ? x_stride : D, x);
+    // accesses of eight bytes
+    bool vec = vec_ok(dt, D, M > 1 ? x_stride : D, x, 8);
     for (const void* t : {initial_state, d_y, d_final_state, (const void*)dx, (const void*)d_initial_state})
-        vec = vec && aligned(t, 16);
+        vec = vec && aligned(t, 8);
     const ConvBwdPlan b = conv_bwd_plan(cu_seqlens != nullptr, N, T, D, vec ? (int)(8 / es) : 1);
     p.cx_log2 = b.cx_log2;
     conv_tiles(p, M, b.tile);

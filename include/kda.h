@@ -452,8 +452,9 @@ kda_status kda_short_conv_fwd(int N, const int* cu_seqlens, int T, int D, int W,
  *   d_initial_state : [N, W-1, D] dt or NULL
  *   workspace : kda_short_conv_bwd_workspace_size(...) bytes (packed: 1 for a
  *               call with cu_seqlens)
- * The convolution is recomputed from x.  No tokens: dweight and dbias are
- * zero, and dL/dfinal_state passes to d_initial_state.
+ * The convolution is recomputed from x.  Accesses are eight bytes wide where
+ * pointers, D and x_stride are multiples of eight bytes.  No tokens: dweight
+ * and dbias are zero, and dL/dfinal_state passes to d_initial_state.
  */
 size_t kda_short_conv_bwd_workspace_size(int N, int packed, int T, int D, int W, kda_dtype dt);
 kda_status kda_short_conv_bwd(int N, const int* cu_seqlens, int T, int D, int W, kda_dtype dt, kda_activation act,

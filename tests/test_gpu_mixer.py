@@ -552,3 +552,25 @@ def test_selective_scan_step_of_a_long_batch():
     y = kda.selective_scan_step(x[:, 7], dt, A, B, C, D, bias, s, dt_softplus=True)
     y2 = kda.selective_scan_step(x[:, 7].contiguous(), dt, A, B, C, D, bias, s2, dt_softplus=True)
     assert torch.equal(y, y2) and torch.equal(s, s2) and torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_short_conv_backward_of_eight_byte_rows(dtype):
+    # the backward's accesses are eight bytes: tensors that start eight bytes
+    # behind a multiple of 16 take the same kernel, and so give the same bits
+    c = conv_case((2, 700, None, 2304, 4, True, True, "silu"), dtype, 13)
+    off = 8 // c["x"].element_size()
+
+    def moved(t):
+        buf = torch.empty(t.numel() + off, dtype=t.dtype, device=DEV)
+        return buf[off:].view(t.shape).copy_(t)
+
+    w, b = dev(c["w"]), dev(c["b"])
+    want = kda.short_conv_bwd(dev(c["x"]), w, b, dev(c["dy"]), dev(c["s"]), dev(c["ds"]))
+    dx = moved(torch.zeros_like(c["x"]))
+    assert dx.data_ptr() % 16 == 8
+    got = kda.short_conv_bwd(moved(c["x"]), w, b, moved(c["dy"]), moved(c["s"]), moved(c["ds"]), dx=dx)
+    for i in range(4):
+        assert torch.equal(got[i], want[i]), i
+    # a width of whole eight bytes, not of 16
+    test_short_conv_backward((2, 90, None, 92 if dtype == torch.bfloat16 else 90, 4, True, True, "silu"), dtype)
