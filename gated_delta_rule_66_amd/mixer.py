@@ -67,10 +67,10 @@ def _call(name: str, dev: int, *args):
 
 
 def _size(name: str, *args) -> int:
+    """The bytes of a workspace; 0 for sizes that are refused: the call, which
+    checks them first, then says why."""
     n = getattr(_k.load_library(), name)(*args)
-    if n == ctypes.c_size_t(-1).value:
-        raise KDAError(_k.KDA_ERR_INVALID_ARG, name)
-    return int(n)
+    return 0 if n == ctypes.c_size_t(-1).value else int(n)
 
 
 def _workspace(workspace: Optional[torch.Tensor], need: int, dev: int):

@@ -574,3 +574,31 @@ def test_short_conv_backward_of_eight_byte_rows(dtype):
         assert torch.equal(got[i], want[i]), i
     # a width of whole eight bytes, not of 16
     test_short_conv_backward((2, 90, None, 92 if dtype == torch.bfloat16 else 90, 4, True, True, "silu"), dtype)
+
+
+def test_refused_sizes_report_the_status_of_the_call():
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=DEV)
+    f = lambda *s: torch.zeros(s, device=DEV)
+
+    def status(fn, *a, **kw):
+        with pytest.raises(kda.KDAError) as e:
+            fn(*a, **kw)
+        return e.value.status
+    unsupported, invalid = kda.kda.KDA_ERR_UNSUPPORTED, kda.kda.KDA_ERR_INVALID_ARG
+    for k, p, st in ((32, 64, unsupported), (64, 96, unsupported), (64, 64, None)):
+        args = (z(2, 5, 4, p), z(2, 5, 4), f(4), z(2, 5, 2, k), z(2, 5, 2, k))
+        if st is not None:
+            assert status(kda.selective_scan_fwd, *args) == st
+            assert status(kda.selective_scan_bwd, *args, None, None, z(2, 5, 4, p)) == st
+            assert status(kda.selective_scan_step, z(2, 4, p), z(2, 4), f(4), z(2, 2, k), z(2, 2, k), None, None,
+                          f(2, 4, k, p)) == st
+    args = (z(2, 5, 3, 64), z(2, 5, 3), f(3), z(2, 5, 2, 64), z(2, 5, 2, 64))       # groups that do not divide heads
+    assert status(kda.selective_scan_fwd, *args) == invalid
+    assert status(kda.selective_scan_bwd, *args, None, None, z(2, 5, 3, 64)) == invalid
+    x = z(2, 5, 8)
+    assert status(kda.short_conv_fwd, x, f(8, 5)) == unsupported
+    assert status(kda.short_conv_bwd, x, f(8, 5), None, x) == unsupported
+    wide = z(2, 32768)
+    assert status(kda.group_norm_fwd, wide, 1, f(32768)) == unsupported
+    assert status(kda.group_norm_bwd, wide, 1, f(32768), None, None, wide) == unsupported
+    assert status(kda.group_norm_bwd, wide, 3, f(32768), None, None, wide) == invalid
