@@ -97,6 +97,7 @@ struct SsmParams {
     int n_seg, cps;
     int seg0;                   // first segment of the launch
     int reverse;                // 1: the adjoint's recurrence, from the last chunk to the first
+    int in_place;               // 1: sT is s0, and there are segments (kda_ssm_chunk_kernel)
     float* gates;               // [chunks][H][5][64] (kda_ssm_device.h)
     // what one segment does to its start state: local states [n_seg][H][K][P]
     // (after the combine: start states) and decays [n_seg][H] (negative: a
@@ -104,7 +105,6 @@ struct SsmParams {
     float* seg_state;
     float* seg_decay;
     float* states;              // [chunks][H][K][P]: the state before each chunk (the states pass)
-
 };
 constexpr int kSsmChunk = 64;
 // chunk_off[i] = chunks of the sequences before i
@@ -124,6 +124,8 @@ enum SsmPass {
 };
 hipError_t launch_ssm_chunks(int dtype, SsmPass pass, int cols, const SsmPair& a, int n, int segs, hipStream_t st);
 hipError_t launch_ssm_combine(const SsmPair& a, int n, hipStream_t st);
+// in_place: the final states that the output pass left in the segments' slots
+hipError_t launch_ssm_final(const SsmParams& p, hipStream_t st);
 
 // Gradients of the scan from the state before each chunk and the adjoint
 // behind it.  A workgroup takes one chunk and heads_per of the heads of a group.

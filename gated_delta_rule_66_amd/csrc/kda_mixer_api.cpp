@@ -449,7 +449,7 @@ static SsmPlan ssm_plan(bool packed, int N, long long M, int T, int H, int G, in
 }
 
 struct SsmLayout {
-    size_t off, gates, seg, dec, s0, total;
+    size_t off, gates, seg, dec, total;
 };
 static SsmLayout ssm_layout(bool packed, int N, int H, int K, int P, const SsmPlan& pl) {
     SsmLayout L;
@@ -459,8 +459,6 @@ static SsmLayout ssm_layout(bool packed, int N, int H, int K, int P, const SsmPl
     L.gates = o; o += align256(ssm_gate_bytes(pl.chunks, H));
     L.seg = o; o += pl.n_seg > 1 ? align256((size_t)pl.n_seg * H * kp) : 0;
     L.dec = o; o += pl.n_seg > 1 ? align256((size_t)pl.n_seg * H * sizeof(float)) : 0;
-    // a copy of the initial states where the final states overwrite them
-    L.s0 = o; o += pl.n_seg > 1 ? align256((size_t)N * H * kp) : 0;
     L.total = o;
     return L;
 }
@@ -540,12 +538,7 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
     p.gates = reinterpret_cast<float*>(ws + L.gates);
     KDA_LAUNCH("scan_gates", launch_ssm_gates((int)dt, p, stream));
     if (pl.n_seg > 1) {
-        if (initial_state && initial_state == final_state) {
-            // segments read initial states while others write final ones
-            float* copy = reinterpret_cast<float*>(ws + L.s0);
-            KDA_LAUNCH("copy_state", launch_copy_state(initial_state, copy, (size_t)N * H * K * P, stream));
-            p.s0 = copy;
-        }
+        p.in_place = initial_state && initial_state == final_state;
         p.seg_state = reinterpret_cast<float*>(ws + L.seg);
         p.seg_decay = reinterpret_cast<float*>(ws + L.dec);
         const SsmPair a{{p, p}};
@@ -556,6 +549,7 @@ kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, in
     p.sT = final_state;
     const SsmPair a{{p, p}};
     KDA_LAUNCH("scan_output", launch_ssm_chunks((int)dt, kSsmOutput, pl.cols, a, 1, pl.n_seg, stream));
+    if (p.in_place) KDA_LAUNCH("scan_final", launch_ssm_final(p, stream));
     return KDA_OK;
 }
 

@@ -60,6 +60,10 @@ __global__ __launch_bounds__(256) void kda_ssm_gates_kernel(SsmParams p) {
 //   states:  the state before each chunk, and the final state
 // blockIdx.y picks one of two recurrences (the backward runs the states and,
 // with C for B, dy for x and the chunks in reverse, their adjoints).
+// Final states over the initial ones: a sequence that came in from the segment
+// before may have its initial state still read there, so its final state goes to
+// this segment's slot (whose start state is in registers), and from there on by
+// kda_ssm_final_kernel.  A segment has one such sequence at most.
 //
 // The state is exact to fp32: delta x e^{..} is split into three bf16 for its
 // product with B, two thirds of the output pass's and all of the summary's
@@ -243,6 +247,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
     fetch(walk, rev ? end - 1 : begin);
     float seg_dec = 1.f;
     int y_t0 = 0, y_len = 0;
+    bool came_in = OUT && p.in_place;       // the sequence opened in a segment before
 
     for (int it = begin; it < end; ++it) {
         const int t0 = walk.t0(), len = walk.len(), seq = walk.seq;
@@ -251,6 +256,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
         if (opens) {
             load_state(p.s0 ? p.s0 + ((size_t)seq * p.H + h) * KP : nullptr);
             seg_dec = -1.f;
+            came_in = false;
         }
         // y of the chunk before leaves from the pieces that stage() writes next
         if (OUT && it > begin) store_y(y_t0, y_len);
@@ -438,7 +444,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
                     st_run<4>(at, o);
                 }
         }
-        if (closes && p.sT && !summary) store_state(p.sT + ((size_t)seq * p.H + h) * KP);
+        if (closes && p.sT && !summary) store_state(came_in ? seg_slot : p.sT + ((size_t)seq * p.H + h) * KP);
         __syncthreads();
     }
     if constexpr (OUT) store_y(y_t0, y_len);
@@ -483,6 +489,21 @@ __global__ __launch_bounds__(256) void kda_ssm_combine_kernel(SsmPair a) {
             }
         }
     }
+}
+
+// The final states that the output pass of an in-place call left in the slots
+// of the segments in which their sequences end.  Four values a thread.
+__global__ __launch_bounds__(256) void kda_ssm_final_kernel(SsmParams p) {
+    const unsigned blocks = (unsigned)(p.K * p.P) / 1024 * (unsigned)p.H;      // a segment
+    const int seg = 1 + (int)(blockIdx.x / blocks), all = total_chunks(p);
+    const int begin = min(seg * p.cps, all), end = min(begin + p.cps, all);
+    if (begin >= end) return;
+    ChunkWalk walk;
+    walk.init(p, begin);
+    if (walk.first() || begin + (walk.nk - walk.k) > end) return;
+    const size_t at = (size_t)(blockIdx.x % blocks) * 256 + threadIdx.x, state = (size_t)blocks * 256;
+    reinterpret_cast<f32x4*>(p.sT)[(size_t)walk.seq * state + at] =
+        reinterpret_cast<const f32x4*>(p.seg_state)[(size_t)seg * state + at];
 }
 
 // The chunk offsets of a packed call: a prefix sum over the sequences' chunks.
@@ -646,6 +667,13 @@ hipError_t launch_ssm_chunks(int dtype, SsmPass pass, int cols, const SsmPair& a
 hipError_t launch_ssm_combine(const SsmPair& a, int n, hipStream_t st) {
     const size_t values = (size_t)a.p[0].H * a.p[0].K * a.p[0].P;
     hipLaunchKernelGGL(kda_ssm_combine_kernel, dim3((unsigned)(values / 1024), (unsigned)n), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_ssm_final(const SsmParams& p, hipStream_t st) {
+    if (p.n_seg < 2) return hipSuccess;
+    const unsigned blocks = (unsigned)((size_t)(p.n_seg - 1) * p.H * p.K * p.P / 1024);
+    hipLaunchKernelGGL(kda_ssm_final_kernel, dim3(blocks), dim3(256), 0, st, p);
     return hipGetLastError();
 }
 

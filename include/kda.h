@@ -590,7 +590,7 @@ kda_status kda_group_norm_bwd(int rows, int C, int groups, kda_dtype dt, kda_act
  * "bwd_states", "bwd_reverse_summary", "bwd_reverse_scan", "bwd_state_reverse",
  * "bwd_value_side", "bwd_solve", "bwd_gated"; the mixer operators'
  * "short_conv", "short_conv_bwd", "short_conv_bwd_sums", "short_conv_step",
- * "scan_prep", "scan_gates", "scan_summary", "scan_combine", "scan_output", "scan_step",
+ * "scan_prep", "scan_gates", "scan_summary", "scan_combine", "scan_output", "scan_final", "scan_step",
  * "scan_bwd_summary", "scan_bwd_combine", "scan_bwd_states", "scan_bwd_grads",
  * "scan_bwd_join", "scan_bwd_sums",
  * "group_norm", "group_norm_bwd", "group_norm_bwd_sums") and durations in milliseconds, releases the

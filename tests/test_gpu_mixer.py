@@ -602,3 +602,30 @@ def test_refused_sizes_report_the_status_of_the_call():
     assert status(kda.group_norm_fwd, wide, 1, f(32768)) == unsupported
     assert status(kda.group_norm_bwd, wide, 1, f(32768), None, None, wide) == unsupported
     assert status(kda.group_norm_bwd, wide, 3, f(32768), None, None, wide) == invalid
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", [
+    (40, 130, None, 4, 1, 64, 64, True, True, True),        # many sequences a segment, some across two
+    (2, 2500, None, 4, 2, 128, 64, True, True, True),       # each across many segments
+    (1, 700, None, 3, 1, 64, 128, True, True, False),
+    (32, 64, None, 2, 1, 64, 64, True, True, True),         # ends of sequences on ends of segments
+    (0, 0, [3, 0, 700, 64, 1, 0, 190, 500, 128], 4, 2, 64, 64, True, True, True),
+    (0, 0, [0] * 40 + [900] + [0] * 30, 4, 2, 64, 64, True, True, True),
+], ids=["many", "long", "one", "even", "packed", "empty"])
+def test_selective_scan_final_states_over_initial_ones(case, dtype):
+    c = scan_case(case, dtype, 14)
+    s, cu = dev(c["s"]), dev(c["cu"])
+    y, fin = kda.selective_scan_fwd(*scan_args(c), s, dt_softplus=True, cu_seqlens=cu)
+    both = s.clone()
+    ws = torch.full((1 << 24,), 77, dtype=torch.uint8, device=DEV)
+    h, p, (g, k) = c["x"].shape[-2], c["x"].shape[-1], c["B"].shape[-2:]
+    t = sum(case[2]) if case[2] is not None else case[1]
+    need = kda.load_library().kda_selective_scan_fwd_workspace_size(
+        c["n"], int(cu is not None), t, h, g, k, p, 1 if dtype == torch.bfloat16 else 0)
+    y2, fin2 = kda.selective_scan_fwd(*scan_args(c), both, dt_softplus=True, cu_seqlens=cu, final_state=both,
+                                      workspace=ws[:need])
+    assert fin2 is both and torch.equal(y, y2) and torch.equal(fin, fin2)
+    assert (ws[need:] == 77).all()
+    if c["x"].numel() < 100000:
+        check_scan(c, dtype, y2, fin2)

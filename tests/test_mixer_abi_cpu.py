@@ -253,3 +253,13 @@ def test_selective_scan_row_strides(name, at):
         assert scan(call, n=1, **{name: most + 8}, **over) == UNSUPPORTED
     assert scan("step", y=8 * M, **{name: most + 8}) == INVALID
     assert scan("step", y=8 * M, **{name: at}) == INVALID
+
+
+def test_selective_scan_workspace_holds_no_copy_of_the_states():
+    # gates, and the segments' states: not the initial states of every sequence
+    a = lambda n: -(-n // 256) * 256
+    state = 32 * 128 * 64 * 4
+    size = lib().kda_selective_scan_fwd_workspace_size(64, 0, 512, 32, 1, 128, 64, BF16)
+    assert size - a(512 * 32 * 5 * 64 * 4) < 33 * (state + 256)
+    size = lib().kda_selective_scan_fwd_workspace_size(256, 1, 32768, 32, 1, 128, 64, BF16)
+    assert size - a(768 * 32 * 5 * 64 * 4) < 33 * (state + 256)
