@@ -48,6 +48,14 @@ __device__ __forceinline__ float sum_groups(float v) {
     r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
+// the sum over the rows of 16 lanes behind the lane's own (g)
+__device__ __forceinline__ float sum_groups_behind(float v, int g) {
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    const float next = (g & 1) ? 0.f : __uint_as_float(r[1]);
+    const float pair = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(pair), __float_as_uint(pair), false, false);
+    return g < 2 ? next + __uint_as_float(r[1]) : next;
+}
 __device__ __forceinline__ float sum64(float v) { return sum_groups(sum16(v)); }
 
 // One workgroup (8 waves) per (chunk, group, part of the group's heads), head by
@@ -207,9 +215,8 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
         // Pairs across token t (i >= t > j) without pairs that cancel, whose
         // rounding would stay: of tiles in t's row of tiles the rows from t on,
         // of those in its column of tiles the columns before t, all of the tiles
-        // behind and before it; only t's own tile takes rows less columns.
+        // behind and before it; t's own tile has them summed (s_row).
         const int own = t * (t + 1) / 2 + t;
-        const double diag = (double)s_row[own][q] - (double)s_cols[own][q];
         double left = 0.0, under = 0.0;
         float cf = s_colf[own][q];
         for (int b = 0; b < t; ++b) left += (double)s_row[t * (t + 1) / 2 + b][q];
@@ -234,8 +241,8 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
         const float c = s_gate[kGateC][lane], rest = s_gate[kGateRest][lane], delta = s_gate[kGateDelta][lane];
         const float cT = s_gate[kGateC][C - 1], restT = s_gate[kGateRest][C - 1];
         rr *= exp2_pair(c, rest);
-        const double rows = diag + left, pr = row_prefix(rows), pu = row_prefix(under);
-        const double pairs = row_last(pr) - pr + rows + pu - under + row_last(row_prefix(past));
+        const double pr = row_prefix(left), pu = row_prefix(under);
+        const double pairs = (double)s_row[own][q] + row_last(pr) - pr + left + pu - under + row_last(row_prefix(past));
         const double through = (double)rr, pre = wave_prefix(through);  // summed over i >= t
         const double suffix = pairs + last_lane(pre) - pre + through;
         const double wz = (double)s_gate[kGateW][lane] * (double)zz;
@@ -290,7 +297,7 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                          ld_frag<T>(sX + (16 * tj[k] + r16) * LDP + 32 * m + 8 * g));
             const int j = 16 * tj[k] + r16, i0 = 16 * ti[k] + 4 * g;
             const float cj = s_gate[kGateC][j], cjl = s_gate[kGateRest][j], dj = s_gate[kGateDelta][j];
-            float mv[4], colf = 0.f, cols = 0.f;
+            float mv[4], pairs[4], colf = 0.f, cols = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = i0 + e;
@@ -300,12 +307,25 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 const float pr = in ? ql * Gt[k][e] : 0.f;
                 mv[e] = in ? Gt[k][e] * l * dj : 0.f;
                 dG[k][e] += ql * dj;
-                const float prs = below ? pr * dj : 0.f;
+                pairs[e] = below ? pr * dj : 0.f;
                 colf += pr;
-                cols += prs;
-                const float row = sum16(prs);
-                if (r16 == 0) s_row[q][4 * g + e] = row;
+                cols += pairs[e];
                 if (i == j) dd += dm[e];
+            }
+            if (ti[k] == tj[k]) {
+                // on the diagonal a token's own rows would hold pairs behind it:
+                // the rows from token 4 g + e on, of the columns before it
+                pairs[2] += pairs[3];
+                pairs[1] += pairs[2];
+                pairs[0] += pairs[1];
+                const float behind = sum_groups_behind(pairs[0], g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pairs[e] = r16 < 4 * g + e ? pairs[e] + behind : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float row = sum16(pairs[e]);
+                if (r16 == 0) s_row[q][4 * g + e] = row;
             }
             st_run<4>(sM + j * LDM + i0, mv);
             colf = sum_groups(colf);
