@@ -33,6 +33,45 @@ def test_selective_scan_tokens_that_clear_the_state(dtype, h, g, k, p):
     G.check_scan(c, dtype, y, fin)
 
 
+# ---- selective scan: chunks behind chunks, heads behind heads -----------------------------
+# (case as in test_gpu_mixer, segments forward, segments backward, parts of a
+# group's heads backward).  A workgroup walks three chunks or more of K = 64 and
+# 128, of a pair of heads or of one, over boundaries of sequences inside a
+# segment, and takes three heads or more of a chunk in the gradient kernel.
+DEEP = {
+    "pair 128x64": ((3, 500, None, 96, 8, 128, 64, True, True, True), 8, 6, 4),
+    "one 128x64": ((3, 500, None, 63, 9, 128, 64, True, True, True), 8, 5, 1),
+    "one 128x128": ((3, 500, None, 56, 8, 128, 128, True, True, True), 8, 5, 1),
+    "pair 64x64": ((3, 500, None, 96, 8, 64, 64, False, False, True), 8, 6, 4),
+    "one 64x128": ((3, 500, None, 48, 8, 64, 128, True, True, False), 8, 6, 1),
+    "packed 128x64": ((0, 0, [64, 300, 1, 0, 200, 64, 256, 90, 33, 260, 257], 63, 9, 128, 64, True, True, True), 9, 5, 2),
+    "packed 64x128": ((0, 0, [64, 300, 1, 0, 200, 64, 256, 90, 33, 260, 257], 48, 8, 64, 128, True, True, True), 9, 6, 2),
+    "alone 128x64": ((2, 200, None, 260, 4, 128, 64, True, True, True), 1, 1, 8),
+    "alone 64x128": ((2, 200, None, 260, 4, 64, 128, True, True, True), 1, 1, 8),
+}
+
+
+def check_plan(case, fwd_segs, bwd_segs, parts, dtype):
+    """The workspaces are those of the segments and parts the case is here for,
+    so that it cannot lose its purpose unseen."""
+    n, t, lens, h, g, k, p = case[:7]
+    if lens is not None:
+        n, t = len(lens), sum(lens)
+        m, chunks = t, t // 64 + n
+    else:
+        m, chunks = n * t, n * -(-t // 64)
+    a = lambda v: -(-v // 256) * 256
+    off = a(4 * (n + 1)) if lens is not None else 0
+    gates, state = a(chunks * h * 5 * 64 * 4), h * k * p * 4
+    segs = lambda s: a(s * state) + a(s * h * 4) if s > 1 else 0
+    lib, code = kda.load_library(), 1 if dtype == torch.bfloat16 else 0
+    sizes = (n, int(lens is not None), t, h, g, k, p, code)
+    assert lib.kda_selective_scan_fwd_workspace_size(*sizes) == off + gates + segs(fwd_segs)
+    part = a(parts * m * g * k * 4) if parts > 1 else 0
+    assert lib.kda_selective_scan_bwd_workspace_size(*sizes) == \
+        off + gates + 2 * segs(bwd_segs) + 2 * a(chunks * state) + a(chunks * 3 * h * 4) + 2 * part
+
+
 def scan_all(c, size=False):
     """Outputs and gradients in 64 bits on the GPU, token by token, or (size) the
     sums of absolute values behind them."""
@@ -103,6 +142,14 @@ def check_all(c, dtype):
         outer = half if name in ("dx", "dB", "dC", "ddt") else 0.0
         R.close(got[name].reshape(want[name].shape), want[name],
                 outer * want[name].abs() + (inner + chain) * size[name], name)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", DEEP)
+def test_selective_scan_of_many_chunks_and_heads_a_workgroup(name, dtype):
+    case = DEEP[name][0]
+    check_plan(*DEEP[name], dtype)
+    check_all(G.scan_case(case, dtype, 22), dtype)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
