@@ -155,3 +155,24 @@ def test_selective_scan_of_many_chunks_and_heads_a_workgroup(name, dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_selective_scan_gradients_behind_tokens_that_clear_the_state(dtype):
     check_all(resets(G.scan_case((2, 200, None, 6, 2, 64, 64, True, False, True), dtype, 23), 24), dtype)
+
+
+# ---- group norm: rows behind rows -----------------------------------------------------------
+ROWS = [
+    # more rows than a launch has teams, forward (4096 waves) and backward (3072)
+    (2600, 2048, 1, "silu", True, True, False, True),       # a block a row
+    (2600, 2048, 1, "silu", True, False, True, True),
+    (600, 8192, 1, "sigmoid", True, False, True, True),     # 1024 threads; fp32 two accesses a lane
+    (60000, 64, 1, "silu", False, False, True, True),       # lanes of a wave
+    (20000, 256, 32, "silu", True, False, False, True),     # one lane a group (bf16)
+    (700, 1500, 1, "silu", False, False, True, True),       # bf16: one channel an access, two accesses a lane
+    (700, 1501, 1, None, False, False, False, True),
+    (500, 4001, 1, "sigmoid", True, True, True, True),      # four accesses a lane
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", ROWS, ids=["%dx%d" % c[:2] + "-%d" % i for i, c in enumerate(ROWS)])
+def test_group_norm_of_many_rows_a_team(case, dtype):
+    G.test_group_norm_forward(case, dtype)
+    G.test_group_norm_backward(case, dtype)
