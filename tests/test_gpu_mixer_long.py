@@ -176,3 +176,66 @@ ROWS = [
 def test_group_norm_of_many_rows_a_team(case, dtype):
     G.test_group_norm_forward(case, dtype)
     G.test_group_norm_backward(case, dtype)
+
+
+# ---- short convolution: tiles behind tiles, and the longer ones ------------------------------
+def conv_all(c, size=False):
+    """y and the gradients of a convolution without states, in 64 bits on the
+    GPU, or the sums of absolute values behind them."""
+    f = (lambda v: v.abs()) if size else (lambda v: v)
+    D, W = c["w"].shape
+    x, w, b, dy = (f(c[k].to(DEV).double()) for k in ("x", "w", "b", "dy"))
+    x, dy = x.reshape(-1, D), dy.reshape(-1, D)
+    pos = torch.cat([torch.arange(hi - lo) for lo, hi in c["ranges"]]).to(DEV)
+    left = torch.cat([hi - lo - 1 - torch.arange(hi - lo) for lo, hi in c["ranges"]]).to(DEV)
+    lag = lambda v, j: torch.where((pos >= j)[:, None], torch.roll(v, j, 0), 0.0)
+    lead = lambda v, j: torch.where((left >= j)[:, None], torch.roll(v, -j, 0), 0.0)
+    pre = b + sum(w[:, W - 1 - j] * lag(x, j) for j in range(W))
+    if size:
+        y, q = pre, dy * (1.1 + pre)
+    else:
+        s = torch.sigmoid(pre)
+        y, q = pre * s, dy * s * (1 + pre * (1 - s))
+    dw = torch.stack([(q * lag(x, W - 1 - i)).sum(0) for i in range(W)], 1)
+    dx = sum(w[:, W - 1 - j] * lead(q, j) for j in range(W))
+    return [v.cpu() for v in (y, dx, dw, q.sum(0))]
+
+
+def ragged(total, longest, seed):
+    gen, lens = torch.Generator().manual_seed(seed), []
+    while sum(lens) < total:
+        lens.append(min(int(torch.randint(1, longest, (1,), generator=gen)), total - sum(lens)))
+    return lens
+
+
+TILES = {
+    "several a thread": (3000, 3, None, 1024, 4),
+    "32 rows": (2, 4100, None, 1024, 3),
+    "64 rows, packed": (0, 0, ragged(16500, 700, 1), 2048, 4),
+    "several of 64 rows, packed, one channel an access": (0, 0, ragged(17000, 900, 2), 4097, 4),
+    "forward of 32 rows": (1, 65600, None, 1024, 2),
+}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", TILES)
+def test_short_conv_of_many_tiles(name, dtype):
+    n, t, lens, d, w = TILES[name]
+    if name == "several a thread":
+        # blocks of four tiles: as many as the workspace has rows of sums
+        code = 1 if dtype == torch.bfloat16 else 0
+        need = kda.load_library().kda_short_conv_bwd_workspace_size(n, 0, t, d, w, code)
+        assert need // (4 * (w + 1) * d) * 4 < n
+    if name.startswith("several of 64"):
+        # 64 channels and four tiles a block, 64 blocks along so many channels
+        assert 2048 // -(-d // 64) <= 64 and 64 * 4 < -(-sum(lens) // 64)
+    c = G.conv_case((n, t, lens, d, w, True, False, "silu"), dtype, 25)
+    y, _ = kda.short_conv_fwd(G.dev(c["x"]), G.dev(c["w"]), G.dev(c["b"]), cu_seqlens=G.dev(c["cu"]))
+    dx, dw, db, _ = kda.short_conv_bwd(G.dev(c["x"]), G.dev(c["w"]), G.dev(c["b"]), G.dev(c["dy"]),
+                                       cu_seqlens=G.dev(c["cu"]))
+    want, size = conv_all(c), conv_all(c, True)
+    half, m = R.HALF[dtype], want[0].shape[0]
+    R.close(y.reshape(m, d), want[0], half * want[0].abs() + 2.0 ** -20 * (size[0] + want[0].abs()), "y")
+    R.close(dx.reshape(m, d), want[1], half * want[1].abs() + 2.0 ** -19 * size[1], "dx")
+    R.close(dw, want[2], (2.0 ** -19 + m * 2.0 ** -24) * size[2], "dweight")
+    R.close(db, want[3], (2.0 ** -19 + m * 2.0 ** -24) * size[3], "dbias")
