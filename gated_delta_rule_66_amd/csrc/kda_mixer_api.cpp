@@ -4,7 +4,6 @@
 #include "kda_internal.h"
 #include "kda_mixer.h"
 
-#include <limits.h>
 #include <stdint.h>
 
 #include <initializer_list>
@@ -723,9 +722,10 @@ kda_status kda_selective_scan_step(int N, int H, int G, int K, int P, kda_dtype 
     kda_status s = ssm_sizes(N, nullptr, 1, H, G, K, P, dt, &M);
     if (s != KDA_OK) return s;
     if (N == 0 || H == 0) return KDA_OK;
-    // the step addresses its rows in 64 bits
+    // the step addresses its rows in 64 bits: any stride whose rows (fewer than
+    // 2^24) span less than 2^63 bytes
     s = ssm_pointers(M, H, G, K, P, dt, x, x_stride, delta, delta_stride, A, B, b_stride, C, c_stride, D, dt_bias, state,
-                     LLONG_MAX);
+                     1LL << 37);
     if (s != KDA_OK) return s;
     if (!state || !y || !aligned(y, 16)) return KDA_ERR_INVALID_ARG;
     const size_t par = (size_t)H * sizeof(float);

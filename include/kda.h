@@ -533,7 +533,7 @@ kda_status kda_selective_scan_bwd(int N, const int* cu_seqlens, int T, int H, in
 /*
  * One token of N sequences: state [N, H, K, P] is updated IN PLACE and read
  * and written once.  x [N, H, P], delta [N, H], B, C [N, G, K], y [N, H, P],
- * with row strides of any length.
+ * with row strides up to 2^37 elements.
  */
 kda_status kda_selective_scan_step(int N, int H, int G, int K, int P, kda_dtype dt, int dt_softplus, const void* x,
                                    long long x_stride, const void* delta, long long delta_stride, const float* A,

@@ -252,6 +252,8 @@ def test_selective_scan_row_strides(name, at):
         assert scan(call, n=1, **{name: most}, **over) == WORKSPACE
         assert scan(call, n=1, **{name: most + 8}, **over) == UNSUPPORTED
     assert scan("step", y=8 * M, **{name: most + 8}) == INVALID
+    assert scan("step", n=1, y=8 * M, **{name: 1 << 37}) == INVALID
+    assert scan("step", n=1, y=8 * M, **{name: (1 << 37) + 8}) == UNSUPPORTED
     assert scan("step", y=8 * M, **{name: at}) == INVALID
 
 
