@@ -117,8 +117,9 @@ ConvBwdPlan conv_bwd_plan(bool packed, int N, int T, int D, int V) {
     b.cx_log2 = cx_log2_for(D, V, 6);
     const long long tys = 256 >> b.cx_log2, cb = (D + (V << b.cx_log2) - 1) / (V << b.cx_log2);
     const long long M = packed ? (long long)T : (long long)N * T;
-    // measured on 18.6K tokens x 2304 bf16: tiles of 16, 32, 64 tokens 108, 91,
-    // 82 us; shorter where that leaves fewer threads than fill the card
+    // bf16 x 2304 channels, tiles of 16, 32, 64 tokens: 32768 tokens 142, 121,
+    // 108 us; 8192 tokens 40, 35, 40; 4096 tokens 25, 27, 32; 512 tokens 16, 20,
+    // 29 (fp32 in the same order): long tiles leave a short call few threads
     const long long work = M * (D / V);
     b.tile = work >= (1LL << 23) ? 64 : work >= (1LL << 21) ? 32 : 16;
     const long long tiles = packed ? (M + b.tile - 1) / b.tile : (long long)N * ((T + b.tile - 1) / b.tile);
@@ -161,8 +162,10 @@ kda_status kda_short_conv_fwd(int N, const int* cu_seqlens, int T, int D, int W,
                      aligned(final_state, 16);
     const int V = vec ? (int)(16 / es) : 1;
     p.cx_log2 = cx_log2_for(D, V, 8);
-    // measured on 8192 x 12288 bf16: tiles of 16, 32, 64 tokens 95, 91, 93 us;
-    // shorter where that leaves fewer threads than fill the card
+    // bf16, tiles of 8, 16, 32, 64 tokens: 8192 x 12288 16 on 95, 91, 93 us;
+    // x 2304 channels: 32768 tokens 98, 82, 72, 77; 16384 tokens 46, 40, 42, 44;
+    // 2048 tokens 12.7, 11.9, 15.7, 23.7; 512 tokens 8.6, 10.7, 16, 27 (fp32 in
+    // the same order): long tiles leave a short call few threads
     const long long work = M * (D / V);
     conv_tiles(p, M, work >= (1LL << 23) ? 32 : work >= (1LL << 21) ? 16 : 8);
     const int tys = 256 >> p.cx_log2;

@@ -67,8 +67,13 @@ __global__ __launch_bounds__(256) void kda_ssm_gates_kernel(SsmParams p) {
 //
 // The state is exact to fp32: delta x e^{..} is split into three bf16 for its
 // product with B, two thirds of the output pass's and all of the summary's
-// matrix work.  y, a bf16, takes the state and the scaled scores rounded once
-// (fp32 tensors: fp32 products throughout).
+// matrix work.  bf16 tokens: y's products take two operands rounded once to
+// bf16, the scaled scores (sG) and the start state (frag_from_tiles), because
+// y itself is rounded to bf16 behind them: 0.0019 of y's root mean square where
+// rounding y alone gives 0.0017, at half and a third of the matrix work that
+// operands split in two or three would take.  Everything else is fp32, the
+// decays' exponents two floats (kGateC, kGateRest).  fp32 tokens: fp32 products
+// throughout.
 // What bounds it: nothing alone.  By count, a chunk of two heads (K = 128,
 // P = 64) takes a CU 2400 cycles of matrix instructions in the output pass,
 // 2600 of LDS accesses and about 3000 of vector operations; it takes 9500 with
@@ -80,9 +85,9 @@ __global__ __launch_bounds__(256) void kda_ssm_gates_kernel(SsmParams p) {
 // columns as long as four of 32 in all passes (more operands read from LDS);
 // scores kept in registers by each wave 1357 us; y stored from registers, 32
 // bytes a token, 1093 instead of 1072.
-// Measured, K = 128, P = 64: output 8K x 32 heads 41 us, 8 x 32K x 32 heads
-// 1072 us (2.1 GB); summary 22 and 470 us; 2 x 8K x 16 heads of 128: output 69,
-// summary 35 us.
+// Measured, K = 128, P = 64: output 8K x 32 heads 43 us, 8 x 32K x 32 heads
+// 1050 us (1.42 GB read, 1.08 GB written); summary 22 and 455 us; 2 x 8K x 16
+// heads of 128: output 71, summary 37 us.
 template <typename T, int K, int P, int COLS, SsmPass PASS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_kernel(SsmPair a) {
     constexpr bool OUT = PASS == kSsmOutput, summary = PASS == kSsmSummary;

@@ -14,7 +14,11 @@
 // The sum over the heads of a group is taken on Q delta (64 x 64) before the
 // products with B and C.  d log a and d delta come from fp32 values of the
 // score tiles and from products whose state operand is split exactly, because
-// their sums over all tokens are fp32 gradients.
+// their sums over all tokens are fp32 gradients.  bf16 tokens: dx, dB and dC,
+// which leave as bf16, take operands rounded once to bf16: the scaled scores of
+// a head (sM), the heads' summed score gradients, and the states and adjoints
+// of dB's and dC's products.  They are at 0.0023 of their root mean square,
+// where rounding them alone gives 0.0017.  fp32 tokens: fp32 products throughout.
 #include "kda_ssm_device.h"
 
 namespace kda {
@@ -69,9 +73,10 @@ __device__ __forceinline__ float sum64(float v) { return sum_groups(sum16(v)); }
 //            summed over the heads in registers
 // A head's rows and states are 80 KB (K = 128, P = 64), which alone take 4 of
 // the 9 us a head, and the LDS holds one workgroup a CU; the rest is the three
-// phases' LDS reads (0.5 MB a head) between barriers.  8K x 32 heads: 148 us
-// (336 MB); four waves with states from memory 314 us, all waves loading the
-// next head at once 166 us.  K = 64, P = 128, 6 heads packed: 65 us.
+// phases' LDS reads (0.5 MB a head) between barriers.  8K x 32 heads: 146 us
+// (347 MB read, 56 MB written); four waves with states from memory 314 us, all
+// waves loading the next head at once 166 us.  K = 64, P = 128, 6 heads packed:
+// 65 us.
 template <typename T, int K, int P>
 __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     constexpr int TH = 512;

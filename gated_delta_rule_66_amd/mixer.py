@@ -295,7 +295,11 @@ def selective_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     x: [B, T, H, P]; dt: [B, T, H]; B, C: [B, T, G, K] (G divides H); packed:
     the same without the batch dimension.  A, D, dt_bias: [H] fp32; states
     [N, H, K, P] fp32.  Returns (y like x, final_state or None);
-    ``final_state`` may be ``initial_state`` itself.
+    ``final_state`` may be ``initial_state`` itself.  The work is done in chunks
+    of 64 tokens: a NaN or infinity reaches its own sequence from the start of its
+    chunk on (the recurrence and the one-token step: from its token on), never
+    another sequence.  bf16 tokens take bf16 products with fp32 states and decays,
+    fp32 tokens fp32 products.
     """
     lead = 2 if cu_seqlens is None else 1
     dev, H, G, K, P, code, xs, ds, bs, cs = _scan_args(x, dt, A, B, C, D, dt_bias, lead)
@@ -409,8 +413,9 @@ def group_norm_fwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
                    activation="silu", gate_first: bool = False, center: bool = False, eps: float = 1e-5,
                    out: Optional[torch.Tensor] = None):
     """Group norm of the last dimension's ``groups`` groups, each token by
-    itself, through ``kda_group_norm_fwd``: act(n) without a gate, n act(gate)
-    with one, or n of x act(gate) with ``gate_first``.  ``center`` subtracts
+    itself, through ``kda_group_norm_fwd``: act(n) without a gate (a plain norm
+    is ``activation=None``), n act(gate) with one, or n of x act(gate) with
+    ``gate_first``.  ``center`` subtracts
     the group's mean (else root mean square).  x, gate: [..., C]; weight,
     bias: [C] fp32 or None.  ``out`` may be x or gate itself."""
     dev, rows, C, code, xs, zs = _norm_args(x, groups, weight, bias, gate)
