@@ -239,3 +239,21 @@ def test_short_conv_of_many_tiles(name, dtype):
     R.close(dx.reshape(m, d), want[1], half * want[1].abs() + 2.0 ** -19 * size[1], "dx")
     R.close(dw, want[2], (2.0 ** -19 + m * 2.0 ** -24) * size[2], "dweight")
     R.close(db, want[3], (2.0 ** -19 + m * 2.0 ** -24) * size[3], "dbias")
+
+
+def test_selective_scan_over_its_own_states_in_a_graph():
+    # each replay continues from the states of the one before
+    c = G.scan_case((3, 500, None, 8, 2, 64, 64, True, True, True), torch.bfloat16, 26)
+    args, s = G.scan_args(c), G.dev(c["s"])
+    own, stream = s.clone(), torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        kda.selective_scan_fwd(*args, s.clone(), dt_softplus=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        y, _ = kda.selective_scan_fwd(*args, own, dt_softplus=True, final_state=own)
+    for _ in range(4):
+        want, s = kda.selective_scan_fwd(*args, s, dt_softplus=True)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(own, s)
