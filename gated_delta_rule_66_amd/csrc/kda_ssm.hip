@@ -66,28 +66,29 @@ __global__ __launch_bounds__(256) void kda_ssm_gates_kernel(SsmParams p) {
 // kda_ssm_final_kernel.  A segment has one such sequence at most.
 //
 // The state is exact to fp32: delta x e^{..} is split into three bf16 for its
-// product with B, two thirds of the output pass's and all of the summary's
-// matrix work.  bf16 tokens: y's products take two operands rounded once to
-// bf16, the scaled scores (sG) and the start state (frag_from_tiles), because
-// y itself is rounded to bf16 behind them: 0.0019 of y's root mean square where
-// rounding y alone gives 0.0017, at half and a third of the matrix work that
-// operands split in two or three would take.  Everything else is fp32, the
-// decays' exponents two floats (kGateC, kGateRest).  fp32 tokens: fp32 products
-// throughout.
+// product with B, half of the output pass's and all of the summary's matrix
+// work.  bf16 tokens: y, which is rounded to bf16, takes the scaled scores (sG,
+// sGL) and the start state as two bf16 each, exact to 2^-16, and so is off by its
+// own rounding alone, 0.0017 of its root mean square.  One bf16 each would make
+// it 0.0019, and the output pass 42 us instead of 48 on 8K x 32 heads, 1045
+// instead of 1180 on 8 x 32K x 32 heads.
+// Everything else is fp32, the decays' exponents two floats (kGateC, kGateRest).
+// fp32 tokens: fp32 products throughout.
 // What bounds it: nothing alone.  By count, a chunk of two heads (K = 128,
-// P = 64) takes a CU 2400 cycles of matrix instructions in the output pass,
-// 2600 of LDS accesses and about 3000 of vector operations; it takes 9500 with
-// two workgroups a CU.  Left out one at a time, loads, stores, scores or update
-// products save 12 to 15 % each.  The summary: 1500 cycles of matrix
-// instructions and 1600 of vector operations out of 5400; without its loads
-// 424 us instead of 485.  Tried on 8 x 32K x 32 heads: one workgroup a CU
-// 1477 us instead of 1117, and more than two do not fit; eight waves of 16
-// columns as long as four of 32 in all passes (more operands read from LDS);
-// scores kept in registers by each wave 1357 us; y stored from registers, 32
-// bytes a token, 1093 instead of 1072.
-// Measured, K = 128, P = 64: output 8K x 32 heads 43 us, 8 x 32K x 32 heads
-// 1050 us (1.42 GB read, 1.08 GB written); summary 22 and 455 us; 2 x 8K x 16
-// heads of 128: output 71, summary 37 us.
+// P = 64) takes a CU 3100 cycles of matrix instructions in the output pass, 2900
+// of LDS accesses and about 3800 of vector operations; it takes 10500 with two
+// workgroups a CU.  The summary: 1500 cycles of matrix instructions and 1600 of
+// vector operations out of 5400; without its loads 424 us instead of 485.  Tried
+// on 8 x 32K x 32 heads with one bf16 each (1117 us; loads, stores, scores or
+// update products left out one at a time saved 12 to 15 %): one workgroup a CU
+// 1477 us, and more than two do not fit; eight waves of 16 columns as long as
+// four of 32 in all passes (more operands read from LDS); scores kept in
+// registers by each wave 1357 us; y stored from registers, 32 bytes a token, 1093
+// instead of 1072.  With two bf16: the lower halves by dot products with -1 1367
+// us instead of 1328, by matrix products with -I 1320 instead of 1298.
+// Measured, K = 128, P = 64: output 8K x 32 heads 48 us, 8 x 32K x 32 heads
+// 1180 us (1.42 GB read, 1.08 GB written); summary 22 and 445 us; 2 x 8K x 16
+// heads of 128: output 80, summary 36 us.
 template <typename T, int K, int P, int COLS, SsmPass PASS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_kernel(SsmPair a) {
     constexpr bool OUT = PASS == kSsmOutput, summary = PASS == kSsmSummary;
@@ -96,7 +97,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
     constexpr int NT = COLS / 16 / NW;          // column tiles a wave
     constexpr int NH = COLS / P;                // heads of the workgroup
     constexpr int PAD = 16 / sizeof(T);
-    constexpr int LDB = K + tr_pad<T>(K), LDX = COLS + tr_pad<T>(COLS), LDK = K + PAD, LDG = C + PAD;
+    // scores: the six lower slabs of 16 rows x 32 tokens, each a fragment in the
+    // order of its lanes (rows of 64 bytes instead: four lanes a bank, 49 us
+    // instead of 47 on 8K x 32 heads)
+    constexpr int SLAB = 512, NG = NH * 6 * SLAB;
+    constexpr int LDB = K + tr_pad<T>(K), LDX = COLS + tr_pad<T>(COLS), LDK = K + PAD;
     constexpr int NTK = K / 16;                 // state row tiles
     constexpr int EPP = 16 / sizeof(T);         // elements of a 16-byte piece
     constexpr int PK = C * K / EPP / TH, PX = C * COLS / EPP / TH;
@@ -104,7 +109,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
     __shared__ T sB[C * LDB];
     __shared__ T sX[C * LDX];
     __shared__ T sC[OUT ? C * LDK : 1];
-    __shared__ T sG[OUT ? NH * C * LDG : 1];
+    __shared__ T sG[OUT ? NG : 1], sGL[OUT && sizeof(T) == 2 ? NG : 1];     // upper and lower halves
     __shared__ __align__(16) float s_gate[NH][kGates][C];
     typedef typename FragOf<T>::type Frag;
 
@@ -185,7 +190,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
     if constexpr (OUT) {
         // the score tiles above the diagonal that products read with their
         // neighbours: zero once, never written again
-        for (int k = tid; k < NH * C * LDG; k += TH) sG[k] = (T)0.f;
+        for (int k = tid; k < NG; k += TH) {
+            sG[k] = (T)0.f;
+            if constexpr (sizeof(T) == 2) sGL[k] = (T)0.f;
+        }
     }
 
     walk.init(p, rev ? end - 1 : begin);
@@ -291,7 +299,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
             auto b_frag = [&](int tj, int m) { return ld_frag_perm<T>(sB + (16 * tj + r16) * LDB + 32 * m + 4 * g); };
             auto c_frag = [&](int ti, int m) { return ld_frag<T>(sC + (16 * ti + r16) * LDK + 32 * m + 8 * g); };
             auto put = [&](int k, int ti, int tj, const float* v) {
-                st_run<4>(sG + (k * C + 16 * ti + r16) * LDG + slot_col(16 * tj + 4 * g), v);
+                const int o = (k * 6 + ti + (tj & 2)) * SLAB + 8 * ln + 4 * (tj & 1);
+                st_near4(sG + o, sGL + o, v);
             };
             auto below = [&](int ti, int tj, f32x4 acc) {
                 const int i = 16 * ti + r16, last = 16 * tj + 15;
@@ -349,15 +358,19 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
             // columns of one token
 #pragma unroll
             for (int m = 0; m < K / 32; ++m) {
-                Frag sf[NT];
+                typename Near<T>::type sf[NT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) sf[n] = frag_from_tiles<T>(S[2 * m][n], S[2 * m + 1][n]);
+                for (int n = 0; n < NT; ++n) {
+                    const f32x4 a = S[2 * m][n], b = S[2 * m + 1][n];
+                    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                    sf[n] = Near<T>::of(v);
+                }
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) {
-                    const Frag cf = ld_frag<T>(sC + (16 * ti + r16) * LDK + 32 * m + 8 * g);
+                    if (m == 0)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        Y[ti][n] = mma(m == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : Y[ti][n], sf[n], cf);
+                        for (int n = 0; n < NT; ++n) Y[ti][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    mma_near(Y[ti], sf, ld_frag<T>(sC + (16 * ti + r16) * LDK + 32 * m + 8 * g));
                 }
             }
 #pragma unroll
@@ -406,7 +419,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void kda_ssm_chunk_ker
             if constexpr (OUT) {
 #pragma unroll
                 for (int ti = 2 * s; ti < 4; ++ti) {
-                    const Frag gf = ld_frag<T>(sG + (hl * C + 16 * ti + r16) * LDG + 32 * s + 8 * g);
+                    const int o = (hl * 6 + ti + 2 * s) * SLAB + 8 * ln;
+                    if constexpr (sizeof(T) == 2) {
+                        const Frag gl = ld_frag<T>(sGL + o);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) Y[ti][n] = mma(Y[ti][n], xf[n], gl);
+                    }
+                    const Frag gf = ld_frag<T>(sG + o);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) Y[ti][n] = mma(Y[ti][n], xf[n], gf);
                 }

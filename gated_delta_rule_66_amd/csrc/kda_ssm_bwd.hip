@@ -15,10 +15,12 @@
 // products with B and C.  d log a and d delta come from fp32 values of the
 // score tiles and from products whose state operand is split exactly, because
 // their sums over all tokens are fp32 gradients.  bf16 tokens: dx, dB and dC,
-// which leave as bf16, take operands rounded once to bf16: the scaled scores of
-// a head (sM), the heads' summed score gradients, and the states and adjoints
-// of dB's and dC's products.  They are at 0.0023 of their root mean square,
-// where rounding them alone gives 0.0017.  fp32 tokens: fp32 products throughout.
+// which leave as bf16, take their fp32 operands (a head's scaled scores, the
+// heads' summed score gradients, and the states and adjoints of dB's and dC's
+// products) as two bf16 each, exact to 2^-16; one bf16 each would put them at
+// 0.0023 of their root mean square instead of the 0.0017 of their own rounding,
+// with the gradient kernel at 146 us instead of 157 on 8K x 32 heads.  fp32
+// tokens: fp32 products throughout.
 #include "kda_ssm_device.h"
 
 namespace kda {
@@ -73,10 +75,10 @@ __device__ __forceinline__ float sum64(float v) { return sum_groups(sum16(v)); }
 //            summed over the heads in registers
 // A head's rows and states are 80 KB (K = 128, P = 64), which alone take 4 of
 // the 9 us a head, and the LDS holds one workgroup a CU; the rest is the three
-// phases' LDS reads (0.5 MB a head) between barriers.  8K x 32 heads: 146 us
-// (347 MB read, 56 MB written); four waves with states from memory 314 us, all
+// phases' LDS reads (0.6 MB a head) between barriers.  8K x 32 heads: 157 us
+// (347 MB read, 56 MB written); with one bf16 an operand 146 us; four waves with states from memory 314 us, all
 // waves loading the next head at once 166 us.  K = 64, P = 128, 6 heads packed:
-// 65 us.
+// 68 us.
 template <typename T, int K, int P>
 __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     constexpr int TH = 512;
@@ -89,6 +91,7 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     static_assert(C * P / EPP % TH == 0 && (K * P / 4) % TH == 0, "whole pieces");
     typedef typename FragOf<T>::type Frag;
     __shared__ T sB[C * LDK], sC[C * LDK], sX[C * LDP], sDY[C * LDP], sM[C * LDM];
+    __shared__ T sML[sizeof(T) == 2 ? C * LDM : 1];     // sM's lower halves
     __shared__ __align__(16) float sS[STAGED ? K * LDS_ : 1], sE[STAGED ? K * LDS_ : 1];
     // what the step sizes' gradients need of a head, for two heads in turn: the
     // last wave works on it beside the next head's pairs (fp32 at K = P = 128
@@ -179,7 +182,10 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
             *reinterpret_cast<uint4*>(sB + row * LDK + col) = buf_load16(br, (unsigned)(row * (int)f.b_stride + col) * sizeof(T));
             *reinterpret_cast<uint4*>(sC + row * LDK + col) = buf_load16(cr, (unsigned)(row * (int)f.c_stride + col) * sizeof(T));
         }
-        for (int q = tid; q < C * LDM; q += TH) sM[q] = (T)0.f;
+        for (int q = tid; q < C * LDM; q += TH) {
+            sM[q] = (T)0.f;
+            if constexpr (sizeof(T) == 2) sML[q] = (T)0.f;
+        }
     }
     __syncthreads();
     // tile k of wave w is lower tile q = (w + 4) % 8 + 8 k: rows 16 ti + 4 g + e, column 16 tj + r16
@@ -332,7 +338,7 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                 const float row = sum16(pairs[e]);
                 if (r16 == 0) s_row[q][4 * g + e] = row;
             }
-            st_run<4>(sM + j * LDM + i0, mv);
+            st_near4(sM + j * LDM + i0, sML + j * LDM + i0, mv);
             colf = sum_groups(colf);
             cols = sum_groups(cols);
             if (g == 0) {
@@ -398,8 +404,11 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
             for (int s = 0; s < 2; ++s) {
                 const Frag gf = ld_frag_tokens(sDY, LDP, 32 * s, col, lane);
 #pragma unroll
-                for (int t = 0; t < 2 + 2 * s; ++t)
-                    dx[t] = mma(dx[t], gf, ld_frag_perm<T>(sM + (16 * t + r16) * LDM + 32 * s + 4 * g));
+                for (int t = 0; t < 2 + 2 * s; ++t) {
+                    const int at = (16 * t + r16) * LDM + 32 * s + 4 * g;
+                    if constexpr (sizeof(T) == 2) dx[t] = mma(dx[t], gf, ld_frag_perm<T>(sML + at));
+                    dx[t] = mma(dx[t], gf, ld_frag_perm<T>(sM + at));
+                }
             }
             const auto xr = row_rsrc<T>(reinterpret_cast<const T*>(p.dx) + h * P + col, p.dx_stride, t0, len, 16);
 #pragma unroll
@@ -414,7 +423,7 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
             const bool is_c = K == 128 ? k == 0 : w < 4;
             const float* st = is_c ? start : dend;
             const T* tok = is_c ? sDY : sX;
-            Frag sf[P / 32];
+            typename Near<T>::type sf[P / 32];
 #pragma unroll
             for (int m = 0; m < P / 32; ++m) {
                 float v[8];
@@ -422,16 +431,22 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
                     ld8f((is_c ? sS : sE) + (16 * nrow + r16) * LDS_ + 32 * m + 8 * g, v);
                 else
                     ld8f(st + (size_t)(16 * nrow + r16) * P + 32 * m + 8 * g, v);
-                sf[m] = frag_from<T>(v);
+                sf[m] = Near<T>::of(v);
+            }
+            f32x4 v[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) v[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < P / 32; ++m) {
+                Frag f[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) f[t] = ld_frag<T>(tok + (16 * t + r16) * LDP + 32 * m + 8 * g);
+                mma_near(v, sf[m], f);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                f32x4 v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int m = 0; m < P / 32; ++m)
-                    v = mma(v, sf[m], ld_frag<T>(tok + (16 * t + r16) * LDP + 32 * m + 8 * g));
                 const int j = 16 * t + r16;
-                acc[k][t] += v * (is_c ? exp2_pair(s_gate[kGateC][j], s_gate[kGateRest][j]) : s_gate[kGateW][j]);
+                acc[k][t] += v[t] * (is_c ? exp2_pair(s_gate[kGateC][j], s_gate[kGateRest][j]) : s_gate[kGateW][j]);
             }
         }
         if (NB == 1 && w == 7) step_sizes(h, 0, my_dt);
@@ -443,7 +458,8 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     for (int k = 0; k < 2; ++k) {
         if (((w + 4) & 7) + 8 * k < 10) {
             float v[4] = {dG[k][0], dG[k][1], dG[k][2], dG[k][3]};
-            st_run<4>(sM + (16 * tj[k] + r16) * LDM + 16 * ti[k] + 4 * g, v);
+            const int o = (16 * tj[k] + r16) * LDM + 16 * ti[k] + 4 * g;
+            st_near4(sM + o, sML + o, v);
         }
     }
     __syncthreads();
@@ -457,12 +473,14 @@ __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 // dB_j: rows i of the slab at or behind j's tile; dC_i: rows j up to i's tile
-                if (is_c) {
-                    if (t >= 2 * s) acc[k][t] = mma(acc[k][t], rf, ld_frag_tokens(sM, LDM, 32 * s, 16 * t, lane));
-                } else {
-                    if (t < 2 + 2 * s)
-                        acc[k][t] = mma(acc[k][t], rf, ld_frag_perm<T>(sM + (16 * t + r16) * LDM + 32 * s + 4 * g));
-                }
+                if (is_c ? t < 2 * s : t >= 2 + 2 * s) continue;
+                auto part = [&](const T* tile) {
+                    const Frag f = is_c ? ld_frag_tokens(tile, LDM, 32 * s, 16 * t, lane)
+                                        : ld_frag_perm<T>(tile + (16 * t + r16) * LDM + 32 * s + 4 * g);
+                    acc[k][t] = mma(acc[k][t], rf, f);
+                };
+                if constexpr (sizeof(T) == 2) part(sML);
+                part(sM);
             }
         }
         const int row = grp * K + 16 * nrow + 4 * g;

@@ -184,6 +184,66 @@ template <> struct Exact<float> {
     static __device__ __forceinline__ f32x8 of(const float* v) { return frag_from<float>(v); }
 };
 
+// v = hi + lo, hi by truncation, lo rounded: off by 2^-16 relative at most.
+// What an output that is rounded to bf16 behind its products takes of an fp32
+// operand; one bf16 alone would add half as much again as the output's own
+// rounding.  (hi rounded too: 2^-17, and the output pass 3 % slower.)
+struct Split2 {
+    bf16x8 hi, lo;
+};
+__device__ __forceinline__ Split2 split2(const float* v) {
+    unsigned h[4];
+    Split2 s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = hi16_pair(v[2 * i], v[2 * i + 1]);
+        s.lo[2 * i] = (bf16)(v[2 * i] - trunc_bf16(v[2 * i]));
+        s.lo[2 * i + 1] = (bf16)(v[2 * i + 1] - trunc_bf16(v[2 * i + 1]));
+    }
+    s.hi = *reinterpret_cast<bf16x8*>(h);
+    return s;
+}
+// acc[i] += v b[i] or v[i] b: all lower halves first, so that the products of
+// one accumulator are apart
+template <int N> __device__ __forceinline__ void mma_near(f32x4 (&acc)[N], const Split2 (&v)[N], bf16x8 b) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = mma(acc[i], v[i].lo, b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = mma(acc[i], v[i].hi, b);
+}
+template <int N> __device__ __forceinline__ void mma_near(f32x4 (&acc)[N], const f32x8 (&v)[N], f32x8 b) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = mma(acc[i], v[i], b);
+}
+template <int N> __device__ __forceinline__ void mma_near(f32x4 (&acc)[N], const Split2& v, const bf16x8 (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = mma(acc[i], v.lo, b[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = mma(acc[i], v.hi, b[i]);
+}
+template <int N> __device__ __forceinline__ void mma_near(f32x4 (&acc)[N], const f32x8& v, const f32x8 (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = mma(acc[i], v, b[i]);
+}
+template <typename T> struct Near;
+template <> struct Near<bf16> {
+    typedef Split2 type;
+    static __device__ __forceinline__ Split2 of(const float* v) { return split2(v); }
+};
+template <> struct Near<float> {
+    typedef f32x8 type;
+    static __device__ __forceinline__ f32x8 of(const float* v) { return frag_from<float>(v); }
+};
+// the same, of four values stored to two tiles (fp32: to one)
+__device__ __forceinline__ void st_near4(bf16* hi, bf16* lo, const float* v) {
+    bf16x4 l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l[i] = (bf16)(v[i] - trunc_bf16(v[i]));
+    *reinterpret_cast<uint2*>(hi) = make_uint2(hi16_pair(v[0], v[1]), hi16_pair(v[2], v[3]));
+    *reinterpret_cast<bf16x4*>(lo) = l;
+}
+__device__ __forceinline__ void st_near4(float* hi, float*, const float* v) { st_run<4>(hi, v); }
+
 // Step sizes and decays of one chunk and head, five arrays of 64 floats:
 //   c      log2 of the decay from the chunk's start to token j, rounded
 //   delta

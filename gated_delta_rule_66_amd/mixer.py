@@ -298,8 +298,7 @@ def selective_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     ``final_state`` may be ``initial_state`` itself.  The work is done in chunks
     of 64 tokens: a NaN or infinity reaches its own sequence from the start of its
     chunk on (the recurrence and the one-token step: from its token on), never
-    another sequence.  bf16 tokens take bf16 products with fp32 states and decays,
-    fp32 tokens fp32 products.
+    another sequence.
     """
     lead = 2 if cu_seqlens is None else 1
     dev, H, G, K, P, code, xs, ds, bs, cs = _scan_args(x, dt, A, B, C, D, dt_bias, lead)

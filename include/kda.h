@@ -495,10 +495,9 @@ kda_status kda_short_conv_step(int N, int D, int W, kda_dtype dt, kda_activation
  * over 64 tokens stays finite.  Non-finite inputs propagate to their sequence
  * from the start of their 64-token chunk on, never to another sequence.  A
  * sequence without tokens passes its state on.
- * bf16 tokens: states, decays and step sizes are fp32, and the chunk form's
- * products for y round their operands (scores, start state) once to bf16, as y
- * is behind them; those of the gradients dx, dB and dC likewise.  fp32 tokens
- * take fp32 products throughout.
+ * bf16 tokens: states, decays, step sizes and sums are fp32; y, dx, dB and dC
+ * are off by their rounding to bf16 and 2^-16 of the sum of the absolute values
+ * of their terms.
  */
 size_t kda_selective_scan_fwd_workspace_size(int N, int packed, int T, int H, int G, int K, int P, kda_dtype dt);
 kda_status kda_selective_scan_fwd(int N, const int* cu_seqlens, int T, int H, int G, int K, int P, kda_dtype dt,
