@@ -74,11 +74,11 @@ __device__ __forceinline__ float sum64(float v) { return sum_groups(sum16(v)); }
 //   dB, dC:  16 state rows of both (K = 128) or of one of them (K = 64) a wave,
 //            summed over the heads in registers
 // A head's rows and states are 80 KB (K = 128, P = 64), which alone take 4 of
-// the 9 us a head, and the LDS holds one workgroup a CU; the rest is the three
+// the 10 us a head, and the LDS holds one workgroup a CU; the rest is the three
 // phases' LDS reads (0.6 MB a head) between barriers.  8K x 32 heads: 157 us
-// (347 MB read, 56 MB written); with one bf16 an operand 146 us; four waves with states from memory 314 us, all
-// waves loading the next head at once 166 us.  K = 64, P = 128, 6 heads packed:
-// 68 us.
+// (347 MB read, 56 MB written).  With one bf16 an operand 146 us; that with all
+// waves loading the next head at once 166 us, and with four waves and states
+// from memory 314.  K = 64, P = 128, 6 heads packed: 68 us.
 template <typename T, int K, int P>
 __global__ __launch_bounds__(512) void kda_ssm_bwd_kernel(SsmBwdParams p) {
     constexpr int TH = 512;
