@@ -162,7 +162,7 @@ def test_selective_scan_gradients_behind_tokens_that_clear_the_state(dtype):
 
 # ---- group norm: rows behind rows -----------------------------------------------------------
 ROWS = [
-    # more rows than a launch has teams, forward (4096 waves) and backward (3072)
+    # more rows than a launch has teams, forward and backward
     (2600, 2048, 1, "silu", True, True, False, True),       # a block a row
     (2600, 2048, 1, "silu", True, False, True, True),
     (600, 8192, 1, "sigmoid", True, False, True, True),     # 1024 threads; fp32 two accesses a lane
