@@ -15,7 +15,8 @@ BUILD_PATH = os.path.join(PKG, "libkda.so")
 LIB_PATH = os.environ.get("KDA_LIBRARY") or BUILD_PATH
 SOURCES = ["kda_api.cpp", "kda_chunk.hip", "kda_split.hip", "kda_decode.hip", "kda_bwd.hip", "kda_bwd_chunk.hip",
            "kda_noalloc.hip", "kda_fused.hip", "kda_mixer_api.cpp", "kda_short_conv.hip", "kda_group_norm.hip",
-           "kda_ssm.hip", "kda_ssm_bwd.hip"]
+           "kda_ssm.hip", "kda_ssm_bwd.hip", "kda_paged_api.cpp", "kda_kv_cache.hip", "kda_paged_attn.hip",
+           "kda_paged_attn_step.hip", "kda_paged_attn_f32.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,239 @@
+// C ABI of the paged cache operators: argument validation, launch plans,
+// launches.  The declarations and their contracts are in include/kda.h.
+#include "kda.h"
+#include "kda_host.h"
+#include "kda_internal.h"
+#include "kda_paged.h"
+
+using namespace kda;
+
+namespace {
+
+int kv_size(kda_kv_dtype dt) { return dt == KDA_KV_F32 ? 4 : dt == KDA_KV_BF16 ? 2 : 1; }
+bool coded(kda_kv_dtype dt) { return dt == KDA_KV_E4M3 || dt == KDA_KV_I8; }
+
+// sizes and types of a call (no pointers)
+kda_status cache_sizes(int N, const int* cu, int T, kda_dtype dt, const kda_paged_cache* c, long long* M) {
+    if (!c || N < 0 || T < 0 || !dtype_ok(dt)) return KDA_ERR_INVALID_ARG;
+    if (c->dt < KDA_KV_F32 || c->dt > KDA_KV_I8 || c->pages < 0 || c->heads <= 0 || c->blocks < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return KDA_ERR_UNSUPPORTED;
+    const int ps = c->page_size;
+    if (ps < 16 || ps > 256 || (ps & (ps - 1))) return KDA_ERR_UNSUPPORTED;
+    if ((long long)c->blocks * ps > 1LL << 30 || c->heads > 65535) return KDA_ERR_UNSUPPORTED;
+    if (!coded(c->dt) && (int)c->dt != (int)dt) return KDA_ERR_UNSUPPORTED;
+    if (!token_count(cu, N, T, M)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+long long page_width(const kda_paged_cache* c) { return (long long)c->heads * c->page_size * c->head_dim; }
+
+// `rows` rows of 4-byte elements `stride` apart stay within 62 bits of bytes
+bool spans(long long rows, long long stride) { return rows <= 1 || (stride <= 1LL << 40 && stride <= (1LL << 60) / rows); }
+
+kda_status cache_pointers(int N, const int* cu, const kda_paged_cache* c) {
+    const int es = kv_size(c->dt);
+    if (!aligned(cu, 4)) return KDA_ERR_INVALID_ARG;
+    if (c->pages > 0) {
+        if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return KDA_ERR_INVALID_ARG;
+        if (c->pages > 1)
+            for (long long st : {c->k_page_stride, c->v_page_stride}) {
+                if (st < page_width(c) || st % (16 / es)) return KDA_ERR_INVALID_ARG;
+                if (!spans(c->pages, st)) return KDA_ERR_UNSUPPORTED;
+            }
+        if (coded(c->dt) && (!c->k_scale || !c->v_scale)) return KDA_ERR_INVALID_ARG;
+    }
+    if (!coded(c->dt) && (c->k_scale || c->v_scale)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)) return KDA_ERR_INVALID_ARG;
+    if (N > 0 && (!c->seq_lens || !aligned(c->seq_lens, 4))) return KDA_ERR_INVALID_ARG;
+    if (N > 0 && c->blocks > 0 && (!c->block_table || !aligned(c->block_table, 4))) return KDA_ERR_INVALID_ARG;
+    if (N > 1 && c->block_table_stride < c->blocks) return KDA_ERR_INVALID_ARG;
+    if (!spans(N, c->block_table_stride)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+PagedCache view_of(const kda_paged_cache* c) {
+    PagedCache v{};
+    const size_t es = (size_t)kv_size(c->dt);
+    v.k = (char*)c->k; v.v = (char*)c->v;
+    v.ks = c->k_scale; v.vs = c->v_scale;
+    v.k_page = (c->pages > 1 ? (size_t)c->k_page_stride : 0) * es;
+    v.v_page = (c->pages > 1 ? (size_t)c->v_page_stride : 0) * es;
+    v.table = c->block_table; v.table_stride = c->block_table_stride;
+    v.lens = c->seq_lens;
+    v.pages = c->pages; v.blocks = c->blocks; v.Hk = c->heads;
+    while ((1 << v.lg_page) < c->page_size) ++v.lg_page;
+    return v;
+}
+
+// the bytes of the cache's tensors
+Span pages_span(const kda_paged_cache* c, const void* p, long long stride) {
+    const long long es = kv_size(c->dt), w = page_width(c) * es;
+    return Span{p, c->pages, c->pages > 1 ? stride * es : w, w};
+}
+Span scale_span(const kda_paged_cache* c, const void* p) {
+    return flat_span(p, (size_t)c->pages * c->heads * c->page_size);
+}
+Span table_span(int N, const kda_paged_cache* c) {
+    return Span{c->block_table, N, (N > 1 ? c->block_table_stride : c->blocks) * 4LL, c->blocks * 4LL};
+}
+// token rows that an access of 16 bytes a lane takes
+bool rows_ok(const void* p, long long M, long long width, long long stride, kda_dtype dt) {
+    return p && aligned(p, 16) && (M <= 1 || (stride >= width && stride % (long long)(16 / esize(dt)) == 0));
+}
+
+// Heads of a block: all of them where the tokens fill the card (the table is
+// looked up once for a block), else fewer.
+int io_heads(long long token_blocks, int heads) {
+    int n = heads;
+    while (n > 1 && token_blocks * ((heads + n - 1) / n) < 2048) n = (n + 1) / 2;
+    return n;
+}
+
+kda_status cache_io(bool write, int N, const int* cu, int T, kda_dtype dt, void* k, long long k_stride, void* v,
+                    long long v_stride, const kda_paged_cache* c, hipStream_t stream) {
+    long long M;
+    kda_status s = cache_sizes(N, cu, T, dt, c, &M);
+    if (s != KDA_OK) return s;
+    if (N == 0 || M == 0) return KDA_OK;
+    s = cache_pointers(N, cu, c);
+    if (s != KDA_OK) return s;
+    const long long width = (long long)c->heads * c->head_dim, es = (long long)esize(dt);
+    if (!rows_ok(k, M, width, k_stride, dt) || !rows_ok(v, M, width, v_stride, dt)) return KDA_ERR_INVALID_ARG;
+    if (!spans(M, k_stride) || !spans(M, v_stride)) return KDA_ERR_UNSUPPORTED;
+    const Span sk{k, M, k_stride * es, width * es}, sv{v, M, v_stride * es, width * es};
+    const Span ck = pages_span(c, c->k, c->k_page_stride), cv = pages_span(c, c->v, c->v_page_stride);
+    const Span ks = scale_span(c, c->k_scale), vs = scale_span(c, c->v_scale);
+    const Span tab = table_span(N, c), len = flat_span(c->seq_lens, (size_t)N * 4);
+    const Span off = flat_span(cu, (size_t)(N + 1) * 4);
+    if (write ? clash({ck, cv, ks, vs}, {sk, sv, tab, len, off}) : clash({sk, sv}, {ck, cv, ks, vs, tab, len, off}))
+        return KDA_ERR_INVALID_ARG;
+    CacheIoParams p{};
+    p.sv = SeqView{cu, N, T};
+    p.c = view_of(c);
+    p.k = (char*)k; p.v = (char*)v;
+    p.k_stride = (size_t)(k_stride * es); p.v_stride = (size_t)(v_stride * es);
+    p.M = (int)M;
+    const long long tb = (M + 15) / 16;
+    p.heads_per_block = io_heads(tb, c->heads);
+    const int hb = (c->heads + p.heads_per_block - 1) / p.heads_per_block;
+    if (tb * hb * 256 >= 1LL << 32) return KDA_ERR_UNSUPPORTED;
+    if (write)
+        KDA_LAUNCH("cache_write", launch_cache_write((int)dt, (int)c->dt, c->head_dim, p, (int)tb, hb, stream));
+    else
+        KDA_LAUNCH("cache_read", launch_cache_read((int)dt, (int)c->dt, c->head_dim, p, (int)tb, hb, stream));
+    return KDA_OK;
+}
+
+struct AttnPlan {
+    AttnKind kind;
+    int M, splits, split_len;
+    long long tiles;
+    int tiles_per_seq;
+    size_t part, bytes;     // of the parts, of the workspace
+};
+// The plan goes by sizes alone, so that a call's plan is its workspace's.
+AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_paged_cache* c) {
+    AttnPlan a{};
+    const long long G = H / c->heads, M = packed ? (long long)T : (long long)N * T;
+    const long long per = N > 0 ? M * G / N : 0;        // rows of a sequence, on average
+    a.kind = dt == KDA_F32 ? kAttnF32 : per <= 16 ? kAttnStep16 : per <= 32 ? kAttnStep32 : kAttnChunk;
+    a.M = a.kind == kAttnStep16 ? 16 : a.kind == kAttnStep32 ? 32 : 128;
+    const bool step = a.kind == kAttnStep16 || a.kind == kAttnStep32;
+    a.tiles_per_seq = packed ? 0 : (int)((T * G + a.M - 1) / a.M);
+    a.tiles = packed ? M * G / a.M + N : (long long)N * a.tiles_per_seq;
+    const long long units = a.tiles * c->heads, ctx = (long long)c->blocks * c->page_size;
+    const long long want = step ? 4096 : 1024, least = step ? 128 : 256;
+    long long n = units > 0 ? want / units : 1;
+    if (n < 1 || M * H >= 1LL << 23) n = 1;
+    long long len = n > 1 ? (ctx + n - 1) / n : ctx;
+    len = (len + 127) / 128 * 128;
+    if (len < least) len = least;
+    a.split_len = (int)len;
+    a.splits = ctx > 0 ? (int)((ctx + len - 1) / len) : 1;
+    if (a.splits > 1) {
+        const size_t rows = (size_t)units * a.splits * a.M;
+        a.part = align256(rows * c->head_dim * sizeof(float));
+        a.bytes = a.part + rows * 2 * sizeof(float);
+    }
+    return a;
+}
+
+kda_status attn_sizes(int N, const int* cu, int T, int H, kda_dtype dt, const kda_paged_cache* c, long long* M) {
+    kda_status s = cache_sizes(N, cu, T, dt, c, M);
+    if (s != KDA_OK) return s;
+    if (H <= 0 || H % c->heads) return KDA_ERR_INVALID_ARG;
+    if (H > 65535 || *M * (H / c->heads) > 2147483647LL - 4096) return KDA_ERR_UNSUPPORTED;
+    if (N == 0) return KDA_OK;
+    const AttnPlan a = attn_plan(N, cu != nullptr, T, H, dt, c);
+    if (a.tiles > 2147483647LL || a.tiles * a.splits * c->heads * 256 >= 1LL << 32) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_kv_cache_write(int N, const int* cu_seqlens, int T, kda_dtype dt, const void* k, long long k_stride,
+                              const void* v, long long v_stride, const kda_paged_cache* cache, hipStream_t stream) {
+    return cache_io(true, N, cu_seqlens, T, dt, const_cast<void*>(k), k_stride, const_cast<void*>(v), v_stride, cache,
+                    stream);
+}
+
+kda_status kda_kv_cache_read(int N, const int* cu_seqlens, int T, kda_dtype dt, void* k, void* v,
+                             const kda_paged_cache* cache, hipStream_t stream) {
+    const long long row = cache ? (long long)cache->heads * cache->head_dim : 0;
+    return cache_io(false, N, cu_seqlens, T, dt, k, row, v, row, cache, stream);
+}
+
+size_t kda_paged_attn_workspace_size(int N, int packed, int T, int H, kda_dtype dt, const kda_paged_cache* cache) {
+    long long M;
+    const int some = 0;
+    if (attn_sizes(N, packed ? &some : nullptr, T, H, dt, cache, &M) != KDA_OK) return (size_t)-1;
+    return N == 0 || M == 0 ? 0 : attn_plan(N, packed != 0, T, H, dt, cache).bytes;
+}
+
+kda_status kda_paged_attn(int N, const int* cu_seqlens, int T, int H, kda_dtype dt, float scale, const void* q,
+                          long long q_stride, const void* gate, long long gate_stride, void* o,
+                          const kda_paged_cache* cache, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    long long M;
+    kda_status s = attn_sizes(N, cu_seqlens, T, H, dt, cache, &M);
+    if (s != KDA_OK) return s;
+    if (!(scale > 0.f) || !(scale <= 3.4028234e38f)) return KDA_ERR_INVALID_ARG;
+    if (N == 0 || M == 0) return KDA_OK;
+    s = cache_pointers(N, cu_seqlens, cache);
+    if (s != KDA_OK) return s;
+    const kda_paged_cache* c = cache;
+    const long long width = (long long)H * c->head_dim, es = (long long)esize(dt);
+    if (!rows_ok(q, M, width, q_stride, dt) || (gate && !rows_ok(gate, M, width, gate_stride, dt)) || !o ||
+        !aligned(o, 16) || !aligned(workspace, 16))
+        return KDA_ERR_INVALID_ARG;
+    if (!spans(M, q_stride) || (gate && !spans(M, gate_stride))) return KDA_ERR_UNSUPPORTED;
+    const AttnPlan a = attn_plan(N, cu_seqlens != nullptr, T, H, dt, c);
+    const Span so{o, M, width * es, width * es}, sq{q, M, q_stride * es, width * es};
+    const Span sz{gate, M, gate_stride * es, width * es};
+    if (clash({so, flat_span(workspace, a.bytes)},
+              {sq, sz, pages_span(c, c->k, c->k_page_stride), pages_span(c, c->v, c->v_page_stride),
+               scale_span(c, c->k_scale), scale_span(c, c->v_scale), table_span(N, c),
+               flat_span(c->seq_lens, (size_t)N * 4), flat_span(cu_seqlens, (size_t)(N + 1) * 4)}))
+        return KDA_ERR_INVALID_ARG;
+    if (a.bytes && (!workspace || workspace_bytes < a.bytes)) return KDA_ERR_WORKSPACE;
+    AttnParams p{};
+    p.sv = SeqView{cu_seqlens, N, T};
+    p.c = view_of(c);
+    p.q = (const char*)q; p.q_stride = (size_t)(q_stride * es);
+    p.z = (const char*)gate; p.z_stride = (size_t)(gate_stride * es);
+    p.o = (char*)o;
+    p.H = H; p.G = H / c->heads;
+    p.c_log2 = scale * 1.4426950408889634f;
+    p.M = a.M; p.tiles = (int)a.tiles; p.tiles_per_seq = a.tiles_per_seq;
+    p.splits = a.splits; p.split_len = a.split_len;
+    p.part = (float*)workspace;
+    p.ml = (float*)((char*)workspace + a.part);
+    const char* name = a.kind == kAttnF32 ? "attn_f32" : a.kind == kAttnChunk ? "attn_chunk" : "attn_step";
+    KDA_LAUNCH(name, launch_attn(a.kind, (int)c->dt, c->head_dim, p, stream));
+    if (a.splits > 1) KDA_LAUNCH("attn_join", launch_attn_join((int)dt, c->head_dim, p, (int)M, stream));
+    return KDA_OK;
+}
+
+}  // extern "C"

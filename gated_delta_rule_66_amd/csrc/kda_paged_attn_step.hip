@@ -1,0 +1,465 @@
+// Attention of few rows (one or a few new tokens a sequence) over a paged cache.
+//
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - max)
+//
+// Bound by reading the cache once.  A tile is 16 NB rows (tokens times the
+// heads that share a cache head); a workgroup's four waves take blocks of 32
+// positions in turn and keep maximum, sum and output of their own, joined at
+// the end.  Nothing of the cache goes through LDS:
+//   * S^T = K Q^T with 16x16x32 products: an operand lane holds eight (bf16) or
+//     two times eight (8 bits) neighbouring channels of one position, which is
+//     one 16-byte load.  The channels' order is free as long as Q has the same.
+//   * O^T = V^T P^T: P^T comes out of S^T as it sits in the accumulator if lane
+//     group g's eight positions are 4 g + i of either half of the block.  A lane
+//     loads D / 16 neighbouring channels of those eight positions (a group of 16
+//     lanes reads whole rows), and eight by eight values are transposed between
+//     its own registers, one instruction for two values; product j then makes
+//     channels (D / 16) rho + j, rho the accumulator's row.
+// P is rounded to bf16 for its product (relative 2^-9, as V's own rounding; the
+// sum is taken before it), everything else is fp32.
+#include "kda_paged_attn.h"
+
+namespace kda {
+
+namespace {
+
+template <int KV> constexpr int kElem = KV == kKvF32 ? 4 : KV == kKvBf16 ? 2 : 1;
+
+// N bytes of a row through a range-checked resource: zeros behind its end
+template <int N> struct Raw {
+    unsigned w[N / 4];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int off) {
+        if constexpr (N == 16) {
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = v[i];
+        } else if constexpr (N == 8) {
+            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+            w[0] = v[0];
+            w[1] = v[1];
+        } else {
+            w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+        }
+    }
+};
+
+// One block of 32 positions as it is loaded.
+template <int KV, int D> struct Block {
+    static constexpr int E = kElem<KV>;
+    static constexpr int KL = D * E / 64;           // 16-byte loads of a K half (16 positions) a lane
+    static constexpr int DV = D / 16;               // channels of V a lane
+    static constexpr bool CODES = KV >= kKvE4m3;
+    Raw<16> k[2][KL];
+    Raw<DV * E> v[8];
+    unsigned ks[2], vs[2][4];                       // scale bytes: K's row of the lane, V's four rows of either half
+    int valid;                                      // bit h: half h's page is there
+
+    // resources of a half's rows of K or V (rows behind the sequence's end read zeros)
+    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rows(const PagedCache& c, const char* base, size_t page_bytes,
+                                                                 int page, int hk, int row, int left) {
+        const char* at = base + (size_t)max(page, 0) * page_bytes + ((((size_t)hk << c.lg_page) + row) * D) * E;
+        return make_rsrc_n(at, page < 0 ? 0u : (unsigned)(min(max(left, 0), 16) * D * E));
+    }
+    __device__ __forceinline__ void load_k(const PagedCache& c, PageWalk& w, int hk, int pos, int end, int lane) {
+        valid = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = pos + 16 * h, page = at < end ? w.page(at >> c.lg_page) : -1;
+            const int row = at & ((1 << c.lg_page) - 1);
+            valid |= (page >= 0) << h;
+            const auto r = rows(c, c.k, c.k_page, page, hk, row, end - at);
+#pragma unroll
+            for (int i = 0; i < KL; ++i) k[h][i].load(r, (lane & 15) * D * E + (4 * i + (lane >> 4)) * 16);
+            if constexpr (CODES) {
+                const auto s = make_rsrc_n(c.ks + ((((size_t)max(page, 0) * c.Hk + hk) << c.lg_page) + row), page < 0 ? 0u : 16u);
+                ks[h] = __builtin_amdgcn_raw_buffer_load_b8(s, lane & 15, 0, 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void load_v(const PagedCache& c, PageWalk& w, int hk, int pos, int end, int lane) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = pos + 16 * h, page = at < end ? w.page(at >> c.lg_page) : -1;
+            const int row = at & ((1 << c.lg_page) - 1);
+            const auto r = rows(c, c.v, c.v_page, page, hk, row, end - at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[4 * h + i].load(r, (4 * (lane >> 4) + i) * D * E + (lane & 15) * DV * E);
+            if constexpr (CODES) {
+                const auto s = make_rsrc_n(c.vs + ((((size_t)max(page, 0) * c.Hk + hk) << c.lg_page) + row), page < 0 ? 0u : 16u);
+                const unsigned b = __builtin_amdgcn_raw_buffer_load_b32(s, 4 * (lane >> 4), 0, 0);
+                vs[h][0] = b;
+            }
+        }
+    }
+    // K operand of product s: channels of Q's operand s
+    __device__ __forceinline__ bf16x8 kfrag(int h, int s) const {
+        u32x4 u;
+        if constexpr (!CODES) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = k[h][s].w[i];
+        } else {
+            const Codes<KV> d(ks[h]);
+            unsigned o[4];
+            d.bf(k[h][s >> 1].w[2 * (s & 1)], o);
+            d.bf(k[h][s >> 1].w[2 * (s & 1) + 1], o + 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = o[i];
+        }
+        return __builtin_bit_cast(bf16x8, u);
+    }
+    // V's eight positions as pairs of bf16: [position][DV / 2]
+    __device__ __forceinline__ void vpairs(unsigned (&o)[8][DV / 2]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (!CODES) {
+#pragma unroll
+                for (int w = 0; w < DV / 2; ++w) o[i][w] = v[i].w[w];
+            } else {
+                const Codes<KV> d(vs[i >> 2][0] >> (8 * (i & 3)) & 255u);
+#pragma unroll
+                for (int w = 0; w < DV / 4; ++w) d.bf(v[i].w[w], &o[i][2 * w]);
+            }
+        }
+    }
+};
+
+// first channel of a lane's operand s of Q, the order of Block::kfrag
+template <int KV> __device__ __forceinline__ int q_channel(int s, int g) {
+    return KV >= kKvE4m3 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
+}
+
+template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 : 2) void kda_attn_step_kernel(AttnParams p) {
+    constexpr int R = 16 * NB, DV = D / 16, KS = D / 32, LD = D + 4;
+    __shared__ float lds_o[2][R][LD];
+    __shared__ float lds_ml[2][R][2];
+    AttnTile t;
+    if (!t.init(p, blockIdx.x)) return;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4, c16 = lane & 15;
+
+    // Q as an operand, zeros behind the sequence's rows
+    bf16x8 q[NB][KS];
+    int lim[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int r = t.r0 + 16 * nb + c16;
+        lim[nb] = t.limit(r, p.G);
+        const int tok = r / p.G, head = t.hk * p.G + r - tok * p.G;
+        const char* row = p.q + (size_t)(t.first + tok) * p.q_stride + (size_t)head * D * 2;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            u32x4 u = {0u, 0u, 0u, 0u};
+            if (r < t.rows) u = *reinterpret_cast<const u32x4*>(row + q_channel<KV>(s, g) * 2);
+            q[nb][s] = __builtin_bit_cast(bf16x8, u);
+        }
+    }
+    const int lim_first = t.limit(t.r0, p.G);
+
+    f32x4 acc[DV][NB];
+    float m[NB], l[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        m[nb] = -INFINITY;
+        l[nb] = 0.f;
+#pragma unroll
+        for (int j = 0; j < DV; ++j) acc[j][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const float c = p.c_log2, lazy = kLazy / c;
+
+    int pos = t.lo + 32 * wave;
+    if (pos < t.hi) {
+        PageWalk walk;
+        walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);
+        Block<KV, D> b;
+        b.load_k(p.c, walk, t.hk, pos, t.hi, lane);
+        b.load_v(p.c, walk, t.hk, pos, t.hi, lane);
+        for (; pos < t.hi; pos += 128) {
+            f32x4 s[2][NB];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) s[h][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bf16x8 kf = b.kfrag(h, k);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) s[h][nb] = mma(s[h][nb], kf, q[nb][k]);
+                }
+            const int valid = b.valid;
+            // rows of the tile that see less than the block, or pages that are not there
+            const bool masked = pos + 31 > lim_first || valid != 3;
+            if (pos + 128 < t.hi) b.load_k(p.c, walk, t.hk, pos + 128, t.hi, lane);
+            if (masked) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (pos + 16 * h + 4 * g + e > lim[nb] || !(valid >> h & 1)) s[h][nb][e] = -INFINITY;
+            }
+            // the running maximum moves for the whole wave, and only when a score passes it by enough
+            bool up = false;
+            float top[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                top[nb] = fmaxf(fmaxf(fmaxf(s[0][nb][0], s[0][nb][1]), fmaxf(s[0][nb][2], s[0][nb][3])),
+                                fmaxf(fmaxf(s[1][nb][0], s[1][nb][1]), fmaxf(s[1][nb][2], s[1][nb][3])));
+                up |= top[nb] > m[nb] + lazy;
+            }
+            if (__any(up)) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    float x = fmaxf(top[nb], __shfl_xor(top[nb], 16));
+                    x = fmaxf(x, __shfl_xor(x, 32));
+                    const float mn = fmaxf(m[nb], x);
+                    const float a = mn == -INFINITY ? 1.f : fast_exp2((m[nb] - mn) * c);
+                    m[nb] = mn;
+                    l[nb] *= a;
+#pragma unroll
+                    for (int j = 0; j < DV; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][nb][e] *= a;
+                }
+            }
+            bf16x8 pf[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const float mc = m[nb] == -INFINITY ? 0.f : m[nb] * c;
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = fast_exp2(fmaf(s[i >> 2][nb][i & 3], c, -mc));
+                    l[nb] += x[i];
+                }
+                pf[nb] = frag_from<bf16>(x);
+            }
+            unsigned vp[8][DV / 2];
+            b.vpairs(vp);
+            bool poison = false;
+            if (masked) {
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int w = 0; w < DV / 2; ++w) bad |= not_finite(vp[i][w]);
+                poison = __any(bad);
+            }
+#pragma unroll
+            for (int j = 0; j < DV; ++j) {
+                u32x4 u;
+                // halves j & 1 of two positions' dword j / 2
+                const unsigned sel = j & 1 ? 0x07060302u : 0x05040100u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[i] = __builtin_amdgcn_perm(vp[2 * i + 1][j >> 1], vp[2 * i][j >> 1], sel);
+                bf16x8 vf = __builtin_bit_cast(bf16x8, u);
+                if (!poison) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) acc[j][nb] = mma(acc[j][nb], vf, pf[nb]);
+                } else {
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float one[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            one[i] = pos + 16 * (i >> 2) + 4 * g + (i & 3) <= lim[nb] && (valid >> (i >> 2) & 1) ? 1.f : 0.f;
+                        const bf16x8 of = frag_from<bf16>(one);
+                        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                        const f32x4 plus = mma(zero, flag8(vf, false), of), minus = mma(zero, flag8(vf, true), of);
+                        acc[j][nb] = mma(acc[j][nb], clean8(vf), pf[nb]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][nb][e] = poisoned(acc[j][nb][e], plus[e], minus[e]);
+                    }
+                }
+            }
+            if (pos + 128 < t.hi) b.load_v(p.c, walk, t.hk, pos + 128, t.hi, lane);
+        }
+    }
+    // sums over the lane groups' positions
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        l[nb] += __shfl_xor(l[nb], 16);
+        l[nb] += __shfl_xor(l[nb], 32);
+    }
+    // waves 2 and 3 join 0 and 1, then 1 joins 0
+#pragma unroll
+    for (int half = 2; half > 0; half >>= 1) {
+        if (wave >= half && wave < 2 * half) {
+            const int to = wave - half;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const int r = 16 * nb + c16;
+                if (g == 0) {
+                    lds_ml[to][r][0] = m[nb];
+                    lds_ml[to][r][1] = l[nb];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int j = 0; j < DV; j += 4)
+                        *reinterpret_cast<f32x4*>(&lds_o[to][r][DV * (4 * g + e) + j]) =
+                            f32x4{acc[j][nb][e], acc[j + 1][nb][e], acc[j + 2][nb][e], acc[j + 3][nb][e]};
+            }
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const int r = 16 * nb + c16;
+                const float mo = lds_ml[wave][r][0], lo = lds_ml[wave][r][1], mn = fmaxf(m[nb], mo);
+                const float a = m[nb] == mn ? 1.f : fast_exp2((m[nb] - mn) * c);
+                const float b = mo == mn ? 1.f : fast_exp2((mo - mn) * c);
+                m[nb] = mn;
+                l[nb] = l[nb] * a + lo * b;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int j = 0; j < DV; j += 4) {
+                        const f32x4 o = *reinterpret_cast<const f32x4*>(&lds_o[wave][r][DV * (4 * g + e) + j]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[j + i][nb][e] = acc[j + i][nb][e] * a + o[i] * b;
+                    }
+            }
+        }
+        __syncthreads();
+    }
+    if (wave) return;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int r = t.r0 + 16 * nb + c16;
+        if (r >= t.rows) continue;
+        if (t.splits > 1) {
+            float* po = p.part + (t.unit * R + 16 * nb + c16) * D;
+            if (g == 0) {
+                p.ml[(t.unit * R + 16 * nb + c16) * 2] = m[nb];
+                p.ml[(t.unit * R + 16 * nb + c16) * 2 + 1] = l[nb];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < DV; j += 4)
+                    *reinterpret_cast<f32x4*>(po + DV * (4 * g + e) + j) =
+                        f32x4{acc[j][nb][e], acc[j + 1][nb][e], acc[j + 2][nb][e], acc[j + 3][nb][e]};
+            continue;
+        }
+        const int tok = r / p.G, head = t.hk * p.G + r - tok * p.G;
+        const float inv = l[nb] == 0.f ? 0.f : 1.f / l[nb];
+        const size_t at = (size_t)head * D;
+        bf16* o = reinterpret_cast<bf16*>(p.o) + (size_t)(t.first + tok) * p.H * D + at;
+        const bf16* z = reinterpret_cast<const bf16*>(p.z + (size_t)(t.first + tok) * p.z_stride) + at;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float x[DV];
+#pragma unroll
+            for (int j = 0; j < DV; ++j) x[j] = acc[j][nb][e] * inv;
+            const int d = DV * (4 * g + e);
+            if (p.z) {
+#pragma unroll
+                for (int j = 0; j < DV; ++j) x[j] = gate_of<bf16>(x[j], (float)z[d + j]);
+            }
+            st_run<DV>(o + d, x);
+        }
+    }
+}
+
+// Joins the ranges of tiles that were split: a team of lanes a row (token and
+// head), D / 4 lanes a range's row, the ranges dealt to the team's slots.
+template <typename T, int D> __global__ __launch_bounds__(512) void kda_attn_join_kernel(AttnParams p, int rows) {
+    constexpr int LANES = D / 4, SLOTS = 512 / LANES;
+    __shared__ float lds[SLOTS][D + 4];
+    __shared__ float lds_l[SLOTS];
+    const int tok = blockIdx.x / p.H, head = blockIdx.x - tok * p.H;
+    const int hk = head / p.G, gq = head - hk * p.G;
+    int seq, first, n, slot0;
+    if (p.sv.cu) {
+        if (tok < p.sv.cu[0] || tok >= p.sv.cu[p.sv.N]) return;
+        int a = 0, b = p.sv.N;
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (p.sv.cu[mid] <= tok)
+                a = mid;
+            else
+                b = mid;
+        }
+        seq = a;
+        slot0 = AttnTile::slot(p, seq);
+    } else {
+        seq = tok / p.sv.T;
+        slot0 = seq * p.tiles_per_seq;
+    }
+    seq_span(p.sv, seq, &first, &n);
+    const int r = (tok - first) * p.G + gq, at = r / p.M;
+    if (tok < first || tok >= first + n || slot0 + at >= p.tiles) return;
+    const int L = seq_positions(p.c, seq);
+    const int end = max(L - n + (min((at + 1) * p.M, n * p.G) - 1) / p.G + 1, 0);
+    const int splits = end > 0 ? (end - 1) / p.split_len + 1 : 1;
+    if (splits <= 1) return;
+    const size_t unit = ((size_t)(slot0 + at) * p.c.Hk + hk) * p.splits;
+    const size_t row = unit * p.M + (r - at * p.M);     // of range 0; ranges are M rows apart
+    float top = -INFINITY;
+    for (int s = 0; s < splits; ++s) top = fmaxf(top, p.ml[(row + (size_t)s * p.M) * 2]);
+    const int lane = threadIdx.x % LANES, my = threadIdx.x / LANES;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;
+    for (int s = my; s < splits; s += SLOTS) {
+        const size_t x = row + (size_t)s * p.M;
+        const float m = p.ml[x * 2], w = m == top ? 1.f : fast_exp2((m - top) * p.c_log2);
+        const f32x4 v = *reinterpret_cast<const f32x4*>(p.part + x * D + 4 * lane);
+        l += w * p.ml[x * 2 + 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += w * v[i];
+    }
+    *reinterpret_cast<f32x4*>(&lds[my][4 * lane]) = o;
+    if (lane == 0) lds_l[my] = l;
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    const int d = threadIdx.x;
+    float sum = 0.f, all = 0.f;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+        sum += lds[s][d];
+        all += lds_l[s];
+    }
+    float x = all == 0.f ? 0.f : sum / all;
+    const size_t col = (size_t)head * D + d;
+    if (p.z) x = gate_of<T>(x, to_f32(reinterpret_cast<const T*>(p.z + (size_t)tok * p.z_stride)[col]));
+    reinterpret_cast<T*>(p.o)[(size_t)tok * p.H * D + col] = from_f32<T>(x);
+}
+
+template <int KV, int D> hipError_t launch_step(AttnKind kind, const AttnParams& p, int grid, hipStream_t st) {
+    if (kind == kAttnStep16)
+        kda_attn_step_kernel<KV, D, 1><<<grid, 256, 0, st>>>(p);
+    else
+        kda_attn_step_kernel<KV, D, 2><<<grid, 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_step(AttnKind kind, int kv, int D, const AttnParams& p, int grid, hipStream_t st) {
+    if (D == 128)
+        return kv == kKvE4m3 ? launch_step<kKvE4m3, 128>(kind, p, grid, st) : kv == kKvI8 ? launch_step<kKvI8, 128>(kind, p, grid, st)
+                                                                                          : launch_step<kKvBf16, 128>(kind, p, grid, st);
+    return kv == kKvE4m3 ? launch_step<kKvE4m3, 64>(kind, p, grid, st) : kv == kKvI8 ? launch_step<kKvI8, 64>(kind, p, grid, st)
+                                                                                     : launch_step<kKvBf16, 64>(kind, p, grid, st);
+}
+
+hipError_t launch_attn_join(int dtype, int D, const AttnParams& p, int M_tokens, hipStream_t st) {
+    const int grid = M_tokens * p.H;
+    if (dtype) {
+        if (D == 128)
+            kda_attn_join_kernel<bf16, 128><<<grid, 512, 0, st>>>(p, grid);
+        else
+            kda_attn_join_kernel<bf16, 64><<<grid, 512, 0, st>>>(p, grid);
+    } else {
+        if (D == 128)
+            kda_attn_join_kernel<float, 128><<<grid, 512, 0, st>>>(p, grid);
+        else
+            kda_attn_join_kernel<float, 64><<<grid, 512, 0, st>>>(p, grid);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace kda

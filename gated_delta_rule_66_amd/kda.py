@@ -52,6 +52,10 @@ EXPORTED_SYMBOLS = (
     "kda_group_norm_fwd",
     "kda_group_norm_bwd_workspace_size",
     "kda_group_norm_bwd",
+    "kda_kv_cache_write",
+    "kda_kv_cache_read",
+    "kda_paged_attn_workspace_size",
+    "kda_paged_attn",
     "kda_profile_start",
     "kda_profile_stop",
 )
@@ -65,6 +69,15 @@ class KDAError(RuntimeError):
 
 class Plan(ctypes.Structure):
     _fields_ = [("n_seg", ctypes.c_int), ("v_block", ctypes.c_int), ("split", ctypes.c_int)]
+
+
+class PagedCache(ctypes.Structure):
+    """kda_paged_cache of include/kda.h."""
+    _fields_ = [("dt", ctypes.c_int), ("pages", ctypes.c_int), ("heads", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("blocks", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_longlong), ("v_page_stride", ctypes.c_longlong),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("block_table_stride", ctypes.c_longlong), ("seq_lens", ctypes.c_void_p)]
 
 
 _lib = None
@@ -125,6 +138,15 @@ def load_library(path: str = LIB_PATH):
     lib.kda_group_norm_fwd.argtypes = [i] * 7 + [f, p, ll, p, p, p, ll, p, p]
     lib.kda_group_norm_bwd_workspace_size.argtypes = [i] * 4
     lib.kda_group_norm_bwd.argtypes = [i] * 7 + [f, p, ll, p, p, p, ll] + [p] * 5 + [p, sz, p]
+    cache = ctypes.POINTER(PagedCache)
+    lib.kda_kv_cache_write.argtypes = [i, p, i, i, p, ll, p, ll, cache, p]
+    lib.kda_kv_cache_write.restype = i
+    lib.kda_kv_cache_read.argtypes = [i, p, i, i, p, p, cache, p]
+    lib.kda_kv_cache_read.restype = i
+    lib.kda_paged_attn_workspace_size.argtypes = [i, i, i, i, i, cache]
+    lib.kda_paged_attn_workspace_size.restype = sz
+    lib.kda_paged_attn.argtypes = [i, p, i, i, i, f, p, ll, p, ll, p, cache, p, sz, p]
+    lib.kda_paged_attn.restype = i
     for name in EXPORTED_SYMBOLS:
         if name.startswith(("kda_short_conv", "kda_selective_scan", "kda_group_norm")):
             getattr(lib, name).restype = sz if name.endswith("_workspace_size") else i

@@ -580,6 +580,104 @@ kda_status kda_group_norm_bwd(int rows, int C, int groups, kda_dtype dt, kda_act
                               float* dweight, float* dbias, void* d_gate, void* workspace, size_t workspace_bytes,
                               hipStream_t stream);
 
+/* ---- paged cache ----------------------------------------------------------------
+ *
+ * The layers between the recurrent ones that attend to every position keep
+ * their keys and values: writing a paged cache (as it is or in 8 bits), reading
+ * it back, and the attention of new tokens over it, from one token a sequence
+ * to whole prompts.  The sequences, token rows, row strides, overlaps and
+ * streams follow the mixer operators' conventions; results are deterministic.
+ *
+ * A sequence has seq_lens[i] positions, its new tokens among them: token t of n
+ * is at position seq_lens[i] - n + t.  Position j is row j % page_size of page
+ * block_table[i][j / page_size].  A position below zero, and one whose page is
+ * outside [0, pages), is not there: it is not written, reads as zeros, and no
+ * token attends to it.  seq_lens outside [0, blocks * page_size] are clamped to
+ * it.  Pages may be shared by sequences that read them; two tokens of one
+ * write must not name the same row (which of them it then holds, and whether
+ * its scale is that one's, is not defined).
+ *
+ * 8-bit caches hold a row (one position's head_dim values of one head) as codes
+ * and the exponent of one power of two: code * 2^(byte - 127), with the least
+ * power from 2^-117 that takes the row's largest magnitude to 448 (e4m3) or 127
+ * (int8), codes rounded to nearest even.  Byte 255 stands for NaN: a row with a
+ * NaN or an infinity gets it, with codes 0.  Every value that is held is exact
+ * in bf16.  Magnitudes of 2^127 and more may round up to infinity.
+ */
+typedef enum kda_kv_dtype {
+    KDA_KV_F32 = 0,
+    KDA_KV_BF16 = 1,
+    KDA_KV_E4M3 = 2,                /* OCP e4m3: no infinities, largest 448 */
+    KDA_KV_I8 = 3,
+    KDA_KV_RANGE_MIN_ = -2147483647 - 1,    /* never valid, as in kda_dtype */
+    KDA_KV_RANGE_MAX_ = 2147483647
+} kda_kv_dtype;
+
+/*
+ *   k, v : [pages, heads, page_size, head_dim] dt, pages k_page_stride and
+ *          v_page_stride elements apart (views of one buffer of both are fine);
+ *          16-byte aligned, strides multiples of 16 bytes and at most 2^40
+ *   k_scale, v_scale : [pages, heads, page_size] bytes, 16-byte aligned, exactly
+ *          where dt has 8 bits; else NULL
+ *   block_table : DEVICE int32 [N, blocks], rows block_table_stride apart
+ *   seq_lens : DEVICE int32 [N]
+ *   head_dim in {64, 128}; page_size in {16, 32, 64, 128, 256}; blocks *
+ *   page_size at most 2^30: others are KDA_ERR_UNSUPPORTED, as is a dt that is
+ *   neither the tokens' own nor one of 8 bits
+ */
+typedef struct kda_paged_cache {
+    kda_kv_dtype dt;
+    int pages, heads, page_size, head_dim, blocks;
+    void* k;
+    void* v;
+    long long k_page_stride, v_page_stride;
+    unsigned char* k_scale;
+    unsigned char* v_scale;
+    const int* block_table;
+    long long block_table_stride;
+    const int* seq_lens;
+} kda_paged_cache;
+
+/*
+ * Writes the new tokens' keys and values to their positions.
+ *   k, v : [tokens, heads, head_dim] dt, row strides k_stride, v_stride;
+ *          16-byte aligned, strides multiples of 16 bytes
+ */
+kda_status kda_kv_cache_write(int N, const int* cu_seqlens, int T, kda_dtype dt, const void* k, long long k_stride,
+                              const void* v, long long v_stride, const kda_paged_cache* cache, hipStream_t stream);
+
+/*
+ * Reads the last positions of every sequence (a sequence of n token rows: its
+ * last n positions) back into k, v [tokens, heads, head_dim] dt, contiguous and
+ * 16-byte aligned.
+ */
+kda_status kda_kv_cache_read(int N, const int* cu_seqlens, int T, kda_dtype dt, void* k, void* v,
+                             const kda_paged_cache* cache, hipStream_t stream);
+
+/*
+ * Attention of the new tokens over the cache, which holds them already:
+ *
+ *   o_t[h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q_t[h] . k_j),
+ *   over the positions j up to the token's own, k and v of cache head
+ *   h / (H / heads);  times sigmoid(gate_t[h]) with a gate
+ *
+ *   q    : [tokens, H, head_dim] dt, row stride q_stride; heads divides H
+ *   gate : [tokens, H, head_dim] dt or NULL, row stride gate_stride
+ *   o    : [tokens, H, head_dim] dt, contiguous; a token with no position to
+ *          attend to gets zeros
+ *   scale: finite, above zero
+ *   workspace : kda_paged_attn_workspace_size(...) bytes
+ * q, gate, o and workspace 16-byte aligned, strides multiples of 16 bytes.
+ * What is at positions that a token does not attend to (behind it, or not
+ * there) does not reach it, NaN and infinities included.  bf16: scores, maxima
+ * and sums are fp32; weights are rounded to bf16 for their product with v, so o
+ * is off by its own rounding and 2^-8 of the weighted mean of |v|.
+ */
+size_t kda_paged_attn_workspace_size(int N, int packed, int T, int H, kda_dtype dt, const kda_paged_cache* cache);
+kda_status kda_paged_attn(int N, const int* cu_seqlens, int T, int H, kda_dtype dt, float scale, const void* q,
+                          long long q_stride, const void* gate, long long gate_stride, void* o,
+                          const kda_paged_cache* cache, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /*
  * Optional per-launch timing, for benchmarks and tracing.  After
  * kda_profile_start(max_launches), each kernel launched by the library
@@ -596,7 +694,9 @@ kda_status kda_group_norm_bwd(int rows, int C, int groups, kda_dtype dt, kda_act
  * "scan_prep", "scan_gates", "scan_summary", "scan_combine", "scan_output", "scan_final", "scan_step",
  * "scan_bwd_summary", "scan_bwd_combine", "scan_bwd_states", "scan_bwd_grads",
  * "scan_bwd_join", "scan_bwd_sums",
- * "group_norm", "group_norm_bwd", "group_norm_bwd_sums") and durations in milliseconds, releases the
+ * "group_norm", "group_norm_bwd", "group_norm_bwd_sums"; the paged cache's
+ * "cache_write", "cache_read", "attn_step", "attn_chunk", "attn_f32",
+ * "attn_join") and durations in milliseconds, releases the
  * events, and returns the number of timed launches (-1: profiling was not
  * started or a HIP event query failed).  The record is process-wide (the one
  * piece of state the library keeps, opt-in): launches from several threads

@@ -1,0 +1,108 @@
+"""Plain 64-bit references of the paged cache operators on the CPU, and the
+bounds that the tests hold the kernels to (test infrastructure)."""
+import torch
+
+LARGEST = {torch.float8_e4m3fn: 448.0, torch.int8: 127.0}
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}   # half a step, relative
+
+
+def spans(n, t, cu):
+    """(first token row, tokens) of each sequence."""
+    if cu is None:
+        return [(i * t, t) for i in range(n)]
+    c = [int(v) for v in cu]
+    return [(a, b - a) for a, b in zip(c[:-1], c[1:])]
+
+
+def quantise(x, kv):
+    """(codes as float64, scale bytes) of float64 rows."""
+    top = LARGEST[kv]
+    most = x.abs().amax(-1)
+    bad = ~torch.isfinite(x).all(-1)
+    most = torch.where(bad, 0.0, most)
+    e = torch.frexp(most / top)[1].to(torch.int64) - 2
+    for _ in range(4):          # frexp's exponent is at most one step off
+        e = torch.where(torch.ldexp(torch.full_like(most, top), e) < most, e + 1, e)
+    e = torch.where(most == 0, -117, e).clamp(min=-117)
+    v = torch.ldexp(torch.where(bad[..., None], 0.0, x), -e[..., None])
+    if kv == torch.int8:
+        code = torch.round(v)
+    else:
+        step = torch.ldexp(torch.ones_like(v), (torch.frexp(v.abs().clamp(min=2.0 ** -6))[1] - 4).to(torch.int64))
+        code = torch.round(v / step) * step
+    return code, torch.where(bad, 255, e + 127).to(torch.uint8)
+
+
+def values(cache, scale):
+    """The numbers that a cache stands for, float64."""
+    v = cache.cpu().to(torch.float32).double()
+    if scale is None:
+        return v
+    b = scale.cpu().view(torch.uint8).to(torch.int64)
+    p = torch.ldexp(torch.ones(b.shape, dtype=torch.float64), b - 127)
+    return v * torch.where(b == 255, float("nan"), p)[..., None]
+
+
+def place(table, positions, page_size, pages, seq, pos):
+    """(page, row) of a position or None."""
+    length = min(max(int(positions[seq]), 0), table.shape[1] * page_size)
+    if pos < 0 or pos >= length:
+        return None
+    page = int(table[seq, pos // page_size])
+    return (page, pos % page_size) if 0 <= page < pages else None
+
+
+def attn(q, k, v, table, positions, ranges, scale, gate=None):
+    """q [M, H, D], k and v [P, Hk, S, D] float64 values.  Returns (o, bound parts): o [M, H, D], the weighted mean of
+    |v| of each output, and each (row, head)'s largest scale sum |q_d k_d|."""
+    M, H, D = q.shape
+    P, Hk, S, _ = k.shape
+    table = table.cpu()
+    o = torch.zeros(M, H, D, dtype=torch.float64)
+    mean = torch.zeros_like(o)
+    size = torch.zeros(M, H, 1, dtype=torch.float64)
+    for i, (first, n) in enumerate(ranges):
+        length = min(max(int(positions[i]), 0), table.shape[1] * S)
+        at = torch.arange(length)
+        pages = table[i].long()[at // S] if length else at
+        there = (pages >= 0) & (pages < P)
+        at, pages = at[there], pages[there]
+        ki, vi = (c[pages, :, at % S].transpose(0, 1) for c in (k, v))      # [Hk, C, D]
+        for t in range(n):
+            m = int((at <= length - n + t).sum())
+            if m == 0:
+                continue
+            for h in range(H):
+                kk, vv = ki[h * Hk // H, :m], vi[h * Hk // H, :m]
+                p = torch.softmax(kk @ q[first + t, h] * scale, 0)
+                o[first + t, h] = p @ vv
+                mean[first + t, h] = p @ vv.abs()
+                size[first + t, h] = (kk.abs() @ q[first + t, h].abs()).amax() * scale
+    if gate is not None:
+        s = torch.sigmoid(gate)
+        o, mean = o * s, mean * s
+    return o, mean, size
+
+
+def attn_bound(o, mean, size, dt, D, positions):
+    """The output's own rounding; a weight's rounding to bf16; and in fp32, doubled because a weight stands above and
+    below the fraction: scores of D products (each sum's and product's rounding relative to the sum of magnitudes),
+    the exponential (its argument's rounding and its own, 2^-21), the sums over the positions, the gate."""
+    fp32 = 2 * ((D + 8) * 2.0 ** -24 * size * 1.5 + 2.0 ** -21 + (positions + 64) * 2.0 ** -24) + 2.0 ** -20
+    weight = 2.0 ** -8 if dt == torch.bfloat16 else 0.0
+    return HALF[dt] * o.abs() + (weight + fp32) * (1 + 2.0 ** -7) * mean + 1e-30
+
+
+def close(got, want, bound, what):
+    """|got - want| <= bound everywhere (float64), NaN where NaN is wanted, the same infinities."""
+    got = got.detach().double().cpu()
+    assert got.shape == want.shape, what
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), "%s: NaN at other places" % what
+    inf = torch.isinf(want)
+    assert torch.equal(torch.isinf(got), inf) and torch.equal(got[inf], want[inf]), "%s: other infinities" % what
+    fine = torch.isfinite(want)
+    over = torch.where(fine, (got - torch.where(fine, want, 0.0)).abs() - bound, -1.0)
+    if over.numel():
+        assert (over <= 0).all(), "%s: over its bound by %.3g at %s (want %.6g, got %.6g)" % (
+            what, over.max(), tuple(int(x) for x in torch.unravel_index(over.argmax(), over.shape)),
+            want.flatten()[over.argmax()], got.flatten()[over.argmax()])

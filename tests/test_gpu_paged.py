@@ -1,0 +1,449 @@
+"""Paged cache operators on the GPU against 64-bit references: writing, reading
+back, attention of new tokens, and a run of them as a layer makes it."""
+import pytest
+import torch
+
+import gated_delta_rule_66_amd as kda
+from tests import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32, E4M3, I8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int8
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+class Cache:
+    """A pool with the tables of some sequences, its pages in random order; rows that no sequence holds are NaN."""
+
+    def __init__(self, lens, kv, hk, d, page, seed, spare=2, blocks=None, views=False):
+        g = gen(seed)
+        self.kv, self.page, self.lens = kv, page, list(lens)
+        held = [-(-max(n, 0) // page) for n in lens]
+        self.pages = sum(held) + spare
+        blocks = max(max(held, default=0), 1) if blocks is None else blocks
+        order = torch.randperm(self.pages, generator=g)
+        table = torch.full((len(lens), blocks), -1, dtype=torch.int32)
+        used = 0
+        held = [min(n, blocks) for n in held]
+        for i, n in enumerate(held):
+            table[i, :n] = order[used:used + n].to(torch.int32)
+            used += n
+        self.table = table.to(DEV)
+        self.seq_lens = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        shape = (self.pages, hk, page, d)
+        self.k_scale = self.v_scale = None
+        pool = [torch.randn(shape, generator=g) for _ in range(2)]
+        if kv in ref.LARGEST:
+            code, byte = zip(*(ref.quantise(x.double(), kv) for x in pool))
+            pool = [c.to(torch.float32) for c in code]
+            self.k_scale, self.v_scale = (b.to(DEV).view(torch.float8_e8m0fnu) for b in byte)
+        if views:       # views of one buffer of both, with another page's room between
+            both = torch.zeros((self.pages, 3, hk, page, d), device=DEV).to(kv)
+            self.k_cache, self.v_cache = both[:, 0], both[:, 2]
+            self.k_cache.copy_(pool[0].to(kv))
+            self.v_cache.copy_(pool[1].to(kv))
+        else:
+            self.k_cache, self.v_cache = (x.to(kv).to(DEV) for x in pool)
+        free = torch.ones(self.pages, page, dtype=torch.bool)
+        for i, n in enumerate(lens):
+            for b in range(held[i]):
+                free[table[i, b], :max(0, min(page, n - b * page))] = False
+        self.free = free
+        self.spoil(free)
+
+    def spoil(self, where):
+        """Rows [pages, page] that must not be read become NaN (int8: their scale)."""
+        at = where[:, None, :].expand(-1, self.k_cache.shape[1], -1).to(DEV)
+        if self.kv == I8 or self.kv == E4M3:
+            for s in (self.k_scale, self.v_scale):
+                s.view(torch.uint8)[at] = 255
+        else:
+            for c in (self.k_cache, self.v_cache):
+                c.masked_fill_(at[..., None], float("nan"))
+
+    def args(self):
+        return self.k_cache, self.v_cache, self.table, self.seq_lens, self.k_scale, self.v_scale
+
+    def values(self):
+        return ref.values(self.k_cache, self.k_scale), ref.values(self.v_cache, self.v_scale)
+
+
+def cu_of(new):
+    return torch.tensor([0] + list(new)).cumsum(0).to(torch.int32).to(DEV)
+
+
+def check_attn(c, q, new, what, gate=None, scale=None, packed=True, **kw):
+    n, t = len(new), max(new, default=0)
+    cu = cu_of(new) if packed else None
+    got = kda.paged_attn(q, *c.args(), gate=gate, scale=scale, cu_seqlens=cu, **kw)
+    torch.cuda.synchronize()
+    H, D = q.shape[-2:]
+    k, v = c.values()
+    flat = lambda x: None if x is None else x.reshape(-1, H, D).cpu().double()
+    o, mean, size = ref.attn(flat(q), k, v, c.table, c.lens, ref.spans(n, t, cu), scale or D ** -0.5, flat(gate))
+    bound = ref.attn_bound(o, mean, size, q.dtype, D, max(list(c.lens) + [1]))
+    ref.close(got.reshape(o.shape), o, torch.nan_to_num(bound), what)
+    return got
+
+
+def rows(dt, n, h, d, seed, std=1.0):
+    return (torch.randn((n, h, d), generator=gen(seed)) * std).to(dt).to(DEV)
+
+
+# ---- writing and reading back ----------------------------------------------------------
+KINDS = [(BF, BF), (BF, E4M3), (BF, I8), (F32, F32), (F32, E4M3), (F32, I8)]
+
+
+def expect_write(c, k, v, new):
+    """Caches (values as stored) and scale bytes after a write, on the CPU."""
+    table, out = c.table.cpu(), []
+    for x, cache, scale in ((k, c.k_cache, c.k_scale), (v, c.v_cache, c.v_scale)):
+        want = cache.cpu().to(torch.float32).double()
+        byte = None if scale is None else scale.cpu().view(torch.uint8).clone()
+        code, b = (x.double().cpu(), None) if scale is None else ref.quantise(x.double().cpu(), c.kv)
+        for i, (first, n) in enumerate(ref.spans(len(new), 0, cu_of(new))):
+            length = min(max(c.lens[i], 0), table.shape[1] * c.page)
+            for t in range(n):
+                at = ref.place(table, c.lens, c.page, c.pages, i, length - n + t)
+                if at is None:
+                    continue
+                want[at[0], :, at[1]] = code[first + t]
+                if byte is not None:
+                    byte[at[0], :, at[1]] = b[first + t]
+        out.append((want, byte))
+    return out
+
+
+def check_write(c, k, v, new, packed=True):
+    want = expect_write(c, k.reshape(-1, *k.shape[-2:]), v.reshape(-1, *v.shape[-2:]), new)
+    kda.kv_cache_write(k, v, *c.args(), cu_seqlens=cu_of(new) if packed else None)
+    torch.cuda.synchronize()
+    for name, cache, scale, (w, b) in (("k", c.k_cache, c.k_scale, want[0]), ("v", c.v_cache, c.v_scale, want[1])):
+        got = cache.cpu().to(torch.float32).double()
+        assert torch.equal(torch.nan_to_num(got, nan=-1e9), torch.nan_to_num(w, nan=-1e9)), name
+        if b is not None:
+            assert torch.equal(scale.cpu().view(torch.uint8), b), name
+
+
+@pytest.mark.parametrize("dt,kv", KINDS)
+@pytest.mark.parametrize("d,hk,page", [(64, 3, 16), (128, 2, 64), (128, 5, 256), (64, 1, 32)])
+def test_write_packed(dt, kv, d, hk, page):
+    new = [1, 37, 0, page + 3, 5]
+    c = Cache([40, 37, 9, page + 3, 2 * page + 1], kv, hk, d, page, seed=1, views=d == 128)
+    m = sum(new)
+    k, v = rows(dt, m + 3, hk, d, 2), rows(dt, m + 3, hk, d, 3, std=30.0)
+    check_write(c, k, v, new)           # three rows behind the last sequence
+
+
+@pytest.mark.parametrize("dt,kv", KINDS)
+def test_write_regular_slices_and_places_that_are_not_there(dt, kv):
+    d, hk, page, t = 128, 2, 16, 20
+    c = Cache([100, 7, 0, 33, -4], kv, hk, d, page, seed=4, blocks=6)       # 100 > 6 * 16 is clamped
+    c.table[3, 1] = -1
+    c.table[0, 5] = c.pages
+    wide = rows(dt, 5 * t, 3 * hk, d, 5).view(5, t, 3 * hk, d)
+    check_write(c, wide[:, :, hk:2 * hk], wide[:, :, 2 * hk:], [t] * 5, packed=False)
+
+
+@pytest.mark.parametrize("kv", [E4M3, I8])
+def test_write_every_bf16_value(kv):
+    """Every finite bf16 magnitude, against largest values of some fractions; and rows of zeros, NaN, infinities."""
+    d, page = 128, 256
+    bits = torch.arange(0x7f00, dtype=torch.int32)      # below 2^127
+    x = (bits << 16).view(torch.float32)
+    x = torch.where(bits % 3 == 0, -x, x).view(-1, d)
+    # rows of neighbouring magnitudes, and the same rows beside a value up to 2^9 times larger
+    big = torch.cat([x * f for f in (1.0, 3.0, 100.0)])
+    mixed = x.repeat(3, 1)
+    mixed[:, 0] = big.abs().amax(-1).clamp(max=1.6e38)
+    x = torch.cat([x, mixed, torch.zeros(1, d), torch.full((1, d), float("nan")), torch.full((1, d), float("inf"))]).to(BF)
+    special = torch.randn(3, d, generator=gen(6)).to(BF)
+    special[0, 5], special[1, 127], special[2, 0] = float("nan"), float("inf"), -float("inf")
+    x = torch.cat([x, special])
+    m = x.shape[0]
+    c = Cache([m], kv, 1, d, page, seed=7)
+    x = x.to(DEV).view(m, 1, d)
+    check_write(c, x, x.flip(0).contiguous(), [m])
+    k, v = kda.kv_cache_read(*c.args(), m, cu_seqlens=cu_of([m]))
+    code, byte = ref.quantise(x.double().cpu(), kv)
+    want = ref.values(code, byte)
+    assert torch.equal(torch.nan_to_num(k.cpu().double(), nan=-1.0), torch.nan_to_num(want, nan=-1.0))
+    assert torch.equal(torch.nan_to_num(v.cpu().double(), nan=-1.0), torch.nan_to_num(want.flip(0), nan=-1.0))
+
+
+@pytest.mark.parametrize("kv", [E4M3, I8])
+def test_write_fp32_near_the_borders(kv):
+    """fp32 values one step to either side of a border between codes, and of a power of the scale."""
+    top, d = ref.LARGEST[kv], 64
+    r = torch.randint(0, 127, (400, d), generator=gen(8)).float() + 0.5
+    x = torch.cat([r, torch.nextafter(r, torch.zeros(())), torch.nextafter(r, torch.full((), 1e9))])
+    x[:, 0] = top
+    x[::3, 0] = torch.nextafter(torch.tensor(top), torch.tensor(1e9))
+    x[1::3, 0] = torch.nextafter(torch.tensor(top), torch.tensor(0.0))
+    x *= torch.ldexp(torch.ones(x.shape[0], 1), torch.randint(-60, 60, (x.shape[0], 1), generator=gen(9)))
+    m = x.shape[0]
+    c = Cache([m], kv, 1, d, 16, seed=10)
+    check_write(c, x.to(DEV).view(m, 1, d), (-x).to(DEV).view(m, 1, d), [m])
+
+
+@pytest.mark.parametrize("dt,kv", KINDS)
+@pytest.mark.parametrize("d,hk,page", [(64, 3, 16), (128, 2, 128)])
+def test_read(dt, kv, d, hk, page):
+    new = [1, 50, 0, page + 3, 12]
+    c = Cache([40, 50, 9, 2 * page + 3, 5], kv, hk, d, page, seed=11, blocks=4 if page == 16 else 3, views=True)
+    c.table[3, 1] = c.pages + 5
+    cu, m = cu_of(new), sum(new)
+    out = [torch.full((m + 2, hk, d), 7.0, dtype=dt, device=DEV) for _ in range(2)]
+    k, v = kda.kv_cache_read(*c.args(), m + 2, dtype=dt, cu_seqlens=cu, k=out[0], v=out[1])
+    torch.cuda.synchronize()
+    assert k is out[0] and v is out[1]
+    for got, val in zip((k, v), c.values()):
+        want = torch.zeros(m + 2, hk, d, dtype=torch.float64)
+        want[m:] = 7.0
+        for i, (first, n) in enumerate(ref.spans(5, 0, cu)):
+            length = min(c.lens[i], c.table.shape[1] * page)
+            for t in range(n):
+                at = ref.place(c.table.cpu(), c.lens, page, c.pages, i, length - n + t)
+                if at is not None:
+                    want[first + t] = val[at[0], :, at[1]]
+        assert torch.equal(got.cpu().double(), want)
+
+
+# ---- attention -------------------------------------------------------------------------
+SHAPES = [  # H, Hk, D, page
+    (4, 4, 64, 16), (8, 2, 128, 64), (6, 1, 64, 32), (5, 5, 128, 256), (12, 3, 128, 16), (16, 1, 64, 128)]
+
+
+@pytest.mark.parametrize("dt,kv", KINDS)
+@pytest.mark.parametrize("H,hk,d,page", SHAPES)
+def test_one_token(dt, kv, H, hk, d, page):
+    lens = [1, 2, 31, 32, 33, 64, 129, 300, 0, 17]
+    c = Cache(lens, kv, hk, d, page, seed=20, views=page == 64)
+    q = rows(dt, len(lens), H, d, 21, std=2.0).view(len(lens), 1, H, d)
+    got = check_attn(c, q, [1] * len(lens), "one token", packed=False)
+    assert not got[8].any()
+
+
+@pytest.mark.parametrize("dt,kv", KINDS)
+@pytest.mark.parametrize("H,hk,d,page", SHAPES)
+@pytest.mark.parametrize("t", [2, 5, 9])
+def test_few_tokens(dt, kv, H, hk, d, page, t):
+    """Some tokens a sequence; sequences of fewer positions than tokens have rows that see nothing."""
+    lens = [t, 40, 3, 0, 161]
+    c = Cache(lens, kv, hk, d, page, seed=22)
+    q = rows(dt, 5 * t, H, d, 23, std=2.0).view(5, t, H, d)
+    z = rows(dt, 5 * t, H, d, 24).view(5, t, H, d)
+    check_attn(c, q, [t] * 5, "few tokens", gate=z, packed=False)
+
+
+@pytest.mark.parametrize("dt,kv", KINDS)
+@pytest.mark.parametrize("H,hk,d,page", SHAPES)
+def test_packed_prompts(dt, kv, H, hk, d, page):
+    """Prompts and single tokens packed, rows behind the last sequence left alone, q and gate slices."""
+    new = [70, 1, 0, 33, 129, 2]
+    lens = [70, 150, 20, 200, 129, 1]
+    c = Cache(lens, kv, hk, d, page, seed=25)
+    m = sum(new)
+    wide = rows(dt, m + 4, 2 * H, d, 26, std=1.5)
+    out = torch.full((m + 4, H, d), 7.0, dtype=dt, device=DEV)
+    q, z = wide[:, :H], wide[:, H:]
+    cu = cu_of(new)
+    got = kda.paged_attn(q, *c.args(), gate=z, cu_seqlens=cu, out=out)
+    torch.cuda.synchronize()
+    assert got is out and (out[m:] == 7.0).all()
+    k, v = c.values()
+    o, mean, size = ref.attn(q[:m].double().cpu(), k, v, c.table, lens, ref.spans(6, 0, cu), d ** -0.5,
+                             z[:m].double().cpu())
+    ref.close(out[:m], o, ref.attn_bound(o, mean, size, dt, d, 200), "packed")
+
+
+@pytest.mark.parametrize("dt,kv", [(BF, BF), (BF, E4M3), (BF, I8), (F32, F32), (F32, I8)])
+@pytest.mark.parametrize("new,length", [([1], 5000), ([3], 4097), ([40], 3000), ([1, 20], 2500), ([150], 150)])
+def test_long_contexts_are_split_and_joined(dt, kv, new, length):
+    c = Cache([length] * len(new), kv, 2, 64, 32, seed=27, blocks=250)
+    q = rows(dt, sum(new), 4, 64, 28, std=2.0)
+    check_attn(c, q, new, "split")
+
+
+@pytest.mark.parametrize("dt,kv", [(BF, BF), (BF, E4M3), (BF, I8), (F32, F32), (F32, E4M3)])
+@pytest.mark.parametrize("t", [1, 4, 50])
+def test_pages_that_are_not_there(dt, kv, t):
+    """Holes in the tables: below zero, behind the pool, and sequences without a page."""
+    c = Cache([300, 200, 90, 64], kv, 2, 64, 16, seed=29, blocks=40)
+    c.table[0, 3:9] = -1
+    c.table[0, 12] = c.pages
+    c.table[1, 0] = -7
+    c.table[1, -2:] = 2 ** 31 - 1
+    c.table[2] = -1
+    c.table[3, 3] = -1          # the last tokens' own page
+    q = rows(dt, 4 * t, 4, 64, 30, std=2.0)
+    got = check_attn(c, q, [t] * 4, "holes")
+    assert not got[2 * t:3 * t].any()
+
+
+@pytest.mark.parametrize("dt,kv", [(BF, BF), (F32, F32), (BF, E4M3), (BF, I8), (F32, I8)])
+@pytest.mark.parametrize("t", [3, 6, 70])
+def test_nothing_reaches_a_token_from_behind_it(dt, kv, t):
+    """NaN and infinities in keys and values of later tokens: earlier tokens stay what they are."""
+    c = Cache([t + 45, t], kv, 2, 64, 32, seed=31)
+    for i, length in enumerate(c.lens):
+        pos = length - t // 2
+        page, row = int(c.table[i, pos // 32]), pos % 32
+        if kv in ref.LARGEST:
+            c.k_scale.view(torch.uint8)[page, 0, row] = 255
+            c.v_scale.view(torch.uint8)[page, 1, row] = 255
+        else:
+            c.k_cache[page, 0, row, 3] = float("nan")
+            c.v_cache[page, 1, row, 5] = float("nan")
+            c.v_cache[page, 1, row, 6] = float("inf")
+            c.v_cache[page, 1, row, 7] = -float("inf")
+            c.v_cache[page, 1, row, 8] = float("inf")
+            if pos + 1 < length:
+                page, row = int(c.table[i, (pos + 1) // 32]), (pos + 1) % 32
+                c.v_cache[page, 1, row, 8] = -float("inf")
+    q = rows(dt, 2 * t, 4, 64, 32)
+    got = check_attn(c, q, [t, t], "later tokens")
+    assert torch.isfinite(got[:t - t // 2]).all()
+
+
+@pytest.mark.parametrize("dt,kv", [(BF, BF), (F32, F32)])
+@pytest.mark.parametrize("t", [1, 40])
+def test_scores_far_apart(dt, kv, t):
+    """Scores that rise along the sequence by far more than an exponential holds, and equal ones."""
+    c = Cache([200, 130], kv, 2, 64, 16, seed=33)
+    ramp = torch.linspace(-300, 300, 224).view(14, 1, 16, 1)
+    order = torch.argsort(c.table[0, :13].cpu().long())
+    for b in range(13):
+        c.k_cache[int(c.table[0, b]), :, :, 0] = ramp[b, 0, :, 0].to(kv).to(DEV)
+    q = rows(dt, 2 * t, 4, 64, 34)
+    q[..., 0] = 8.0
+    q[t:, :, 1:] = 0.0
+    assert order.numel() == 13
+    check_attn(c, q, [t, t], "far apart", scale=1.0)
+    q.zero_()
+    check_attn(c, q, [t, t], "equal")
+
+
+def test_no_sequences_no_tokens():
+    c = Cache([40, 3], BF, 2, 64, 16, seed=35)
+    none = torch.empty((0, 4, 64), dtype=BF, device=DEV)
+    assert kda.paged_attn(none, *c.args(), cu_seqlens=cu_of([0, 0])).shape == (0, 4, 64)
+    before = c.k_cache.clone()
+    kda.kv_cache_write(none[:, :2], none[:, :2], *c.args(), cu_seqlens=cu_of([0, 0]))
+    k, _ = kda.kv_cache_read(*c.args(), 0)
+    assert k.shape == (2, 0, 2, 64) and torch.equal(before.nan_to_num(), c.k_cache.nan_to_num())
+    empty = Cache([], BF, 2, 64, 16, seed=36)
+    assert kda.paged_attn(none.view(0, 1, 4, 64), *empty.args()).numel() == 0
+    nopages = Cache([0, 0], BF, 2, 64, 16, seed=36, spare=0)
+    q = rows(BF, 2, 4, 64, 37).view(2, 1, 4, 64)
+    assert not kda.paged_attn(q, *nopages.args()).any()
+
+
+# ---- together --------------------------------------------------------------------------
+@pytest.mark.parametrize("dt,kv", [(BF, BF), (BF, E4M3), (BF, I8), (F32, F32)])
+def test_prompt_chunks_and_steps(dt, kv):
+    """A layer's life: a prompt in chunks, then single tokens, each written before it is attended to; the whole equals
+    the attention of the values that the cache holds."""
+    H, hk, d, page = 4, 2, 64, 16
+    lens = [90, 47]
+    total = Cache(lens, kv, hk, d, page, seed=40)
+    total.spoil(torch.ones(total.pages, page, dtype=torch.bool))
+    g = gen(41)
+    q, k, v, z = ([torch.randn((n, h, d), generator=g).to(dt).to(DEV) for n in lens] for h in (H, hk, hk, H))
+    outs = [[], []]
+    done = [0, 0]
+    steps = [(40, 16), (30, 20)] + [(1, 1)] * 11 + [(9, 0)]
+    for new in steps:
+        cu = cu_of(new)
+        total.seq_lens = torch.tensor([a + b for a, b in zip(done, new)], dtype=torch.int32, device=DEV)
+        part = lambda x: torch.cat([x[i][done[i]:done[i] + new[i]] for i in range(2)])
+        kda.kv_cache_write(part(k), part(v), *total.args(), cu_seqlens=cu)
+        o = kda.paged_attn(part(q), *total.args(), gate=part(z), cu_seqlens=cu)
+        for i in range(2):
+            outs[i].append(o[int(cu[i]):int(cu[i + 1])])
+            done[i] += new[i]
+    assert done == lens
+    rk, rv = kda.kv_cache_read(*total.args(), sum(lens), dtype=dt, cu_seqlens=cu_of(lens))
+    torch.cuda.synchronize()
+    kv_, vv_ = total.values()
+    flat = lambda x: torch.cat(x).cpu().double()
+    cu = cu_of(lens)
+    o, mean, size = ref.attn(flat(q), kv_, vv_, total.table, lens, ref.spans(2, 0, cu), d ** -0.5, flat(z))
+    ref.close(torch.cat([torch.cat(x) for x in outs]), o, ref.attn_bound(o, mean, size, dt, d, 90), "steps")
+    want = flat(k)
+    if kv in ref.LARGEST:
+        want = ref.values(*ref.quantise(want, kv))
+    assert torch.equal(rk.double().cpu(), want)
+
+
+@pytest.mark.parametrize("dt,kv,new", [(BF, BF, [1, 1, 1]), (BF, E4M3, [40, 1, 30]), (F32, I8, [9, 1, 2])])
+def test_captured_and_replayed(dt, kv, new):
+    """Write, attention and read in one graph, replayed with other tokens and lengths, eager work in between."""
+    H, hk, d, page = 4, 2, 128, 32
+    c = Cache([700, 90, 64], kv, hk, d, page, seed=42)
+    c.spoil(torch.zeros(c.pages, page, dtype=torch.bool))
+    m = sum(new)
+    q, k, v = rows(dt, m, H, d, 43), rows(dt, m, hk, d, 44), rows(dt, m, hk, d, 45)
+    cu, out = cu_of(new), torch.empty((m, H, d), dtype=dt, device=DEV)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    rk, rv = (torch.empty((m, hk, d), dtype=dt, device=DEV) for _ in range(2))
+
+    def call():
+        kda.kv_cache_write(k, v, *c.args(), cu_seqlens=cu)
+        kda.paged_attn(q, *c.args(), cu_seqlens=cu, out=out, workspace=ws)
+        kda.kv_cache_read(*c.args(), m, dtype=dt, cu_seqlens=cu, k=rk, v=rv)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for step in range(4):
+        q.copy_(rows(dt, m, H, d, 50 + step))
+        k.copy_(rows(dt, m, hk, d, 60 + step))
+        c.seq_lens.copy_(torch.tensor([700 - 100 * step, 90 - step, 64], dtype=torch.int32))
+        out.fill_(float("nan"))
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (out, rk, rv, c.k_cache.to(torch.float32), c.v_cache.to(torch.float32))]
+        ws.fill_(127)
+        call()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (out, rk, rv, c.k_cache.to(torch.float32), c.v_cache.to(torch.float32))):
+            assert torch.equal(a.nan_to_num(), b.nan_to_num()), step
+        assert torch.isfinite(out).all()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with a workspace and an output of its own, equal the same calls in turn."""
+    c = Cache([6000, 900], BF, 2, 128, 64, seed=46)
+    q = [rows(BF, 2, 8, 128, 47 + i).view(2, 1, 8, 128) for i in range(2)]
+    want = [kda.paged_attn(x, *c.args()) for x in q]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s, x in zip(streams, q):
+            with torch.cuda.stream(s):
+                got.append(kda.paged_attn(x, *c.args()))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_profile_names():
+    c = Cache([6000], E4M3, 2, 128, 64, seed=48)
+    q = rows(BF, 1, 8, 128, 49)
+    kda.profile_start(8)
+    kda.kv_cache_write(q[:, :2], q[:, 2:4], *c.args(), cu_seqlens=cu_of([1]))
+    kda.paged_attn(q, *c.args(), cu_seqlens=cu_of([1]))
+    kda.kv_cache_read(*c.args(), 1)
+    names = [n for n, _ in kda.profile_stop(8)]
+    assert names == ["cache_write", "attn_step", "attn_join", "cache_read"]
