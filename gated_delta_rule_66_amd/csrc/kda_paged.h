@@ -10,6 +10,25 @@ namespace kda {
 // kda_kv_dtype
 enum { kKvF32 = 0, kKvBf16 = 1, kKvE4m3 = 2, kKvI8 = 3 };
 
+// Quotients of 0 <= n < 2^31 by a divisor that the host knows: with
+// 2^(s-1) < d <= 2^s and m = floor(2^32 (2^s - d) / d) + 1,
+// n / d = (n m / 2^32 + n) >> s, and the sum stays below 2^32.
+struct FastDiv {
+    unsigned m, s, d;
+    void set(unsigned by) {
+        d = by;
+        for (s = 0; s < 31 && (1u << s) < by; ++s) {}
+        m = (unsigned)(((1ull << 32) * ((1ull << s) - by)) / by + 1);
+    }
+    __host__ __device__ int div(int n) const {
+#ifdef __HIP_DEVICE_COMPILE__
+        return (int)((__umulhi((unsigned)n, m) + (unsigned)n) >> s);
+#else
+        return (int)(((((unsigned long long)(unsigned)n * m) >> 32) + (unsigned)n) >> s);
+#endif
+    }
+};
+
 // The cache as the kernels see it.  Sequence i's position j is in row
 // j % page of page table[i][j / page]; a page outside [0, pages) is not there.
 struct PagedCache {
@@ -56,9 +75,10 @@ struct AttnParams {
     size_t q_stride, z_stride;  // bytes between token rows
     int H, G;
     float c_log2;           // scale log2(e)
-    int M;                  // rows a tile
+    int M, lg_m;            // rows a tile
     int tiles, tiles_per_seq;
     int splits, split_len;
+    FastDiv by_g, by_hk, by_splits, by_tiles, by_len;   // G, Hk, splits, tiles_per_seq, split_len
     float* part;            // [tiles][Hk][splits][M][D]
     float* ml;              // [tiles][Hk][splits][M][2]: running maximum (of q.k) and sum
 };

@@ -228,6 +228,12 @@ kda_status kda_paged_attn(int N, const int* cu_seqlens, int T, int H, kda_dtype 
     p.c_log2 = scale * 1.4426950408889634f;
     p.M = a.M; p.tiles = (int)a.tiles; p.tiles_per_seq = a.tiles_per_seq;
     p.splits = a.splits; p.split_len = a.split_len;
+    while ((1 << p.lg_m) < p.M) ++p.lg_m;
+    p.by_g.set((unsigned)p.G);
+    p.by_hk.set((unsigned)c->heads);
+    p.by_splits.set((unsigned)p.splits);
+    p.by_tiles.set((unsigned)(p.tiles_per_seq > 0 ? p.tiles_per_seq : 1));
+    p.by_len.set((unsigned)p.split_len);
     p.part = (float*)workspace;
     p.ml = (float*)((char*)workspace + a.part);
     const char* name = a.kind == kAttnF32 ? "attn_f32" : a.kind == kAttnChunk ? "attn_chunk" : "attn_step";

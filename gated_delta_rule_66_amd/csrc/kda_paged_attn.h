@@ -19,10 +19,10 @@ struct AttnTile {
     size_t unit;            // its place in the parts
     // false: nothing to do
     __device__ __forceinline__ bool init(const AttnParams& p, int block) {
-        hk = block % p.c.Hk;
-        const int u = block / p.c.Hk;
-        split = u % p.splits;
-        const int tile = p.tiles - 1 - u / p.splits;        // a sequence's long tiles first
+        const int u = p.by_hk.div(block), v = p.by_splits.div(u);
+        hk = block - u * p.c.Hk;
+        split = u - v * p.splits;
+        const int tile = p.tiles - 1 - v;       // a sequence's long tiles first
         int at;
         if (p.sv.cu) {
             int a = 0, b = p.sv.N;      // slot(a) <= tile < slot(b)
@@ -36,18 +36,18 @@ struct AttnTile {
             seq = uniform(a);
             at = tile - slot(p, seq);
         } else {
-            seq = tile / p.tiles_per_seq;
+            seq = p.by_tiles.div(tile);
             at = tile - seq * p.tiles_per_seq;
         }
         seq_span(p.sv, seq, &first, &n);
         first = uniform(first);
         n = uniform(n);
         rows = n * p.G;
-        if (at < 0 || (long long)at * p.M >= rows) return false;
-        r0 = at * p.M;
+        if (at < 0 || ((long long)at << p.lg_m) >= rows) return false;
+        r0 = at << p.lg_m;
         L = uniform(seq_positions(p.c, seq));
-        end = max(L - n + (min(r0 + p.M, rows) - 1) / p.G + 1, 0);
-        splits = end > 0 ? (end - 1) / p.split_len + 1 : 1;
+        end = max(L - n + p.by_g.div(min(r0 + p.M, rows) - 1) + 1, 0);
+        splits = end > 0 ? p.by_len.div(end - 1) + 1 : 1;
         if (split >= splits) return false;
         lo = split * p.split_len;
         hi = min(end, lo + p.split_len);
@@ -56,49 +56,65 @@ struct AttnTile {
     }
     static __device__ __forceinline__ int slot(const AttnParams& p, int i) {
         const int c = uniform(min(max(p.sv.cu[i], 0), p.sv.T));
-        return (int)((long long)c * p.G / p.M) + i;
+        return ((c * p.G) >> p.lg_m) + i;
     }
     // the last position that row r sees; below zero: none
-    __device__ __forceinline__ int limit(int r, int G) const { return r < rows ? L - n + r / G : -1; }
+    __device__ __forceinline__ int limit(int r, const AttnParams& p) const { return r < rows ? L - n + p.by_g.div(r) : -1; }
 };
 
 // sigmoid gate of one value
 template <typename T> __device__ __forceinline__ float gate_of(float o, float z) { return o * sigmoid_of<T>(z); }
 
-// A masked place of V that is not a number or infinite must not reach a row
-// through its weight of zero.  Such values are taken out of V (clean), and the
-// rows that do see them get them back as what two products of ones count:
-// places of +inf or NaN, and of -inf or NaN.
+// ---- values of V that are not finite ---------------------------------------------------
+// A place that a row does not see has weight zero, and zero times NaN or an
+// infinity is NaN.  Where some row of a tile does not see all of it, such values
+// are therefore made zero before the product, and afterwards added to the rows
+// that do see them (mend_*).  A second addition changes nothing, so the mending
+// may go over positions whose values were left in.
 __device__ __forceinline__ bool not_finite(unsigned pair) {
     return (pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u;
 }
-__device__ __forceinline__ unsigned clean_half(unsigned h) { return (h & 0x7f80u) == 0x7f80u ? 0u : h; }
 __device__ __forceinline__ unsigned clean(unsigned pair) {
-    return clean_half(pair & 0xffffu) | clean_half(pair >> 16) << 16;
+    return ((pair & 0x7f80u) == 0x7f80u ? 0u : pair & 0xffffu) | ((pair & 0x7f800000u) == 0x7f800000u ? 0u : pair & 0xffff0000u);
 }
-// bf16 one where the half is NaN or the infinity of this sign
-__device__ __forceinline__ unsigned flag_half(unsigned h, unsigned inf) {
-    return h == inf || ((h & 0x7f80u) == 0x7f80u && (h & 0x7fu)) ? 0x3f80u : 0u;
-}
-__device__ __forceinline__ unsigned flag(unsigned pair, unsigned inf) {
-    return flag_half(pair & 0xffffu, inf) | flag_half(pair >> 16, inf) << 16;
-}
-template <class F> __device__ __forceinline__ bf16x8 map_pairs(bf16x8 v, F&& f) {
-    u32x4 u = __builtin_bit_cast(u32x4, v);
+__device__ __forceinline__ bool finite_f(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
+
+// Four neighbouring channels of V at a position; zeros where it is not there.
+template <int KV, int D>
+__device__ __forceinline__ void load_v4(const PagedCache& c, int seq, int hk, int pos, int ch, float* f) {
+    const int pg = c.table[(long long)seq * c.table_stride + (pos >> c.lg_page)];
+    f[0] = f[1] = f[2] = f[3] = 0.f;
+    if ((unsigned)pg >= (unsigned)c.pages) return;
+    const size_t r = ((size_t)hk << c.lg_page) + (pos & ((1 << c.lg_page) - 1));
+    const char* at = c.v + (size_t)pg * c.v_page;
+    if constexpr (KV == kKvF32) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(at + (r * D + ch) * 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = f(u[i]);
-    return __builtin_bit_cast(bf16x8, u);
+        for (int i = 0; i < 4; ++i) f[i] = v[i];
+    } else if constexpr (KV == kKvBf16) {
+        const bf16x4 v = *reinterpret_cast<const bf16x4*>(at + (r * D + ch) * 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = (float)v[i];
+    } else {
+        const Codes<KV> d(c.vs[(((size_t)pg * c.Hk) << c.lg_page) + r]);
+        d.f32(*reinterpret_cast<const unsigned*>(at + r * D + ch), f);
+    }
 }
-__device__ __forceinline__ bf16x8 clean8(bf16x8 v) {
-    return map_pairs(v, [](unsigned x) { return clean(x); });
-}
-__device__ __forceinline__ bf16x8 flag8(bf16x8 v, bool minus) {
-    return map_pairs(v, [=](unsigned x) { return flag(x, minus ? 0xff80u : 0x7f80u); });
-}
-__device__ __forceinline__ float poisoned(float o, float plus, float minus) {
-    if (plus > 0.f) o += __uint_as_float(0x7f800000u);
-    if (minus > 0.f) o -= __uint_as_float(0x7f800000u);
-    return o;
+// acc[db][4 j + i]: channel 32 db + 8 j + 4 h + i of the lane's row
+template <int KV, int D>
+__device__ __forceinline__ void mend_rows(f32x16 (&acc)[D / 32], const AttnParams& p, const AttnTile& t, int from, int lim, int h) {
+#pragma unroll 1
+    for (int pos = from; pos < t.hi; ++pos)
+#pragma unroll
+        for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float f[4];
+                load_v4<KV, D>(p.c, t.seq, t.hk, pos, 32 * db + 8 * j + 4 * h, f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (pos <= lim && !finite_f(f[i])) acc[db][4 * j + i] += f[i];
+            }
 }
 
 // A score's maximum is moved only when a tile passes it by more than this many

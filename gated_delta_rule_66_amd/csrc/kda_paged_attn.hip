@@ -36,38 +36,92 @@ template <int D> __device__ __forceinline__ int v_piece(int row, int piece) {
     return D == 128 ? piece ^ ((row & 3) << 2 | (row & 2)) : piece ^ ((row & 3) << 1);
 }
 
-// A tile of K or V on its way: what a thread loads of it.
-template <int KV, int D> struct Stage {
+// 64 lanes' 16 bytes at base + off straight into 1024 bytes of LDS.  Written out
+// because the compiler would wait for a builtin's loads before any read of LDS,
+// those of the tile before included: the wait is Stage::store's.  (m0, the LDS
+// address, has to stand one instruction before its use; the compiler has no use
+// of its own for it in this kernel.)
+__device__ __forceinline__ void load_lds16(const char* base, unsigned off, char* to) {
+    typedef __attribute__((address_space(3))) char lds_c;
+    const unsigned at = (unsigned)uniform((int)(unsigned)(uintptr_t)(lds_c*)to);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(at), "v"(off), "s"(base)
+                 : "memory");
+}
+
+// Pages of a tile's four groups of 16 positions: -1 where there is none.
+struct TilePages {
+    int pg[kTile / 16];
+    int pos;
+    bool whole;             // every position of the tile is there
+    __device__ __forceinline__ void find(PageWalk& w, int lg_page, int at, int end) {
+        pos = at;
+        whole = at + kTile <= end;
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i) {
+            pg[i] = at + 16 * i < end ? w.page((at + 16 * i) >> lg_page) : -1;
+            whole = whole && pg[i] >= 0;
+        }
+    }
+    // bit i: the 16 positions of group i have a page
+    __device__ __forceinline__ int valid() const {
+        int v = 0;
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i) v |= (pg[i] >= 0) << i;
+        return v;
+    }
+};
+
+// A tile of K or V on its way to LDS: four waves' loads of 1024 bytes, each of
+// one page.  bf16 rows go straight to their places, the pieces permuted by what
+// a lane loads; codes go through registers.  Places without a position (behind
+// the last, or on no page) get what the page, or page 0, holds there: such
+// scores are masked, and such values of V with them.
+template <int KV, int D, bool V> struct Stage {
     static constexpr int E = KV == kKvBf16 ? 2 : 1;
     static constexpr int RB = D * E;                // bytes of a row
     static constexpr int PER = 1024 / RB;           // rows of a wave's load
-    static constexpr int N = kTile / (4 * PER);     // loads of a thread
+    static constexpr int N = kTile / (4 * PER);     // loads of a wave
     u32x4 w[N];
     unsigned s[N];
-    __device__ __forceinline__ static int row(int i, int wave, int lane) { return (i * 4 + wave) * PER + lane / (64 / PER); }
-    __device__ __forceinline__ void load(const PagedCache& c, const char* base, const unsigned char* scale,
-                                         size_t page_bytes, PageWalk& walk, int hk, int pos, int end, int wave, int lane) {
+    unsigned voff;          // a lane's bytes in a load
+    __device__ __forceinline__ void init(int wave, int lane) {
+        const int r = wave * PER + lane / (64 / PER), piece = lane % (64 / PER);
+        if constexpr (KV == kKvBf16)
+            voff = (unsigned)((lane / (64 / PER)) * RB + 16 * (V ? v_piece<D>(r, piece) : k_piece<D>(r, piece)));
+        else
+            voff = (unsigned)lane * 16;
+    }
+    __device__ __forceinline__ void load(const PagedCache& c, const TilePages& t, int hk, char* tile, int wave, int lane) {
+        const char* base = V ? c.v : c.k;
+        const size_t page_bytes = V ? c.v_page : c.k_page;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int at = pos + (i * 4 + wave) * PER, page = at < end ? walk.page(at >> c.lg_page) : -1;
-            const size_t r = ((size_t)hk << c.lg_page) + (at & ((1 << c.lg_page) - 1));
-            const auto rs = make_rsrc_n(base + (size_t)max(page, 0) * page_bytes + r * RB,
-                                        page < 0 ? 0u : (unsigned)(min(end - at, PER) * RB));
-            w[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, lane * 16, 0, 0);
-            if constexpr (KV >= kKvE4m3) {
-                const auto ss = make_rsrc_n(scale + (((size_t)max(page, 0) * c.Hk) << c.lg_page) + r, page < 0 ? 0u : (unsigned)PER);
-                s[i] = __builtin_amdgcn_raw_buffer_load_b8(ss, lane / (64 / PER), 0, 0);
+            const int r0 = (i * 4 + wave) * PER;    // of the tile
+            int pg = t.pg[i * 4 / N];
+            if constexpr (N == 2) pg = wave >= 2 ? t.pg[i * 2 + 1] : t.pg[i * 2];
+            if constexpr (N == 1) pg = wave >= 2 ? (wave == 3 ? t.pg[3] : t.pg[2]) : (wave == 1 ? t.pg[1] : t.pg[0]);
+            pg = max(pg, 0);
+            const size_t r = ((size_t)hk << c.lg_page) + ((t.pos + r0) & ((1 << c.lg_page) - 1));
+            const char* at = base + (size_t)pg * page_bytes + r * RB;
+            if constexpr (KV == kKvBf16) {
+                load_lds16(at, voff, tile + r0 * D * 2);
+            } else {
+                w[i] = *reinterpret_cast<const u32x4*>(at + voff);
+                s[i] = (V ? c.vs : c.ks)[(((size_t)pg * c.Hk) << c.lg_page) + r + lane / (64 / PER)];
             }
         }
     }
-    template <bool V> __device__ __forceinline__ void store(bf16* tile, int wave, int lane) const {
+    // what was loaded is in LDS once the workgroup has passed a barrier
+    __device__ __forceinline__ void store(char* tile, int wave, int lane) const {
+        if constexpr (KV == kKvBf16) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = row(i, wave, lane), p = lane % (64 / PER);
-            u32x4* to = reinterpret_cast<u32x4*>(tile + r * D);
-            if constexpr (KV == kKvBf16) {
-                to[V ? v_piece<D>(r, p) : k_piece<D>(r, p)] = w[i];
-            } else {
+            for (int i = 0; i < N; ++i) {
+                const int r = (i * 4 + wave) * PER + lane / (64 / PER), p = lane % (64 / PER);
+                u32x4* to = reinterpret_cast<u32x4*>(tile + r * D * 2);
                 const Codes<KV> d(s[i]);
                 unsigned o[8];
 #pragma unroll
@@ -79,96 +133,68 @@ template <int KV, int D> struct Stage {
     }
 };
 
-// K operand: lane: position 32 b + l % 32, channels 16 s + 8 (l / 32) ..
-template <int D> __device__ __forceinline__ bf16x8 k_frag(const bf16* tile, int b, int s, int lane) {
-    const int r = 32 * b + (lane & 31);
-    return *reinterpret_cast<const bf16x8*>(tile + r * D + 8 * k_piece<D>(r, 2 * s + (lane >> 5)));
-}
-// V operand: lane: channel 32 db + l % 32, positions 16 s + 4 h + i and 16 s + 8 + 4 h + i
-template <int D> __device__ __forceinline__ bf16x8 v_frag(const bf16* tile, int db, int s, int lane) {
-    const int r = 16 * s + 4 * (lane >> 5) + (lane >> 2 & 3), col = 32 * db + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
-    typedef __attribute__((address_space(3))) bf16x4 lds_x4;
-    const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_x4*)(tile + r * D + 8 * v_piece<D>(r, col >> 3) + (col & 7)));
-    const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-        (lds_x4*)(tile + (r + 8) * D + 8 * v_piece<D>(r + 8, col >> 3) + (col & 7)));
-    bf16x8 f;
+// A lane's byte offsets in the tiles; what changes between the products of a
+// tile is added as the reads' own constants.
+template <int D> struct Offsets {
+    static constexpr int KS = D / 16, RB = 2 * D;
+    int k[KS], v[D / 32];
+    __device__ __forceinline__ void init(int lane) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[i] = a[i];
-        f[4 + i] = b[i];
+        for (int s = 0; s < KS; ++s) k[s] = opaque((lane & 31) * RB + 16 * k_piece<D>(lane & 31, 2 * s + (lane >> 5)));
+        const int r = 4 * (lane >> 5) + (lane >> 2 & 3);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const int col = 32 * i + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
+            v[i] = opaque(r * RB + 16 * v_piece<D>(r, col >> 3) + 2 * (col & 7));
+        }
     }
-    return f;
-}
-
-template <int KV, int D> __global__ __launch_bounds__(256, 2) void kda_attn_chunk_kernel(AttnParams p) {
-    constexpr int KS = D / 16, DB = D / 32, M = 128;
-    __shared__ __align__(16) bf16 lds_k[2][kTile * D];
-    __shared__ __align__(16) bf16 lds_v[2][kTile * D];
-    AttnTile t;
-    if (!t.init(p, blockIdx.x)) return;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
-
-    const int r = t.r0 + 32 * wave + (lane & 31), tok = r / p.G, head = t.hk * p.G + r - tok * p.G;
-    const int lim = t.limit(r, p.G);
-    // the wave's first and last limits
-    const int w0 = t.r0 + 32 * wave, lim_first = t.limit(w0, p.G);
-    const int lim_last = w0 < t.rows ? t.limit(min(w0 + 31, t.rows - 1), p.G) : -1;
-    bf16x8 q[KS];
-    const char* row = p.q + (size_t)(t.first + tok) * p.q_stride + (size_t)head * D * 2;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-        u32x4 u = {0u, 0u, 0u, 0u};
-        if (r < t.rows) u = *reinterpret_cast<const u32x4*>(row + (16 * s + 8 * h) * 2);
-        q[s] = __builtin_bit_cast(bf16x8, u);
+    // K operand: position 32 b + l % 32, channels 16 s + 8 (l / 32) ..
+    __device__ __forceinline__ bf16x8 k_frag(const char* tile, int b, int s) const {
+        return *reinterpret_cast<const bf16x8*>(tile + k[s] + 32 * b * RB);
     }
-    f32x16 acc[DB];
-#pragma unroll
-    for (int db = 0; db < DB; ++db)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[db][e] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    const float c = p.c_log2, lazy = kLazy / c;
-
-    PageWalk walk;
-    walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);
-    Stage<KV, D> sk, sv;
-    if (t.lo < t.hi) {
-        sk.load(p.c, p.c.k, p.c.ks, p.c.k_page, walk, t.hk, t.lo, t.hi, wave, lane);
-        sv.load(p.c, p.c.v, p.c.vs, p.c.v_page, walk, t.hk, t.lo, t.hi, wave, lane);
-    }
-    int buf = 0;
-    for (int pos = t.lo; pos < t.hi; pos += kTile, buf ^= 1) {
-        sk.template store<false>(lds_k[buf], wave, lane);
-        sv.template store<true>(lds_v[buf], wave, lane);
-        __syncthreads();
-        // which 16 positions have a page
-        int valid = 0;
+    // V operand: channel 32 db + l % 32, positions 16 s + 4 h + i and 16 s + 8 + 4 h + i
+    __device__ __forceinline__ bf16x8 v_frag(const char* tile, int db, int s) const {
+        typedef __attribute__((address_space(3))) bf16x4 lds_x4;
+        const char* p = tile + v[db] + 16 * s * RB;
+        const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_x4*)p);
+        const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_x4*)(p + 8 * RB));
+        bf16x8 f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int at = pos + 16 * i;
-            valid |= (at < t.hi && walk.page(at >> p.c.lg_page) >= 0) << i;
+            f[i] = a[i];
+            f[4 + i] = b[i];
         }
-        if (pos + kTile < t.hi) {
-            sk.load(p.c, p.c.k, p.c.ks, p.c.k_page, walk, t.hk, pos + kTile, t.hi, wave, lane);
-            sv.load(p.c, p.c.v, p.c.vs, p.c.v_page, walk, t.hk, pos + kTile, t.hi, wave, lane);
-        }
-        if (pos > lim_last) continue;       // the wave's rows see nothing of it
+        return f;
+    }
+};
+
+// What a wave keeps of its 32 rows.
+template <int D> struct Rows {
+    static constexpr int KS = D / 16, DB = D / 32;
+    bf16x8 q[KS];
+    f32x16 acc[DB];
+    float m, l;
+    Offsets<D> at;
+
+    // One tile.  masked: some rows see only a part of it.
+    __device__ __forceinline__ void tile(const char* tk, const char* tv, float c, bool masked, int pos, int lim, int valid,
+                                         int lane) {
+        const int h = lane >> 5;
         f32x16 s[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) s[b] = mma32(s[b], k_frag<D>(lds_k[buf], b, k, lane), q[k]);
+            for (int k = 0; k < KS; ++k) s[b] = mma32(s[b], at.k_frag(tk, b, k), q[k]);
         }
-        const bool masked = pos + kTile - 1 > lim_first || valid != 15;
         if (masked) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const int at = 32 * b + 8 * (e >> 2) + 4 * h + (e & 3);
-                    if (pos + at > lim || !(valid >> (2 * b + (e >> 3)) & 1)) s[b][e] = -INFINITY;
+                    const int j = 32 * b + 8 * (e >> 2) + 4 * h + (e & 3);
+                    if (pos + j > lim || !(valid >> (2 * b + (e >> 3)) & 1)) s[b][e] = -INFINITY;
                 }
         }
         float top = s[0][0];
@@ -176,7 +202,7 @@ template <int KV, int D> __global__ __launch_bounds__(256, 2) void kda_attn_chun
         for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
-        if (__any(top > m + lazy)) {
+        if (__any(top > m + kLazy / c)) {
             const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
             const float a = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * c);
             m = mn;
@@ -198,84 +224,136 @@ template <int KV, int D> __global__ __launch_bounds__(256, 2) void kda_attn_chun
             }
             pf[k] = frag_from<bf16>(x);
         }
-        bool poison = false;
-        if (masked) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[db] = mma32(acc[db], at.v_frag(tv, db, k), pf[k]);
+    }
+};
+
+template <int KV, int D> __global__ __launch_bounds__(256, 2) void kda_attn_chunk_kernel(AttnParams p) {
+    constexpr int KS = D / 16, DB = D / 32, M = 128;
+    constexpr int TB = kTile * D * 2;
+    __shared__ __align__(16) char lds[4 * TB];      // K, V, K, V
+    __shared__ int lds_bad;                         // the first tile of V with a value taken out, or -1
+    AttnTile t;
+    if (!t.init(p, blockIdx.x)) return;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
+
+    const int r = t.r0 + 32 * wave + (lane & 31), tok = p.by_g.div(r), head = t.hk * p.G + r - tok * p.G;
+    const int lim = t.limit(r, p);
+    // the wave's first and last limits
+    const int w0 = t.r0 + 32 * wave, lim_first = t.limit(w0, p), t_first = t.limit(t.r0, p);
+    const int lim_last = w0 < t.rows ? t.limit(min(w0 + 31, t.rows - 1), p) : -1;
+    Rows<D> x;
+    const char* row = p.q + (size_t)(t.first + tok) * p.q_stride + (size_t)head * D * 2;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        u32x4 u = {0u, 0u, 0u, 0u};
+        if (r < t.rows) u = *reinterpret_cast<const u32x4*>(row + (16 * s + 8 * h) * 2);
+        x.q[s] = __builtin_bit_cast(bf16x8, u);
+    }
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x.acc[db][e] = 0.f;
+    x.m = -INFINITY;
+    x.l = 0.f;
+    const float c = p.c_log2;
+
+    PageWalk walk;
+    walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);
+    Stage<KV, D, false> sk;
+    Stage<KV, D, true> sv;
+    sk.init(wave, lane);
+    sv.init(wave, lane);
+    x.at.init(lane);
+    TilePages next;
+    if (t.lo < t.hi) {
+        next.find(walk, p.c.lg_page, t.lo, t.hi);
+        sk.load(p.c, next, t.hk, lds, wave, lane);
+        sv.load(p.c, next, t.hk, lds + TB, wave, lane);
+    }
+    if (threadIdx.x == 0) lds_bad = -1;
+    // a tile's K and V lie at `here`, the next one's go to `there`
+    auto step = [&](int pos, char* here, char* there) {
+        sk.store(here, wave, lane);
+        sv.store(here + TB, wave, lane);
+        const bool partly = pos + kTile - 1 > t_first || !next.whole;       // for a row of the tile's
+        const bool masked = pos + kTile - 1 > lim_first || !next.whole;     // for a row of the wave's
+        const int valid = next.valid();
+        __syncthreads();
+        if (partly) {
             bool bad = false;
-            const u32x4* v = reinterpret_cast<const u32x4*>(lds_v[buf]) + lane;
+            u32x4* v = reinterpret_cast<u32x4*>(here + TB) + threadIdx.x;
 #pragma unroll
-            for (int i = 0; i < kTile * D / 512; ++i) {
-                const u32x4 x = v[64 * i];
-                bad |= not_finite(x[0]) | not_finite(x[1]) | not_finite(x[2]) | not_finite(x[3]);
-            }
-            poison = __any(bad);
-        }
-        if (!poison) {
-#pragma unroll
-            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[db] = mma32(acc[db], v_frag<D>(lds_v[buf], db, k, lane), pf[k]);
-        } else {
-#pragma unroll 1
-            for (int minus = 0; minus < 2; ++minus) {
-#pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    f32x16 n;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) n[e] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float one[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int at = 16 * k + 8 * (i >> 2) + 4 * h + (i & 3);
-                            one[i] = pos + at <= lim && (valid >> k & 1) ? 1.f : 0.f;
-                        }
-                        n = mma32(n, flag8(v_frag<D>(lds_v[buf], db, k, lane), minus), frag_from<bf16>(one));
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[db][e] = poisoned(acc[db][e], minus ? 0.f : n[e], minus ? n[e] : 0.f);
+            for (int i = 0; i < TB / 4096; ++i) {
+                u32x4 y = v[256 * i];
+                if (not_finite(y[0]) || not_finite(y[1]) || not_finite(y[2]) || not_finite(y[3])) {
+                    v[256 * i] = u32x4{clean(y[0]), clean(y[1]), clean(y[2]), clean(y[3])};
+                    bad = true;
                 }
             }
-#pragma unroll
-            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[db] = mma32(acc[db], clean8(v_frag<D>(lds_v[buf], db, k, lane)), pf[k]);
+            if (bad && lds_bad < 0) lds_bad = pos;
+            __syncthreads();
         }
+        if (pos + kTile < t.hi) {
+            next.find(walk, p.c.lg_page, pos + kTile, t.hi);
+            sk.load(p.c, next, t.hk, there, wave, lane);
+            sv.load(p.c, next, t.hk, there + TB, wave, lane);
+        }
+        if (pos <= lim_last)        // the wave's rows see some of it
+            x.tile(here, here + TB, c, masked, pos, lim, valid, lane);
+    };
+    for (int pos = t.lo; pos < t.hi; pos += 2 * kTile) {
+        step(pos, lds, lds + 2 * TB);
+        if (pos + kTile < t.hi) step(pos + kTile, lds + 2 * TB, lds);
     }
+    __syncthreads();
+    if (lds_bad >= 0) mend_rows<KV, D>(x.acc, p, t, lds_bad, lim, h);
+    const float m = x.m;
+    float l = x.l;
     l += __shfl_xor(l, 32);
     if (r >= t.rows) return;
     if (t.splits > 1) {
-        const size_t x = t.unit * M + 32 * wave + (lane & 31);
-        float* po = p.part + x * D;
+        const size_t at = t.unit * M + 32 * wave + (lane & 31);
+        float* po = p.part + at * D;
         if (h == 0) {
-            p.ml[x * 2] = m;
-            p.ml[x * 2 + 1] = l;
+            p.ml[at * 2] = m;
+            p.ml[at * 2 + 1] = l;
         }
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<f32x4*>(po + 32 * db + 8 * j + 4 * h) =
-                    f32x4{acc[db][4 * j], acc[db][4 * j + 1], acc[db][4 * j + 2], acc[db][4 * j + 3]};
+                    f32x4{x.acc[db][4 * j], x.acc[db][4 * j + 1], x.acc[db][4 * j + 2], x.acc[db][4 * j + 3]};
         return;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    bf16* o = reinterpret_cast<bf16*>(p.o) + ((size_t)(t.first + tok) * p.H + head) * D;
-    const bf16* z = reinterpret_cast<const bf16*>(p.z + (size_t)(t.first + tok) * p.z_stride) + (size_t)head * D;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x.acc[db][e] *= inv;
+    const size_t out = ((size_t)head * D + 4 * h) * 2;
+    if (p.z) {
+        const char* z = p.z + (size_t)(t.first + tok) * p.z_stride + out;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bf16x4 zz = *reinterpret_cast<const bf16x4*>(z + 64 * db + 16 * j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x.acc[db][4 * j + i] = gate_of<bf16>(x.acc[db][4 * j + i], (float)zz[i]);
+            }
+    }
+    char* o = p.o + (size_t)(t.first + tok) * p.H * D * 2 + out;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int d = 32 * db + 8 * j + 4 * h;
-            float x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = acc[db][4 * j + i] * inv;
-            if (p.z) {
-                const bf16x4 zz = *reinterpret_cast<const bf16x4*>(z + d);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = gate_of<bf16>(x[i], (float)zz[i]);
-            }
-            st_run<4>(o + d, x);
+            const float y[4] = {x.acc[db][4 * j], x.acc[db][4 * j + 1], x.acc[db][4 * j + 2], x.acc[db][4 * j + 3]};
+            st_run<4>(reinterpret_cast<bf16*>(o + 64 * db + 16 * j), y);
         }
 }
 

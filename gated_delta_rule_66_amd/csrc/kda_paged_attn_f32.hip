@@ -63,19 +63,18 @@ template <int KV, int D> struct StageF {
     }
 };
 
-__device__ __forceinline__ bool finite_f(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
-
 template <int KV, int D> __global__ __launch_bounds__(256, 1) void kda_attn_f32_kernel(AttnParams p) {
     constexpr int KS = D / 8, DB = D / 32, M = 128, LD = D + 4;
     __shared__ __align__(16) float lds_k[kTileF * LD];
     __shared__ __align__(16) float lds_v[kTileF * LD];
+    __shared__ int lds_bad;                         // the first tile of V with a value taken out, or -1
     AttnTile t;
     if (!t.init(p, blockIdx.x)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
-    const int r = t.r0 + 32 * wave + (lane & 31), tok = r / p.G, head = t.hk * p.G + r - tok * p.G;
-    const int lim = t.limit(r, p.G);
-    const int w0 = t.r0 + 32 * wave, lim_first = t.limit(w0, p.G);
-    const int lim_last = w0 < t.rows ? t.limit(min(w0 + 31, t.rows - 1), p.G) : -1;
+    const int r = t.r0 + 32 * wave + (lane & 31), tok = p.by_g.div(r), head = t.hk * p.G + r - tok * p.G;
+    const int lim = t.limit(r, p);
+    const int w0 = t.r0 + 32 * wave, lim_first = t.limit(w0, p), t_first = t.limit(t.r0, p);
+    const int lim_last = w0 < t.rows ? t.limit(min(w0 + 31, t.rows - 1), p) : -1;
     // operand 4 s + i: channels 8 s + 4 h + i
     f32x4 q[KS];
     const char* row = p.q + (size_t)(t.first + tok) * p.q_stride + (size_t)head * D * 4;
@@ -99,15 +98,28 @@ template <int KV, int D> __global__ __launch_bounds__(256, 1) void kda_attn_f32_
         sk.load(p.c, p.c.k, p.c.ks, p.c.k_page, walk, t.hk, t.lo, t.hi, tid);
         sv.load(p.c, p.c.v, p.c.vs, p.c.v_page, walk, t.hk, t.lo, t.hi, tid);
     }
+    if (tid == 0) lds_bad = -1;
     for (int pos = t.lo; pos < t.hi; pos += kTileF) {
-        sk.template store<LD>(lds_k, tid);
-        sv.template store<LD>(lds_v, tid);
-        __syncthreads();
         int valid = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int at = pos + 16 * i;
             valid |= (at < t.hi && walk.page(at >> p.c.lg_page) >= 0) << i;
+        }
+        sk.template store<LD>(lds_k, tid);
+        sv.template store<LD>(lds_v, tid);
+        __syncthreads();
+        if (pos + kTileF - 1 > t_first || valid != 3) {      // for a row of the tile's
+            bool bad = false;
+            for (int i = tid; i < kTileF * D; i += 256) {
+                float* y = lds_v + i / D * LD + i % D;
+                if (!finite_f(*y)) {
+                    *y = 0.f;
+                    bad = true;
+                }
+            }
+            if (bad && lds_bad < 0) lds_bad = pos;
+            __syncthreads();
         }
         if (pos + kTileF < t.hi) {
             sk.load(p.c, p.c.k, p.c.ks, p.c.k_page, walk, t.hk, pos + kTileF, t.hi, tid);
@@ -148,42 +160,16 @@ template <int KV, int D> __global__ __launch_bounds__(256, 1) void kda_attn_f32_
                 s[e] = fast_exp2(fmaf(s[e], c, -mc));
                 l += s[e];
             }
-            bool poison = false;
-            if (masked) {
-                bool bad = false;
-                for (int i = lane; i < kTileF * D; i += 64) bad |= !finite_f(lds_v[i / D * LD + i % D]);
-                poison = __any(bad);
-            }
             // operand e: positions 8 (e / 4) + 4 h + e % 4
             const float* v = lds_v + 4 * h * LD + (lane & 31);
-            if (!poison) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 16; ++e)
 #pragma unroll
-                    for (int db = 0; db < DB; ++db) acc[db] = mma2(acc[db], v[(8 * (e >> 2) + (e & 3)) * LD + 32 * db], s[e]);
-            } else {
-                // a value that is not finite reaches the rows that see it, and only these
-#pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    f32x16 plus, minus;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) plus[e] = minus[e] = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float x = v[(8 * (e >> 2) + (e & 3)) * LD + 32 * db];
-                        const float one = pos + 8 * (e >> 2) + 4 * h + (e & 3) <= lim && (valid >> (e >> 3) & 1) ? 1.f : 0.f;
-                        const bool nan = x != x;
-                        acc[db] = mma2(acc[db], finite_f(x) ? x : 0.f, s[e]);
-                        plus = mma2(plus, nan || x == INFINITY ? 1.f : 0.f, one);
-                        minus = mma2(minus, nan || x == -INFINITY ? 1.f : 0.f, one);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[db][e] = poisoned(acc[db][e], plus[e], minus[e]);
-                }
-            }
+                for (int db = 0; db < DB; ++db) acc[db] = mma2(acc[db], v[(8 * (e >> 2) + (e & 3)) * LD + 32 * db], s[e]);
         }
         __syncthreads();
     }
+    if (lds_bad >= 0) mend_rows<KV, D>(acc, p, t, lds_bad, lim, h);
     l += __shfl_xor(l, 32);
     if (r >= t.rows) return;
     if (t.splits > 1) {

@@ -143,8 +143,8 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 :
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         const int r = t.r0 + 16 * nb + c16;
-        lim[nb] = t.limit(r, p.G);
-        const int tok = r / p.G, head = t.hk * p.G + r - tok * p.G;
+        lim[nb] = t.limit(r, p);
+        const int tok = p.by_g.div(r), head = t.hk * p.G + r - tok * p.G;
         const char* row = p.q + (size_t)(t.first + tok) * p.q_stride + (size_t)head * D * 2;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -153,7 +153,7 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 :
             q[nb][s] = __builtin_bit_cast(bf16x8, u);
         }
     }
-    const int lim_first = t.limit(t.r0, p.G);
+    const int lim_first = t.limit(t.r0, p);
 
     f32x4 acc[DV][NB];
     float m[NB], l[NB];
@@ -166,6 +166,7 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 :
     }
     const float c = p.c_log2, lazy = kLazy / c;
 
+    int bad_from = -1;      // the wave's first block of V with a value taken out
     int pos = t.lo + 32 * wave;
     if (pos < t.hi) {
         PageWalk walk;
@@ -238,14 +239,19 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 :
             }
             unsigned vp[8][DV / 2];
             b.vpairs(vp);
-            bool poison = false;
             if (masked) {
                 bool bad = false;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
                     for (int w = 0; w < DV / 2; ++w) bad |= not_finite(vp[i][w]);
-                poison = __any(bad);
+                if (__any(bad)) {
+                    if (bad_from < 0) bad_from = pos;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int w = 0; w < DV / 2; ++w) vp[i][w] = clean(vp[i][w]);
+                }
             }
 #pragma unroll
             for (int j = 0; j < DV; ++j) {
@@ -254,28 +260,28 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 :
                 const unsigned sel = j & 1 ? 0x07060302u : 0x05040100u;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) u[i] = __builtin_amdgcn_perm(vp[2 * i + 1][j >> 1], vp[2 * i][j >> 1], sel);
-                bf16x8 vf = __builtin_bit_cast(bf16x8, u);
-                if (!poison) {
+                const bf16x8 vf = __builtin_bit_cast(bf16x8, u);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) acc[j][nb] = mma(acc[j][nb], vf, pf[nb]);
-                } else {
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        float one[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            one[i] = pos + 16 * (i >> 2) + 4 * g + (i & 3) <= lim[nb] && (valid >> (i >> 2) & 1) ? 1.f : 0.f;
-                        const bf16x8 of = frag_from<bf16>(one);
-                        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-                        const f32x4 plus = mma(zero, flag8(vf, false), of), minus = mma(zero, flag8(vf, true), of);
-                        acc[j][nb] = mma(acc[j][nb], clean8(vf), pf[nb]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[j][nb][e] = poisoned(acc[j][nb][e], plus[e], minus[e]);
-                    }
-                }
+                for (int nb = 0; nb < NB; ++nb) acc[j][nb] = mma(acc[j][nb], vf, pf[nb]);
             }
             if (pos + 128 < t.hi) b.load_v(p.c, walk, t.hk, pos + 128, t.hi, lane);
         }
+    }
+    if (bad_from >= 0) {
+#pragma unroll 1
+        for (int i = bad_from; i < t.hi; i += i % 32 == 31 ? 97 : 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < DV; j += 4) {
+                    float f[4];
+                    load_v4<KV, D>(p.c, t.seq, t.hk, i, DV * (4 * g + e) + j, f);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            if (i <= lim[nb] && !finite_f(f[k])) acc[j + k][nb][e] += f[k];
+                }
     }
     // sums over the lane groups' positions
 #pragma unroll
@@ -344,7 +350,7 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 :
                         f32x4{acc[j][nb][e], acc[j + 1][nb][e], acc[j + 2][nb][e], acc[j + 3][nb][e]};
             continue;
         }
-        const int tok = r / p.G, head = t.hk * p.G + r - tok * p.G;
+        const int tok = p.by_g.div(r), head = t.hk * p.G + r - tok * p.G;
         const float inv = l[nb] == 0.f ? 0.f : 1.f / l[nb];
         const size_t at = (size_t)head * D;
         bf16* o = reinterpret_cast<bf16*>(p.o) + (size_t)(t.first + tok) * p.H * D + at;

@@ -78,9 +78,9 @@ __device__ __forceinline__ void seq_span(const SeqView& sv, int i, int* first, i
         *n = sv.T;
     }
 }
-// positions of sequence i, at most what its table's row holds
+// positions of sequence i, at most what its table's row holds; none without pages
 __device__ __forceinline__ int seq_positions(const PagedCache& c, int i) {
-    return min(max(c.lens[i], 0), c.blocks << c.lg_page);
+    return c.pages > 0 ? min(max(c.lens[i], 0), c.blocks << c.lg_page) : 0;
 }
 
 // A wave's page numbers along a sequence: lane l holds entry at + l of the
