@@ -143,7 +143,7 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     a.tiles_per_seq = packed ? 0 : (int)((T * G + a.M - 1) / a.M);
     a.tiles = packed ? M * G / a.M + N : (long long)N * a.tiles_per_seq;
     const long long units = a.tiles * c->heads, ctx = (long long)c->blocks * c->page_size;
-    const long long want = step ? 4096 : 1024, least = step ? 128 : 256;
+    const long long want = step ? 1536 : 1024, least = 512;
     long long n = units > 0 ? want / units : 1;
     if (n < 1 || M * H >= 1LL << 23) n = 1;
     long long len = n > 1 ? (ctx + n - 1) / n : ctx;
@@ -234,6 +234,8 @@ kda_status kda_paged_attn(int N, const int* cu_seqlens, int T, int H, kda_dtype 
     p.by_splits.set((unsigned)p.splits);
     p.by_tiles.set((unsigned)(p.tiles_per_seq > 0 ? p.tiles_per_seq : 1));
     p.by_len.set((unsigned)p.split_len);
+    p.by_h.set((unsigned)H);
+    p.by_t.set((unsigned)(T > 0 ? T : 1));
     p.part = (float*)workspace;
     p.ml = (float*)((char*)workspace + a.part);
     const char* name = a.kind == kAttnF32 ? "attn_f32" : a.kind == kAttnChunk ? "attn_chunk" : "attn_step";

@@ -25,71 +25,69 @@ namespace {
 
 template <int KV> constexpr int kElem = KV == kKvF32 ? 4 : KV == kKvBf16 ? 2 : 1;
 
-// N bytes of a row through a range-checked resource: zeros behind its end
+// N bytes at a wave's base and a lane's offset
 template <int N> struct Raw {
     unsigned w[N / 4];
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int off) {
+    __device__ __forceinline__ void load(const char* base, unsigned off) {
         if constexpr (N == 16) {
-            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+            const u32x4 v = *reinterpret_cast<const u32x4*>(base + off);
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = v[i];
         } else if constexpr (N == 8) {
-            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+            const u32x2 v = *reinterpret_cast<const u32x2*>(base + off);
             w[0] = v[0];
             w[1] = v[1];
         } else {
-            w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+            w[0] = *reinterpret_cast<const unsigned*>(base + off);
         }
     }
 };
 
-// One block of 32 positions as it is loaded.
+// One block of 32 positions as it is loaded, in two halves of one page each.
+// Places without a position (behind the last, or on no page) get what the page,
+// or page 0, holds there: such scores are masked, and such values of V with them.
 template <int KV, int D> struct Block {
-    static constexpr int E = kElem<KV>;
-    static constexpr int KL = D * E / 64;           // 16-byte loads of a K half (16 positions) a lane
+    static constexpr int E = kElem<KV>, RB = D * E;
+    static constexpr int KL = RB / 64;              // 16-byte loads of a K half (16 positions) a lane
     static constexpr int DV = D / 16;               // channels of V a lane
     static constexpr bool CODES = KV >= kKvE4m3;
     Raw<16> k[2][KL];
     Raw<DV * E> v[8];
-    unsigned ks[2], vs[2][4];                       // scale bytes: K's row of the lane, V's four rows of either half
-    int valid;                                      // bit h: half h's page is there
+    unsigned ks[2], vs[2];                          // scale bytes: K's row of the lane, V's four rows of either half
+    int pg[2];
+    unsigned koff, voff;
 
-    // resources of a half's rows of K or V (rows behind the sequence's end read zeros)
-    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rows(const PagedCache& c, const char* base, size_t page_bytes,
-                                                                 int page, int hk, int row, int left) {
-        const char* at = base + (size_t)max(page, 0) * page_bytes + ((((size_t)hk << c.lg_page) + row) * D) * E;
-        return make_rsrc_n(at, page < 0 ? 0u : (unsigned)(min(max(left, 0), 16) * D * E));
+    __device__ __forceinline__ void init(int lane) {
+        koff = (unsigned)((lane & 15) * RB + (lane >> 4) * 16);
+        voff = (unsigned)((lane >> 4) * 4 * RB + (lane & 15) * DV * E);
     }
-    __device__ __forceinline__ void load_k(const PagedCache& c, PageWalk& w, int hk, int pos, int end, int lane) {
-        valid = 0;
+    __device__ __forceinline__ void find(const PagedCache& c, PageWalk& w, int pos, int end) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) pg[h] = pos + 16 * h < end ? w.page((pos + 16 * h) >> c.lg_page) : -1;
+    }
+    __device__ __forceinline__ int valid() const { return (pg[0] >= 0) | (pg[1] >= 0) << 1; }
+    __device__ __forceinline__ static size_t row(const PagedCache& c, int hk, int at) {
+        return ((size_t)hk << c.lg_page) + (at & ((1 << c.lg_page) - 1));
+    }
+    __device__ __forceinline__ void load_k(const PagedCache& c, int hk, int pos, int lane) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int at = pos + 16 * h, page = at < end ? w.page(at >> c.lg_page) : -1;
-            const int row = at & ((1 << c.lg_page) - 1);
-            valid |= (page >= 0) << h;
-            const auto r = rows(c, c.k, c.k_page, page, hk, row, end - at);
+            const size_t page = (size_t)max(pg[h], 0), r = row(c, hk, pos + 16 * h);
+            const char* at = c.k + page * c.k_page + r * RB;
 #pragma unroll
-            for (int i = 0; i < KL; ++i) k[h][i].load(r, (lane & 15) * D * E + (4 * i + (lane >> 4)) * 16);
-            if constexpr (CODES) {
-                const auto s = make_rsrc_n(c.ks + ((((size_t)max(page, 0) * c.Hk + hk) << c.lg_page) + row), page < 0 ? 0u : 16u);
-                ks[h] = __builtin_amdgcn_raw_buffer_load_b8(s, lane & 15, 0, 0);
-            }
+            for (int i = 0; i < KL; ++i) k[h][i].load(at + 64 * i, koff);
+            if constexpr (CODES) ks[h] = (c.ks + ((page * c.Hk) << c.lg_page) + r)[lane & 15];
         }
     }
-    __device__ __forceinline__ void load_v(const PagedCache& c, PageWalk& w, int hk, int pos, int end, int lane) {
+    __device__ __forceinline__ void load_v(const PagedCache& c, int hk, int pos, int lane) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int at = pos + 16 * h, page = at < end ? w.page(at >> c.lg_page) : -1;
-            const int row = at & ((1 << c.lg_page) - 1);
-            const auto r = rows(c, c.v, c.v_page, page, hk, row, end - at);
+            const size_t page = (size_t)max(pg[h], 0), r = row(c, hk, pos + 16 * h);
+            const char* at = c.v + page * c.v_page + r * RB;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[4 * h + i].load(r, (4 * (lane >> 4) + i) * D * E + (lane & 15) * DV * E);
-            if constexpr (CODES) {
-                const auto s = make_rsrc_n(c.vs + ((((size_t)max(page, 0) * c.Hk + hk) << c.lg_page) + row), page < 0 ? 0u : 16u);
-                const unsigned b = __builtin_amdgcn_raw_buffer_load_b32(s, 4 * (lane >> 4), 0, 0);
-                vs[h][0] = b;
-            }
+            for (int i = 0; i < 4; ++i) v[4 * h + i].load(at + i * RB, voff);
+            if constexpr (CODES)
+                vs[h] = *reinterpret_cast<const unsigned*>(c.vs + ((page * c.Hk) << c.lg_page) + r + 4 * (lane >> 4));
         }
     }
     // K operand of product s: channels of Q's operand s
@@ -116,7 +114,7 @@ template <int KV, int D> struct Block {
 #pragma unroll
                 for (int w = 0; w < DV / 2; ++w) o[i][w] = v[i].w[w];
             } else {
-                const Codes<KV> d(vs[i >> 2][0] >> (8 * (i & 3)) & 255u);
+                const Codes<KV> d(vs[i >> 2] >> (8 * (i & 3)) & 255u);
 #pragma unroll
                 for (int w = 0; w < DV / 4; ++w) d.bf(v[i].w[w], &o[i][2 * w]);
             }
@@ -129,7 +127,7 @@ template <int KV> __device__ __forceinline__ int q_channel(int s, int g) {
     return KV >= kKvE4m3 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
 }
 
-template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 : 2) void kda_attn_step_kernel(AttnParams p) {
+template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(KV == kKvBf16 && D == 128) ? 3 : 2) void kda_attn_step_kernel(AttnParams p) {
     constexpr int R = 16 * NB, DV = D / 16, KS = D / 32, LD = D + 4;
     __shared__ float lds_o[2][R][LD];
     __shared__ float lds_ml[2][R][2];
@@ -172,8 +170,10 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 :
         PageWalk walk;
         walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);
         Block<KV, D> b;
-        b.load_k(p.c, walk, t.hk, pos, t.hi, lane);
-        b.load_v(p.c, walk, t.hk, pos, t.hi, lane);
+        b.init(lane);
+        b.find(p.c, walk, pos, t.hi);
+        b.load_k(p.c, t.hk, pos, lane);
+        b.load_v(p.c, t.hk, pos, lane);
         for (; pos < t.hi; pos += 128) {
             f32x4 s[2][NB];
 #pragma unroll
@@ -188,10 +188,14 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 :
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) s[h][nb] = mma(s[h][nb], kf, q[nb][k]);
                 }
-            const int valid = b.valid;
+            const int valid = b.valid();
             // rows of the tile that see less than the block, or pages that are not there
             const bool masked = pos + 31 > lim_first || valid != 3;
-            if (pos + 128 < t.hi) b.load_k(p.c, walk, t.hk, pos + 128, t.hi, lane);
+            const int next = pos + 128;
+            if (next < t.hi) {
+                b.find(p.c, walk, next, t.hi);
+                b.load_k(p.c, t.hk, next, lane);
+            }
             if (masked) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -264,7 +268,7 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 :
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) acc[j][nb] = mma(acc[j][nb], vf, pf[nb]);
             }
-            if (pos + 128 < t.hi) b.load_v(p.c, walk, t.hk, pos + 128, t.hi, lane);
+            if (next < t.hi) b.load_v(p.c, t.hk, next, lane);
         }
     }
     if (bad_from >= 0) {
@@ -370,14 +374,18 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 ? 3 :
     }
 }
 
-// Joins the ranges of tiles that were split: a team of lanes a row (token and
-// head), D / 4 lanes a range's row, the ranges dealt to the team's slots.
-template <typename T, int D> __global__ __launch_bounds__(512) void kda_attn_join_kernel(AttnParams p, int rows) {
-    constexpr int LANES = D / 4, SLOTS = 512 / LANES;
-    __shared__ float lds[SLOTS][D + 4];
-    __shared__ float lds_l[SLOTS];
-    const int tok = blockIdx.x / p.H, head = blockIdx.x - tok * p.H;
-    const int hk = head / p.G, gq = head - hk * p.G;
+// Joins the ranges of tiles that were split.  D / 4 lanes take a range's row;
+// a block of 256 threads takes TEAMS rows (token and head), the ranges of a row
+// dealt to the lanes' slots of its team: one row where there are many ranges.
+template <typename T, int D, int TEAMS> __global__ __launch_bounds__(256) void kda_attn_join_kernel(AttnParams p, int rows) {
+    constexpr int LANES = D / 4, SLOTS = 256 / LANES / TEAMS;
+    __shared__ f32x4 lds[SLOTS > 1 ? 256 : 1];
+    __shared__ float lds_l[SLOTS > 1 ? SLOTS : 1];
+    static_assert(TEAMS == 1 || SLOTS == 1, "a row a block, or a slot a row");
+    const int lane = threadIdx.x % LANES, my = TEAMS == 1 ? threadIdx.x / LANES : 0;
+    const int id = blockIdx.x * TEAMS + (TEAMS == 1 ? 0 : threadIdx.x / LANES);
+    if (id >= rows) return;
+    const int tok = p.by_h.div(id), head = id - tok * p.H, hk = p.by_g.div(head), gq = head - hk * p.G;
     int seq, first, n, slot0;
     if (p.sv.cu) {
         if (tok < p.sv.cu[0] || tok >= p.sv.cu[p.sv.N]) return;
@@ -390,48 +398,68 @@ template <typename T, int D> __global__ __launch_bounds__(512) void kda_attn_joi
                 b = mid;
         }
         seq = a;
-        slot0 = AttnTile::slot(p, seq);
+        seq_span(p.sv, seq, &first, &n);
+        slot0 = ((first * p.G) >> p.lg_m) + seq;
     } else {
-        seq = tok / p.sv.T;
+        seq = p.by_t.div(tok);
+        seq_span(p.sv, seq, &first, &n);
         slot0 = seq * p.tiles_per_seq;
     }
-    seq_span(p.sv, seq, &first, &n);
-    const int r = (tok - first) * p.G + gq, at = r / p.M;
-    if (tok < first || tok >= first + n || slot0 + at >= p.tiles) return;
+    if ((unsigned)(tok - first) >= (unsigned)n) return;
+    const int r = (tok - first) * p.G + gq, at = r >> p.lg_m;
+    if (slot0 + at >= p.tiles) return;
     const int L = seq_positions(p.c, seq);
-    const int end = max(L - n + (min((at + 1) * p.M, n * p.G) - 1) / p.G + 1, 0);
-    const int splits = end > 0 ? (end - 1) / p.split_len + 1 : 1;
+    const int end = max(L - n + p.by_g.div(min((at + 1) << p.lg_m, n * p.G) - 1) + 1, 0);
+    const int splits = end > 0 ? p.by_len.div(end - 1) + 1 : 1;
     if (splits <= 1) return;
     const size_t unit = ((size_t)(slot0 + at) * p.c.Hk + hk) * p.splits;
-    const size_t row = unit * p.M + (r - at * p.M);     // of range 0; ranges are M rows apart
+    const size_t row = (unit << p.lg_m) + (r - (at << p.lg_m));     // of range 0; ranges are M rows apart
+    const float2* ml = reinterpret_cast<const float2*>(p.ml) + row;
     float top = -INFINITY;
-    for (int s = 0; s < splits; ++s) top = fmaxf(top, p.ml[(row + (size_t)s * p.M) * 2]);
-    const int lane = threadIdx.x % LANES, my = threadIdx.x / LANES;
+    for (int s = lane; s < splits; s += LANES) top = fmaxf(top, ml[(size_t)s << p.lg_m].x);
+#pragma unroll
+    for (int m = LANES / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     float l = 0.f;
+    const float* part = p.part + row * D + 4 * lane;
+#pragma unroll 4
     for (int s = my; s < splits; s += SLOTS) {
-        const size_t x = row + (size_t)s * p.M;
-        const float m = p.ml[x * 2], w = m == top ? 1.f : fast_exp2((m - top) * p.c_log2);
-        const f32x4 v = *reinterpret_cast<const f32x4*>(p.part + x * D + 4 * lane);
-        l += w * p.ml[x * 2 + 1];
+        const float2 x = ml[(size_t)s << p.lg_m];
+        const f32x4 v = *reinterpret_cast<const f32x4*>(part + ((size_t)s << p.lg_m) * D);
+        const float w = x.x == top ? 1.f : fast_exp2((x.x - top) * p.c_log2);
+        l += w * x.y;
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] += w * v[i];
     }
-    *reinterpret_cast<f32x4*>(&lds[my][4 * lane]) = o;
-    if (lane == 0) lds_l[my] = l;
-    __syncthreads();
-    if (threadIdx.x >= D) return;
-    const int d = threadIdx.x;
-    float sum = 0.f, all = 0.f;
+    if constexpr (SLOTS > 1) {
+        lds[threadIdx.x] = o;
+        if (lane == 0) lds_l[my] = l;
+        __syncthreads();
+        if (my) return;
+        for (int s = 1; s < SLOTS; ++s) {
+            l += lds_l[s];
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-        sum += lds[s][d];
-        all += lds_l[s];
+            for (int i = 0; i < 4; ++i) o[i] += lds[s * LANES + lane][i];
+        }
     }
-    float x = all == 0.f ? 0.f : sum / all;
-    const size_t col = (size_t)head * D + d;
-    if (p.z) x = gate_of<T>(x, to_f32(reinterpret_cast<const T*>(p.z + (size_t)tok * p.z_stride)[col]));
-    reinterpret_cast<T*>(p.o)[(size_t)tok * p.H * D + col] = from_f32<T>(x);
+    const size_t col = (size_t)head * D + 4 * lane;
+    const T* z = p.z ? reinterpret_cast<const T*>(p.z + (size_t)tok * p.z_stride) + col : nullptr;
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[i] = l == 0.f ? 0.f : o[i] / l;
+        if (z) y[i] = gate_of<T>(y[i], to_f32(z[i]));
+    }
+    st_run<4>(reinterpret_cast<T*>(p.o) + (size_t)tok * p.H * D + col, y);
+}
+
+template <typename T, int D> hipError_t launch_join(const AttnParams& p, int rows, hipStream_t st) {
+    constexpr int TEAMS = 1024 / D;
+    if (p.splits > 8)
+        kda_attn_join_kernel<T, D, 1><<<rows, 256, 0, st>>>(p, rows);
+    else
+        kda_attn_join_kernel<T, D, TEAMS><<<(rows + TEAMS - 1) / TEAMS, 256, 0, st>>>(p, rows);
+    return hipGetLastError();
 }
 
 template <int KV, int D> hipError_t launch_step(AttnKind kind, const AttnParams& p, int grid, hipStream_t st) {
@@ -453,19 +481,9 @@ hipError_t launch_attn_step(AttnKind kind, int kv, int D, const AttnParams& p, i
 }
 
 hipError_t launch_attn_join(int dtype, int D, const AttnParams& p, int M_tokens, hipStream_t st) {
-    const int grid = M_tokens * p.H;
-    if (dtype) {
-        if (D == 128)
-            kda_attn_join_kernel<bf16, 128><<<grid, 512, 0, st>>>(p, grid);
-        else
-            kda_attn_join_kernel<bf16, 64><<<grid, 512, 0, st>>>(p, grid);
-    } else {
-        if (D == 128)
-            kda_attn_join_kernel<float, 128><<<grid, 512, 0, st>>>(p, grid);
-        else
-            kda_attn_join_kernel<float, 64><<<grid, 512, 0, st>>>(p, grid);
-    }
-    return hipGetLastError();
+    const int rows = M_tokens * p.H;
+    if (dtype) return D == 128 ? launch_join<bf16, 128>(p, rows, st) : launch_join<bf16, 64>(p, rows, st);
+    return D == 128 ? launch_join<float, 128>(p, rows, st) : launch_join<float, 64>(p, rows, st);
 }
 
 }  // namespace kda

@@ -23,6 +23,7 @@ zeros, attended to by no token.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -36,10 +37,8 @@ _SCALE = torch.float8_e8m0fnu
 
 
 def _page_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between the pages of a cache."""
+    """Elements between the pages of a cache whose strides are not simply nested."""
     P, H, S, D = t.shape
-    if t.is_contiguous():
-        return H * S * D
     st = t.stride()
     if (D != 1 and st[3] != 1) or (S != 1 and st[2] != D) or (H != 1 and st[1] != S * D):
         raise ValueError("%s must be contiguous within its pages" % name)
@@ -47,40 +46,64 @@ def _page_stride(t: torch.Tensor, name: str) -> int:
 
 
 def _cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, dev: int) -> PagedCache:
-    if k_cache.dim() != 4:
+    """The C struct of a call's cache.  (As in the mixer operators, what is right passes by few host steps, which are
+    what counts in one-token calls; what is not is named by the slower checks.)"""
+    shape, ty = k_cache.shape, k_cache.dtype
+    if len(shape) != 4:
         raise ValueError("k_cache is [pages, heads, page_size, D]")
-    try:
-        code = _KV[k_cache.dtype]
-    except KeyError:
-        raise ValueError("a cache is bf16, fp32, float8_e4m3fn or int8, got %s" % k_cache.dtype) from None
-    shape = k_cache.shape
-    if k_cache.get_device() != dev or v_cache.get_device() != dev or v_cache.shape != shape or \
-            v_cache.dtype != k_cache.dtype:
-        _refuse(k_cache, "k_cache", shape, k_cache.dtype, dev)
-        _refuse(v_cache, "v_cache", shape, k_cache.dtype, dev)
-    if max(shape) > _INT_MAX:
+    code = _KV.get(ty)
+    if code is None:
+        raise ValueError("a cache is bf16, fp32, float8_e4m3fn or int8, got %s" % ty)
+    if k_cache.get_device() != dev or v_cache.get_device() != dev or v_cache.shape != shape or v_cache.dtype != ty:
+        _refuse(k_cache, "k_cache", shape, ty, dev)
+        _refuse(v_cache, "v_cache", shape, ty, dev)
+    P, H, S, D = shape
+    if P > _INT_MAX or H > _INT_MAX or S > _INT_MAX or D > _INT_MAX:
         raise KDAError(_k.KDA_ERR_UNSUPPORTED, "a cache of shape %s" % (tuple(shape),))
+    kst, vst = k_cache.stride(), v_cache.stride()
+    inner = (S * D, D, 1)
+    ks = kst[0] if kst[1:] == inner else _page_stride(k_cache, "k_cache")
+    vs = vst[0] if vst[1:] == inner else _page_stride(v_cache, "v_cache")
     if code >= 2:
         if k_scale is None or v_scale is None:
             raise ValueError("an 8-bit cache needs k_scale and v_scale")
         _check(k_scale, "k_scale", shape[:3], _SCALE, dev)
         _check(v_scale, "v_scale", shape[:3], _SCALE, dev)
+        kp, vp = k_scale.data_ptr(), v_scale.data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale belong to 8-bit caches")
-    if block_table.dim() != 2:
+    else:
+        kp = vp = None
+    tshape = block_table.shape
+    if len(tshape) != 2:
         raise ValueError("block_table is [N, blocks]")
-    N, blocks = block_table.shape
+    N, blocks = tshape
     if block_table.dtype != torch.int32 or block_table.get_device() != dev:
-        _refuse(block_table, "block_table", block_table.shape, torch.int32, dev)
-    ts = blocks
-    if not block_table.is_contiguous():
-        ts = block_table.stride(0) if N > 1 else blocks
-        if (blocks > 1 and block_table.stride(1) != 1) or ts < blocks:
-            raise ValueError("block_table must have contiguous rows of its own")
+        _refuse(block_table, "block_table", tshape, torch.int32, dev)
+    ts, one = block_table.stride()
+    if (one != 1 and blocks > 1) or (ts < blocks and N > 1):
+        raise ValueError("block_table must have contiguous rows of its own")
     _check(seq_lens, "seq_lens", (N,), torch.int32, dev)
-    return PagedCache(code, shape[0], shape[1], shape[2], shape[3], blocks, k_cache.data_ptr(), v_cache.data_ptr(),
-                      _page_stride(k_cache, "k_cache"), _page_stride(v_cache, "v_cache"), _p(k_scale), _p(v_scale),
+    return PagedCache(code, P, H, S, D, blocks, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, kp, vp,
                       block_table.data_ptr(), ts, seq_lens.data_ptr())
+
+
+def _tokens(t: torch.Tensor, name: str, shape, lead: int, dtype, dev: int) -> int:
+    """Elements between the token rows of a token tensor, as mixer._rows, which it leaves the unusual ones to."""
+    if t.shape == shape and t.dtype == dtype and t.get_device() == dev and t.numel() <= _INT_MAX:
+        st = t.stride()
+        h, d = shape[lead:]
+        if st[lead + 1] == 1 and st[lead] == d:
+            if lead == 1:
+                row = st[0]
+            else:
+                n, tokens = shape[:2]
+                row = st[1] if tokens != 1 else st[0]
+                if n != 1 and tokens != 1 and st[0] != row * tokens:
+                    row = -1
+            if row >= h * d:
+                return row
+    return _rows(t, name, shape, lead, dtype, dev)
 
 
 def _batch(shape, seq_lens, cu_seqlens, dev: int, name: str):
@@ -110,8 +133,8 @@ def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     c = _cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, dev)
     lead, N, T = _batch(k.shape, seq_lens, cu_seqlens, dev, "k")
     shape = k.shape[:lead] + (c.heads, c.head_dim)
-    ks = _rows(k, "k", shape, lead, k.dtype, dev)
-    vs = _rows(v, "v", shape, lead, k.dtype, dev)
+    ks = _tokens(k, "k", shape, lead, k.dtype, dev)
+    vs = _tokens(v, "v", shape, lead, k.dtype, dev)
     _call("kda_kv_cache_write", dev, N, _p(cu_seqlens), T, _dtype_code(k.dtype), _p(k), ks, _p(v), vs,
           ctypes.byref(c))
 
@@ -143,6 +166,13 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: tor
     return out[0], out[1]
 
 
+@functools.lru_cache(maxsize=1024)
+def _attn_workspace(N, packed, T, H, code, *sizes) -> int:
+    """The bytes of a call's workspace, which go by its sizes alone."""
+    c = PagedCache(sizes[0], *sizes[1:])
+    return _size("kda_paged_attn_workspace_size", N, int(packed), T, H, code, ctypes.byref(c))
+
+
 def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                seq_lens: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
                v_scale: Optional[torch.Tensor] = None, *, scale: Optional[float] = None,
@@ -164,14 +194,15 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     H = q.shape[-2]
     shape = q.shape[:lead] + (H, c.head_dim)
     code = _dtype_code(q.dtype)
-    qs = _rows(q, "q", shape, lead, q.dtype, dev)
-    zs = _rows(gate, "gate", shape, lead, q.dtype, dev) if gate is not None else qs
+    qs = _tokens(q, "q", shape, lead, q.dtype, dev)
+    zs = _tokens(gate, "gate", shape, lead, q.dtype, dev) if gate is not None else qs
     if out is None:
         out = _like(q)
     else:
         _check(out, "out", shape, q.dtype, dev)
     ref = ctypes.byref(c)
-    need = _size("kda_paged_attn_workspace_size", N, int(cu_seqlens is not None), T, H, code, ref)
+    need = _attn_workspace(N, cu_seqlens is not None, T, H, code, c.dt, c.pages, c.heads, c.page_size, c.head_dim,
+                           c.blocks)
     workspace, have = _workspace(workspace, need, dev)
     _call("kda_paged_attn", dev, N, _p(cu_seqlens), T, H, code, c.head_dim ** -0.5 if scale is None else float(scale),
           _p(q), qs, _p(gate), zs, _p(out), ref, _p(workspace), have)
