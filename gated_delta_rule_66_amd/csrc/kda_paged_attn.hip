@@ -177,16 +177,46 @@ template <int D> struct Rows {
     Offsets<D> at;
 
     // One tile.  masked: some rows see only a part of it.
+    // LDS reads go out ahead of the products that take them, and the weights of
+    // the next 16 positions are made beside the products of the present ones:
+    // left to itself, the compiler reads each operand just before its product.
     __device__ __forceinline__ void tile(const char* tk, const char* tv, float c, bool masked, int pos, int lim, int valid,
                                          int lane) {
         const int h = lane >> 5;
         f32x16 s[2];
+        bf16x8 kf[2][KS];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) s[b] = mma32(s[b], at.k_frag(tk, b, k), q[k]);
+            for (int k = 0; k < KS; ++k) kf[b][k] = at.k_frag(tk, b, k);
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int k = 0; k < KS; ++k) s[b] = mma32(s[b], kf[b][k], q[k]);
+        bf16x8 vf[2][DB];
+#pragma unroll
+        for (int db = 0; db < DB; ++db) vf[0][db] = at.v_frag(tv, db, 0);
+        float top = s[0][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
+        // four reads ahead, then a read beside each product
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * KS - 4; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (i >= KS) __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, DB / 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
         }
         if (masked) {
 #pragma unroll
@@ -196,12 +226,12 @@ template <int D> struct Rows {
                     const int j = 32 * b + 8 * (e >> 2) + 4 * h + (e & 3);
                     if (pos + j > lim || !(valid >> (2 * b + (e >> 3)) & 1)) s[b][e] = -INFINITY;
                 }
+            top = s[0][0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
         }
-        float top = s[0][0];
-#pragma unroll
-        for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
         if (__any(top > m + kLazy / c)) {
             const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
             const float a = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * c);
@@ -213,21 +243,37 @@ template <int D> struct Rows {
                 for (int e = 0; e < 16; ++e) acc[db][e] *= a;
         }
         const float mc = m == -INFINITY ? 0.f : m * c;
-        bf16x8 pf[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        auto weights = [&](int k) {
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 x[i] = fast_exp2(fmaf(s[k >> 1][8 * (k & 1) + i], c, -mc));
                 l += x[i];
             }
-            pf[k] = frag_from<bf16>(x);
+            return frag_from<bf16>(x);
+        };
+        bf16x8 pf[2];
+        pf[0] = weights(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k < 3) {
+#pragma unroll
+                for (int db = 0; db < DB; ++db) vf[(k + 1) & 1][db] = at.v_frag(tv, db, k + 1);
+            }
+#pragma unroll
+            for (int db = 0; db < DB; ++db) acc[db] = mma32(acc[db], vf[k & 1][db], pf[k & 1]);
+            if (k < 3) pf[(k + 1) & 1] = weights(k + 1);
+#pragma unroll
+            for (int db = 0; db < DB; ++db) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (k < 3) {
+                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x402, 28 / DB, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[db] = mma32(acc[db], at.v_frag(tv, db, k), pf[k]);
     }
 };
 
@@ -259,6 +305,8 @@ template <int KV, int D> __global__ __launch_bounds__(256, 2) void kda_attn_chun
         for (int e = 0; e < 16; ++e) x.acc[db][e] = 0.f;
     x.m = -INFINITY;
     x.l = 0.f;
+    // the loads of Q end here: a wait for them in the loop would be one for the tiles on their way
+    __builtin_amdgcn_s_waitcnt(0x0f70);
     const float c = p.c_log2;
 
     PageWalk walk;
