@@ -36,40 +36,40 @@ template <int D> __device__ __forceinline__ int v_piece(int row, int piece) {
     return D == 128 ? piece ^ ((row & 3) << 2 | (row & 2)) : piece ^ ((row & 3) << 1);
 }
 
-// 64 lanes' 16 bytes at base + off straight into 1024 bytes of LDS.  Written out
-// because the compiler would wait for a builtin's loads before any read of LDS,
-// those of the tile before included: the wait is Stage::store's.  (m0, the LDS
-// address, has to stand one instruction before its use; the compiler has no use
-// of its own for it in this kernel.)
-__device__ __forceinline__ void load_lds16(const char* base, unsigned off, char* to) {
-    typedef __attribute__((address_space(3))) char lds_c;
-    const unsigned at = (unsigned)uniform((int)(unsigned)(uintptr_t)(lds_c*)to);
+// 64 lanes' 16 bytes at base + off straight into 1024 bytes of LDS at `to`.
+// Written out because the compiler would wait for a builtin's loads before any
+// read of LDS, those of the tile before included: the wait is Stage::store's.
+// (m0, the LDS address, has to stand one instruction before its use; the
+// compiler has no use of its own for it in this kernel.)
+__device__ __forceinline__ void load_lds16(const char* base, unsigned off, unsigned to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(at), "v"(off), "s"(base)
+                 : "s"(to), "v"(off), "s"(base)
                  : "memory");
 }
+__device__ __forceinline__ unsigned lds_address(const char* p) {
+    typedef __attribute__((address_space(3))) const char lds_c;
+    return (unsigned)(uintptr_t)(lds_c*)p;
+}
 
-// Pages of a tile's four groups of 16 positions: -1 where there is none.
+// Pages of a tile: of its groups of 16 positions where pages are smaller than
+// tiles, else one page.  -1: not there.
 struct TilePages {
     int pg[kTile / 16];
-    int pos;
-    bool whole;             // every position of the tile is there
+    int pos, valid;         // valid: bit i where group i has a page
     __device__ __forceinline__ void find(PageWalk& w, int lg_page, int at, int end) {
         pos = at;
-        whole = at + kTile <= end;
+        if (lg_page >= 6) {
+            pg[0] = w.page(at >> lg_page);
+            valid = pg[0] >= 0 ? 15 : 0;
+            return;
+        }
+        valid = 0;
 #pragma unroll
         for (int i = 0; i < kTile / 16; ++i) {
             pg[i] = at + 16 * i < end ? w.page((at + 16 * i) >> lg_page) : -1;
-            whole = whole && pg[i] >= 0;
+            valid |= (pg[i] >= 0) << i;
         }
-    }
-    // bit i: the 16 positions of group i have a page
-    __device__ __forceinline__ int valid() const {
-        int v = 0;
-#pragma unroll
-        for (int i = 0; i < kTile / 16; ++i) v |= (pg[i] >= 0) << i;
-        return v;
     }
 };
 
@@ -85,17 +85,39 @@ template <int KV, int D, bool V> struct Stage {
     static constexpr int N = kTile / (4 * PER);     // loads of a wave
     u32x4 w[N];
     unsigned s[N];
-    unsigned voff;          // a lane's bytes in a load
-    __device__ __forceinline__ void init(int wave, int lane) {
+    unsigned voff[N];       // a lane's bytes in a load, from the tile's first row (small pages: from the load's)
+    __device__ __forceinline__ void init(int wave, int lane, bool small) {
         const int r = wave * PER + lane / (64 / PER), piece = lane % (64 / PER);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            unsigned at = (unsigned)lane * 16;
+            if constexpr (KV == kKvBf16)
+                at = (unsigned)((lane / (64 / PER)) * RB + 16 * (V ? v_piece<D>(r, piece) : k_piece<D>(r, piece)));
+            voff[i] = at + (small ? 0u : (unsigned)((i * 4 + wave) * PER * RB));
+        }
+    }
+    __device__ __forceinline__ void one(const char* at, int i, char* tile, int wave) {
         if constexpr (KV == kKvBf16)
-            voff = (unsigned)((lane / (64 / PER)) * RB + 16 * (V ? v_piece<D>(r, piece) : k_piece<D>(r, piece)));
+            load_lds16(at, voff[i], lds_address(tile) + (unsigned)((i * 4 + wave) * PER * D * 2));
         else
-            voff = (unsigned)lane * 16;
+            w[i] = *reinterpret_cast<const u32x4*>(at + voff[i]);
     }
     __device__ __forceinline__ void load(const PagedCache& c, const TilePages& t, int hk, char* tile, int wave, int lane) {
         const char* base = V ? c.v : c.k;
+        const unsigned char* scale = V ? c.vs : c.ks;
         const size_t page_bytes = V ? c.v_page : c.k_page;
+        const int mask = (1 << c.lg_page) - 1;
+        if (c.lg_page >= 6) {
+            const size_t pg = (size_t)max(t.pg[0], 0), r = ((size_t)hk << c.lg_page) + (t.pos & mask);
+            const char* at = base + pg * page_bytes + r * RB;
+            const unsigned char* sc = scale + ((pg * c.Hk) << c.lg_page) + r;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                one(at, i, tile, wave);
+                if constexpr (KV != kKvBf16) s[i] = sc[(i * 4 + wave) * PER + lane / (64 / PER)];
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int r0 = (i * 4 + wave) * PER;    // of the tile
@@ -103,14 +125,9 @@ template <int KV, int D, bool V> struct Stage {
             if constexpr (N == 2) pg = wave >= 2 ? t.pg[i * 2 + 1] : t.pg[i * 2];
             if constexpr (N == 1) pg = wave >= 2 ? (wave == 3 ? t.pg[3] : t.pg[2]) : (wave == 1 ? t.pg[1] : t.pg[0]);
             pg = max(pg, 0);
-            const size_t r = ((size_t)hk << c.lg_page) + ((t.pos + r0) & ((1 << c.lg_page) - 1));
-            const char* at = base + (size_t)pg * page_bytes + r * RB;
-            if constexpr (KV == kKvBf16) {
-                load_lds16(at, voff, tile + r0 * D * 2);
-            } else {
-                w[i] = *reinterpret_cast<const u32x4*>(at + voff);
-                s[i] = (V ? c.vs : c.ks)[(((size_t)pg * c.Hk) << c.lg_page) + r + lane / (64 / PER)];
-            }
+            const size_t r = ((size_t)hk << c.lg_page) + ((t.pos + r0) & mask);
+            one(base + (size_t)pg * page_bytes + r * RB, i, tile, wave);
+            if constexpr (KV != kKvBf16) s[i] = scale[(((size_t)pg * c.Hk) << c.lg_page) + r + lane / (64 / PER)];
         }
     }
     // what was loaded is in LDS once the workgroup has passed a barrier
@@ -313,8 +330,8 @@ template <int KV, int D> __global__ __launch_bounds__(256, 2) void kda_attn_chun
     walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);
     Stage<KV, D, false> sk;
     Stage<KV, D, true> sv;
-    sk.init(wave, lane);
-    sv.init(wave, lane);
+    sk.init(wave, lane, p.c.lg_page < 6);
+    sv.init(wave, lane, p.c.lg_page < 6);
     x.at.init(lane);
     TilePages next;
     if (t.lo < t.hi) {
@@ -327,9 +344,9 @@ template <int KV, int D> __global__ __launch_bounds__(256, 2) void kda_attn_chun
     auto step = [&](int pos, char* here, char* there) {
         sk.store(here, wave, lane);
         sv.store(here + TB, wave, lane);
-        const bool partly = pos + kTile - 1 > t_first || !next.whole;       // for a row of the tile's
-        const bool masked = pos + kTile - 1 > lim_first || !next.whole;     // for a row of the wave's
-        const int valid = next.valid();
+        const int valid = next.valid;
+        const bool partly = pos + kTile - 1 > t_first || valid != 15;       // for a row of the tile's
+        const bool masked = pos + kTile - 1 > lim_first || valid != 15;     // for a row of the wave's
         __syncthreads();
         if (partly) {
             bool bad = false;
