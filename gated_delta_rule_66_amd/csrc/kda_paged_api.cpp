@@ -138,7 +138,7 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     const long long G = H / c->heads, M = packed ? (long long)T : (long long)N * T;
     const long long per = N > 0 ? M * G / N : 0;        // rows of a sequence, on average
     a.kind = dt == KDA_F32 ? kAttnF32 : per <= 16 ? kAttnStep16 : per <= 32 ? kAttnStep32 : kAttnChunk;
-    a.M = a.kind == kAttnStep16 ? 16 : a.kind == kAttnStep32 ? 32 : 128;
+    a.M = a.kind == kAttnStep16 ? 16 : a.kind == kAttnStep32 ? 32 : a.kind == kAttnF32 ? 128 : c->head_dim == 128 ? 256 : 128;
     const bool step = a.kind == kAttnStep16 || a.kind == kAttnStep32;
     a.tiles_per_seq = packed ? 0 : (int)((T * G + a.M - 1) / a.M);
     a.tiles = packed ? M * G / a.M + N : (long long)N * a.tiles_per_seq;

@@ -21,6 +21,8 @@ namespace kda {
 namespace {
 
 constexpr int kTile = 64;
+// waves of a workgroup
+template <int D> constexpr int kWaves = D == 128 ? 8 : 4;
 
 __device__ __forceinline__ f32x16 mma32(f32x16 acc, bf16x8 a, bf16x8 b) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
@@ -57,7 +59,7 @@ __device__ __forceinline__ unsigned lds_address(const char* p) {
 struct TilePages {
     int pg[kTile / 16];
     int pos, valid;         // valid: bit i where group i has a page
-    __device__ __forceinline__ void find(PageWalk& w, int lg_page, int at, int end) {
+    __device__ __forceinline__ void find(PageWalk<false>& w, int lg_page, int at, int end) {
         pos = at;
         if (lg_page >= 6) {
             pg[0] = w.page(at >> lg_page);
@@ -82,7 +84,8 @@ template <int KV, int D, bool V> struct Stage {
     static constexpr int E = KV == kKvBf16 ? 2 : 1;
     static constexpr int RB = D * E;                // bytes of a row
     static constexpr int PER = 1024 / RB;           // rows of a wave's load
-    static constexpr int N = kTile / (4 * PER);     // loads of a wave
+    static constexpr int W = kWaves<D>;
+    static constexpr int N = kTile / (W * PER);     // loads of a wave
     u32x4 w[N];
     unsigned s[N];
     unsigned voff[N];       // a lane's bytes in a load, from the tile's first row (small pages: from the load's)
@@ -93,12 +96,12 @@ template <int KV, int D, bool V> struct Stage {
             unsigned at = (unsigned)lane * 16;
             if constexpr (KV == kKvBf16)
                 at = (unsigned)((lane / (64 / PER)) * RB + 16 * (V ? v_piece<D>(r, piece) : k_piece<D>(r, piece)));
-            voff[i] = at + (small ? 0u : (unsigned)((i * 4 + wave) * PER * RB));
+            voff[i] = at + (small ? 0u : (unsigned)((i * W + wave) * PER * RB));
         }
     }
     __device__ __forceinline__ void one(const char* at, int i, char* tile, int wave) {
         if constexpr (KV == kKvBf16)
-            load_lds16(at, voff[i], lds_address(tile) + (unsigned)((i * 4 + wave) * PER * D * 2));
+            load_lds16(uniform(at), voff[i], lds_address(tile) + (unsigned)((i * W + wave) * PER * D * 2));
         else
             w[i] = *reinterpret_cast<const u32x4*>(at + voff[i]);
     }
@@ -114,17 +117,16 @@ template <int KV, int D, bool V> struct Stage {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 one(at, i, tile, wave);
-                if constexpr (KV != kKvBf16) s[i] = sc[(i * 4 + wave) * PER + lane / (64 / PER)];
+                if constexpr (KV != kKvBf16) s[i] = sc[(i * W + wave) * PER + lane / (64 / PER)];
             }
             return;
         }
+        // copies: a choice among the members themselves would put them into memory
+        const int p0 = t.pg[0], p1 = t.pg[1], p2 = t.pg[2], p3 = t.pg[3];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int r0 = (i * 4 + wave) * PER;    // of the tile
-            int pg = t.pg[i * 4 / N];
-            if constexpr (N == 2) pg = wave >= 2 ? t.pg[i * 2 + 1] : t.pg[i * 2];
-            if constexpr (N == 1) pg = wave >= 2 ? (wave == 3 ? t.pg[3] : t.pg[2]) : (wave == 1 ? t.pg[1] : t.pg[0]);
-            pg = max(pg, 0);
+            const int r0 = (i * W + wave) * PER;    // of the tile
+            const int pg = max(r0 >= 32 ? (r0 >= 48 ? p3 : p2) : (r0 >= 16 ? p1 : p0), 0);
             const size_t r = ((size_t)hk << c.lg_page) + ((t.pos + r0) & mask);
             one(base + (size_t)pg * page_bytes + r * RB, i, tile, wave);
             if constexpr (KV != kKvBf16) s[i] = scale[(((size_t)pg * c.Hk) << c.lg_page) + r + lane / (64 / PER)];
@@ -137,7 +139,7 @@ template <int KV, int D, bool V> struct Stage {
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int r = (i * 4 + wave) * PER + lane / (64 / PER), p = lane % (64 / PER);
+                const int r = (i * W + wave) * PER + lane / (64 / PER), p = lane % (64 / PER);
                 u32x4* to = reinterpret_cast<u32x4*>(tile + r * D * 2);
                 const Codes<KV> d(s[i]);
                 unsigned o[8];
@@ -185,22 +187,18 @@ template <int D> struct Offsets {
     }
 };
 
-// What a wave keeps of its 32 rows.
+// What a wave keeps of its 32 rows.  Scores are a tile ahead: while a tile's
+// weights are made and multiplied with V, the matrix units have the next tile's
+// scores to go on with.
 template <int D> struct Rows {
     static constexpr int KS = D / 16, DB = D / 32;
+    typedef f32x16 Scores[2];
     bf16x8 q[KS];
     f32x16 acc[DB];
-    float m, l;
+    float m, l, mc;
     Offsets<D> at;
 
-    // One tile.  masked: some rows see only a part of it.
-    // LDS reads go out ahead of the products that take them, and the weights of
-    // the next 16 positions are made beside the products of the present ones:
-    // left to itself, the compiler reads each operand just before its product.
-    __device__ __forceinline__ void tile(const char* tk, const char* tv, float c, bool masked, int pos, int lim, int valid,
-                                         int lane) {
-        const int h = lane >> 5;
-        f32x16 s[2];
+    __device__ __forceinline__ void scores(Scores& s, const char* tk) {
         bf16x8 kf[2][KS];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -213,29 +211,20 @@ template <int D> struct Rows {
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int k = 0; k < KS; ++k) s[b] = mma32(s[b], kf[b][k], q[k]);
-        bf16x8 vf[2][DB];
-#pragma unroll
-        for (int db = 0; db < DB; ++db) vf[0][db] = at.v_frag(tv, db, 0);
+    }
+    static __device__ __forceinline__ float largest(const Scores& s) {
         float top = s[0][0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
-        // four reads ahead, then a read beside each product
-        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-#pragma unroll
-        for (int i = 0; i < 2 * KS - 4; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            if (i >= KS) __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, DB / 2, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
-        }
+        return top;
+    }
+    // Scores of the tile at pos become weights' logarithms: masked where some
+    // row of the wave sees only a part of it, and the maximum moved.
+    __device__ __forceinline__ void settle(Scores& s, float top, float c, bool masked, int pos, int lim, int valid, int lane) {
         if (masked) {
+            const int h = lane >> 5;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -243,35 +232,35 @@ template <int D> struct Rows {
                     const int j = 32 * b + 8 * (e >> 2) + 4 * h + (e & 3);
                     if (pos + j > lim || !(valid >> (2 * b + (e >> 3)) & 1)) s[b][e] = -INFINITY;
                 }
-            top = s[0][0];
-#pragma unroll
-            for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
+            top = largest(s);
         }
         if (__any(top > m + kLazy / c)) {
             const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
             const float a = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * c);
             m = mn;
+            mc = m == -INFINITY ? 0.f : m * c;
             l *= a;
 #pragma unroll
             for (int db = 0; db < DB; ++db)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[db][e] *= a;
         }
-        const float mc = m == -INFINITY ? 0.f : m * c;
-        auto weights = [&](int k) {
-            float x[8];
+    }
+    __device__ __forceinline__ bf16x8 weights(const Scores& s, int k, float c) {
+        float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = fast_exp2(fmaf(s[k >> 1][8 * (k & 1) + i], c, -mc));
-                l += x[i];
-            }
-            return frag_from<bf16>(x);
-        };
-        bf16x8 pf[2];
-        pf[0] = weights(0);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < 8; ++i) {
+            x[i] = fast_exp2(fmaf(s[k >> 1][8 * (k & 1) + i], c, -mc));
+            l += x[i];
+        }
+        return frag_from<bf16>(x);
+    }
+    // One tile's weights and product with V, 16 positions at a time: the weights
+    // of the next beside the products of the present ones.  `made` of the four
+    // are made already; `last` is the vector work beside the third's products.
+    template <class F>
+    __device__ __forceinline__ void product(const Scores& s, bf16x8 (&pf)[4], int made, bf16x8 (&vf)[2][DB], const char* tv,
+                                            float c, F&& last) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (k < 3) {
@@ -279,8 +268,9 @@ template <int D> struct Rows {
                 for (int db = 0; db < DB; ++db) vf[(k + 1) & 1][db] = at.v_frag(tv, db, k + 1);
             }
 #pragma unroll
-            for (int db = 0; db < DB; ++db) acc[db] = mma32(acc[db], vf[k & 1][db], pf[k & 1]);
-            if (k < 3) pf[(k + 1) & 1] = weights(k + 1);
+            for (int db = 0; db < DB; ++db) acc[db] = mma32(acc[db], vf[k & 1][db], pf[k]);
+            if (k + made < 4) pf[k + made] = weights(s, k + made, c);
+            if (k == 2) last();
 #pragma unroll
             for (int db = 0; db < DB; ++db) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
@@ -292,12 +282,61 @@ template <int D> struct Rows {
             __builtin_amdgcn_sched_barrier(0);
         }
     }
+    // One tile, and the next one's scores; returns their largest.  The groups
+    // order what the compiler otherwise puts apart: LDS reads go out some
+    // products ahead, vector work stands between the products.
+    // D = 128: products take longer than the vector work (32 cycles each, 4096 a
+    // pair of tiles and SIMD), and the next scores' products stand beside the first weights.
+    // D = 64: the vector work is longer; the scores come last, in the registers
+    // of those before, and three waves a SIMD instead of two hide more of it
+    // (48 sequences over int8: 236 -> 217 us).
+    __device__ __forceinline__ float tile(const Scores& s, Scores& next, const char* tk, const char* tv, float c) {
+        bf16x8 vf[2][DB], pf[4];
+        float top;
+        if constexpr (D == 128) {
+            scores(next, tk);
+#pragma unroll
+            for (int db = 0; db < DB; ++db) vf[0][db] = at.v_frag(tv, db, 0);
+            pf[0] = weights(s, 0, c);
+            pf[1] = weights(s, 1, c);
+            __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+            for (int i = 0; i < 2 * KS - 4; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x402, 4, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, DB / 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x402, 4, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            product(s, pf, 2, vf, tv, c, [&]() { top = largest(next); });
+        } else {
+#pragma unroll
+            for (int db = 0; db < DB; ++db) vf[0][db] = at.v_frag(tv, db, 0);
+            pf[0] = weights(s, 0, c);
+            __builtin_amdgcn_sched_barrier(0);
+            product(s, pf, 1, vf, tv, c, []() {});
+            scores(next, tk);
+            top = largest(next);
+            __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+            for (int i = 0; i < 2 * KS - 4; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+        }
+        return top;
+    }
 };
 
-template <int KV, int D> __global__ __launch_bounds__(256, 2) void kda_attn_chunk_kernel(AttnParams p) {
-    constexpr int KS = D / 16, DB = D / 32, M = 128;
+template <int KV, int D> __global__ __launch_bounds__(64 * kWaves<D>, D == 128 ? 2 : 3) void kda_attn_chunk_kernel(AttnParams p) {
+    constexpr int KS = D / 16, DB = D / 32, W = kWaves<D>, M = 32 * W;
     constexpr int TB = kTile * D * 2;
-    __shared__ __align__(16) char lds[4 * TB];      // K, V, K, V
+    __shared__ __align__(16) char lds[4 * TB];      // two tiles of K, two of V
     __shared__ int lds_bad;                         // the first tile of V with a value taken out, or -1
     AttnTile t;
     if (!t.init(p, blockIdx.x)) return;
@@ -321,58 +360,70 @@ template <int KV, int D> __global__ __launch_bounds__(256, 2) void kda_attn_chun
 #pragma unroll
         for (int e = 0; e < 16; ++e) x.acc[db][e] = 0.f;
     x.m = -INFINITY;
-    x.l = 0.f;
-    // the loads of Q end here: a wait for them in the loop would be one for the tiles on their way
-    __builtin_amdgcn_s_waitcnt(0x0f70);
+    x.l = x.mc = 0.f;
     const float c = p.c_log2;
 
-    PageWalk walk;
-    walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);
+    PageWalk<false> walk;
+    walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);       // waits for its load, and Q's with it
     Stage<KV, D, false> sk;
     Stage<KV, D, true> sv;
     sk.init(wave, lane, p.c.lg_page < 6);
     sv.init(wave, lane, p.c.lg_page < 6);
     x.at.init(lane);
-    TilePages next;
+    if (threadIdx.x == 0) lds_bad = -1;
+    typename Rows<D>::Scores sa, sb;
+    TilePages next;         // of the tile behind the present one
+    int valid = 15;         // of the present one
     if (t.lo < t.hi) {
         next.find(walk, p.c.lg_page, t.lo, t.hi);
+        valid = next.valid;
         sk.load(p.c, next, t.hk, lds, wave, lane);
-        sv.load(p.c, next, t.hk, lds + TB, wave, lane);
-    }
-    if (threadIdx.x == 0) lds_bad = -1;
-    // a tile's K and V lie at `here`, the next one's go to `there`
-    auto step = [&](int pos, char* here, char* there) {
-        sk.store(here, wave, lane);
-        sv.store(here + TB, wave, lane);
-        const int valid = next.valid;
-        const bool partly = pos + kTile - 1 > t_first || valid != 15;       // for a row of the tile's
-        const bool masked = pos + kTile - 1 > lim_first || valid != 15;     // for a row of the wave's
+        sv.load(p.c, next, t.hk, lds + 2 * TB, wave, lane);
+        sk.store(lds, wave, lane);
         __syncthreads();
-        if (partly) {
+        if (t.lo + kTile < t.hi) {
+            next.find(walk, p.c.lg_page, t.lo + kTile, t.hi);
+            sk.load(p.c, next, t.hk, lds + TB, wave, lane);
+        }
+        if (t.lo <= lim_last) {
+            x.scores(sa, lds);
+            x.settle(sa, x.largest(sa), c, t.lo + kTile - 1 > lim_first || valid != 15, t.lo, lim, valid, lane);
+        }
+    }
+    // The tile at pos, whose scores are in s: its V lies at v, the next tile's K
+    // at k; the K behind that and the next V go to k_to and v_to.
+    auto step = [&](int pos, typename Rows<D>::Scores& s, typename Rows<D>::Scores& n, char* k, char* v, char* k_to, char* v_to) {
+        sk.store(k, wave, lane);
+        sv.store(v, wave, lane);
+        __syncthreads();
+        if (pos + kTile - 1 > t_first || valid != 15) {     // some row of the tile's sees only a part
             bool bad = false;
-            u32x4* v = reinterpret_cast<u32x4*>(here + TB) + threadIdx.x;
+            u32x4* w = reinterpret_cast<u32x4*>(v) + threadIdx.x;
 #pragma unroll
-            for (int i = 0; i < TB / 4096; ++i) {
-                u32x4 y = v[256 * i];
+            for (int i = 0; i < TB / (1024 * W); ++i) {
+                u32x4 y = w[64 * W * i];
                 if (not_finite(y[0]) || not_finite(y[1]) || not_finite(y[2]) || not_finite(y[3])) {
-                    v[256 * i] = u32x4{clean(y[0]), clean(y[1]), clean(y[2]), clean(y[3])};
+                    w[64 * W * i] = u32x4{clean(y[0]), clean(y[1]), clean(y[2]), clean(y[3])};
                     bad = true;
                 }
             }
             if (bad && lds_bad < 0) lds_bad = pos;
             __syncthreads();
         }
-        if (pos + kTile < t.hi) {
-            next.find(walk, p.c.lg_page, pos + kTile, t.hi);
-            sk.load(p.c, next, t.hk, there, wave, lane);
-            sv.load(p.c, next, t.hk, there + TB, wave, lane);
+        valid = next.valid;
+        if (pos + kTile < t.hi) sv.load(p.c, next, t.hk, v_to, wave, lane);
+        if (pos + 2 * kTile < t.hi) {
+            next.find(walk, p.c.lg_page, pos + 2 * kTile, t.hi);
+            sk.load(p.c, next, t.hk, k_to, wave, lane);
         }
-        if (pos <= lim_last)        // the wave's rows see some of it
-            x.tile(here, here + TB, c, masked, pos, lim, valid, lane);
+        if (pos > lim_last) return;         // the wave's rows see nothing of it
+        const float top = x.tile(s, n, k, v, c);
+        pos += kTile;
+        if (pos <= lim_last) x.settle(n, top, c, pos + kTile - 1 > lim_first || valid != 15, pos, lim, valid, lane);
     };
     for (int pos = t.lo; pos < t.hi; pos += 2 * kTile) {
-        step(pos, lds, lds + 2 * TB);
-        if (pos + kTile < t.hi) step(pos + kTile, lds + 2 * TB, lds);
+        step(pos, sa, D == 128 ? sb : sa, lds + TB, lds + 2 * TB, lds, lds + 3 * TB);
+        if (pos + kTile < t.hi) step(pos + kTile, D == 128 ? sb : sa, sa, lds, lds + 3 * TB, lds + TB, lds + 2 * TB);
     }
     __syncthreads();
     if (lds_bad >= 0) mend_rows<KV, D>(x.acc, p, t, lds_bad, lim, h);
@@ -423,7 +474,7 @@ template <int KV, int D> __global__ __launch_bounds__(256, 2) void kda_attn_chun
 }
 
 template <int KV, int D> hipError_t launch_chunk_kv(const AttnParams& p, int grid, hipStream_t st) {
-    kda_attn_chunk_kernel<KV, D><<<grid, 256, 0, st>>>(p);
+    kda_attn_chunk_kernel<KV, D><<<grid, 64 * kWaves<D>, 0, st>>>(p);
     return hipGetLastError();
 }
 

@@ -28,7 +28,7 @@ template <int KV, int D> struct StageF {
     unsigned w[N][W];
     unsigned s[N];
     __device__ __forceinline__ void load(const PagedCache& c, const char* base, const unsigned char* scale,
-                                         size_t page_bytes, PageWalk& walk, int hk, int pos, int end, int tid) {
+                                         size_t page_bytes, PageWalk<true>& walk, int hk, int pos, int end, int tid) {
         constexpr int PER = 256 / PIECES, WPER = 64 / PIECES;       // rows of a load, of a wave's part
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -91,7 +91,7 @@ template <int KV, int D> __global__ __launch_bounds__(256, 1) void kda_attn_f32_
     float m = -INFINITY, l = 0.f;
     const float c = p.c_log2, lazy = kLazy / c;
 
-    PageWalk walk;
+    PageWalk<true> walk;
     walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);
     StageF<KV, D> sk, sv;
     if (t.lo < t.hi) {

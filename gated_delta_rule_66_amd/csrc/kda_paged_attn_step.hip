@@ -61,7 +61,7 @@ template <int KV, int D> struct Block {
         koff = (unsigned)((lane & 15) * RB + (lane >> 4) * 16);
         voff = (unsigned)((lane >> 4) * 4 * RB + (lane & 15) * DV * E);
     }
-    __device__ __forceinline__ void find(const PagedCache& c, PageWalk& w, int pos, int end) {
+    __device__ __forceinline__ void find(const PagedCache& c, PageWalk<true>& w, int pos, int end) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) pg[h] = pos + 16 * h < end ? w.page((pos + 16 * h) >> c.lg_page) : -1;
     }
@@ -167,7 +167,7 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
     int bad_from = -1;      // the wave's first block of V with a value taken out
     int pos = t.lo + 32 * wave;
     if (pos < t.hi) {
-        PageWalk walk;
+        PageWalk<true> walk;
         walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);
         Block<KV, D> b;
         b.init(lane);

@@ -11,6 +11,11 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const char* uniform(const char* p) {
+    const unsigned long long v = reinterpret_cast<uintptr_t>(p);
+    const unsigned lo = (unsigned)uniform((int)(unsigned)v), hi = (unsigned)uniform((int)(unsigned)(v >> 32));
+    return reinterpret_cast<const char*>((unsigned long long)hi << 32 | lo);
+}
 
 // ---- 8-bit codes --------------------------------------------------------------------
 // A row's scale is 2^(byte - 127), so that a code times its scale is exact in
@@ -84,8 +89,10 @@ __device__ __forceinline__ int seq_positions(const PagedCache& c, int i) {
 }
 
 // A wave's page numbers along a sequence: lane l holds entry at + l of the
-// table's row, and the 64 entries behind are in flight.
-struct PageWalk {
+// table's row.  AHEAD: the 64 entries behind are in flight; without, they are
+// waited for where they are needed, so that no load is open in the loop (the
+// compiler would wait for it, and for all that came after it, in every pass).
+template <bool AHEAD> struct PageWalk {
     const int* row;
     int entries;            // entries that hold positions
     int pages;
@@ -99,14 +106,22 @@ struct PageWalk {
         pages = c.pages;
         at = first;
         here = entry(at + (int)(threadIdx.x & 63));
-        ahead = entry(at + 64 + (int)(threadIdx.x & 63));
+        if constexpr (AHEAD)
+            ahead = entry(at + 64 + (int)(threadIdx.x & 63));
+        else
+            __builtin_amdgcn_s_waitcnt(0x0f70);         // vmcnt(0)
     }
     // page of entry i, i not below those asked before by more than the lanes hold; -1: not there
     __device__ __forceinline__ int page(int i) {
         while (i >= at + 64) {
             at += 64;
-            here = ahead;
-            ahead = entry(at + 64 + (int)(threadIdx.x & 63));
+            if constexpr (AHEAD) {
+                here = ahead;
+                ahead = entry(at + 64 + (int)(threadIdx.x & 63));
+            } else {
+                here = entry(at + (int)(threadIdx.x & 63));
+                __builtin_amdgcn_s_waitcnt(0x0f70);
+            }
         }
         const int pg = __builtin_amdgcn_readlane(here, i - at);
         return (unsigned)pg < (unsigned)pages ? pg : -1;
