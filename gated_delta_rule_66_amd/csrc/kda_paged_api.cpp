@@ -138,13 +138,21 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     const long long G = H / c->heads, M = packed ? (long long)T : (long long)N * T;
     const long long per = N > 0 ? M * G / N : 0;        // rows of a sequence, on average
     a.kind = dt == KDA_F32 ? kAttnF32 : per <= 16 ? kAttnStep16 : per <= 32 ? kAttnStep32 : kAttnChunk;
-    a.M = a.kind == kAttnStep16 ? 16 : a.kind == kAttnStep32 ? 32 : a.kind == kAttnF32 ? 128 : c->head_dim == 128 ? 256 : 128;
+    a.M = a.kind == kAttnStep16 ? 16 : a.kind != kAttnChunk ? 32 : c->head_dim == 128 ? 256 : 128;
     const bool step = a.kind == kAttnStep16 || a.kind == kAttnStep32;
     a.tiles_per_seq = packed ? 0 : (int)((T * G + a.M - 1) / a.M);
     a.tiles = packed ? M * G / a.M + N : (long long)N * a.tiles_per_seq;
     const long long units = a.tiles * c->heads, ctx = (long long)c->blocks * c->page_size;
-    const long long want = step ? 1536 : 1024, least = 512;
+    // Ranges: enough of them to fill the card about twice, a single sequence's,
+    // which are alike, once (a 1M step with 64, 192, 384 ranges a head 376, 387,
+    // 398 us; 64 sequences x 8 heads with 3, 6, 12: 228, 230, 234 us).  Lengths
+    // of a batch differ, so single tokens of many sequences are split in three
+    // all the same (256 x 8 heads: 771 -> 743 us; chunks lose by it: 4 x 2K over
+    // 32K 3.9 -> 4.1 ms).  At least 512 positions: below that the join's launch
+    // costs more than the ranges save.
+    const long long want = !step ? 1024 : N > 1 ? 1536 : 512, least = 512;
     long long n = units > 0 ? want / units : 1;
+    if (step && N > 1 && n < 3) n = 3;
     if (n < 1 || M * H >= 1LL << 23) n = 1;
     long long len = n > 1 ? (ctx + n - 1) / n : ctx;
     len = (len + 127) / 128 * 128;

@@ -3,139 +3,156 @@
 //
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i.k_j - max_i),  j <= position of i
 //
-// Bound by its products: 32x32x2 fp32, a sixteenth of the bf16 rate.  The
-// layout is that of the bf16 kernel (the row in the lane, S^T = K Q^T, O^T =
-// V^T P^T): a workgroup of four waves takes 128 rows and walks tiles of 32
-// positions, which the threads hold in registers while the tile before is
-// multiplied.
+// Bound by its products: 32x32x2 fp32, a sixteenth of the bf16 rate, 64 cycles
+// each.  That leaves so much time for loads that nothing of the cache is shared
+// through LDS, and a tile can be 32 rows (tokens times the heads that share a
+// cache head): a workgroup's four waves take blocks of 32 positions in turn and
+// keep maximum, sum and output of their own, joined at the end.  (128 rows, 32 a
+// wave, and blocks shared in LDS left ragged batches with too few workgroups: 16
+// sequences x 5 heads of 64, 184 us.)
+//   * S^T = K Q^T, the row in the lane: lane half h holds neighbouring channels
+//     of one position, one 16-byte load; their order is free if Q has the same.
+//   * O^T = V^T P^T: a result register of S^T, position 8 (e / 4) + 4 h + e % 4,
+//     is the operand P^T as it stands.  A lane loads D / 32 neighbouring channels
+//     of a position (32 lanes read a whole row); product j makes channels
+//     (D / 32) rho + j, rho the accumulator's row.
 #include "kda_paged_attn.h"
+
+#include <type_traits>
 
 namespace kda {
 
 namespace {
 
-constexpr int kTileF = 32;
-
 __device__ __forceinline__ f32x16 mma2(f32x16 acc, float a, float b) {
     return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, acc, 0, 0, 0);
 }
 
-template <int KV, int D> struct StageF {
-    static constexpr int E = KV == kKvF32 ? 4 : 1;
-    static constexpr int W = KV == kKvF32 ? 4 : 1;  // dwords of a thread's four values
-    static constexpr int PIECES = D / 4;            // threads of a row
-    static constexpr int N = kTileF * PIECES / 256; // pieces of a thread
-    unsigned w[N][W];
-    unsigned s[N];
-    __device__ __forceinline__ void load(const PagedCache& c, const char* base, const unsigned char* scale,
-                                         size_t page_bytes, PageWalk<true>& walk, int hk, int pos, int end, int tid) {
-        constexpr int PER = 256 / PIECES, WPER = 64 / PIECES;       // rows of a load, of a wave's part
+// One block of 32 positions as it is loaded, in two halves of one page each.
+// Places without a position get what the page, or page 0, holds there.
+template <int KV, int D> struct BlockF {
+    static constexpr int E = KV == kKvF32 ? 4 : 1, RB = D * E;
+    static constexpr int CH = 16 / E;               // channels of K a load
+    static constexpr int KL = D / (2 * CH);         // loads of K a lane
+    static constexpr int DV = D / 32;               // channels of V a lane
+    static constexpr bool CODES = KV >= kKvE4m3;
+    u32x4 k[KL];
+    typedef typename std::conditional<CODES, typename std::conditional<DV == 4, unsigned, unsigned short>::type,
+                                      typename std::conditional<DV == 4, f32x4, float2>::type>::type Vec;
+    Vec v[16];
+    unsigned ks, vs[4];     // scale bytes: K's row of the lane, V's sixteen rows
+    int pg[2];
+
+    __device__ __forceinline__ void find(const PagedCache& c, PageWalk<true>& w, int pos, int end) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = uniform(pos + i * PER + (tid >> 6) * WPER), page = at < end ? walk.page(at >> c.lg_page) : -1;
-            const size_t r = ((size_t)hk << c.lg_page) + (at & ((1 << c.lg_page) - 1));
-            const auto rs = make_rsrc_n(base + (size_t)max(page, 0) * page_bytes + r * D * E,
-                                        page < 0 ? 0u : (unsigned)(min(end - at, WPER) * D * E));
-            if constexpr (KV == kKvF32) {
-                const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, (tid & 63) * 16, 0, 0);
+        for (int h = 0; h < 2; ++h) pg[h] = pos + 16 * h < end ? w.page((pos + 16 * h) >> c.lg_page) : -1;
+    }
+    __device__ __forceinline__ int valid() const { return (pg[0] >= 0) | (pg[1] >= 0) << 1; }
+    __device__ __forceinline__ static size_t row(const PagedCache& c, int hk, int at) {
+        return ((size_t)hk << c.lg_page) + (at & ((1 << c.lg_page) - 1));
+    }
+    __device__ __forceinline__ void load_k(const PagedCache& c, int hk, int pos, int lane) {
+        // the lane's half of the block
+        const int half = lane >> 4 & 1;
+        const size_t page = (size_t)max(half ? pg[1] : pg[0], 0), r = row(c, hk, pos + 16 * half) + (lane & 15);
+        const char* at = c.k + page * c.k_page + r * RB + (lane >> 5) * 16;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[i][k] = v[k];
-            } else {
-                w[i][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, (tid & 63) * 4, 0, 0);
-                const auto ss = make_rsrc_n(scale + (((size_t)max(page, 0) * c.Hk) << c.lg_page) + r, page < 0 ? 0u : (unsigned)WPER);
-                s[i] = __builtin_amdgcn_raw_buffer_load_b8(ss, (tid & 63) / PIECES, 0, 0);
+        for (int i = 0; i < KL; ++i) k[i] = *reinterpret_cast<const u32x4*>(at + 32 * i);
+        if constexpr (CODES) ks = (c.ks + ((page * c.Hk) << c.lg_page))[r];
+    }
+    __device__ __forceinline__ void load_v(const PagedCache& c, int hk, int pos, int lane) {
+        const unsigned off = (unsigned)((lane >> 5) * 4 * RB + (lane & 31) * DV * E);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const size_t page = (size_t)max(pg[h], 0), r = row(c, hk, pos + 16 * h);
+            const char* at = c.v + page * c.v_page + r * RB;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[8 * h + e] = *reinterpret_cast<const Vec*>(at + (8 * (e >> 2) + (e & 3)) * RB + off);
+            if constexpr (CODES) {
+                const unsigned char* s = c.vs + ((page * c.Hk) << c.lg_page) + r + 4 * (lane >> 5);
+                vs[2 * h] = *reinterpret_cast<const unsigned*>(s);
+                vs[2 * h + 1] = *reinterpret_cast<const unsigned*>(s + 8);
             }
         }
     }
-    template <int LD> __device__ __forceinline__ void store(float* tile, int tid) const {
+    // channels 2 CH i + CH h + 4 w .. of the lane's position
+    __device__ __forceinline__ void kvals(int i, int w, float (&o)[4]) const {
+        if constexpr (CODES)
+            Codes<KV>(ks).f32(k[i][w], o);
+        else
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int row = i * (256 / PIECES) + tid / PIECES, d = 4 * (tid % PIECES);
+            for (int j = 0; j < 4; ++j) o[j] = __uint_as_float(k[i][j]);
+    }
+    // channels DV (l % 32) .. of operand e's position
+    __device__ __forceinline__ void vvals(int e, float (&o)[DV]) const {
+        if constexpr (CODES) {
             float f[4];
-            if constexpr (KV == kKvF32) {
+            Codes<KV>(vs[e >> 2] >> (8 * (e & 3)) & 255u).f32((unsigned)v[e], f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(w[i][k]);
-            } else {
-                Codes<KV>(s[i]).f32(w[i][0], f);
-            }
-            *reinterpret_cast<f32x4*>(tile + row * LD + d) = f32x4{f[0], f[1], f[2], f[3]};
+            for (int j = 0; j < DV; ++j) o[j] = f[j];
+        } else {
+            __builtin_memcpy(o, &v[e], sizeof(o));
         }
     }
 };
 
-template <int KV, int D> __global__ __launch_bounds__(256, 1) void kda_attn_f32_kernel(AttnParams p) {
-    constexpr int KS = D / 8, DB = D / 32, M = 128, LD = D + 4;
-    __shared__ __align__(16) float lds_k[kTileF * LD];
-    __shared__ __align__(16) float lds_v[kTileF * LD];
-    __shared__ int lds_bad;                         // the first tile of V with a value taken out, or -1
+template <int KV, int D> __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void kda_attn_f32_kernel(AttnParams p) {
+    typedef BlockF<KV, D> Block;
+    constexpr int R = 32, DV = Block::DV, CH = Block::CH, KL = Block::KL, LD = D + 4;
+    __shared__ __align__(16) float lds_o[2][R][LD];
+    __shared__ float lds_ml[2][R][2];
     AttnTile t;
     if (!t.init(p, blockIdx.x)) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
-    const int r = t.r0 + 32 * wave + (lane & 31), tok = p.by_g.div(r), head = t.hk * p.G + r - tok * p.G;
-    const int lim = t.limit(r, p);
-    const int w0 = t.r0 + 32 * wave, lim_first = t.limit(w0, p), t_first = t.limit(t.r0, p);
-    const int lim_last = w0 < t.rows ? t.limit(min(w0 + 31, t.rows - 1), p) : -1;
-    // operand 4 s + i: channels 8 s + 4 h + i
-    f32x4 q[KS];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5, c32 = lane & 31;
+    const int r = t.r0 + c32, tok = p.by_g.div(r), head = t.hk * p.G + r - tok * p.G;
+    const int lim = t.limit(r, p), lim_first = t.limit(t.r0, p);
+    // Q in the order of Block::kvals, zeros behind the sequence's rows
+    f32x4 q[D / 8];
     const char* row = p.q + (size_t)(t.first + tok) * p.q_stride + (size_t)head * D * 4;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-        q[s] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (r < t.rows) q[s] = *reinterpret_cast<const f32x4*>(row + (8 * s + 4 * h) * 4);
-    }
-    f32x16 acc[DB];
+    for (int i = 0; i < KL; ++i)
 #pragma unroll
-    for (int db = 0; db < DB; ++db)
+        for (int w = 0; w < CH / 4; ++w) {
+            q[i * (CH / 4) + w] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (r < t.rows) q[i * (CH / 4) + w] = *reinterpret_cast<const f32x4*>(row + (2 * CH * i + CH * h + 4 * w) * 4);
+        }
+    f32x16 acc[DV];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[db][e] = 0.f;
+    for (int j = 0; j < DV; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[j][e] = 0.f;
     float m = -INFINITY, l = 0.f;
     const float c = p.c_log2, lazy = kLazy / c;
 
-    PageWalk<true> walk;
-    walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);
-    StageF<KV, D> sk, sv;
-    if (t.lo < t.hi) {
-        sk.load(p.c, p.c.k, p.c.ks, p.c.k_page, walk, t.hk, t.lo, t.hi, tid);
-        sv.load(p.c, p.c.v, p.c.vs, p.c.v_page, walk, t.hk, t.lo, t.hi, tid);
-    }
-    if (tid == 0) lds_bad = -1;
-    for (int pos = t.lo; pos < t.hi; pos += kTileF) {
-        int valid = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = pos + 16 * i;
-            valid |= (at < t.hi && walk.page(at >> p.c.lg_page) >= 0) << i;
-        }
-        sk.template store<LD>(lds_k, tid);
-        sv.template store<LD>(lds_v, tid);
-        __syncthreads();
-        if (pos + kTileF - 1 > t_first || valid != 3) {      // for a row of the tile's
-            bool bad = false;
-            for (int i = tid; i < kTileF * D; i += 256) {
-                float* y = lds_v + i / D * LD + i % D;
-                if (!finite_f(*y)) {
-                    *y = 0.f;
-                    bad = true;
-                }
-            }
-            if (bad && lds_bad < 0) lds_bad = pos;
-            __syncthreads();
-        }
-        if (pos + kTileF < t.hi) {
-            sk.load(p.c, p.c.k, p.c.ks, p.c.k_page, walk, t.hk, pos + kTileF, t.hi, tid);
-            sv.load(p.c, p.c.v, p.c.vs, p.c.v_page, walk, t.hk, pos + kTileF, t.hi, tid);
-        }
-        if (pos <= lim_last) {
+    int bad_from = -1;      // the wave's first block of V with a value taken out
+    int pos = t.lo + 32 * wave;
+    if (pos < t.hi) {
+        PageWalk<true> walk;
+        walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);
+        Block b;
+        b.find(p.c, walk, pos, t.hi);
+        b.load_k(p.c, t.hk, pos, lane);
+        b.load_v(p.c, t.hk, pos, lane);
+        for (; pos < t.hi; pos += 128) {
             f32x16 s;
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const f32x4 kf = *reinterpret_cast<const f32x4*>(lds_k + (lane & 31) * LD + 8 * k + 4 * h);
+            for (int i = 0; i < KL; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s = mma2(s, kf[i], q[k][i]);
+                for (int w = 0; w < CH / 4; ++w) {
+                    float f[4];
+                    b.kvals(i, w, f);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s = mma2(s, f[j], q[i * (CH / 4) + w][j]);
+                }
+            const int valid = b.valid(), next = pos + 128;
+            const bool masked = pos + 31 > lim_first || valid != 3;
+            if (next < t.hi) {
+                b.find(p.c, walk, next, t.hi);
+                b.load_k(p.c, t.hk, next, lane);
             }
-            const bool masked = pos + kTileF - 1 > lim_first || valid != 3;
             if (masked) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
@@ -150,9 +167,9 @@ template <int KV, int D> __global__ __launch_bounds__(256, 1) void kda_attn_f32_
                 m = mn;
                 l *= a;
 #pragma unroll
-                for (int db = 0; db < DB; ++db)
+                for (int j = 0; j < DV; ++j)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[db][e] *= a;
+                    for (int e = 0; e < 16; ++e) acc[j][e] *= a;
             }
             const float mc = m == -INFINITY ? 0.f : m * c;
 #pragma unroll
@@ -160,50 +177,95 @@ template <int KV, int D> __global__ __launch_bounds__(256, 1) void kda_attn_f32_
                 s[e] = fast_exp2(fmaf(s[e], c, -mc));
                 l += s[e];
             }
-            // operand e: positions 8 (e / 4) + 4 h + e % 4
-            const float* v = lds_v + 4 * h * LD + (lane & 31);
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                float f[DV];
+                b.vvals(e, f);
+                if (masked) {       // what is not finite must not meet a weight of zero
+#pragma unroll
+                    for (int j = 0; j < DV; ++j) {
+                        bad |= !finite_f(f[j]);
+                        f[j] = finite_f(f[j]) ? f[j] : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < DV; ++j) acc[j] = mma2(acc[j], f[j], s[e]);
+            }
+            if (masked && bad_from < 0 && __any(bad)) bad_from = pos;
+            if (next < t.hi) b.load_v(p.c, t.hk, next, lane);
+        }
+    }
+    if (bad_from >= 0) {
+#pragma unroll 1
+        for (int i = bad_from; i < t.hi; i += i % 32 == 31 ? 97 : 1)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                // DV channels from a multiple of DV on, within one load of four
+                const int ch = DV * (8 * (e >> 2) + 4 * h + (e & 3));
+                float f[4];
+                load_v4<KV, D>(p.c, t.seq, t.hk, i, ch & ~3, f);
+#pragma unroll
+                for (int j = 0; j < DV; ++j) {
+                    const float x = DV == 4 ? f[j] : (e & 1) ? f[2 + j] : f[j];
+                    if (i <= lim && !finite_f(x)) acc[j][e] += x;
+                }
+            }
+    }
+    l += __shfl_xor(l, 32);
+    // waves 2 and 3 join 0 and 1, then 1 joins 0
+#pragma unroll
+    for (int half = 2; half > 0; half >>= 1) {
+        if (wave >= half && wave < 2 * half) {
+            if (h == 0) {
+                lds_ml[wave - half][c32][0] = m;
+                lds_ml[wave - half][c32][1] = l;
+            }
 #pragma unroll
             for (int e = 0; e < 16; ++e)
 #pragma unroll
-                for (int db = 0; db < DB; ++db) acc[db] = mma2(acc[db], v[(8 * (e >> 2) + (e & 3)) * LD + 32 * db], s[e]);
+                for (int j = 0; j < DV; ++j)
+                    lds_o[wave - half][c32][DV * (8 * (e >> 2) + 4 * h + (e & 3)) + j] = acc[j][e];
+        }
+        __syncthreads();
+        if (wave < half) {
+            const float mo = lds_ml[wave][c32][0], lo = lds_ml[wave][c32][1], mn = fmaxf(m, mo);
+            const float a = m == mn ? 1.f : fast_exp2((m - mn) * c);
+            const float b = mo == mn ? 1.f : fast_exp2((mo - mn) * c);
+            m = mn;
+            l = l * a + lo * b;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+#pragma unroll
+                for (int j = 0; j < DV; ++j)
+                    acc[j][e] = acc[j][e] * a + lds_o[wave][c32][DV * (8 * (e >> 2) + 4 * h + (e & 3)) + j] * b;
         }
         __syncthreads();
     }
-    if (lds_bad >= 0) mend_rows<KV, D>(acc, p, t, lds_bad, lim, h);
-    l += __shfl_xor(l, 32);
-    if (r >= t.rows) return;
-    if (t.splits > 1) {
-        const size_t x = t.unit * M + 32 * wave + (lane & 31);
-        float* po = p.part + x * D;
-        if (h == 0) {
-            p.ml[x * 2] = m;
-            p.ml[x * 2 + 1] = l;
-        }
-#pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<f32x4*>(po + 32 * db + 8 * j + 4 * h) =
-                    f32x4{acc[db][4 * j], acc[db][4 * j + 1], acc[db][4 * j + 2], acc[db][4 * j + 3]};
-        return;
+    if (wave || r >= t.rows) return;
+    const size_t col = (size_t)head * D;
+    const bool parts = t.splits > 1;
+    float* o = parts ? p.part + (t.unit * R + c32) * D : reinterpret_cast<float*>(p.o) + (size_t)(t.first + tok) * p.H * D + col;
+    const float* z = reinterpret_cast<const float*>(p.z + (size_t)(t.first + tok) * p.z_stride) + col;
+    if (parts && h == 0) {
+        p.ml[(t.unit * R + c32) * 2] = m;
+        p.ml[(t.unit * R + c32) * 2 + 1] = l;
     }
-    float* o = reinterpret_cast<float*>(p.o) + ((size_t)(t.first + tok) * p.H + head) * D;
-    const float* z = reinterpret_cast<const float*>(p.z + (size_t)(t.first + tok) * p.z_stride) + (size_t)head * D;
 #pragma unroll
-    for (int db = 0; db < DB; ++db)
+    for (int e = 0; e < 16; e += 4 / DV) {
+        const int d = DV * (8 * (e >> 2) + 4 * h + (e & 3));
+        f32x4 y;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int d = 32 * db + 8 * j + 4 * h;
-            f32x4 x;
+        for (int i = 0; i < 4; ++i) y[i] = acc[i % DV][e + i / DV];
+        if (!parts) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = l == 0.f ? 0.f : acc[db][4 * j + i] / l;
-            if (p.z) {
-                const f32x4 zz = *reinterpret_cast<const f32x4*>(z + d);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = gate_of<float>(x[i], zz[i]);
+            for (int i = 0; i < 4; ++i) {
+                y[i] = l == 0.f ? 0.f : y[i] / l;
+                if (p.z) y[i] = gate_of<float>(y[i], z[d + i]);
             }
-            *reinterpret_cast<f32x4*>(o + d) = x;
         }
+        *reinterpret_cast<f32x4*>(o + d) = y;
+    }
 }
 
 template <int D> hipError_t launch_f32_kv(int kv, const AttnParams& p, int grid, hipStream_t st) {
