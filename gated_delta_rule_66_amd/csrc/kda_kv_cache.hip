@@ -128,46 +128,62 @@ template <typename T, int KV, int D> __global__ __launch_bounds__(kIoTokens * D 
     const int h0 = blockIdx.y * p.heads_per_block, h1 = min(h0 + p.heads_per_block, p.c.Hk);
     const char* k = p.k + (size_t)t * p.k_stride + lane * 8 * sizeof(T);
     const char* v = p.v + (size_t)t * p.v_stride + lane * 8 * sizeof(T);
+    // a head's rows are on their way while those before are written
+    Pack8<T> nk, nv;
+    nk.load(reinterpret_cast<const T*>(k) + (size_t)h0 * D);
+    nv.load(reinterpret_cast<const T*>(v) + (size_t)h0 * D);
     for (int h = h0; h < h1; ++h) {
-        Pack8<T> xk, xv;
-        xk.load(reinterpret_cast<const T*>(k) + (size_t)h * D);
-        xv.load(reinterpret_cast<const T*>(v) + (size_t)h * D);
+        const Pack8<T> xk = nk, xv = nv;
+        if (h + 1 < h1) {
+            nk.load(reinterpret_cast<const T*>(k) + (size_t)(h + 1) * D);
+            nv.load(reinterpret_cast<const T*>(v) + (size_t)(h + 1) * D);
+        }
         write_row<T, KV, D>(xk, p.c.k, p.c.ks, p.c.k_page, p.c.Hk, p.c.lg_page, page, h, row, lane);
         write_row<T, KV, D>(xv, p.c.v, p.c.vs, p.c.v_page, p.c.Hk, p.c.lg_page, page, h, row, lane);
     }
 }
 
-template <typename T, int KV, int D>
-__device__ __forceinline__ void read_row(T* to, const char* cache, const unsigned char* scale, size_t page_bytes,
-                                         int Hk, int lg_page, int page, int h, int row, int lane) {
-    constexpr int E = KV == kKvF32 ? 4 : KV == kKvBf16 ? 2 : 1;
-    const size_t r = ((size_t)h << lg_page) + row;
-    const char* from = cache + (size_t)page * page_bytes + (r * D + lane * 8) * E;
-    if constexpr (KV <= kKvBf16) {
-        Pack8<T> x;
-        x.load(reinterpret_cast<const T*>(from));
-        if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<uint4*>(to) = x.d;
-        else {
-            *reinterpret_cast<float4*>(to) = x.a;
-            *reinterpret_cast<float4*>(to + 4) = x.b;
-        }
-    } else {
-        const u32x2 c = *reinterpret_cast<const u32x2*>(from);
-        const Codes<KV> d(scale[(((size_t)page * Hk) << lg_page) + r]);
-        if constexpr (sizeof(T) == 2) {
-            unsigned o[4];
-            d.bf(c[0], o);
-            d.bf(c[1], o + 2);
-            *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+// A lane's part of a row of the cache, as it is loaded and as it is read.
+template <typename T, int KV, int D> struct Row {
+    static constexpr int E = KV == kKvF32 ? 4 : KV == kKvBf16 ? 2 : 1;
+    Pack8<T> x;             // codes: not used
+    u32x2 c;
+    unsigned byte;
+    __device__ __forceinline__ void load(const char* cache, const unsigned char* scale, size_t page_bytes, int Hk,
+                                         int lg_page, int page, int h, int row, int lane) {
+        const size_t r = ((size_t)h << lg_page) + row;
+        const char* from = cache + (size_t)page * page_bytes + (r * D + lane * 8) * E;
+        if constexpr (KV <= kKvBf16) {
+            x.load(reinterpret_cast<const T*>(from));
         } else {
-            float o[8];
-            d.f32(c[0], o);
-            d.f32(c[1], o + 4);
-            st8(to, o);
+            c = *reinterpret_cast<const u32x2*>(from);
+            byte = scale[(((size_t)page * Hk) << lg_page) + r];
         }
     }
-}
+    __device__ __forceinline__ void store(T* to) const {
+        if constexpr (KV <= kKvBf16) {
+            if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<uint4*>(to) = x.d;
+            } else {
+                *reinterpret_cast<float4*>(to) = x.a;
+                *reinterpret_cast<float4*>(to + 4) = x.b;
+            }
+        } else {
+            const Codes<KV> d(byte);
+            if constexpr (sizeof(T) == 2) {
+                unsigned o[4];
+                d.bf(c[0], o);
+                d.bf(c[1], o + 2);
+                *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                float o[8];
+                d.f32(c[0], o);
+                d.f32(c[1], o + 4);
+                st8(to, o);
+            }
+        }
+    }
+};
 
 template <typename T, int KV, int D> __global__ __launch_bounds__(kIoTokens * D / 8) void kda_cache_read_kernel(CacheIoParams p) {
     constexpr int TEAM = D / 8;
@@ -177,15 +193,25 @@ template <typename T, int KV, int D> __global__ __launch_bounds__(kIoTokens * D 
     const int h0 = blockIdx.y * p.heads_per_block, h1 = min(h0 + p.heads_per_block, p.c.Hk);
     T* k = reinterpret_cast<T*>(p.k + (size_t)t * p.k_stride) + lane * 8;
     T* v = reinterpret_cast<T*>(p.v + (size_t)t * p.v_stride) + lane * 8;
-    for (int h = h0; h < h1; ++h) {
-        if (page < 0) {
-            const float zero[8] = {};
+    if (page < 0) {
+        const float zero[8] = {};
+        for (int h = h0; h < h1; ++h) {
             st8(k + (size_t)h * D, zero);
             st8(v + (size_t)h * D, zero);
-            continue;
         }
-        read_row<T, KV, D>(k + (size_t)h * D, p.c.k, p.c.ks, p.c.k_page, p.c.Hk, p.c.lg_page, page, h, row, lane);
-        read_row<T, KV, D>(v + (size_t)h * D, p.c.v, p.c.vs, p.c.v_page, p.c.Hk, p.c.lg_page, page, h, row, lane);
+        return;
+    }
+    Row<T, KV, D> nk, nv;
+    nk.load(p.c.k, p.c.ks, p.c.k_page, p.c.Hk, p.c.lg_page, page, h0, row, lane);
+    nv.load(p.c.v, p.c.vs, p.c.v_page, p.c.Hk, p.c.lg_page, page, h0, row, lane);
+    for (int h = h0; h < h1; ++h) {
+        const Row<T, KV, D> xk = nk, xv = nv;
+        if (h + 1 < h1) {
+            nk.load(p.c.k, p.c.ks, p.c.k_page, p.c.Hk, p.c.lg_page, page, h + 1, row, lane);
+            nv.load(p.c.v, p.c.vs, p.c.v_page, p.c.Hk, p.c.lg_page, page, h + 1, row, lane);
+        }
+        xk.store(k + (size_t)h * D);
+        xv.store(v + (size_t)h * D);
     }
 }
 

@@ -78,6 +78,7 @@ struct AttnParams {
     int M, lg_m;            // rows a tile
     int tiles, tiles_per_seq;
     int splits, split_len;
+    int by_length;          // tiles in order of their sequences' positions (N at most 64)
     FastDiv by_g, by_hk, by_splits, by_tiles, by_len, by_h, by_t;   // G, Hk, splits, tiles_per_seq, split_len, H, T
     float* part;            // [tiles][Hk][splits][M][D]
     float* ml;              // [tiles][Hk][splits][M][2]: running maximum (of q.k) and sum

@@ -22,22 +22,25 @@ struct AttnTile {
         const int u = p.by_hk.div(block), v = p.by_splits.div(u);
         hk = block - u * p.c.Hk;
         split = u - v * p.splits;
-        const int tile = p.tiles - 1 - v;       // a sequence's long tiles first
         int at;
-        if (p.sv.cu) {
-            int a = 0, b = p.sv.N;      // slot(a) <= tile < slot(b)
-            while (b - a > 1) {
-                const int mid = (a + b) >> 1;
-                if (slot(p, mid) <= tile)
-                    a = mid;
-                else
-                    b = mid;
-            }
-            seq = uniform(a);
-            at = tile - slot(p, seq);
+        if (p.by_length) {
+            if (!longest_first(p, v, &at)) return false;
         } else {
-            seq = p.by_tiles.div(tile);
-            at = tile - seq * p.tiles_per_seq;
+            const int tile = p.tiles - 1 - v;       // a sequence's long tiles first
+            if (p.sv.cu) {
+                int a = 0, b = p.sv.N;      // slot(a) <= tile < slot(b)
+                while (b - a > 1) {
+                    const int mid = (a + b) >> 1;
+                    if (slot(p, mid) <= tile)
+                        a = mid;
+                    else
+                        b = mid;
+                }
+                seq = uniform(a);
+            } else {
+                seq = p.by_tiles.div(tile);
+            }
+            at = tile - slot(p, seq);
         }
         seq_span(p.sv, seq, &first, &n);
         first = uniform(first);
@@ -51,10 +54,34 @@ struct AttnTile {
         if (split >= splits) return false;
         lo = split * p.split_len;
         hi = min(end, lo + p.split_len);
-        unit = ((size_t)tile * p.c.Hk + hk) * p.splits + split;
+        unit = ((size_t)(slot(p, seq) + at) * p.c.Hk + hk) * p.splits + split;
         return true;
     }
+    // The v-th tile of the sequences in order of their positions, most first:
+    // workgroups then take the long tiles first and the short ones fill the end.
+    // Lane i counts the tiles of the sequences before its own, the i-th.
+    __device__ __forceinline__ bool longest_first(const AttnParams& p, int v, int* at) {
+        const int i = (int)(threadIdx.x & 63);
+        int f = 0, m = 0, len = -1;
+        if (i < p.sv.N) {
+            seq_span(p.sv, i, &f, &m);
+            len = seq_positions(p.c, i);
+        }
+        const int tiles = (m * p.G + p.M - 1) >> p.lg_m;
+        int before = 0;
+        for (int j = 0; j < p.sv.N; ++j) {
+            const int lj = __builtin_amdgcn_readlane(len, j), tj = __builtin_amdgcn_readlane(tiles, j);
+            before += lj > len || (lj == len && j < i) ? tj : 0;
+        }
+        const unsigned long long mine = __ballot(i < p.sv.N && v >= before && v < before + tiles);
+        if (!mine) return false;
+        seq = uniform(__ffsll(mine) - 1);
+        *at = __builtin_amdgcn_readlane(before + tiles, seq) - 1 - v;
+        return true;
+    }
+    // the first tile slot of sequence i
     static __device__ __forceinline__ int slot(const AttnParams& p, int i) {
+        if (!p.sv.cu) return i * p.tiles_per_seq;
         const int c = uniform(min(max(p.sv.cu[i], 0), p.sv.T));
         return ((c * p.G) >> p.lg_m) + i;
     }
