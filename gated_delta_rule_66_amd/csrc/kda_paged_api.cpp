@@ -148,11 +148,11 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     // 398 us; 64 sequences x 8 heads with 3, 6, 12: 228, 230, 234 us).  Lengths
     // of a batch differ, so single tokens of many sequences are split in three
     // all the same (256 x 8 heads: 771 -> 743 us; chunks lose by it: 4 x 2K over
-    // 32K 3.9 -> 4.1 ms).  At least 512 positions: below that the join's launch
+    // 32K 3.9 -> 4.1 ms), up to 12288 ranges, whose parts are 200 MB at most.  At least 512 positions: below that the join's launch
     // costs more than the ranges save.
     const long long want = !step ? 1024 : N > 1 ? 1536 : 512, least = 512;
     long long n = units > 0 ? want / units : 1;
-    if (step && N > 1 && n < 3) n = 3;
+    if (step && N > 1 && n < 3 && 3 * units <= 12288) n = 3;
     if (n < 1 || M * H >= 1LL << 23) n = 1;
     long long len = n > 1 ? (ctx + n - 1) / n : ctx;
     len = (len + 127) / 128 * 128;
@@ -174,7 +174,7 @@ kda_status attn_sizes(int N, const int* cu, int T, int H, kda_dtype dt, const kd
     if (H > 65535 || *M * (H / c->heads) > 2147483647LL - 4096) return KDA_ERR_UNSUPPORTED;
     if (N == 0) return KDA_OK;
     const AttnPlan a = attn_plan(N, cu != nullptr, T, H, dt, c);
-    if (a.tiles > 2147483647LL || a.tiles * a.splits * c->heads * 256 >= 1LL << 32) return KDA_ERR_UNSUPPORTED;
+    if (a.tiles > 2147483647LL || a.tiles * a.splits * c->heads * 512 >= 1LL << 32) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -207,7 +207,8 @@ kda_status kda_paged_attn(int N, const int* cu_seqlens, int T, int H, kda_dtype 
     long long M;
     kda_status s = attn_sizes(N, cu_seqlens, T, H, dt, cache, &M);
     if (s != KDA_OK) return s;
-    if (!(scale > 0.f) || !(scale <= 3.4028234e38f)) return KDA_ERR_INVALID_ARG;
+    const float c_log2 = scale * 1.4426950408889634f;
+    if (!(scale > 0.f) || !(c_log2 <= 3.4028234e38f)) return KDA_ERR_INVALID_ARG;
     if (N == 0 || M == 0) return KDA_OK;
     s = cache_pointers(N, cu_seqlens, cache);
     if (s != KDA_OK) return s;
@@ -233,7 +234,7 @@ kda_status kda_paged_attn(int N, const int* cu_seqlens, int T, int H, kda_dtype 
     p.z = (const char*)gate; p.z_stride = (size_t)(gate_stride * es);
     p.o = (char*)o;
     p.H = H; p.G = H / c->heads;
-    p.c_log2 = scale * 1.4426950408889634f;
+    p.c_log2 = c_log2;
     p.M = a.M; p.tiles = (int)a.tiles; p.tiles_per_seq = a.tiles_per_seq;
     p.splits = a.splits; p.split_len = a.split_len;
     while ((1 << p.lg_m) < p.M) ++p.lg_m;

@@ -342,6 +342,91 @@ def test_no_sequences_no_tokens():
     assert not kda.paged_attn(q, *nopages.args()).any()
 
 
+@pytest.mark.parametrize("dt,kv", [(BF, BF), (BF, E4M3), (F32, F32), (F32, I8)])
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("n,t,length", [(70, 9, 40), (64, 12, 30), (65, 1, 50)])
+def test_many_sequences(dt, kv, packed, n, t, length):
+    """Batches around the number of lanes that order their tiles by length, lengths that tie among them."""
+    g = torch.Generator().manual_seed(51)
+    lens = [length - 3 * int(torch.randint(0, 4, (1,), generator=g)) for _ in range(n)]
+    new = [int(torch.randint(0, t + 1, (1,), generator=g)) for _ in range(n)] if packed else [t] * n
+    new[3] = t
+    c = Cache(lens, kv, 2, 64, 16, seed=52)
+    q = rows(dt, sum(new), 10, 64, 53, std=2.0)
+    check_attn(c, q if packed else q.view(n, t, 10, 64), new, "many", packed=packed)
+
+
+@pytest.mark.parametrize("dt,kv", [(BF, BF), (BF, E4M3), (BF, I8), (F32, F32)])
+@pytest.mark.parametrize("H,hk,t", [(20, 1, 1), (40, 1, 2), (64, 1, 5), (33, 3, 7)])
+def test_many_heads_of_one_cache_head(dt, kv, H, hk, t):
+    c = Cache([t + 70, 5], kv, hk, 128, 32, seed=54)
+    q = rows(dt, 2 * t, H, 128, 55).view(2, t, H, 128)
+    check_attn(c, q, [t, t], "many heads", packed=False)
+
+
+@pytest.mark.parametrize("dt,kv", [(BF, E4M3), (BF, I8), (F32, E4M3), (F32, I8)])
+def test_scales_of_every_size(dt, kv):
+    """Scale bytes from 1 (2^-126) to 253, what a cache written elsewhere may hold, read back exactly; 255 is NaN."""
+    c = Cache([256], kv, 1, 64, 16, seed=56)
+    codes = torch.arange(256, dtype=torch.int32).repeat(64).view(256, 64).to(torch.uint8)
+    if kv == E4M3:      # its NaN codes are tested as such below; 2^8 * 1.75 * 2^120 is the largest that fp32 holds
+        codes = torch.where((codes & 127) == 127, 0, codes.int()).to(torch.uint8)
+    byte = torch.arange(256).clamp(min=1, max=246)
+    byte[255] = 255
+    for cache, scale in ((c.k_cache, c.k_scale), (c.v_cache, c.v_scale)):
+        for pos in range(256):
+            page = int(c.table[0, pos // 16])
+            cache.view(torch.uint8)[page, 0, pos % 16] = codes[pos].to(DEV)
+            scale.view(torch.uint8)[page, 0, pos % 16] = int(byte[pos])
+    k, v = kda.kv_cache_read(*c.args(), 256, dtype=dt)
+    want = codes.view(kv).float().double() * torch.ldexp(torch.ones(256, 1, dtype=torch.float64), byte[:, None] - 127)
+    want[255] = float("nan")
+    # Exact but for subnormal products (below 2^-126, of scales below 2^-117 that no write makes): bf16 holds these in
+    # steps of 2^-133, so they are off by half a step, 2^-134, or come as zeros.
+    small = want.abs() < 2.0 ** -126
+    for got in (k, v):
+        got = got.view(256, 64).double().cpu()
+        same = (got == want) | (small & ((got == 0) | ((got - want).abs() <= 2.0 ** -134))) | (torch.isnan(got) & torch.isnan(want))
+        assert same.all(), torch.nonzero(~same)[:4]
+    # a NaN code under an ordinary scale
+    if kv == E4M3:
+        c.v_cache.view(torch.uint8)[int(c.table[0, 0]), 0, 3, 5] = 0x7f
+        c.v_scale.view(torch.uint8).fill_(127)
+        c.k_scale.view(torch.uint8).fill_(120)
+        c.seq_lens.fill_(6)
+        c.lens = [6]
+        got = check_attn(c, rows(dt, 5, 2, 64, 57), [5], "a NaN code")
+        assert torch.isfinite(got[:2]).all() and torch.isnan(got[2:, :, 5]).all()
+
+
+@pytest.mark.parametrize("dt,kv,t", [(BF, BF, 1), (BF, BF, 40), (BF, E4M3, 40), (F32, F32, 3)])
+def test_pools_beyond_four_gigabytes(dt, kv, t):
+    """The same pages at the end of a large pool and in a small one: the same bits."""
+    hk, d, page = 8, 128, 256
+    c = Cache([700, 300], kv, hk, d, page, seed=58)
+    each = hk * d * page * c.k_cache.element_size()
+    pages = (5 << 30) // each
+    m = 2 * t
+    q, k, v = rows(dt, m, 16, d, 59).view(2, t, 16, d), rows(dt, m, hk, d, 60), rows(dt, m, hk, d, 61)
+    k, v = k.view(2, t, hk, d), v.view(2, t, hk, d)
+    big = [torch.empty((pages, hk, page, d), dtype=kv, device=DEV) for _ in range(2)]
+    scales = [None, None]
+    for b, cache in zip(big, (c.k_cache, c.v_cache)):
+        b[pages - c.pages:].copy_(cache)
+    if c.k_scale is not None:
+        scales = [torch.full((pages, hk, page), 127, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        for b, s in zip(scales, (c.k_scale, c.v_scale)):
+            b[pages - c.pages:].copy_(s.view(torch.uint8))
+        scales = [s.view(torch.float8_e8m0fnu) for s in scales]
+    table = torch.where(c.table >= 0, c.table + (pages - c.pages), -1).to(torch.int32)
+    there = (big[0], big[1], table, c.seq_lens, *scales)
+    kda.kv_cache_write(k, v, *c.args())
+    kda.kv_cache_write(k, v, *there)
+    assert torch.equal(kda.paged_attn(q, *c.args()), kda.paged_attn(q, *there))
+    for a, b in zip(kda.kv_cache_read(*c.args(), t, dtype=dt), kda.kv_cache_read(*there, t, dtype=dt)):
+        assert torch.equal(a, b)
+
+
 # ---- together --------------------------------------------------------------------------
 @pytest.mark.parametrize("dt,kv", [(BF, BF), (BF, E4M3), (BF, I8), (F32, F32)])
 def test_prompt_chunks_and_steps(dt, kv):

@@ -121,7 +121,7 @@ def test_refused_strides_and_overlaps():
     assert attn(ws=M) == INVALID or need(2, 0, 5, 4) == 0
     assert attn(h=3) == INVALID and attn(h=0) == INVALID
     assert attn(qs=252) == INVALID and attn(zs=260) == INVALID and attn(qs=1 << 58) == UNSUPPORTED
-    for scale in (0.0, -1.0, float("nan"), float("inf")):
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 3e38):
         assert attn(scale=scale) == INVALID, scale
 
 
