@@ -15,8 +15,12 @@
 //     lanes reads whole rows), and eight by eight values are transposed between
 //     its own registers, one instruction for two values; product j then makes
 //     channels (D / 16) rho + j, rho the accumulator's row.
-// P is rounded to bf16 for its product (relative 2^-9, as V's own rounding; the
-// sum is taken before it), everything else is fp32.
+// Up to 16 rows, P goes into its product as two bf16, itself and what its
+// rounding left (2^-16 of it stay out): with the products far from being the
+// bound, the second costs nothing (256 sequences 743 us, 64 x 4 tokens 228, with
+// and without), and outputs are off by their own rounding alone.  With 32 rows
+// the registers for it would have to be spilled: there P is rounded to bf16.
+// Everything else is fp32.
 #include "kda_paged_attn.h"
 
 namespace kda {
@@ -129,6 +133,7 @@ template <int KV> __device__ __forceinline__ int q_channel(int s, int g) {
 
 template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(KV == kKvBf16 && D == 128) ? 3 : 2) void kda_attn_step_kernel(AttnParams p) {
     constexpr int R = 16 * NB, DV = D / 16, KS = D / 32, LD = D + 4;
+    constexpr bool TWO = NB == 1;       // two blocks of rows have no registers for it
     __shared__ float lds_o[2][R][LD];
     __shared__ float lds_ml[2][R][2];
     AttnTile t;
@@ -229,7 +234,7 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
                         for (int e = 0; e < 4; ++e) acc[j][nb][e] *= a;
                 }
             }
-            bf16x8 pf[NB];
+            bf16x8 pf[NB], pl[TWO ? NB : 1];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const float mc = m[nb] == -INFINITY ? 0.f : m[nb] * c;
@@ -240,6 +245,11 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
                     l[nb] += x[i];
                 }
                 pf[nb] = frag_from<bf16>(x);
+                if constexpr (TWO) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] -= (float)pf[nb][i];
+                    pl[nb] = frag_from<bf16>(x);
+                }
             }
             unsigned vp[8][DV / 2];
             b.vpairs(vp);
@@ -266,7 +276,10 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
                 for (int i = 0; i < 4; ++i) u[i] = __builtin_amdgcn_perm(vp[2 * i + 1][j >> 1], vp[2 * i][j >> 1], sel);
                 const bf16x8 vf = __builtin_bit_cast(bf16x8, u);
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) acc[j][nb] = mma(acc[j][nb], vf, pf[nb]);
+                for (int nb = 0; nb < NB; ++nb) {
+                    if constexpr (TWO) acc[j][nb] = mma(acc[j][nb], vf, pl[nb]);
+                    acc[j][nb] = mma(acc[j][nb], vf, pf[nb]);
+                }
             }
             if (next < t.hi) b.load_v(p.c, t.hk, next, lane);
         }
