@@ -137,7 +137,13 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     AttnPlan a{};
     const long long G = H / c->heads, M = packed ? (long long)T : (long long)N * T;
     const long long per = N > 0 ? M * G / N : 0;        // rows of a sequence, on average
-    a.kind = dt == KDA_F32 ? kAttnF32 : per <= 16 ? kAttnStep16 : per <= 32 ? kAttnStep32 : kAttnChunk;
+    // Few rows go to the kernel that splits positions over its waves, 16 or 32
+    // rows a workgroup, more to the one that splits rows.  64 sequences of up to
+    // 8K x 8 heads of 128, 16 / 32 / chunk, bf16: 16 rows 199, 196, 258 us; 32 rows
+    // 233, 205, 262; 64 rows 340, 247, 270 (4 sequences: 42, 37, 33); 128 rows 609,
+    // 361, 285.  e4m3: 16 rows 122, 126, 250; 64 rows 243, 192, 260 (39, 35, 35); 128
+    // rows 434, 316, 278.
+    a.kind = dt == KDA_F32 ? kAttnF32 : per <= 16 ? kAttnStep16 : per <= (coded(c->dt) ? 64 : 32) ? kAttnStep32 : kAttnChunk;
     a.M = a.kind == kAttnStep16 ? 16 : a.kind != kAttnChunk ? 32 : c->head_dim == 128 ? 256 : 128;
     const bool step = a.kind == kAttnStep16 || a.kind == kAttnStep32;
     a.tiles_per_seq = packed ? 0 : (int)((T * G + a.M - 1) / a.M);
