@@ -65,7 +65,7 @@ hipError_t launch_cache_read(int dtype, int kv, int D, const CacheIoParams& p, i
 // A tile's positions may be split into `splits` ranges of split_len; a tile of
 // more than one non-empty range leaves unnormalised parts that a second launch
 // joins.
-enum AttnKind { kAttnStep16, kAttnStep32, kAttnChunk, kAttnF32 };
+enum AttnKind { kAttnStep16, kAttnStep32, kAttnChunk, kAttnF32, kAttnChunk256 };
 struct AttnParams {
     SeqView sv;
     PagedCache c;
@@ -85,7 +85,7 @@ struct AttnParams {
 };
 hipError_t launch_attn(AttnKind kind, int kv, int D, const AttnParams& p, hipStream_t st);
 hipError_t launch_attn_step(AttnKind kind, int kv, int D, const AttnParams& p, int grid, hipStream_t st);
-hipError_t launch_attn_chunk(int kv, int D, const AttnParams& p, int grid, hipStream_t st);
+hipError_t launch_attn_chunk(AttnKind kind, int kv, int D, const AttnParams& p, int grid, hipStream_t st);
 hipError_t launch_attn_f32(int kv, int D, const AttnParams& p, int grid, hipStream_t st);
 hipError_t launch_attn_join(int dtype, int D, const AttnParams& p, int M_tokens, hipStream_t st);
 

@@ -144,19 +144,27 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     // 361, 285.  e4m3: 16 rows 122, 126, 250; 64 rows 243, 192, 260 (39, 35, 35); 128
     // rows 434, 316, 278.
     a.kind = dt == KDA_F32 ? kAttnF32 : per <= 16 ? kAttnStep16 : per <= (coded(c->dt) ? 64 : 32) ? kAttnStep32 : kAttnChunk;
-    a.M = a.kind == kAttnStep16 ? 16 : a.kind != kAttnChunk ? 32 : c->head_dim == 128 ? 256 : 128;
+    // Rows of a chunk's workgroup, heads of 128: 256 read the cache half as often
+    // as 128 (4 x 2K over 32K in e4m3 3.9 and 4.2 ms, a 4K prompt 143 and 152 us),
+    // but need enough of them for the card (2K prompt 63 and 52 us, 8 x 300 over
+    // 3K 81 and 66) and sequences that fill them (64 x up to 200 over 4K 341 and 325).
+    if (a.kind == kAttnChunk && c->head_dim == 128 && per >= 1024 && M * G / 256 * c->heads >= 512) a.kind = kAttnChunk256;
+    a.M = a.kind == kAttnStep16 ? 16 : a.kind == kAttnChunk ? 128 : a.kind == kAttnChunk256 ? 256 : 32;
     const bool step = a.kind == kAttnStep16 || a.kind == kAttnStep32;
     a.tiles_per_seq = packed ? 0 : (int)((T * G + a.M - 1) / a.M);
     a.tiles = packed ? M * G / a.M + N : (long long)N * a.tiles_per_seq;
     const long long units = a.tiles * c->heads, ctx = (long long)c->blocks * c->page_size;
-    // Ranges: enough of them to fill the card about twice, a single sequence's,
-    // which are alike, once (a 1M step with 64, 192, 384 ranges a head 376, 387,
-    // 398 us; 64 sequences x 8 heads with 3, 6, 12: 228, 230, 234 us).  Lengths
-    // of a batch differ, so single tokens of many sequences are split in three
-    // all the same (256 x 8 heads: 771 -> 743 us; chunks lose by it: 4 x 2K over
-    // 32K 3.9 -> 4.1 ms), up to 12288 ranges, whose parts are 200 MB at most.  At least 512 positions: below that the join's launch
-    // costs more than the ranges save.
-    const long long want = !step ? 1024 : N > 1 ? 1536 : 512, least = 512;
+    // Ranges: as many as the card takes at a time where tiles alone are fewer
+    // (chunks of 128 rows, two workgroups a CU: 512 tokens over 8K with 256, 512,
+    // 1024 wanted 88, 82, 94 us, 2K over 2K 52, 52, 71; a 1M step with 64, 192, 384
+    // ranges a head 376, 387, 398), three times that for the lengths of a batch of
+    // single tokens, which differ (64 sequences x 8 heads with 3, 6, 12: 228, 230,
+    // 234); many of them are split in three all the same (256 x 8 heads: 771 -> 743
+    // us), up to 12288 ranges, whose parts are 200 MB at most.  At least 512
+    // positions, 1024 in chunks: below that the join's launch costs more than the
+    // ranges save (a 1K prompt in two 34 us, in one 27).
+    const long long want = a.kind == kAttnChunk256 ? 256 : step && N > 1 ? 1536 : 512;
+    const long long least = a.kind == kAttnChunk || a.kind == kAttnChunk256 ? 1024 : 512;
     long long n = units > 0 ? want / units : 1;
     if (step && N > 1 && n < 3 && 3 * units <= 12288) n = 3;
     if (n < 1 || M * H >= 1LL << 23) n = 1;
@@ -254,10 +262,10 @@ kda_status kda_paged_attn(int N, const int* cu_seqlens, int T, int H, kda_dtype 
     // Workgroups of chunks bound by their products end together if long tiles
     // come first (48 sequences over int8 216 -> 166 us, 16 in fp32 136 -> 116); a lane a sequence finds the
     // order, and with more sequences than lanes chance does what is needed.
-    p.by_length = (a.kind == kAttnChunk || a.kind == kAttnF32) && N > 1 && N <= 64;
+    p.by_length = (a.kind == kAttnChunk || a.kind == kAttnChunk256 || a.kind == kAttnF32) && N > 1 && N <= 64;
     p.part = (float*)workspace;
     p.ml = (float*)((char*)workspace + a.part);
-    const char* name = a.kind == kAttnF32 ? "attn_f32" : a.kind == kAttnChunk ? "attn_chunk" : "attn_step";
+    const char* name = a.kind == kAttnF32 ? "attn_f32" : a.kind == kAttnChunk || a.kind == kAttnChunk256 ? "attn_chunk" : "attn_step";
     KDA_LAUNCH(name, launch_attn(a.kind, (int)c->dt, c->head_dim, p, stream));
     if (a.splits > 1) KDA_LAUNCH("attn_join", launch_attn_join((int)dt, c->head_dim, p, (int)M, stream));
     return KDA_OK;

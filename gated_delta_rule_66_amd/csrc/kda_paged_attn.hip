@@ -21,8 +21,6 @@ namespace kda {
 namespace {
 
 constexpr int kTile = 64;
-// waves of a workgroup
-template <int D> constexpr int kWaves = D == 128 ? 8 : 4;
 
 __device__ __forceinline__ f32x16 mma32(f32x16 acc, bf16x8 a, bf16x8 b) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
@@ -80,11 +78,10 @@ struct TilePages {
 // a lane loads; codes go through registers.  Places without a position (behind
 // the last, or on no page) get what the page, or page 0, holds there: such
 // scores are masked, and such values of V with them.
-template <int KV, int D, bool V> struct Stage {
+template <int KV, int D, bool V, int W> struct Stage {
     static constexpr int E = KV == kKvBf16 ? 2 : 1;
     static constexpr int RB = D * E;                // bytes of a row
     static constexpr int PER = 1024 / RB;           // rows of a wave's load
-    static constexpr int W = kWaves<D>;
     static constexpr int N = kTile / (W * PER);     // loads of a wave
     u32x4 w[N];
     unsigned s[N];
@@ -333,8 +330,8 @@ template <int D> struct Rows {
     }
 };
 
-template <int KV, int D> __global__ __launch_bounds__(64 * kWaves<D>, D == 128 ? 2 : 3) void kda_attn_chunk_kernel(AttnParams p) {
-    constexpr int KS = D / 16, DB = D / 32, W = kWaves<D>, M = 32 * W;
+template <int KV, int D, int W> __global__ __launch_bounds__(64 * W, D == 128 ? 2 : 3) void kda_attn_chunk_kernel(AttnParams p) {
+    constexpr int KS = D / 16, DB = D / 32, M = 32 * W;
     constexpr int TB = kTile * D * 2;
     __shared__ __align__(16) char lds[4 * TB];      // two tiles of K, two of V
     __shared__ int lds_bad;                         // the first tile of V with a value taken out, or -1
@@ -365,8 +362,8 @@ template <int KV, int D> __global__ __launch_bounds__(64 * kWaves<D>, D == 128 ?
 
     PageWalk<false> walk;
     walk.init(p.c, t.seq, t.L, t.lo >> p.c.lg_page);       // waits for its load, and Q's with it
-    Stage<KV, D, false> sk;
-    Stage<KV, D, true> sv;
+    Stage<KV, D, false, W> sk;
+    Stage<KV, D, true, W> sv;
     sk.init(wave, lane, p.c.lg_page < 6);
     sv.init(wave, lane, p.c.lg_page < 6);
     x.at.init(lane);
@@ -473,25 +470,32 @@ template <int KV, int D> __global__ __launch_bounds__(64 * kWaves<D>, D == 128 ?
         }
 }
 
-template <int KV, int D> hipError_t launch_chunk_kv(const AttnParams& p, int grid, hipStream_t st) {
-    kda_attn_chunk_kernel<KV, D><<<grid, 64 * kWaves<D>, 0, st>>>(p);
+template <int KV, int D> hipError_t launch_chunk_kv(AttnKind kind, const AttnParams& p, int grid, hipStream_t st) {
+    if constexpr (D == 128) {
+        if (kind == kAttnChunk256) {
+            kda_attn_chunk_kernel<KV, D, 8><<<grid, 512, 0, st>>>(p);
+            return hipGetLastError();
+        }
+    }
+    kda_attn_chunk_kernel<KV, D, 4><<<grid, 256, 0, st>>>(p);
     return hipGetLastError();
+}
+template <int D> hipError_t launch_chunk_d(AttnKind kind, int kv, const AttnParams& p, int grid, hipStream_t st) {
+    if (kv == kKvE4m3) return launch_chunk_kv<kKvE4m3, D>(kind, p, grid, st);
+    if (kv == kKvI8) return launch_chunk_kv<kKvI8, D>(kind, p, grid, st);
+    return launch_chunk_kv<kKvBf16, D>(kind, p, grid, st);
 }
 
 }  // namespace
 
-hipError_t launch_attn_chunk(int kv, int D, const AttnParams& p, int grid, hipStream_t st) {
-    if (D == 128)
-        return kv == kKvE4m3 ? launch_chunk_kv<kKvE4m3, 128>(p, grid, st) : kv == kKvI8 ? launch_chunk_kv<kKvI8, 128>(p, grid, st)
-                                                                                        : launch_chunk_kv<kKvBf16, 128>(p, grid, st);
-    return kv == kKvE4m3 ? launch_chunk_kv<kKvE4m3, 64>(p, grid, st) : kv == kKvI8 ? launch_chunk_kv<kKvI8, 64>(p, grid, st)
-                                                                                   : launch_chunk_kv<kKvBf16, 64>(p, grid, st);
+hipError_t launch_attn_chunk(AttnKind kind, int kv, int D, const AttnParams& p, int grid, hipStream_t st) {
+    return D == 128 ? launch_chunk_d<128>(kind, kv, p, grid, st) : launch_chunk_d<64>(kind, kv, p, grid, st);
 }
 
 hipError_t launch_attn(AttnKind kind, int kv, int D, const AttnParams& p, hipStream_t st) {
     const int grid = p.tiles * p.splits * p.c.Hk;
     if (kind == kAttnF32) return launch_attn_f32(kv, D, p, grid, st);
-    if (kind == kAttnChunk) return launch_attn_chunk(kv, D, p, grid, st);
+    if (kind == kAttnChunk || kind == kAttnChunk256) return launch_attn_chunk(kind, kv, D, p, grid, st);
     return launch_attn_step(kind, kv, D, p, grid, st);
 }
 
