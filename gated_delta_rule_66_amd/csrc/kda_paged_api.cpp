@@ -163,8 +163,8 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     // us), up to 12288 ranges, whose parts are 200 MB at most.  At least 512
     // positions, 1024 in chunks: below that the join's launch costs more than the
     // ranges save (a 1K prompt in two 34 us, in one 27).
-    const long long want = a.kind == kAttnChunk256 ? 256 : step && N > 1 ? 1536 : 512;
-    const long long least = a.kind == kAttnChunk || a.kind == kAttnChunk256 ? 1024 : 512;
+    const long long want = step && N > 1 ? 1536 : 512;
+    const long long least = a.kind == kAttnChunk ? 1024 : 512;
     long long n = units > 0 ? want / units : 1;
     if (step && N > 1 && n < 3 && 3 * units <= 12288) n = 3;
     if (n < 1 || M * H >= 1LL << 23) n = 1;

@@ -84,6 +84,40 @@ def attn(q, k, v, table, positions, ranges, scale, gate=None):
     return o, mean, size
 
 
+def attn_wide(q, k, v, table, positions, ranges, scale, gate=None):
+    """attn() of whole sequences at a time, on the tensors' own device."""
+    M, H, D = q.shape
+    P, Hk, S, _ = k.shape
+    o, mean, size = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(q[..., :1])
+    for i, (first, n) in enumerate(ranges):
+        length = min(max(int(positions[i]), 0), table.shape[1] * S)
+        at = torch.arange(length, device=q.device)
+        pages = table[i].long()[at // S]
+        there = (pages >= 0) & (pages < P)
+        at, pages = at[there], pages[there]
+        ki, vi = (c[pages, :, at % S].transpose(0, 1).contiguous() for c in (k, v))         # [Hk, C, D]
+        seen = at <= (length - n + torch.arange(n, device=q.device))[:, None]               # [n, C]
+        for h in range(Hk):
+            rows = slice(h * H // Hk, (h + 1) * H // Hk)
+            qq = q[first:first + n, rows].transpose(0, 1)                                   # [G, n, D]
+            score = torch.where(seen, (qq.reshape(-1, D) @ ki[h].T).view(len(qq), n, -1) * scale, -torch.inf)
+            p = torch.where(seen.any(-1)[:, None], torch.softmax(score, -1), 0.0)
+            use = torch.where(seen.any(0)[:, None], vi[h], 0.0)
+            clean = torch.nan_to_num(use, nan=0.0, posinf=0.0, neginf=0.0)
+            got = (p.reshape(-1, len(at)) @ clean).view(len(qq), n, D)
+            bad = use - clean           # NaN and infinities reach the rows that see them
+            for j in torch.nonzero(~torch.isfinite(vi[h]).all(-1)).flatten().tolist():
+                got = got + torch.where(seen[:, j, None] & ~torch.isfinite(bad[j]), bad[j], 0.0)
+            o[first:first + n, rows] = got.transpose(0, 1)
+            mean[first:first + n, rows] = (p.reshape(-1, len(at)) @ clean.abs()).view(len(qq), n, D).transpose(0, 1)
+            terms = (qq.abs().reshape(-1, D) @ ki[h].abs().T).view(len(qq), n, -1)
+            size[first:first + n, rows] = torch.where(seen, terms, 0.0).amax(-1, keepdim=True).transpose(0, 1) * scale
+    if gate is not None:
+        s = torch.sigmoid(gate)
+        o, mean = o * s, mean * s
+    return o, mean, size
+
+
 def attn_bound(o, mean, size, dt, D, positions):
     """The output's own rounding; a weight's rounding to bf16; and in fp32, doubled because a weight stands above and
     below the fraction: scores of D products (each sum's and product's rounding relative to the sum of magnitudes),

@@ -327,6 +327,35 @@ def test_scores_far_apart(dt, kv, t):
     check_attn(c, q, [t, t], "equal")
 
 
+@pytest.mark.parametrize("kv", [BF, E4M3, I8])
+@pytest.mark.parametrize("page,hk", [(16, 16), (64, 16), (128, 32)])
+def test_prompts_that_fill_the_card(kv, page, hk):
+    """Prompts of many rows, with holes in the tables, a NaN behind most tokens, and a gate.  (The widest workgroups.)"""
+    new, lens = [1024, 1100], [1024 + 77, 1100]
+    c = Cache(lens, kv, hk, 128, page, seed=62)
+    c.table[0, 64 // page + 1] = -1
+    c.table[1, 5] = c.pages
+    page_of, row = int(c.table[1, 900 // page]), 900 % page
+    if kv == BF:
+        c.v_cache[page_of, 1, row, 5] = float("nan")
+        c.v_cache[page_of, 1, row, 70] = float("inf")
+        c.k_cache[page_of, 2, row, 7] = float("nan")
+    else:
+        c.v_scale.view(torch.uint8)[page_of, 1, row] = 255
+        c.k_scale.view(torch.uint8)[page_of, 2, row] = 255
+    H, m = 4 * hk, sum(new)
+    q, z = rows(BF, m, H, 128, 63, std=1.5), rows(BF, m, H, 128, 64)
+    cu = cu_of(new)
+    got = kda.paged_attn(q, *c.args(), gate=z, cu_seqlens=cu)
+    k, v = (x.to(DEV) for x in c.values())
+    o, mean, size = ref.attn_wide(q.double(), k, v, c.table, lens, ref.spans(2, 0, cu), 128 ** -0.5, z.double())
+    o, mean, size = o.cpu(), mean.cpu(), size.cpu()
+    ref.close(got, o, torch.nan_to_num(ref.attn_bound(o, mean, size, BF, 128, 1101), nan=0.0, posinf=0.0), "prompts")
+    # tokens before position 900 of the second sequence, and its heads of other cache heads, are numbers
+    assert torch.isfinite(got[:1024]).all() and torch.isfinite(got[1024:1924]).all() and torch.isfinite(got[:, :4]).all()
+    assert torch.isnan(got[1924:, 4:8, 5]).all() and torch.isnan(got[1924:, 8:12]).all()
+
+
 def test_no_sequences_no_tokens():
     c = Cache([40, 3], BF, 2, 64, 16, seed=35)
     none = torch.empty((0, 4, 64), dtype=BF, device=DEV)
