@@ -179,7 +179,8 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
         b.find(p.c, walk, pos, t.hi);
         b.load_k(p.c, t.hk, pos, lane);
         b.load_v(p.c, t.hk, pos, lane);
-        for (; pos < t.hi; pos += 128) {
+        // (the next V's loads stand in every pass that comes back: a wait for K then leaves them open)
+        for (;;) {
             f32x4 s[2][NB];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -281,7 +282,9 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
                     acc[j][nb] = mma(acc[j][nb], vf, pf[nb]);
                 }
             }
-            if (next < t.hi) b.load_v(p.c, t.hk, next, lane);
+            if (next >= t.hi) break;
+            b.load_v(p.c, t.hk, next, lane);
+            pos = next;
         }
     }
     if (bad_from >= 0) {
