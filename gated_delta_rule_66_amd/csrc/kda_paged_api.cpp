@@ -144,11 +144,23 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     // 361, 285.  e4m3: 16 rows 122, 126, 250; 64 rows 243, 192, 260 (39, 35, 35); 128
     // rows 434, 316, 278.
     a.kind = dt == KDA_F32 ? kAttnF32 : per <= 16 ? kAttnStep16 : per <= (coded(c->dt) ? 64 : 32) ? kAttnStep32 : kAttnChunk;
-    // Rows of a chunk's workgroup, heads of 128: 256 read the cache half as often
-    // as 128 (4 x 2K over 32K in e4m3 3.9 and 4.2 ms, a 4K prompt 143 and 152 us),
-    // but need enough of them for the card (2K prompt 63 and 52 us, 8 x 300 over
-    // 3K 81 and 66) and sequences that fill them (64 x up to 200 over 4K 341 and 325).
-    if (a.kind == kAttnChunk && c->head_dim == 128 && per >= 1024 && M * G / 256 * c->heads >= 512) a.kind = kAttnChunk256;
+    // Rows of a chunk's workgroup, 128 or 256.  Heads of 128, eight waves of 32:
+    // half the reads of the cache (4 x 2K over 32K in e4m3 3.9 and 4.2 ms, a 4K
+    // prompt 143 and 152 us), but there have to be enough of them for the card (2K
+    // prompt 63 and 52 us, 8 x 300 over 3K 81 and 66) and sequences that fill them
+    // (64 x up to 200 over 4K 341 and 325).  Heads of 64, four waves of 64: a code
+    // is turned into bf16 half as often and V is read from LDS half as often (4 x
+    // 2K over 32K 1.11 and 1.18 ms, in int8 1.25 and 1.43; 512 over 64K in int8 338
+    // and 408 us), but with two waves a SIMD instead of three, which pays where a
+    // workgroup walks some thousand positions (512 over 32K in int8 178 and 211 us,
+    // over 8K 58 and 55, a 4K prompt 106 and 95, 2K 53 and 39).  Sequences of a batch
+    // are taken for half as long as their table is wide (16 x 777 over up to 8K 212
+    // and 182, 48 up to 777 over up to 4K in int8 180 and 166, 8 over up to 32K 470 and 688).
+    if (a.kind == kAttnChunk && per >= 1024) {
+        const long long units = M * G / 256 * c->heads, at_a_time = units < 512 ? units : 512;
+        const long long before = (long long)c->blocks * c->page_size / (N > 1 ? 2 : 1) - M / N / 2;
+        if (c->head_dim == 128 ? units >= 512 : before * at_a_time >= 512 * 3800) a.kind = kAttnChunk256;
+    }
     a.M = a.kind == kAttnStep16 ? 16 : a.kind == kAttnChunk ? 128 : a.kind == kAttnChunk256 ? 256 : 32;
     const bool step = a.kind == kAttnStep16 || a.kind == kAttnStep32;
     a.tiles_per_seq = packed ? 0 : (int)((T * G + a.M - 1) / a.M);
@@ -164,7 +176,7 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     // positions, 1024 in chunks: below that the join's launch costs more than the
     // ranges save (a 1K prompt in two 34 us, in one 27).
     const long long want = step && N > 1 ? 1536 : 512;
-    const long long least = a.kind == kAttnChunk ? 1024 : 512;
+    const long long least = step || a.kind == kAttnF32 ? 512 : 1024;
     long long n = units > 0 ? want / units : 1;
     if (step && N > 1 && n < 3 && 3 * units <= 12288) n = 3;
     if (n < 1 || M * H >= 1LL << 23) n = 1;

@@ -3,8 +3,8 @@
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i.k_j - max_i),  j <= position of i
 //
 // Bound by its products (4 D flops a pair of row and position).  A workgroup of
-// four waves takes 128 rows (tokens times the heads that share a cache head),
-// 32 a wave, and walks tiles of 64 positions that all waves share in LDS.
+// W waves takes 128 or 256 rows (tokens times the heads that share a cache
+// head), 32 NR a wave, and walks tiles of 64 positions that all waves share in LDS.
 // Products are 32x32x16 with the row in the lane:
 //   * S^T = K Q^T: a lane has 32 of a tile's 64 scores of its row, so maximum
 //     and sum need no exchange but between two lanes, and that only when the
@@ -12,7 +12,7 @@
 //   * O^T = V^T P^T: S^T as it sits in the accumulator is the operand P^T if a
 //     product's 16 positions are 8 (i / 4) + 4 h + i % 4 (lane half h), which
 //     the transposing reads of V deliver as well.
-// P is rounded to bf16 for its product (relative 2^-9, as V's own rounding; the
+// P is rounded to bf16 for its product (relative 2^-8, as V's own rounding; the
 // sum is taken before it), everything else is fp32.
 #include "kda_paged_attn.h"
 
@@ -184,15 +184,16 @@ template <int D> struct Offsets {
     }
 };
 
-// What a wave keeps of its 32 rows.  Scores are a tile ahead: while a tile's
-// weights are made and multiplied with V, the matrix units have the next tile's
-// scores to go on with.
-template <int D> struct Rows {
+// What a wave keeps of its NR times 32 rows.  Scores are a tile ahead: while a
+// tile's weights are made and multiplied with V, the matrix units have the next
+// tile's scores to go on with.
+template <int D, int NR> struct Rows {
     static constexpr int KS = D / 16, DB = D / 32;
-    typedef f32x16 Scores[2];
-    bf16x8 q[KS];
-    f32x16 acc[DB];
-    float m, l, mc;
+    typedef f32x16 Scores[NR][2];
+    bf16x8 q[NR][KS];
+    f32x16 acc[NR][DB];
+    float m[NR], l[NR], mc[NR];
+    int lim[NR];            // the last positions that the lane's rows see
     Offsets<D> at;
 
     __device__ __forceinline__ void scores(Scores& s, const char* tk) {
@@ -200,55 +201,70 @@ template <int D> struct Rows {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[n][b][e] = 0.f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) kf[b][k] = at.k_frag(tk, b, k);
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int k = 0; k < KS; ++k) s[b] = mma32(s[b], kf[b][k], q[k]);
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int n = 0; n < NR; ++n) s[n][b] = mma32(s[n][b], kf[b][k], q[n][k]);
     }
-    static __device__ __forceinline__ float largest(const Scores& s) {
-        float top = s[0][0];
+    struct Top {
+        float v[NR];
+    };
+    static __device__ __forceinline__ Top largest(const Scores& s) {
+        Top t;
 #pragma unroll
-        for (int e = 1; e < 16; ++e) top = fmaxf(top, s[0][e]);
+        for (int n = 0; n < NR; ++n) {
+            t.v[n] = s[n][0][0];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[1][e]);
-        return top;
+            for (int e = 1; e < 16; ++e) t.v[n] = fmaxf(t.v[n], s[n][0][e]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) t.v[n] = fmaxf(t.v[n], s[n][1][e]);
+        }
+        return t;
     }
     // Scores of the tile at pos become weights' logarithms: masked where some
     // row of the wave sees only a part of it, and the maximum moved.
-    __device__ __forceinline__ void settle(Scores& s, float top, float c, bool masked, int pos, int lim, int valid, int lane) {
+    __device__ __forceinline__ void settle(Scores& s, Top top, float c, bool masked, int pos, int valid, int lane) {
         if (masked) {
             const int h = lane >> 5;
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int j = 32 * b + 8 * (e >> 2) + 4 * h + (e & 3);
-                    if (pos + j > lim || !(valid >> (2 * b + (e >> 3)) & 1)) s[b][e] = -INFINITY;
-                }
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int j = 32 * b + 8 * (e >> 2) + 4 * h + (e & 3);
+                        if (pos + j > lim[n] || !(valid >> (2 * b + (e >> 3)) & 1)) s[n][b][e] = -INFINITY;
+                    }
             top = largest(s);
         }
-        if (__any(top > m + kLazy / c)) {
-            const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
-            const float a = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * c);
-            m = mn;
-            mc = m == -INFINITY ? 0.f : m * c;
-            l *= a;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            if (!__any(top.v[n] > m[n] + kLazy / c)) continue;
+            const float mn = fmaxf(m[n], fmaxf(top.v[n], __shfl_xor(top.v[n], 32)));
+            const float a = mn == -INFINITY ? 1.f : fast_exp2((m[n] - mn) * c);
+            m[n] = mn;
+            mc[n] = mn == -INFINITY ? 0.f : mn * c;
+            l[n] *= a;
 #pragma unroll
             for (int db = 0; db < DB; ++db)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) acc[db][e] *= a;
+                for (int e = 0; e < 16; ++e) acc[n][db][e] *= a;
         }
     }
-    __device__ __forceinline__ bf16x8 weights(const Scores& s, int k, float c) {
+    __device__ __forceinline__ bf16x8 weights(const Scores& s, int n, int k, float c) {
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            x[i] = fast_exp2(fmaf(s[k >> 1][8 * (k & 1) + i], c, -mc));
-            l += x[i];
+            x[i] = fast_exp2(fmaf(s[n][k >> 1][8 * (k & 1) + i], c, -mc[n]));
+            l[n] += x[i];
         }
         return frag_from<bf16>(x);
     }
@@ -256,8 +272,8 @@ template <int D> struct Rows {
     // of the next beside the products of the present ones.  `made` of the four
     // are made already; `last` is the vector work beside the third's products.
     template <class F>
-    __device__ __forceinline__ void product(const Scores& s, bf16x8 (&pf)[4], int made, bf16x8 (&vf)[2][DB], const char* tv,
-                                            float c, F&& last) {
+    __device__ __forceinline__ void product(const Scores& s, bf16x8 (&pf)[NR][4], int made, bf16x8 (&vf)[2][DB],
+                                            const char* tv, float c, F&& last) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (k < 3) {
@@ -265,14 +281,19 @@ template <int D> struct Rows {
                 for (int db = 0; db < DB; ++db) vf[(k + 1) & 1][db] = at.v_frag(tv, db, k + 1);
             }
 #pragma unroll
-            for (int db = 0; db < DB; ++db) acc[db] = mma32(acc[db], vf[k & 1][db], pf[k]);
-            if (k + made < 4) pf[k + made] = weights(s, k + made, c);
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int db = 0; db < DB; ++db) acc[n][db] = mma32(acc[n][db], vf[k & 1][db], pf[n][k]);
+            if (k + made < 4) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n) pf[n][k + made] = weights(s, n, k + made, c);
+            }
             if (k == 2) last();
 #pragma unroll
-            for (int db = 0; db < DB; ++db) {
+            for (int i = 0; i < DB * NR; ++i) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 if (k < 3) {
-                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, NR == 1 ? 2 : 1, 0);
                     __builtin_amdgcn_sched_group_barrier(0x402, 28 / DB, 0);
                 }
             }
@@ -285,17 +306,16 @@ template <int D> struct Rows {
     // D = 128: products take longer than the vector work (32 cycles each, 4096 a
     // pair of tiles and SIMD), and the next scores' products stand beside the first weights.
     // D = 64: the vector work is longer; the scores come last, in the registers
-    // of those before, and three waves a SIMD instead of two hide more of it
-    // (48 sequences over int8: 236 -> 217 us).
-    __device__ __forceinline__ float tile(const Scores& s, Scores& next, const char* tk, const char* tv, float c) {
-        bf16x8 vf[2][DB], pf[4];
-        float top;
+    // of those before.
+    __device__ __forceinline__ Top tile(const Scores& s, Scores& next, const char* tk, const char* tv, float c) {
+        bf16x8 vf[2][DB], pf[NR][4];
+        Top top;
         if constexpr (D == 128) {
             scores(next, tk);
 #pragma unroll
             for (int db = 0; db < DB; ++db) vf[0][db] = at.v_frag(tv, db, 0);
-            pf[0] = weights(s, 0, c);
-            pf[1] = weights(s, 1, c);
+            pf[0][0] = weights(s, 0, 0, c);
+            pf[0][1] = weights(s, 0, 1, c);
             __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
             for (int i = 0; i < 2 * KS - 4; ++i) {
@@ -314,7 +334,8 @@ template <int D> struct Rows {
         } else {
 #pragma unroll
             for (int db = 0; db < DB; ++db) vf[0][db] = at.v_frag(tv, db, 0);
-            pf[0] = weights(s, 0, c);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) pf[n][0] = weights(s, n, 0, c);
             __builtin_amdgcn_sched_barrier(0);
             product(s, pf, 1, vf, tv, c, []() {});
             scores(next, tk);
@@ -322,7 +343,7 @@ template <int D> struct Rows {
             __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
             for (int i = 0; i < 2 * KS - 4; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, NR, 0);
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
         }
@@ -330,8 +351,10 @@ template <int D> struct Rows {
     }
 };
 
-template <int KV, int D, int W> __global__ __launch_bounds__(64 * W, D == 128 ? 2 : 3) void kda_attn_chunk_kernel(AttnParams p) {
-    constexpr int KS = D / 16, DB = D / 32, M = 32 * W;
+// W waves of 32 NR rows.
+template <int KV, int D, int W, int NR>
+__global__ __launch_bounds__(64 * W, D == 128 || NR == 2 ? 2 : 3) void kda_attn_chunk_kernel(AttnParams p) {
+    constexpr int KS = D / 16, DB = D / 32, RW = 32 * NR, M = RW * W;
     constexpr int TB = kTile * D * 2;
     __shared__ __align__(16) char lds[4 * TB];      // two tiles of K, two of V
     __shared__ int lds_bad;                         // the first tile of V with a value taken out, or -1
@@ -339,25 +362,28 @@ template <int KV, int D, int W> __global__ __launch_bounds__(64 * W, D == 128 ? 
     if (!t.init(p, blockIdx.x)) return;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
 
-    const int r = t.r0 + 32 * wave + (lane & 31), tok = p.by_g.div(r), head = t.hk * p.G + r - tok * p.G;
-    const int lim = t.limit(r, p);
     // the wave's first and last limits
-    const int w0 = t.r0 + 32 * wave, lim_first = t.limit(w0, p), t_first = t.limit(t.r0, p);
-    const int lim_last = w0 < t.rows ? t.limit(min(w0 + 31, t.rows - 1), p) : -1;
-    Rows<D> x;
-    const char* row = p.q + (size_t)(t.first + tok) * p.q_stride + (size_t)head * D * 2;
+    const int w0 = t.r0 + RW * wave, lim_first = t.limit(w0, p), t_first = t.limit(t.r0, p);
+    const int lim_last = w0 < t.rows ? t.limit(min(w0 + RW - 1, t.rows - 1), p) : -1;
+    Rows<D, NR> x;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-        u32x4 u = {0u, 0u, 0u, 0u};
-        if (r < t.rows) u = *reinterpret_cast<const u32x4*>(row + (16 * s + 8 * h) * 2);
-        x.q[s] = __builtin_bit_cast(bf16x8, u);
+    for (int n = 0; n < NR; ++n) {
+        const int r = w0 + 32 * n + (lane & 31), tok = p.by_g.div(r), head = t.hk * p.G + r - tok * p.G;
+        x.lim[n] = t.limit(r, p);
+        const char* row = p.q + (size_t)(t.first + tok) * p.q_stride + (size_t)head * D * 2;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            u32x4 u = {0u, 0u, 0u, 0u};
+            if (r < t.rows) u = *reinterpret_cast<const u32x4*>(row + (16 * s + 8 * h) * 2);
+            x.q[n][s] = __builtin_bit_cast(bf16x8, u);
+        }
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x.acc[n][db][e] = 0.f;
+        x.m[n] = -INFINITY;
+        x.l[n] = x.mc[n] = 0.f;
     }
-#pragma unroll
-    for (int db = 0; db < DB; ++db)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x.acc[db][e] = 0.f;
-    x.m = -INFINITY;
-    x.l = x.mc = 0.f;
     const float c = p.c_log2;
 
     PageWalk<false> walk;
@@ -368,7 +394,7 @@ template <int KV, int D, int W> __global__ __launch_bounds__(64 * W, D == 128 ? 
     sv.init(wave, lane, p.c.lg_page < 6);
     x.at.init(lane);
     if (threadIdx.x == 0) lds_bad = -1;
-    typename Rows<D>::Scores sa, sb;
+    typename Rows<D, NR>::Scores sa, sb;
     TilePages next;         // of the tile behind the present one
     int valid = 15;         // of the present one
     if (t.lo < t.hi) {
@@ -384,12 +410,12 @@ template <int KV, int D, int W> __global__ __launch_bounds__(64 * W, D == 128 ? 
         }
         if (t.lo <= lim_last) {
             x.scores(sa, lds);
-            x.settle(sa, x.largest(sa), c, t.lo + kTile - 1 > lim_first || valid != 15, t.lo, lim, valid, lane);
+            x.settle(sa, x.largest(sa), c, t.lo + kTile - 1 > lim_first || valid != 15, t.lo, valid, lane);
         }
     }
     // The tile at pos, whose scores are in s: its V lies at v, the next tile's K
     // at k; the K behind that and the next V go to k_to and v_to.
-    auto step = [&](int pos, typename Rows<D>::Scores& s, typename Rows<D>::Scores& n, char* k, char* v, char* k_to, char* v_to) {
+    auto step = [&](int pos, typename Rows<D, NR>::Scores& s, typename Rows<D, NR>::Scores& n, char* k, char* v, char* k_to, char* v_to) {
         sk.store(k, wave, lane);
         sv.store(v, wave, lane);
         __syncthreads();
@@ -414,70 +440,72 @@ template <int KV, int D, int W> __global__ __launch_bounds__(64 * W, D == 128 ? 
             sk.load(p.c, next, t.hk, k_to, wave, lane);
         }
         if (pos > lim_last) return;         // the wave's rows see nothing of it
-        const float top = x.tile(s, n, k, v, c);
+        const auto top = x.tile(s, n, k, v, c);
         pos += kTile;
-        if (pos <= lim_last) x.settle(n, top, c, pos + kTile - 1 > lim_first || valid != 15, pos, lim, valid, lane);
+        if (pos <= lim_last) x.settle(n, top, c, pos + kTile - 1 > lim_first || valid != 15, pos, valid, lane);
     };
     for (int pos = t.lo; pos < t.hi; pos += 2 * kTile) {
         step(pos, sa, D == 128 ? sb : sa, lds + TB, lds + 2 * TB, lds, lds + 3 * TB);
         if (pos + kTile < t.hi) step(pos + kTile, D == 128 ? sb : sa, sa, lds, lds + 3 * TB, lds + TB, lds + 2 * TB);
     }
     __syncthreads();
-    if (lds_bad >= 0) mend_rows<KV, D>(x.acc, p, t, lds_bad, lim, h);
-    const float m = x.m;
-    float l = x.l;
-    l += __shfl_xor(l, 32);
-    if (r >= t.rows) return;
-    if (t.splits > 1) {
-        const size_t at = t.unit * M + 32 * wave + (lane & 31);
-        float* po = p.part + at * D;
-        if (h == 0) {
-            p.ml[at * 2] = m;
-            p.ml[at * 2 + 1] = l;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        if (lds_bad >= 0) mend_rows<KV, D>(x.acc[n], p, t, lds_bad, x.lim[n], h);
+        const int r = w0 + 32 * n + (lane & 31), tok = p.by_g.div(r), head = t.hk * p.G + r - tok * p.G;
+        const float l = x.l[n] + __shfl_xor(x.l[n], 32);
+        if (r >= t.rows) continue;
+        auto& acc = x.acc[n];
+        if (t.splits > 1) {
+            const size_t at = t.unit * M + (r - t.r0);
+            float* po = p.part + at * D;
+            if (h == 0) {
+                p.ml[at * 2] = x.m[n];
+                p.ml[at * 2 + 1] = l;
+            }
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<f32x4*>(po + 32 * db + 8 * j + 4 * h) =
+                        f32x4{acc[db][4 * j], acc[db][4 * j + 1], acc[db][4 * j + 2], acc[db][4 * j + 3]};
+            continue;
         }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<f32x4*>(po + 32 * db + 8 * j + 4 * h) =
-                    f32x4{x.acc[db][4 * j], x.acc[db][4 * j + 1], x.acc[db][4 * j + 2], x.acc[db][4 * j + 3]};
-        return;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+            for (int e = 0; e < 16; ++e) acc[db][e] *= inv;
+        const size_t out = ((size_t)head * D + 4 * h) * 2;
+        if (p.z) {
+            const char* z = p.z + (size_t)(t.first + tok) * p.z_stride + out;
 #pragma unroll
-    for (int db = 0; db < DB; ++db)
+            for (int db = 0; db < DB; ++db)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x.acc[db][e] *= inv;
-    const size_t out = ((size_t)head * D + 4 * h) * 2;
-    if (p.z) {
-        const char* z = p.z + (size_t)(t.first + tok) * p.z_stride + out;
+                for (int j = 0; j < 4; ++j) {
+                    const bf16x4 zz = *reinterpret_cast<const bf16x4*>(z + 64 * db + 16 * j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[db][4 * j + i] = gate_of<bf16>(acc[db][4 * j + i], (float)zz[i]);
+                }
+        }
+        char* o = p.o + (size_t)(t.first + tok) * p.H * D * 2 + out;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bf16x4 zz = *reinterpret_cast<const bf16x4*>(z + 64 * db + 16 * j);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x.acc[db][4 * j + i] = gate_of<bf16>(x.acc[db][4 * j + i], (float)zz[i]);
+                const float y[4] = {acc[db][4 * j], acc[db][4 * j + 1], acc[db][4 * j + 2], acc[db][4 * j + 3]};
+                st_run<4>(reinterpret_cast<bf16*>(o + 64 * db + 16 * j), y);
             }
     }
-    char* o = p.o + (size_t)(t.first + tok) * p.H * D * 2 + out;
-#pragma unroll
-    for (int db = 0; db < DB; ++db)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float y[4] = {x.acc[db][4 * j], x.acc[db][4 * j + 1], x.acc[db][4 * j + 2], x.acc[db][4 * j + 3]};
-            st_run<4>(reinterpret_cast<bf16*>(o + 64 * db + 16 * j), y);
-        }
 }
 
 template <int KV, int D> hipError_t launch_chunk_kv(AttnKind kind, const AttnParams& p, int grid, hipStream_t st) {
-    if constexpr (D == 128) {
-        if (kind == kAttnChunk256) {
-            kda_attn_chunk_kernel<KV, D, 8><<<grid, 512, 0, st>>>(p);
-            return hipGetLastError();
-        }
-    }
-    kda_attn_chunk_kernel<KV, D, 4><<<grid, 256, 0, st>>>(p);
+    if (kind != kAttnChunk256)
+        kda_attn_chunk_kernel<KV, D, 4, 1><<<grid, 256, 0, st>>>(p);
+    else if constexpr (D == 128)
+        kda_attn_chunk_kernel<KV, D, 8, 1><<<grid, 512, 0, st>>>(p);
+    else
+        kda_attn_chunk_kernel<KV, D, 4, 2><<<grid, 256, 0, st>>>(p);
     return hipGetLastError();
 }
 template <int D> hipError_t launch_chunk_d(AttnKind kind, int kv, const AttnParams& p, int grid, hipStream_t st) {

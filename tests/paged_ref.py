@@ -90,6 +90,8 @@ def attn_wide(q, k, v, table, positions, ranges, scale, gate=None):
     P, Hk, S, _ = k.shape
     o, mean, size = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(q[..., :1])
     for i, (first, n) in enumerate(ranges):
+        if n == 0:
+            continue
         length = min(max(int(positions[i]), 0), table.shape[1] * S)
         at = torch.arange(length, device=q.device)
         pages = table[i].long()[at // S]

@@ -356,6 +356,30 @@ def test_prompts_that_fill_the_card(kv, page, hk):
     assert torch.isnan(got[1924:, 4:8, 5]).all() and torch.isnan(got[1924:, 8:12]).all()
 
 
+@pytest.mark.parametrize("kv", [BF, E4M3, I8])
+@pytest.mark.parametrize("page,new,lens,width", [(16, [256, 300], [12000, 3001], 32768), (64, [777, 260], [777, 4096], 16384),
+                                                 (128, [500, 0, 1200], [500, 70, 1333], 32768), (64, [1025], [17000], 17024)])
+def test_long_contexts_of_narrow_heads(kv, page, new, lens, width):
+    """Heads of 64 under tables wide enough for the widest workgroups, whose rows end inside them, with a gate."""
+    hk, m = 16, sum(new)
+    c = Cache(lens, kv, hk, 64, page, seed=71)
+    more = torch.full((len(lens), width // page - c.table.shape[1]), -1, dtype=torch.int32, device=DEV)
+    c.table = torch.cat([c.table, more], 1).contiguous()
+    c.table[0, 100 // page] = -1
+    page_of, row = int(c.table[-1, 600 // page]), 600 % page
+    if kv == BF:
+        c.v_cache[page_of, 1, row, 5] = float("nan")
+    else:
+        c.v_scale.view(torch.uint8)[page_of, 1, row] = 255
+    q, z = rows(BF, m, 4 * hk, 64, 72, std=1.5), rows(BF, m, 4 * hk, 64, 73)
+    cu = cu_of(new)
+    got = kda.paged_attn(q, *c.args(), gate=z, cu_seqlens=cu)
+    k, v = (x.to(DEV) for x in c.values())
+    o, mean, size = ref.attn_wide(q.double(), k, v, c.table, lens, ref.spans(len(new), 0, cu), 64 ** -0.5, z.double())
+    o, mean, size = o.cpu(), mean.cpu(), size.cpu()
+    ref.close(got, o, torch.nan_to_num(ref.attn_bound(o, mean, size, BF, 64, max(lens)), nan=0.0, posinf=0.0), "narrow")
+
+
 def test_no_sequences_no_tokens():
     c = Cache([40, 3], BF, 2, 64, 16, seed=35)
     none = torch.empty((0, 4, 64), dtype=BF, device=DEV)
