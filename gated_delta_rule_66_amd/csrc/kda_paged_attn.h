@@ -96,7 +96,7 @@ template <typename T> __device__ __forceinline__ float gate_of(float o, float z)
 // A place that a row does not see has weight zero, and zero times NaN or an
 // infinity is NaN.  Where some row of a tile does not see all of it, such values
 // are therefore made zero before the product, and afterwards added to the rows
-// that do see them (mend_*).  A second addition changes nothing, so the mending
+// that do see them (mend_rows).  A second addition changes nothing, so the mending
 // may go over positions whose values were left in.
 __device__ __forceinline__ bool not_finite(unsigned pair) {
     return (pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u;

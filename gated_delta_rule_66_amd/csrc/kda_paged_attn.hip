@@ -14,6 +14,17 @@
 //     the transposing reads of V deliver as well.
 // P is rounded to bf16 for its product (relative 2^-8, as V's own rounding; the
 // sum is taken before it), everything else is fp32.
+//
+// Measured: 8K prompt, 32 heads of 128 over 8, bf16, gate: 522 us (1053 TFLOP/s,
+// 74 % of a large library product); 4 x 2K tokens over 32K 3.61 ms in bf16 (1181
+// TFLOP/s), 3.95 in e4m3, 4.07 in int8; 48 packed sequences over int8, 12 heads of
+// 64 over 3: 166 us.  Heads of 128: matrix units are busy half of the time, and the
+// card's clock falls as they get busier (a tenth fewer cycles a call left its time
+// as it was); 8-bit codes add their conversion on the way to LDS.  Heads of 64: the
+// exponentials and conversions of the vector units.
+// Tried and left out: a higher wave priority during products (bf16 1.5 % faster,
+// e4m3 2.5 % slower); heads of 64 with sums from a product with ones (2 % slower)
+// or with scores a tile ahead beside them (spills at three waves a SIMD).
 #include "kda_paged_attn.h"
 
 namespace kda {

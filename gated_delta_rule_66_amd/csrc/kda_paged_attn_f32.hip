@@ -9,7 +9,9 @@
 // cache head): a workgroup's four waves take blocks of 32 positions in turn and
 // keep maximum, sum and output of their own, joined at the end.  (128 rows, 32 a
 // wave, and blocks shared in LDS left ragged batches with too few workgroups: 16
-// sequences x 5 heads of 64, 184 us.)
+// sequences x 5 heads of 64, 184 us; now 116, 79 TFLOP/s, half of a large library
+// product; 8 x 512 over 4K, heads of 64, 106 TFLOP/s.  Eight waves: 142 us; 64 rows a
+// workgroup: 132; two accumulators a product: no change.)
 //   * S^T = K Q^T, the row in the lane: lane half h holds neighbouring channels
 //     of one position, one 16-byte load; their order is free if Q has the same.
 //   * O^T = V^T P^T: a result register of S^T, position 8 (e / 4) + 4 h + e % 4,

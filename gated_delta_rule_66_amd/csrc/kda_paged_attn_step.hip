@@ -21,6 +21,11 @@
 // and without), and outputs are off by their own rounding alone.  With 32 rows
 // the registers for it would have to be spilled: there P is rounded to bf16.
 // Everything else is fp32.
+//
+// Measured: 256 sequences of up to 8K, 32 heads of 128 over 8, one token each: bf16
+// 743 us, 5.75 TB/s (a large copy moves 5.1); e4m3 5.4 TB/s, int8 5.0, heads of 64
+// 4.9 to 5.6; one sequence of 1M in e4m3 376 us, 5.7 TB/s; 64 x 4 tokens 227 us.
+// One sequence of 501 positions takes 11 us, the host's way into the call.
 #include "kda_paged_attn.h"
 
 namespace kda {

@@ -672,7 +672,9 @@ kda_status kda_kv_cache_read(int N, const int* cu_seqlens, int T, kda_dtype dt, 
  * there) does not reach it, NaN and infinities included.  A token whose scores
  * are all -infinity is as one without a position.  bf16: scores, maxima
  * and sums are fp32; weights are rounded to bf16 for their product with v, so o
- * is off by its own rounding and 2^-8 of the weighted mean of |v|.
+ * is off by its own rounding and 2^-8 of the weighted mean of |v|; where a batch
+ * has up to 16 rows (tokens times H / heads) a sequence on average, they go into
+ * it as two bf16, and o is off by its own rounding and 2^-16 of that mean.
  */
 size_t kda_paged_attn_workspace_size(int N, int packed, int T, int H, kda_dtype dt, const kda_paged_cache* cache);
 kda_status kda_paged_attn(int N, const int* cu_seqlens, int T, int H, kda_dtype dt, float scale, const void* q,
