@@ -97,6 +97,8 @@ def attn_wide(q, k, v, table, positions, ranges, scale, gate=None):
         pages = table[i].long()[at // S]
         there = (pages >= 0) & (pages < P)
         at, pages = at[there], pages[there]
+        if len(at) == 0:
+            continue
         ki, vi = (c[pages, :, at % S].transpose(0, 1).contiguous() for c in (k, v))         # [Hk, C, D]
         seen = at <= (length - n + torch.arange(n, device=q.device))[:, None]               # [n, C]
         for h in range(Hk):

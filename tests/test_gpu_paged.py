@@ -560,6 +560,38 @@ def test_captured_and_replayed(dt, kv, new):
         assert torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("dt,kv,d,t,hk,width", [(BF, BF, 128, 1, 2, 16384), (BF, E4M3, 64, 8, 2, 16384),
+                                                (BF, I8, 128, 40, 2, 16384), (BF, BF, 64, 300, 16, 32768),
+                                                (F32, F32, 64, 9, 2, 16384)])
+def test_replays_whose_lengths_cross_ranges(dt, kv, d, t, hk, width):
+    """One graph, lengths from none to the table's end in any order: ranges that appear and vanish between replays leave
+    nothing of the replay before.  (One token, few, a chunk, the widest rows, fp32.)"""
+    c = Cache([width, width], kv, hk, d, 64, seed=81)
+    q = rows(dt, 2 * t, 4 * hk, d, 82).view(2, t, 4 * hk, d)
+    out = torch.empty_like(q)
+    call = lambda o: kda.paged_attn(q, *c.args(), out=o)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(out)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out)
+    for lens in ([width, 1], [1, 0], [5000, width], [width, width - 1], [0, 0], [700, 9000], [width, 1]):
+        c.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got, eager = out.clone(), call(None)
+        assert torch.equal(got, eager), lens
+        k, v = (x.to(DEV) for x in c.values())
+        flat = q.reshape(-1, 4 * hk, d).double()
+        o, mean, size = (x.cpu() for x in ref.attn_wide(flat, k, v, c.table, lens, ref.spans(2, t, None), d ** -0.5))
+        ref.close(got.reshape(o.shape), o, ref.attn_bound(o, mean, size, dt, d, width), lens)
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with a workspace and an output of its own, equal the same calls in turn."""
     c = Cache([6000, 900], BF, 2, 128, 64, seed=46)
