@@ -5,6 +5,8 @@
 #include "kda_internal.h"
 #include "kda_paged.h"
 
+#include <algorithm>
+
 using namespace kda;
 
 namespace {
@@ -154,12 +156,13 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     // and 408 us), but with two waves a SIMD instead of three, which pays where a
     // workgroup walks some thousand positions (512 over 32K in int8 178 and 211 us,
     // over 8K 58 and 55, a 4K prompt 106 and 95, 2K 53 and 39).  Sequences of a batch
-    // are taken for half as long as their table is wide (16 x 777 over up to 8K 212
-    // and 182, 48 up to 777 over up to 4K in int8 180 and 166, 8 over up to 32K 470 and 688).
+    // are taken for half as long as their table is wide, and have to fill several
+    // tiles (packed, 32 heads over 8, 6 up to 600 over up to 16K 344 and 166, 8 up to
+    // 777 353 and 320; 4 x 2K over 32K, 12 over 3, in int8 958 and 1047).
     if (a.kind == kAttnChunk && per >= 1024) {
         const long long units = M * G / 256 * c->heads, at_a_time = units < 512 ? units : 512;
         const long long before = (long long)c->blocks * c->page_size / (N > 1 ? 2 : 1) - M / N / 2;
-        if (c->head_dim == 128 ? units >= 512 : before * at_a_time >= 512 * 3800) a.kind = kAttnChunk256;
+        if (c->head_dim == 128 ? units >= 512 : (N == 1 || per >= 4096) && before * at_a_time >= 512 * 3800) a.kind = kAttnChunk256;
     }
     a.M = a.kind == kAttnStep16 ? 16 : a.kind == kAttnChunk ? 128 : a.kind == kAttnChunk256 ? 256 : 32;
     const bool step = a.kind == kAttnStep16 || a.kind == kAttnStep32;
@@ -175,14 +178,20 @@ AttnPlan attn_plan(int N, bool packed, int T, int H, kda_dtype dt, const kda_pag
     // us), up to 12288 ranges, whose parts are 200 MB at most.  At least 512
     // positions, 1024 in chunks: below that the join's launch costs more than the
     // ranges save (a 1K prompt in two 34 us, in one 27).
-    const long long want = step && N > 1 ? 1536 : 512;
-    const long long least = step || a.kind == kAttnF32 ? 512 : 1024;
-    long long n = units > 0 ? want / units : 1;
-    if (step && N > 1 && n < 3 && 3 * units <= 12288) n = 3;
-    if (n < 1 || M * H >= 1LL << 23) n = 1;
-    long long len = n > 1 ? (ctx + n - 1) / n : ctx;
-    len = (len + 127) / 128 * 128;
-    if (len < least) len = least;
+    // Chunks of a batch differ in length too, and its longest would end alone: up to
+    // four times as many where that splits a tile in three or more (12 heads of 128
+    // over 3, 4 x 777 over up to 32K 527 -> 294 us, in int8 776 -> 359; 3 packed up
+    // to 1500, 32 heads over 8, 1172 -> 1030; equal lengths that fill the card as they
+    // are, 2 x 1K over 16K, 488 -> 529), at least 2048 positions each.  In two costs
+    // the join for little (8 packed up to 777 over up to 16K 491 and 583).  Of 256 rows
+    // (4 x 2K over 32K, 12 heads of 64 over 3, in int8) 512, 1024: 1205, 958 us.
+    auto length = [&](long long n) { return n > 1 ? ((ctx + n - 1) / n + 127) / 128 * 128 : (ctx + 127) / 128 * 128; };
+    const bool joined = M * H < 1LL << 23 && units > 0, batch = joined && N > 1;
+    const long long want = step && N > 1 ? 1536 : a.kind == kAttnChunk256 && N > 1 && units < 512 ? 1024 : 512;
+    long long n = joined ? want / units : 1;
+    if (batch && step && n < 3 && 3 * units <= 12288) n = 3;
+    long long len = std::max(length(n), step || a.kind == kAttnF32 ? 512LL : 1024LL);
+    if (batch && a.kind == kAttnChunk && 2048 / units >= 3) len = std::min(len, std::max(length(2048 / units), 2048LL));
     a.split_len = (int)len;
     a.splits = ctx > 0 ? (int)((ctx + len - 1) / len) : 1;
     if (a.splits > 1) {

@@ -358,9 +358,11 @@ def test_prompts_that_fill_the_card(kv, page, hk):
 
 @pytest.mark.parametrize("kv", [BF, E4M3, I8])
 @pytest.mark.parametrize("page,new,lens,width", [(16, [256, 300], [12000, 3001], 32768), (64, [777, 260], [777, 4096], 16384),
-                                                 (128, [500, 0, 1200], [500, 70, 1333], 32768), (64, [1025], [17000], 17024)])
+                                                 (128, [500, 0, 1200], [500, 70, 1333], 32768), (64, [1025], [17000], 17024),
+                                                 (16, [1100, 1000], [2000, 1200], 16384),
+                                                 (64, [1500, 600], [17000, 601], 32768)])
 def test_long_contexts_of_narrow_heads(kv, page, new, lens, width):
-    """Heads of 64 under tables wide enough for the widest workgroups, whose rows end inside them, with a gate."""
+    """Heads of 64 under wide tables, whose rows end inside workgroups (the widest, where they fill several), with a gate."""
     hk, m = 16, sum(new)
     c = Cache(lens, kv, hk, 64, page, seed=71)
     more = torch.full((len(lens), width // page - c.table.shape[1]), -1, dtype=torch.int32, device=DEV)
@@ -562,10 +564,11 @@ def test_captured_and_replayed(dt, kv, new):
 
 @pytest.mark.parametrize("dt,kv,d,t,hk,width", [(BF, BF, 128, 1, 2, 16384), (BF, E4M3, 64, 8, 2, 16384),
                                                 (BF, I8, 128, 40, 2, 16384), (BF, BF, 64, 300, 16, 32768),
+                                                (BF, E4M3, 64, 1024, 8, 32768), (BF, BF, 128, 200, 4, 16384),
                                                 (F32, F32, 64, 9, 2, 16384)])
 def test_replays_whose_lengths_cross_ranges(dt, kv, d, t, hk, width):
     """One graph, lengths from none to the table's end in any order: ranges that appear and vanish between replays leave
-    nothing of the replay before.  (One token, few, a chunk, the widest rows, fp32.)"""
+    nothing of the replay before.  (One token, few, chunks, the widest rows, fp32.)"""
     c = Cache([width, width], kv, hk, d, 64, seed=81)
     q = rows(dt, 2 * t, 4 * hk, d, 82).view(2, t, 4 * hk, d)
     out = torch.empty_like(q)
