@@ -373,9 +373,10 @@ __global__ __launch_bounds__(64 * W, D == 128 || NR == 2 ? 2 : 3) void kda_attn_
     if (!t.init(p, blockIdx.x)) return;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
 
-    // the wave's first and last limits
+    // The wave's first and last limits.  The last is cut off at the range's end: the
+    // scores behind its last tile are those of K that an earlier tile left.
     const int w0 = t.r0 + RW * wave, lim_first = t.limit(w0, p), t_first = t.limit(t.r0, p);
-    const int lim_last = w0 < t.rows ? t.limit(min(w0 + RW - 1, t.rows - 1), p) : -1;
+    const int lim_last = w0 < t.rows ? min(t.limit(min(w0 + RW - 1, t.rows - 1), p), t.hi - 1) : -1;
     Rows<D, NR> x;
 #pragma unroll
     for (int n = 0; n < NR; ++n) {

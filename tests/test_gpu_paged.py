@@ -620,3 +620,42 @@ def test_profile_names():
     kda.kv_cache_read(*c.args(), 1)
     names = [n for n, _ in kda.profile_stop(8)]
     assert names == ["cache_write", "attn_step", "attn_join", "cache_read"]
+
+
+# kernel -> (tokens, heads, cache heads, head dim, dtypes, width of the table, positions, length of a range)
+SPLIT = {"step16": (1, 8, 2, 128, 8192, 2600, 512), "step32": (5, 8, 2, 64, 8192, 2600, 512),
+         "chunk": (70, 8, 2, 128, 8192, 4200, 1024), "chunk narrow": (70, 8, 2, 64, 8192, 4200, 1024),
+         "chunk wide rows": (64, 32, 2, 64, 262144, 9300, 4096), "fp32": (9, 8, 2, 64, 8192, 2600, 512)}
+
+
+@pytest.mark.parametrize("poison", [3e4, float("inf"), float("nan")])
+@pytest.mark.parametrize("page,at", [(16, -128), (16, -64), (16, 0), (64, -128), (64, -64), (64, 0)])
+@pytest.mark.parametrize("kernel,kv", [(k, kv) for k in SPLIT for kv in ((F32, I8) if k == "fp32" else (BF, E4M3, I8))])
+def test_holes_where_ranges_meet(kernel, kv, page, at, poison):
+    """64 positions without a page in the first, the second last or the last tile of every range.  Page 0, which no
+    sequence has, holds keys and values that would drown every other."""
+    t, H, hk, d, width, length, span = SPLIT[kernel]
+    dt = F32 if kernel == "fp32" else BF
+    c = Cache([length], kv, hk, d, page, seed=91, blocks=width // page)
+    take = int((~torch.isin(torch.arange(c.pages, dtype=torch.int32), c.table.cpu())).nonzero()[0])
+    for cache in (c.k_cache, c.v_cache, c.k_scale, c.v_scale):
+        if cache is not None:
+            raw = cache if cache.dtype == kv else cache.view(torch.uint8)
+            raw[take] = raw[0].clone()
+    c.table[c.table == 0] = take
+    if kv in ref.LARGEST:       # the codes' largest number, or their NaN
+        for cache, scale in ((c.k_cache, c.k_scale), (c.v_cache, c.v_scale)):
+            cache[0] = torch.tensor(ref.LARGEST[kv]).to(kv).to(DEV)
+            scale.view(torch.uint8)[0] = 133 if poison == 3e4 else 255
+    else:
+        c.k_cache[0] = 1.0 if poison == float("inf") else poison
+        c.k_cache[0, ..., 0] = poison
+        c.v_cache[0] = poison
+    for b in range(span, length, span):
+        first = b + at
+        c.table[0, first // page:(first + 64) // page] = -1
+    q = rows(dt, t, H, d, 92, std=1.5)
+    got = kda.paged_attn(q.view(1, t, H, d), *c.args()).view(t, H, d)
+    k, v = (x.to(DEV) for x in c.values())
+    o, mean, size = (x.cpu() for x in ref.attn_wide(q.double(), k, v, c.table, [length], [(0, t)], d ** -0.5))
+    ref.close(got, o, ref.attn_bound(o, mean, size, dt, d, length), kernel)
