@@ -94,12 +94,23 @@ template <typename T> __device__ __forceinline__ float gate_of(float o, float z)
 
 // ---- values of V that are not finite ---------------------------------------------------
 // A place that a row does not see has weight zero, and zero times NaN or an
-// infinity is NaN.  Where some row of a tile does not see all of it, such values
-// are therefore made zero before the product, and afterwards added to the rows
-// that do see them (mend_rows).  A second addition changes nothing, so the mending
-// may go over positions whose values were left in.
+// infinity is NaN.  Where some row of a tile does not see all of it (and where a
+// weight has two parts), such values are therefore made zero before the product,
+// and afterwards added to the rows that do see them (mend_rows).  A second addition
+// changes nothing, so the mending may go over positions whose values were left in.
 __device__ __forceinline__ bool not_finite(unsigned pair) {
     return (pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u;
+}
+// some value of a block's pairs: the largest exponents
+template <int A, int B> __device__ __forceinline__ bool not_finite(const unsigned (&pairs)[A][B]) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int a = 0; a < A; ++a)
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, pairs[a][b] & 0x7f807f80u));
+    return not_finite(__builtin_bit_cast(unsigned, top));
 }
 __device__ __forceinline__ unsigned clean(unsigned pair) {
     return ((pair & 0x7f80u) == 0x7f80u ? 0u : pair & 0xffffu) | ((pair & 0x7f800000u) == 0x7f800000u ? 0u : pair & 0xffff0000u);

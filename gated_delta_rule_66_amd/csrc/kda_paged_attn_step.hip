@@ -117,6 +117,12 @@ template <int KV, int D> struct Block {
         }
         return __builtin_bit_cast(bf16x8, u);
     }
+    // Whether some scale of the lane's rows of V is from 2^113 on: no code under a
+    // smaller one reaches 2^128, which is infinity in bf16.  (The byte's upper four bits.)
+    __device__ __forceinline__ bool large_scales() const {
+        const unsigned a = vs[0] & vs[0] << 1, b = vs[1] & vs[1] << 1;
+        return ((a & a << 2) | (b & b << 2)) & 0x80808080u;
+    }
     // V's eight positions as pairs of bf16: [position][DV / 2]
     __device__ __forceinline__ void vpairs(unsigned (&o)[8][DV / 2]) const {
 #pragma unroll
@@ -176,7 +182,7 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
     }
     const float c = p.c_log2, lazy = kLazy / c;
 
-    int bad_from = -1;      // the wave's first block of V with a value taken out
+    int bad_from = -1, bad_to = -1;     // the wave's first and last blocks of V with a value taken out
     int pos = t.lo + 32 * wave;
     if (pos < t.hi) {
         PageWalk<true> walk;
@@ -261,14 +267,14 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
             }
             unsigned vp[8][DV / 2];
             b.vpairs(vp);
-            if (masked) {
-                bool bad = false;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int w = 0; w < DV / 2; ++w) bad |= not_finite(vp[i][w]);
-                if (__any(bad)) {
+            // A weight's second part may be zero or below zero, so that it must not meet an
+            // infinity at all: with two parts these are looked for in every block.
+            bool look = masked;
+            if constexpr (TWO) look = masked || !Block<KV, D>::CODES || __any(b.large_scales());
+            if (look) {
+                if (__any(not_finite(vp))) {
                     if (bad_from < 0) bad_from = pos;
+                    bad_to = pos;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -296,7 +302,7 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
     }
     if (bad_from >= 0) {
 #pragma unroll 1
-        for (int i = bad_from; i < t.hi; i += i % 32 == 31 ? 97 : 1)
+        for (int i = bad_from; i < min(t.hi, bad_to + 32); i += i % 32 == 31 ? 97 : 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll

@@ -659,3 +659,44 @@ def test_holes_where_ranges_meet(kernel, kv, page, at, poison):
     k, v = (x.to(DEV) for x in c.values())
     o, mean, size = (x.cpu() for x in ref.attn_wide(q.double(), k, v, c.table, [length], [(0, t)], d ** -0.5))
     ref.close(got, o, ref.attn_bound(o, mean, size, dt, d, length), kernel)
+
+
+@pytest.mark.parametrize("dt,kv", [(BF, BF), (F32, F32)])
+@pytest.mark.parametrize("H,hk,d,page", [(8, 2, 128, 64), (16, 1, 64, 16), (4, 4, 64, 32)])
+@pytest.mark.parametrize("t", [1, 5, 24, 70])
+def test_infinities_that_every_token_sees(dt, kv, H, hk, d, page, t):
+    """Infinities and NaN among the values of positions that all rows see whole blocks around: every token's sum has
+    them, whatever its weights (a weight's own rounding may leave zero or fall below it)."""
+    lens = [300, 700]
+    c = Cache(lens, kv, hk, d, page, seed=93)
+    inf = float("inf")
+    for i, pos in ((0, 5), (0, 40), (1, 5), (1, 130), (1, 513)):
+        at = int(c.table[i, pos // page]), slice(None), pos % page
+        c.v_cache[at][:, 3] = inf
+        c.v_cache[at][:, 20] = -inf
+        c.v_cache[at][:, 37] = float("nan")
+        c.v_cache[at][:, 50] = inf if pos == 5 else -inf        # both: NaN
+    q = rows(dt, 2 * t, H, d, 94).view(2, t, H, d)
+    got = check_attn(c, q, [t, t], "infinities", packed=False)
+    assert (got[..., 3] == inf).all() and (got[..., 20] == -inf).all()
+    assert torch.isnan(got[..., 37]).all() and torch.isnan(got[..., 50]).all()
+    got[..., [3, 20, 37, 50]] = 0.0
+    assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("kv", [E4M3, I8])
+@pytest.mark.parametrize("t", [1, 5, 24, 70])
+def test_codes_beyond_the_largest_number(dt, kv, t):
+    """Codes whose values pass 2^128 are infinite or the largest numbers: never NaN, where every token sees them."""
+    H, hk, d, page = 8, 2, 64, 16
+    c = Cache([300, 700], kv, hk, d, page, seed=95)
+    sign = torch.where(torch.arange(d) % 3 == 0, -1.0, 1.0)
+    for i, pos in ((0, 5), (1, 130), (1, 513)):
+        at = int(c.table[i, pos // page]), slice(None), pos % page
+        c.v_cache[at] = (sign * ref.LARGEST[kv]).expand(hk, d).to(kv).to(DEV)
+        c.v_scale.view(torch.uint8)[at] = 254
+    q = rows(dt, 2 * t, H, d, 96).view(2, t, H, d)
+    got = kda.paged_attn(q, *c.args()).float().cpu()
+    assert not torch.isnan(got).any()
+    assert (got * sign > 2.0 ** 96).all()       # weights here are above 2^-24, the rest of a sum below 2^4
