@@ -144,3 +144,42 @@ def close(got, want, bound, what):
         assert (over <= 0).all(), "%s: over its bound by %.3g at %s (want %.6g, got %.6g)" % (
             what, over.max(), tuple(int(x) for x in torch.unravel_index(over.argmax(), over.shape)),
             want.flatten()[over.argmax()], got.flatten()[over.argmax()])
+
+
+def attn_bound_two(o, mean, positions):
+    """attn_bound() of cancelling(): bf16, weights as two bf16 (2^-16 of each stays out), scores that are exact.  What
+    scores of up to 2 lose in fp32 on their way to a weight: the rounding of log2(e), of the maximum times it and of
+    the exponent (5 x 2 x 2^-24), the same again for each of four moves of the maximum (6 x 2 x 2^-24 each), five
+    exponentials (2^-23 each); then the sum over the positions, and the same of the divisor relative to o."""
+    fp32 = (58 + 10 + 2 * (positions + 64)) * 2.0 ** -24
+    return (HALF[torch.bfloat16] + 2.0 ** -16 + fp32) * o.abs() + (2.0 ** -16 + fp32) * (1 + 2.0 ** -7) * mean + 1e-30
+
+
+def cancelling(n, t, length, H, hk, d, kv, seed):
+    """n sequences of t tokens at the end of `length` positions whose outputs nearly vanish, so that their own rounding
+    hides nothing of their weights': (q [n t, H, d], k and v [n length, hk, d]), exact in bf16.  Scores (scale 1) are
+    products of one channel; the first position's value takes back what the others add up to, in each channel for one
+    of the rows."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.zeros(n * t, H, d)
+    q[..., 5] = torch.rand(n * t, H, generator=g) / 2 + 0.5
+    q = q.to(torch.bfloat16).double()
+    k = (torch.rand(n * length, hk, d, generator=g) * 4 - 2).to(torch.bfloat16).double()
+    v = torch.randn(n * length, hk, d, generator=g).to(torch.bfloat16).double()
+    held = k if kv not in LARGEST else values(*quantise(k, kv))
+    for i in range(n):
+        vi = v[i * length:(i + 1) * length]
+        for h in range(hk):
+            r = 0
+            for c in range(d):
+                tok, head = r // (H // hk), h * (H // hk) + r % (H // hk)
+                m = length - t + tok + 1
+                p = torch.exp(held[i * length:i * length + m, h, 5] * q[i * t + tok, head, 5])
+                vi[0, h, c] = (-(p[1:] @ vi[1:m, h, c]) / p[0]).to(torch.bfloat16).double()
+                r = (r + 1) % (t * (H // hk))
+    return q, k, v
+
+
+TWO_PARTS = [  # n, t, length, H, hk, d, page: up to 16 rows (tokens times heads a cache head) a sequence
+    (2, 1, 3, 4, 4, 64, 16), (2, 1, 40, 16, 1, 64, 32), (3, 1, 130, 32, 8, 128, 64), (2, 4, 130, 8, 2, 128, 16),
+    (1, 16, 70, 3, 3, 128, 256), (2, 2, 33, 14, 2, 64, 128)]

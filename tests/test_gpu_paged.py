@@ -700,3 +700,15 @@ def test_codes_beyond_the_largest_number(dt, kv, t):
     got = kda.paged_attn(q, *c.args()).float().cpu()
     assert not torch.isnan(got).any()
     assert (got * sign > 2.0 ** 96).all()       # weights here are above 2^-24, the rest of a sum below 2^4
+
+
+@pytest.mark.parametrize("kv", [BF, E4M3, I8])
+@pytest.mark.parametrize("n,t,length,H,hk,d,page", ref.TWO_PARTS)
+def test_weights_in_two_parts(kv, n, t, length, H, hk, d, page):
+    """Up to 16 rows a sequence: weights are off by 2^-16, not by a rounding to bf16."""
+    c = Cache([length] * n, kv, hk, d, page, seed=97)
+    q, k, v = (x.to(BF).to(DEV) for x in ref.cancelling(n, t, length, H, hk, d, kv, 98))
+    kda.kv_cache_write(k.view(n, length, hk, d), v.view(n, length, hk, d), *c.args())
+    got = kda.paged_attn(q.view(n, t, H, d), *c.args(), scale=1.0).view(n * t, H, d)
+    o, mean, _ = ref.attn(q.cpu().double(), *c.values(), c.table, c.lens, ref.spans(n, t, None), 1.0)
+    ref.close(got, o, ref.attn_bound_two(o, mean, length), "two parts")
