@@ -147,7 +147,7 @@ template <int KV> __device__ __forceinline__ int q_channel(int s, int g) {
 template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(KV == kKvBf16 && D == 128) ? 3 : 2) void kda_attn_step_kernel(AttnParams p) {
     constexpr int R = 16 * NB, DV = D / 16, KS = D / 32, LD = D + 4;
     constexpr bool TWO = NB == 1;       // two blocks of rows have no registers for it
-    __shared__ float lds_o[2][R][LD];
+    __shared__ __align__(16) float lds_o[2][R][LD];     // read and written as f32x4
     __shared__ float lds_ml[2][R][2];
     AttnTile t;
     if (!t.init(p, blockIdx.x)) return;
