@@ -17,6 +17,8 @@
 // Measured: 8K tokens x 32 heads of 128 from bf16 to e4m3 46 us, 4.4 TB/s (floor 39
 // at a large copy's rate); eight prefixes of up to 32K x 8 heads from e4m3 back to
 // bf16 146 us, 5.05 TB/s (floor 144); one token of 256 sequences 3.6 us, in a call of 10.5.
+// As they are: 8K tokens x 32 heads of 128 written in bf16 57 us (floor 52.5), in fp32
+// 105 (105); 8 x 16K tokens x 8 heads read in bf16 211 us (210), in fp32 434 (420).
 #include "kda_paged.h"
 #include "kda_paged_device.h"
 
@@ -96,19 +98,39 @@ template <int KV> __device__ __forceinline__ u32x2 encode(const float* x, unsign
     return r;
 }
 
+// A lane's eight values, held as the compiler's own vectors: HIP's uint4 and
+// float4 are structs, and the loops below, which keep a row from one turn to the
+// next, kept it in scratch memory (the fp32 read above took 851 us, the bf16 one 277).
+template <typename T> struct Eight {
+    static constexpr int N = sizeof(T) / 2;
+    u32x4 w[N];
+    __device__ __forceinline__ void load(const char* p) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
+    }
+    __device__ __forceinline__ void store(char* p) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) reinterpret_cast<u32x4*>(p)[i] = w[i];
+    }
+    __device__ __forceinline__ void to_f32(float* x) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (N == 1)
+                x[i] = __uint_as_float(i & 1 ? w[0][i / 2] & 0xffff0000u : w[0][i / 2] << 16);
+            else
+                x[i] = __uint_as_float(w[i / 4][i % 4]);
+        }
+    }
+};
+
 template <typename T, int KV, int D>
-__device__ __forceinline__ void write_row(const Pack8<T>& x, char* cache, unsigned char* scale, size_t page_bytes,
+__device__ __forceinline__ void write_row(const Eight<T>& x, char* cache, unsigned char* scale, size_t page_bytes,
                                           int Hk, int lg_page, int page, int h, int row, int lane) {
     constexpr int E = KV == kKvF32 ? 4 : KV == kKvBf16 ? 2 : 1, TEAM = D / 8;
     const size_t r = ((size_t)h << lg_page) + row;
     char* to = cache + (size_t)page * page_bytes + (r * D + lane * 8) * E;
     if constexpr (KV <= kKvBf16) {
-        if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<uint4*>(to) = x.d;
-        else {
-            *reinterpret_cast<float4*>(to) = x.a;
-            *reinterpret_cast<float4*>(to + 16) = x.b;
-        }
+        x.store(to);
     } else {
         float f[8];
         x.to_f32(f);
@@ -132,14 +154,14 @@ template <typename T, int KV, int D> __global__ __launch_bounds__(kIoTokens * D 
     const char* k = p.k + (size_t)t * p.k_stride + lane * 8 * sizeof(T);
     const char* v = p.v + (size_t)t * p.v_stride + lane * 8 * sizeof(T);
     // a head's rows are on their way while those before are written
-    Pack8<T> nk, nv;
-    nk.load(reinterpret_cast<const T*>(k) + (size_t)h0 * D);
-    nv.load(reinterpret_cast<const T*>(v) + (size_t)h0 * D);
+    Eight<T> nk, nv;
+    nk.load(k + (size_t)h0 * D * sizeof(T));
+    nv.load(v + (size_t)h0 * D * sizeof(T));
     for (int h = h0; h < h1; ++h) {
-        const Pack8<T> xk = nk, xv = nv;
+        const Eight<T> xk = nk, xv = nv;
         if (h + 1 < h1) {
-            nk.load(reinterpret_cast<const T*>(k) + (size_t)(h + 1) * D);
-            nv.load(reinterpret_cast<const T*>(v) + (size_t)(h + 1) * D);
+            nk.load(k + (size_t)(h + 1) * D * sizeof(T));
+            nv.load(v + (size_t)(h + 1) * D * sizeof(T));
         }
         write_row<T, KV, D>(xk, p.c.k, p.c.ks, p.c.k_page, p.c.Hk, p.c.lg_page, page, h, row, lane);
         write_row<T, KV, D>(xv, p.c.v, p.c.vs, p.c.v_page, p.c.Hk, p.c.lg_page, page, h, row, lane);
@@ -149,7 +171,7 @@ template <typename T, int KV, int D> __global__ __launch_bounds__(kIoTokens * D 
 // A lane's part of a row of the cache, as it is loaded and as it is read.
 template <typename T, int KV, int D> struct Row {
     static constexpr int E = KV == kKvF32 ? 4 : KV == kKvBf16 ? 2 : 1;
-    Pack8<T> x;             // codes: not used
+    Eight<T> x;             // codes: not used
     u32x2 c;
     unsigned byte;
     __device__ __forceinline__ void load(const char* cache, const unsigned char* scale, size_t page_bytes, int Hk,
@@ -157,7 +179,7 @@ template <typename T, int KV, int D> struct Row {
         const size_t r = ((size_t)h << lg_page) + row;
         const char* from = cache + (size_t)page * page_bytes + (r * D + lane * 8) * E;
         if constexpr (KV <= kKvBf16) {
-            x.load(reinterpret_cast<const T*>(from));
+            x.load(from);
         } else {
             c = *reinterpret_cast<const u32x2*>(from);
             byte = scale[(((size_t)page * Hk) << lg_page) + r];
@@ -165,12 +187,7 @@ template <typename T, int KV, int D> struct Row {
     }
     __device__ __forceinline__ void store(T* to) const {
         if constexpr (KV <= kKvBf16) {
-            if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<uint4*>(to) = x.d;
-            } else {
-                *reinterpret_cast<float4*>(to) = x.a;
-                *reinterpret_cast<float4*>(to + 4) = x.b;
-            }
+            x.store(reinterpret_cast<char*>(to));
         } else {
             const Codes<KV> d(byte);
             if constexpr (sizeof(T) == 2) {
