@@ -439,7 +439,8 @@ __global__ __launch_bounds__(64 * W, D == 128 || NR == 2 ? 2 : 3) void kda_attn_
                 u32x4 y = w[64 * W * i];
                 if (not_finite(y[0]) || not_finite(y[1]) || not_finite(y[2]) || not_finite(y[3])) {
                     w[64 * W * i] = u32x4{clean(y[0]), clean(y[1]), clean(y[2]), clean(y[3])};
-                    bad = true;
+                    // (what stands in for a place that is not there is no row's to have back)
+                    bad |= valid >> ((threadIdx.x + 64 * W * i) / (2 * D)) & 1;
                 }
             }
             if (bad && lds_bad < 0) lds_bad = pos;

@@ -187,7 +187,8 @@ template <int KV, int D> __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void
                 if (masked) {       // what is not finite must not meet a weight of zero
 #pragma unroll
                     for (int j = 0; j < DV; ++j) {
-                        bad |= !finite_f(f[j]);
+                        // (what stands in for a place that is not there is no row's to have back)
+                        bad |= !finite_f(f[j]) && (valid >> (e >> 3) & 1);
                         f[j] = finite_f(f[j]) ? f[j] : 0.f;
                     }
                 }

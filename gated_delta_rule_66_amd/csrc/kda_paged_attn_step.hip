@@ -272,6 +272,12 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
             bool look = masked;
             if constexpr (TWO) look = masked || !Block<KV, D>::CODES || __any(b.large_scales());
             if (look) {
+                // (what stands in for a place that is not there is no row's to have back)
+                if (valid != 3)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int w = 0; w < DV / 2; ++w) vp[i][w] = valid >> (i >> 2) & 1 ? vp[i][w] : 0u;
                 if (__any(not_finite(vp))) {
                     if (bad_from < 0) bad_from = pos;
                     bad_to = pos;

@@ -712,3 +712,35 @@ def test_weights_in_two_parts(kv, n, t, length, H, hk, d, page):
     got = kda.paged_attn(q.view(n, t, H, d), *c.args(), scale=1.0).view(n * t, H, d)
     o, mean, _ = ref.attn(q.cpu().double(), *c.values(), c.table, c.lens, ref.spans(n, t, None), 1.0)
     ref.close(got, o, ref.attn_bound_two(o, mean, length), "two parts")
+
+
+@pytest.mark.parametrize("dt,n,t,H,hk,d,page", [(BF, 4, 512, 32, 8, 128, 16), (BF, 4, 512, 32, 8, 64, 64), (BF, 1, 1, 8, 2, 128, 64),
+                                                (BF, 8, 4, 16, 2, 128, 16), (F32, 1, 9, 8, 2, 64, 64)])
+def test_time_does_not_go_by_what_stands_in_for_missing_pages(dt, n, t, H, hk, d, page):
+    """Long sequences whose first pages are gone, and a page 0, no sequence's, of NaN or of zeros: the same bits, and
+    no more than twice the time (it was 3 to 37 times)."""
+    length = 16384
+    blocks = length // page
+    pool = [torch.randn((n * blocks + 1, hk, page, d), generator=gen(99 + i)).to(dt).to(DEV) for i in range(2)]
+    table = torch.randperm(n * blocks, generator=gen(101)).view(n, blocks) + 1
+    table[:, :blocks // 8] = -1
+    table, lens = table.to(torch.int32).to(DEV), torch.full((n,), length, dtype=torch.int32, device=DEV)
+    q = rows(dt, n * t, H, d, 102).view(n, t, H, d)
+    outs, times = [], []
+    for fill in (0.0, float("nan")):
+        for p in pool:
+            p[0] = fill
+        out = torch.empty_like(q)
+        best = float("inf")
+        for _ in range(6):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            for _ in range(3):
+                kda.paged_attn(q, *pool, table, lens, out=out)
+            end.record()
+            torch.cuda.synchronize()
+            best = min(best, start.elapsed_time(end))
+        outs.append(out)
+        times.append(best)
+    assert torch.equal(*outs) and torch.isfinite(outs[0]).all()
+    assert times[1] < 2 * times[0], times
