@@ -484,11 +484,11 @@ __global__ __launch_bounds__(64 * W, D == 128 || NR == 2 ? 2 : 3) void kda_attn_
                         f32x4{acc[db][4 * j], acc[db][4 * j + 1], acc[db][4 * j + 2], acc[db][4 * j + 3]};
             continue;
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = 1.f / l;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[db][e] *= inv;
+            for (int e = 0; e < 16; ++e) acc[db][e] = l == 0.f ? 0.f : acc[db][e] * inv;
         const size_t out = ((size_t)head * D + 4 * h) * 2;
         if (p.z) {
             const char* z = p.z + (size_t)(t.first + tok) * p.z_stride + out;

@@ -390,7 +390,7 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
             continue;
         }
         const int tok = p.by_g.div(r), head = t.hk * p.G + r - tok * p.G;
-        const float inv = l[nb] == 0.f ? 0.f : 1.f / l[nb];
+        const float inv = 1.f / l[nb];
         const size_t at = (size_t)head * D;
         bf16* o = reinterpret_cast<bf16*>(p.o) + (size_t)(t.first + tok) * p.H * D + at;
         const bf16* z = reinterpret_cast<const bf16*>(p.z + (size_t)(t.first + tok) * p.z_stride) + at;
@@ -398,7 +398,7 @@ template <int KV, int D, int NB> __global__ __launch_bounds__(256, NB == 1 && !(
         for (int e = 0; e < 4; ++e) {
             float x[DV];
 #pragma unroll
-            for (int j = 0; j < DV; ++j) x[j] = acc[j][nb][e] * inv;
+            for (int j = 0; j < DV; ++j) x[j] = l[nb] == 0.f ? 0.f : acc[j][nb][e] * inv;
             const int d = DV * (4 * g + e);
             if (p.z) {
 #pragma unroll

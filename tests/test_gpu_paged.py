@@ -744,3 +744,21 @@ def test_time_does_not_go_by_what_stands_in_for_missing_pages(dt, n, t, H, hk, d
         times.append(best)
     assert torch.equal(*outs) and torch.isfinite(outs[0]).all()
     assert times[1] < 2 * times[0], times
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("length", [130, 5000])
+@pytest.mark.parametrize("t", [1, 5, 24, 70])
+def test_scores_of_minus_infinity(dt, t, length):
+    """A token whose scores are all -infinity gets zeros, whatever the values; one that sees another position gets that one's."""
+    H, hk, d, page = 8, 2, 64, 16
+    c = Cache([length, length], dt, hk, d, page, seed=103)
+    c.k_cache[..., 0] = -float("inf")
+    c.v_cache[int(c.table[0, 1]), :, 3, 7] = float("inf")
+    c.v_cache[int(c.table[0, 2]), :, 4, 9] = float("nan")
+    at = int(c.table[1, 3]), slice(None), 5
+    c.k_cache[at][:, 0] = 1.0
+    q = rows(dt, 2 * t, H, d, 104).view(2, t, H, d)
+    q[..., 0] = 1.0
+    got = kda.paged_attn(q, *c.args())
+    assert not got[0].any() and torch.equal(got[1], c.v_cache[at].repeat_interleave(H // hk, 0).expand(t, H, d))
