@@ -18,9 +18,11 @@
 // Up to 16 rows, P goes into its product as two bf16, itself and what its
 // rounding left (2^-16 of it stay out): with the products far from being the
 // bound, the second costs nothing (256 sequences 743 us, 64 x 4 tokens 228, with
-// and without), and outputs are off by their own rounding alone.  With 32 rows
-// the registers for it would have to be spilled: there P is rounded to bf16.
-// Everything else is fp32.
+// and without), and outputs are off by their own rounding alone.  The second part
+// may be zero or negative, which an infinity in V must not meet: V is looked
+// through in every block, by a running maximum of its exponents (the same times
+// with and without; comparisons of each value spilled some 140 scalar registers).  With 32 rows the registers for a second part would have to be
+// spilled: there P is rounded to bf16.  Everything else is fp32.
 //
 // Measured: 256 sequences of up to 8K, 32 heads of 128 over 8, one token each: bf16
 // 743 us, 5.75 TB/s (a large copy moves 5.1); e4m3 5.4 TB/s, int8 5.0, heads of 64

@@ -665,12 +665,15 @@ kda_status kda_kv_cache_read(int N, const int* cu_seqlens, int T, kda_dtype dt, 
  *   gate : [tokens, H, head_dim] dt or NULL, row stride gate_stride
  *   o    : [tokens, H, head_dim] dt, contiguous; a token with no position to
  *          attend to gets zeros
- *   scale: above zero, scale log2(e) finite
+ *   scale: above zero, scale log2(e) finite; where it takes a finite q.k out of
+ *          fp32's range, that token's output is not defined
  *   workspace : kda_paged_attn_workspace_size(...) bytes
  * q, gate, o and workspace 16-byte aligned, strides multiples of 16 bytes.
  * What is at positions that a token does not attend to (behind it, or not
- * there) does not reach it, NaN and infinities included.  A token whose scores
- * are all -infinity is as one without a position.  bf16: scores, maxima
+ * there) does not reach it, NaN and infinities included; an infinite value at a
+ * position that it does attend to makes its sum that infinity (NaN beside a NaN
+ * or the other infinity, and maybe under a weight below 2^-126).  A token whose
+ * scores are all -infinity is as one without a position.  bf16: scores, maxima
  * and sums are fp32; weights are rounded to bf16 for their product with v, so o
  * is off by its own rounding and 2^-8 of the weighted mean of |v|; where a batch
  * has up to 16 rows (tokens times H / heads) a sequence on average, they go into
