@@ -19,8 +19,8 @@
 // 74 % of a large library product); 4 x 2K tokens over 32K 3.61 ms in bf16 (1181
 // TFLOP/s), 3.95 in e4m3, 4.07 in int8; 48 packed sequences over int8, 12 heads of
 // 64 over 3: 166 us.  Heads of 128: matrix units are busy half of the time, and the
-// card's clock falls as they get busier (2.0 GHz in the prompt, 53 % busy, 1.7 in
-// 4 x 2K over 32K in bf16, 59 %, 2.4 where they rest; a tenth fewer cycles a call
+// card's clock falls as they get busier (2.03 GHz in the prompt, 53 % busy, 1.93 in
+// 4 x 2K over 32K in bf16, 59 %, 2.40 where they rest; a tenth fewer cycles a call
 // left its time as it was); 8-bit codes add their conversion on the way to LDS.  Heads of 64: the
 // exponentials and conversions of the vector units.
 // Tried and left out: a higher wave priority during products (bf16 1.5 % faster,
