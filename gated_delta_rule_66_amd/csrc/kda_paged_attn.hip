@@ -433,18 +433,18 @@ __global__ __launch_bounds__(64 * W, D == 128 || NR == 2 ? 2 : 3) void kda_attn_
         sv.store(v, wave, lane);
         __syncthreads();
         if (pos + kTile - 1 > t_first || valid != 15) {     // some row of the tile's sees only a part
-            bool bad = false;
+            int bad = 0;            // bits of groups of 16 rows, from the thread's first on
             u32x4* w = reinterpret_cast<u32x4*>(v) + threadIdx.x;
 #pragma unroll
             for (int i = 0; i < TB / (1024 * W); ++i) {
                 u32x4 y = w[64 * W * i];
                 if (not_finite(y[0]) || not_finite(y[1]) || not_finite(y[2]) || not_finite(y[3])) {
                     w[64 * W * i] = u32x4{clean(y[0]), clean(y[1]), clean(y[2]), clean(y[3])};
-                    // (what stands in for a place that is not there is no row's to have back)
-                    bad |= valid >> ((threadIdx.x + 64 * W * i) / (2 * D)) & 1;
+                    bad |= 1 << (64 * W / (2 * D)) * i;
                 }
             }
-            if (bad && lds_bad < 0) lds_bad = pos;
+            // (what stands in for a place that is not there is no row's to have back)
+            if (bad && (bad << threadIdx.x / (2 * D) & valid) && lds_bad < 0) lds_bad = pos;
             __syncthreads();
         }
         valid = next.valid;
